@@ -173,8 +173,9 @@ def _values(x, random=None):
 
 def _encode(x):
     """x [rows, cols] as the library holds it: codes [rows, 128 ceil(cols/256)],
-    two to a byte (even element in the low half), and scale bytes [rows,
-    16 ceil(cols/512)]; codes past the end are 0, scale bytes 127."""
+    two to a byte (even element in the low half), and scale bytes
+    [ceil(cols/512), rows, 16], the 16 blocks of 512 columns of a row side by
+    side; codes past the end are 0, scale bytes 127."""
     rows, cols = x.shape
     g, s = _fake_quantize(x)
     a = g.abs()
@@ -186,11 +187,20 @@ def _encode(x):
     q = code[:, 0::2] + 16 * code[:, 1::2]
     sb = (torch.frexp(s)[1] + 126).to(torch.uint8)
     sb = torch.nn.functional.pad(sb, (0, -(-cols // 512) * 16 - sb.shape[1]), value=127)
-    return q, sb
+    return q, sb.reshape(rows, -1, 16).transpose(0, 1).contiguous()
+
+
+def _encode_experts(x, experts):
+    """The same of `experts` matrices stacked in x: codes [experts, rows, ..],
+    scale bytes [experts, ceil(cols/512), rows, 16]."""
+    q, sb = _encode(x)
+    sb = sb.reshape(sb.shape[0], experts, -1, 16).transpose(0, 1).contiguous()
+    return q.reshape(experts, -1, q.shape[1]), sb
 
 
 def _decode(q, sb, cols):
     """Codes and scale bytes to fp32 values [..., cols]."""
+    sb = sb.transpose(-3, -2).flatten(-2)
     code = torch.stack((q & 15, q >> 4), -1).reshape(*q.shape[:-1], -1)[..., : -(-cols // BLOCK) * BLOCK]
     c = (code & 7).float()
     mag = torch.where(c < 4, 0.5 * c, torch.where(c < 6, c - 2, 2 * c - 8))
@@ -314,10 +324,8 @@ def prepare(case, seed):
         t, e, h, i = c["tokens"], c["experts"], c["hidden"], c["inner"]
         s["x"] = _normal(g, (t, h), 1.0, device).bfloat16()
         s["router"] = _normal(g, (e, h), h ** -0.5, device).bfloat16()
-        q, sb = _encode(_normal(g, (e * 2 * i, h), h ** -0.5, device))
-        s["w1q"], s["w1s"] = q.reshape(e, 2 * i, -1), sb.reshape(e, 2 * i, -1)
-        q, sb = _encode(_normal(g, (e * h, i), i ** -0.5, device))
-        s["w2q"], s["w2s"] = q.reshape(e, h, -1), sb.reshape(e, h, -1)
+        s["w1q"], s["w1s"] = _encode_experts(_normal(g, (e * 2 * i, h), h ** -0.5, device), e)
+        s["w2q"], s["w2s"] = _encode_experts(_normal(g, (e * h, i), i ** -0.5, device), e)
     return s
 
 
@@ -330,7 +338,9 @@ def _held_values(q, sb, cols):
     pairs = torch.stack((table[(q % 16).long()], table[torch.div(q, 16, rounding_mode="floor").long()]), -1)
     v = pairs.flatten(-2)[..., :cols]
     at = torch.arange(cols, device=q.device) // BLOCK
-    return v * torch.exp2(sb.double() - 127)[..., at]
+    rows = torch.arange(q.shape[-2], device=q.device)
+    scale = torch.exp2(sb.double() - 127)[..., at[None, :] // 16, rows[:, None], at[None, :] % 16]
+    return v * scale
 
 
 def _bits(rows, cols, seed, device):
