@@ -36,6 +36,7 @@ EXPORTED = [
     "fp8_scaled_mm_workspace_size", "fp8_scaled_mm",
     "fp8_quantize_scaled_mm_workspace_size", "fp8_quantize_scaled_mm",
     "fp8_requant_workspace_size", "fp8_requant_weights",
+    "fp8_mx4_quantize", "fp8_mx4_dequantize", "fp8_mx4_mm_workspace_size", "fp8_mx4_mm",
     "fp8_counters_reset", "fp8_debug_set_wait_limit",
 ]
 
@@ -103,6 +104,14 @@ def lib():
         L.fp8_requant_weights.restype = i32
         L.fp8_requant_weights.argtypes = [ctypes.POINTER(WeightCacheDesc), ctypes.POINTER(vp),
                                           ctypes.POINTER(ctypes.c_int), ctypes.c_int32, vp, sz, vp]
+        L.fp8_mx4_quantize.restype = i32
+        L.fp8_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp]
+        L.fp8_mx4_dequantize.restype = i32
+        L.fp8_mx4_dequantize.argtypes = [vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]
+        L.fp8_mx4_mm_workspace_size.restype = sz
+        L.fp8_mx4_mm_workspace_size.argtypes = [i64, i64, i64]
+        L.fp8_mx4_mm.restype = i32
+        L.fp8_mx4_mm.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, sz, vp, vp]
         L.fp8_counters_reset.restype = i32
         L.fp8_counters_reset.argtypes = [vp, vp]
         L.fp8_debug_set_wait_limit.restype = ctypes.c_int32
@@ -168,6 +177,18 @@ def fp8_requant_weights(descs, masters, dtypes, workspace, workspace_bytes, stre
     mp = (ctypes.c_void_p * n)(*masters)
     dt = (ctypes.c_int * n)(*dtypes)
     return lib().fp8_requant_weights(arr, mp, dt, n, workspace, workspace_bytes, stream)
+
+
+def fp8_mx4_quantize(x, dtype, rows, cols, ld, q, ldq, s, ps, q_t, ldq_t, s_t, ps_t, seed, ctr, stream) -> int:
+    return lib().fp8_mx4_quantize(x, dtype, rows, cols, ld, q, ldq, s, ps, q_t, ldq_t, s_t, ps_t, seed, ctr, stream)
+
+
+def fp8_mx4_dequantize(q, ldq, s, ps, rows, cols, y, dtype, ldy, stream) -> int:
+    return lib().fp8_mx4_dequantize(q, ldq, s, ps, rows, cols, y, dtype, ldy, stream)
+
+
+def fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, workspace, workspace_bytes, ctr, stream) -> int:
+    return lib().fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, workspace, workspace_bytes, ctr, stream)
 
 
 def fp8_counters_reset(ctr, stream) -> int:
@@ -530,3 +551,144 @@ def requant_weights(caches: list[WeightCache], masters: list) -> None:
     if not caches:
         return
     RequantPlan(caches, masters)()
+
+
+# ---------------------------------------------------------------- 4-bit operands
+def mx4_shapes(rows: int, cols: int) -> tuple[tuple[int, int], tuple[int, int, int]]:
+    """Shapes of the codes and the scale bytes of a quantized [rows, cols]."""
+    return (rows, 128 * -(-cols // 256)), (-(-cols // 512), rows, 16)
+
+
+class Mx4:
+    """A tensor [..., rows, cols] in OCP microscaling FP4: `q` uint8 codes
+    [..., rows, 128 ceil(cols/256)] (two to a byte, the even column in the low
+    half, 0 past cols) and `s` uint8 E8M0 scales [..., ceil(cols/512), rows,
+    16] (one for 32 elements of a row, 127 past cols).  Rows of q and panels
+    of s may lie further apart, by multiples of 16 bytes.  One leading
+    dimension (experts) is taken by MoeMx4."""
+    __slots__ = ("q", "s", "cols")
+
+    def __init__(self, q, s, cols: int):
+        torch = _torch()
+        if q.dtype != torch.uint8 or s.dtype != torch.uint8:
+            raise ValueError(f"q and s must be torch.uint8, got {q.dtype} and {s.dtype}")
+        cols = int(cols)
+        if q.dim() not in (2, 3) or cols < 0 or q.shape[-1] != 128 * -(-cols // 256):
+            raise ValueError(f"q of {cols} columns must have shape [..., rows, {128 * -(-cols // 256)}], "
+                             f"got {tuple(q.shape)}")
+        want = (*q.shape[:-2], -(-cols // 512), q.shape[-2], 16)
+        if tuple(s.shape) != want:
+            raise ValueError(f"s must have shape {want}, got {tuple(s.shape)}")
+        if q.numel() and (q.stride(-1) != 1 or s.stride(-1) != 1 or (s.shape[-2] > 1 and s.stride(-2) != 16)):
+            raise ValueError("the bytes of a row of q and of a panel of s must be adjacent")
+        self.q, self.s, self.cols = q, s, cols
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda"):
+        torch = _torch()
+        nq, ns = mx4_shapes(rows, cols)
+        return cls(torch.empty(nq, dtype=torch.uint8, device=device),
+                   torch.empty(ns, dtype=torch.uint8, device=device), cols)
+
+    @property
+    def rows(self) -> int:
+        return self.q.shape[-2]
+
+    @property
+    def shape(self) -> tuple:
+        return (*self.q.shape[:-1], self.cols)
+
+    def _args(self):
+        """data pointer and distance of the rows of codes, of the scale panels."""
+        q, s = self.q, self.s
+        rows = q.shape[-2]
+        ldq = q.stride(-2) if rows > 1 else max(q.shape[-1], 16)
+        ps = s.stride(-3) if s.shape[-3] > 1 else 16 * rows
+        return q.data_ptr(), ldq, s.data_ptr(), ps
+
+
+def _check_mx4(t, name, rows=None, cols=None):
+    if not isinstance(t, Mx4):
+        raise ValueError(f"{name} must be an Mx4, got {type(t).__name__}")
+    if t.q.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {t.shape}")
+    if (rows is not None and t.rows != rows) or (cols is not None and t.cols != cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {t.shape}")
+
+
+def mx4_quantize(x, want_t: bool = False, seed=None, counters: Counters | None = None, out: Mx4 | None = None,
+                 out_t: Mx4 | None = None):
+    """x [rows, cols] bf16 or fp32 to (Mx4 of x, Mx4 of x^T or None).  seed:
+    None rounds to nearest even; an int64 device tensor of one element rounds
+    stochastically with the bits it draws (a captured graph reads it anew at
+    each replay)."""
+    torch = _torch()
+    _check_tensor(x, "x", (torch.bfloat16, torch.float32), unit_col_stride=True)
+    rows, cols = x.shape
+    if seed is not None:
+        _check_tensor(seed, "seed", (torch.int64,), (1,))
+    if out is not None:
+        _check_mx4(out, "out", rows, cols)
+    if out_t is not None:
+        if not want_t:
+            raise ValueError("out_t given without want_t=True")
+        _check_mx4(out_t, "out_t", cols, rows)
+    _check_devices(x, seed, out and out.q, out and out.s, out_t and out_t.q, out_t and out_t.s,
+                   counters.buf if counters else None)
+    q = out if out is not None else Mx4.empty(rows, cols, x.device)
+    qt = None
+    if want_t:
+        qt = out_t if out_t is not None else Mx4.empty(cols, rows, x.device)
+    t_args = qt._args() if qt is not None else (None, 0, None, 0)
+    if rows == 0 or cols == 0:
+        t_args = (None, 0, None, 0)
+    check(lib().fp8_mx4_quantize(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), *q._args(), *t_args,
+                                 _ptr(seed), counters.ptr() if counters else None, _stream()))
+    return q, qt
+
+
+def mx4_dequantize(a: Mx4, dtype=None, out=None):
+    """The values of a quantized matrix, in bf16 (the default) or fp32."""
+    torch = _torch()
+    _check_mx4(a, "a")
+    rows, cols = a.shape
+    if out is not None:
+        _check_tensor(out, "out", (torch.bfloat16, torch.float32), (rows, cols), unit_col_stride=True)
+        if dtype is not None and out.dtype != dtype:
+            raise ValueError(f"out must be {dtype}, got {out.dtype}")
+    elif dtype not in (None, torch.bfloat16, torch.float32):
+        raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
+    _check_devices(a.q, a.s, out)
+    y = out if out is not None else torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=a.q.device)
+    check(lib().fp8_mx4_dequantize(*a._args(), rows, cols, y.data_ptr(), _dtype_code(y), _ld(y), _stream()))
+    return y
+
+
+def mx4_mm(a: Mx4, b: Mx4, out=None, counters: Counters | None = None, workspace=None):
+    """y = A B^T of two quantized operands a [m, k] and b [n, k], bf16 [m, n].
+    workspace: optional uint8 device tensor of at least
+    fp8_mx4_mm_workspace_size(m, n, k) bytes (allocated per call when None)."""
+    torch = _torch()
+    _check_mx4(a, "a")
+    _check_mx4(b, "b")
+    m, k = a.shape
+    n = b.rows
+    if b.cols != k:
+        raise ValueError("a and b disagree on k")
+    if out is not None:
+        _check_tensor(out, "out", (torch.bfloat16,), (m, n), unit_col_stride=True)
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", (torch.uint8,), contiguous=True)
+    _check_devices(a.q, a.s, b.q, b.s, out, workspace, counters.buf if counters else None)
+    c = out if out is not None else torch.empty((m, n), dtype=torch.bfloat16, device=a.q.device)
+    L = lib()
+    wsb = L.fp8_mx4_mm_workspace_size(m, n, k)
+    if workspace is None:
+        if wsb:
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=c.device)
+    elif workspace.numel() < wsb:
+        raise ValueError(f"workspace needs {wsb} bytes, got {workspace.numel()}")
+    check(L.fp8_mx4_mm(*a._args(), *b._args(), m, n, k, c.data_ptr(), _ld(c), _ptr(workspace),
+                       workspace.numel() if workspace is not None else 0,
+                       counters.ptr() if counters else None, _stream()))
+    return c

@@ -116,6 +116,29 @@ fp8_status check_quantize_args(const void* x, fp8_dtype dtype, int64_t rows, int
     return FP8_OK;
 }
 
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// A quantized 4-bit operand [rows, cols].
+fp8_status check_mx4(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t ps, int64_t rows, int64_t cols,
+                     const char* name)
+{
+    static thread_local char buf[160];
+    const auto bad = [&](fp8_status st, const char* what) {
+        std::snprintf(buf, sizeof buf, "%s: %s", name, what);
+        return fail(st, buf);
+    };
+    if (rows < 0 || cols < 0) return bad(FP8_ERR_INVALID_ARG, "negative size");
+    if (rows >= ((int64_t)1 << 31) || cols >= ((int64_t)1 << 31))
+        return bad(FP8_ERR_UNSUPPORTED_SHAPE, "rows and cols must be below 2^31");
+    if (rows == 0 || cols == 0) return FP8_OK;
+    if (!q || !s) return bad(FP8_ERR_INVALID_ARG, "null pointer");
+    if (ldq < 128 * cdiv(cols, 256)) return bad(FP8_ERR_INVALID_ARG, "rows of codes are 128 ceil(cols/256) bytes");
+    if (cols > 512 && ps < 16 * rows) return bad(FP8_ERR_INVALID_ARG, "scale panels are 16 rows bytes");
+    if (misaligned(q, 16) || misaligned(s, 16) || ldq % 16 != 0 || ps % 16 != 0)
+        return bad(FP8_ERR_INVALID_ARG, "q, s, their row and panel distances must be multiples of 16 bytes");
+    return FP8_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -494,6 +517,100 @@ fp8_status fp8_requant_weights(const fp8_weight_cache* caches, const void* const
     }
     hipError_t e = launch_requant(args.data(), count, stream);
     return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_requant_weights launch");
+}
+
+fp8_status fp8_mx4_quantize(const void* x, fp8_dtype dtype, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
+                            int64_t ldq, uint8_t* s, int64_t ps, uint8_t* q_t, int64_t ldq_t, uint8_t* s_t,
+                            int64_t ps_t, const uint64_t* seed, fp8_counters* ctr, hipStream_t stream)
+{
+    if (!valid_dtype(dtype)) return fail(FP8_ERR_INVALID_ARG, "unknown input dtype");
+    fp8_status st;
+    if ((st = check_2d(x, rows, cols, ld, "x")) != FP8_OK) return st;
+    if ((st = check_mx4(q, ldq, s, ps, rows, cols, "q")) != FP8_OK) return st;
+    if ((q_t == nullptr) != (s_t == nullptr)) return fail(FP8_ERR_INVALID_ARG, "q_t and s_t go together");
+    if (q_t && (st = check_mx4(q_t, ldq_t, s_t, ps_t, cols, rows, "q_t")) != FP8_OK) return st;
+    if (misaligned(x, dtype == FP8_IN_BF16 ? 2 : 4)) return fail(FP8_ERR_INVALID_ARG, "x: misaligned");
+    if (misaligned(seed, 8)) return fail(FP8_ERR_INVALID_ARG, "seed: must be 8-byte aligned");
+    // one workgroup per 256 x 128 tile or 16 rows x 512 columns
+    if (cdiv(rows, 512) * cdiv(cols, 512) >= ((int64_t)1 << 27))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "tensor too large");
+    if ((st = check_device()) != FP8_OK) return st;
+    Mx4QuantArgs a;
+    a.x = x;
+    a.dtype = dtype;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld = ld;
+    a.q = q;
+    a.ldq = ldq;
+    a.s = s;
+    a.sps = ps;
+    a.qt = q_t;
+    a.ldqt = ldq_t;
+    a.st = s_t;
+    a.stps = ps_t;
+    a.seed = seed;
+    a.ctr = ctr;
+    hipError_t e = launch_mx4_quantize(a, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_quantize launch");
+}
+
+fp8_status fp8_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t ps, int64_t rows, int64_t cols,
+                              void* y, fp8_dtype dtype, int64_t ldy, hipStream_t stream)
+{
+    if (!valid_dtype(dtype)) return fail(FP8_ERR_INVALID_ARG, "unknown output dtype");
+    fp8_status st;
+    if ((st = check_mx4(q, ldq, s, ps, rows, cols, "q")) != FP8_OK) return st;
+    if ((st = check_2d(y, rows, cols, ldy, "y")) != FP8_OK) return st;
+    if (misaligned(y, dtype == FP8_IN_BF16 ? 2 : 4)) return fail(FP8_ERR_INVALID_ARG, "y: misaligned");
+    if (cdiv(rows, 512) * cdiv(cols, 512) >= ((int64_t)1 << 27))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "tensor too large");
+    if ((st = check_device()) != FP8_OK) return st;
+    hipError_t e = launch_mx4_dequantize(q, ldq, s, ps, rows, cols, y, dtype, ldy, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_dequantize launch");
+}
+
+size_t fp8_mx4_mm_workspace_size(int64_t m, int64_t n, int64_t k)
+{
+    if (m <= 0 || n <= 0 || k <= 0) return 0;
+    return mx4_gemm_workspace(m, n, k);
+}
+
+fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t psa, const uint8_t* b, int64_t ldb,
+                      const uint8_t* sb, int64_t psb, int64_t m, int64_t n, int64_t k, void* c_bf16, int64_t ldc,
+                      void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream)
+{
+    fp8_status st;
+    if ((st = check_mx4(a, lda, sa, psa, m, k, "a")) != FP8_OK) return st;
+    if ((st = check_mx4(b, ldb, sb, psb, n, k, "b")) != FP8_OK) return st;
+    if ((st = check_2d(c_bf16, m, n, ldc, "c")) != FP8_OK) return st;
+    if (misaligned(c_bf16, 2)) return fail(FP8_ERR_INVALID_ARG, "c must be 2-byte aligned");
+    if (misaligned(workspace, 16)) return fail(FP8_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    // byte offsets inside one 256-row operand or output tile are 32-bit
+    if (m > 0 && n > 0 && (lda >= ((int64_t)1 << 22) || ldb >= ((int64_t)1 << 22) || ldc >= ((int64_t)1 << 21)))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "lda, ldb must be below 2^22 and ldc below 2^21");
+    // tiles are 32 x 64 at least, one workgroup each
+    if (cdiv(m, 32) * cdiv(n, 64) >= ((int64_t)1 << 31)) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "output too large");
+    if ((st = check_device()) != FP8_OK) return st;
+    Mx4GemmArgs g;
+    g.a = a;
+    g.lda = lda;
+    g.sa = sa;
+    g.psa = psa;
+    g.b = b;
+    g.ldb = ldb;
+    g.sb = sb;
+    g.psb = psb;
+    g.m = m;
+    g.n = n;
+    g.k = k;
+    g.c = c_bf16;
+    g.ldc = ldc;
+    g.ws = static_cast<float*>(workspace);
+    g.ws_bytes = workspace ? workspace_bytes : 0;
+    g.ctr = ctr;
+    hipError_t e = launch_mx4_gemm(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_mm launch");
 }
 
 fp8_status fp8_counters_reset(fp8_counters* ctr, hipStream_t stream)

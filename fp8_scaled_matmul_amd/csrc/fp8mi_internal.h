@@ -140,4 +140,50 @@ int gemm_num_cus();
 hipError_t launch_gemm_persistent(const GemmArgs& g, int num_cus, hipStream_t stream);
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream);
 
+// 4-bit quantizer (mx4_quantize.hip).  Scale panels of 16 bytes a row lie
+// `sps` (`stps`) bytes apart.
+struct Mx4QuantArgs {
+    const void* x;
+    int dtype;
+    int64_t rows, cols, ld;
+    uint8_t* q;
+    int64_t ldq;
+    uint8_t* s;
+    int64_t sps;
+    uint8_t* qt;            // nullable: no transposed copy
+    int64_t ldqt;
+    uint8_t* st;
+    int64_t stps;
+    const uint64_t* seed;   // nullable: round to nearest even
+    fp8_counters* ctr;      // nullable
+};
+hipError_t launch_mx4_quantize(const Mx4QuantArgs& g, hipStream_t stream);
+hipError_t launch_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t sps, int64_t rows,
+                                 int64_t cols, void* y, int dtype, int64_t ldy, hipStream_t stream);
+
+// 4-bit GEMM (mx4_gemm.hip).  lda, ldb, psa, psb in bytes.
+struct Mx4GemmArgs {
+    const uint8_t* a;
+    int64_t lda;
+    const uint8_t* sa;
+    int64_t psa;
+    const uint8_t* b;
+    int64_t ldb;
+    const uint8_t* sb;
+    int64_t psb;
+    int64_t m, n, k;
+    void* c;
+    int64_t ldc;
+    float* ws;              // split-K partials, or nullptr
+    size_t ws_bytes;
+    fp8_counters* ctr;
+};
+size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream);
+// Pieces of gemm.hip that the 4-bit GEMM uses too: zeros (k = 0), and the
+// fixed-order sum of split-K partials.
+hipError_t launch_zero_bf16(uint16_t* c, int m, int n, int64_t ldc, hipStream_t stream);
+hipError_t launch_splitk_sum(const float* ws, int splits, int m, int n, uint16_t* c, int64_t ldc, fp8_counters* ctr,
+                             hipStream_t stream);
+
 }  // namespace fp8mi

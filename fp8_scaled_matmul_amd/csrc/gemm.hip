@@ -935,6 +935,31 @@ hipError_t gemm_fmt(const KArgs& p, int grid, int mode, hipStream_t stream)
 
 }  // namespace
 
+hipError_t launch_zero_bf16(uint16_t* c, int m, int n, int64_t ldc, hipStream_t stream)
+{
+    const int grid = (int)std::min<int64_t>(((int64_t)m * n + 255) / 256, 4096);
+    hipLaunchKernelGGL(k_zero_bf16, dim3(grid), dim3(256), 0, stream, c, m, n, ldc);
+    return hipGetLastError();
+}
+
+hipError_t launch_splitk_sum(const float* ws, int splits, int m, int n, uint16_t* c, int64_t ldc, fp8_counters* ctr,
+                             hipStream_t stream)
+{
+    KArgs p{};
+    p.ws = const_cast<float*>(ws);
+    p.splits = splits;
+    p.m = m;
+    p.n = n;
+    p.c = c;
+    GemmArgs g{};
+    g.m = m;
+    g.n = n;
+    g.c = c;
+    g.ldc = ldc;
+    g.ctr = ctr;
+    return launch_reduce(p, g, 0.0f, stream);
+}
+
 int gemm_num_cus()
 {
     static int n = 0;
@@ -965,11 +990,7 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream)
 {
     if (g.m == 0 || g.n == 0) return hipSuccess;
     if (g.k == 0) {
-        const int64_t total = g.m * g.n;
-        const int grid = (int)std::min<int64_t>((total + 255) / 256, 4096);
-        hipLaunchKernelGGL(k_zero_bf16, dim3(grid), dim3(256), 0, stream, static_cast<uint16_t*>(g.c), (int)g.m,
-                           (int)g.n, g.ldc);
-        return hipGetLastError();
+        return launch_zero_bf16(static_cast<uint16_t*>(g.c), (int)g.m, (int)g.n, g.ldc, stream);
     }
     KArgs p;
     p.a = g.a;

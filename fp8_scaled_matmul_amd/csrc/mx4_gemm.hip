@@ -1,0 +1,314 @@
+// 4-bit (OCP MXFP4) GEMM for gfx950: y = A B^T, A [m, k] and B [n, k] rows of
+// E2M1 codes with one E8M0 scale byte per 32 elements, fp32 accumulation,
+// bf16 output.
+//
+// y[i, j] = sum_b 2^(ea[i,b]-127) 2^(eb[j,b]-127) sum_{e in block b} A[i,e] B[j,e].
+// v_mfma_scale_f32_32x32x64_f8f6f4 computes exactly that sum for a 32 x 32
+// tile and 64 K: lane l holds 32 consecutive elements (16 bytes) of row l % 32
+// of each operand and the byte of its own block's scale, so the scales cost no
+// arithmetic and the products are exact before the fp32 sum.  The instruction
+// runs at twice the FP8 rate (about 10 PFLOP/s for the chip), which leaves
+// the feeding of operands from L2 as the bound of the large products.
+#include <algorithm>
+
+#include "device_common.h"
+#include "fp8mi_internal.h"
+#include "gemm_common.h"
+#include "mx4_common.h"
+
+namespace fp8mi {
+
+namespace {
+
+using gemm::v4f;
+using gemm::v4u;
+using gemm::v8i;
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+constexpr int kRowBytes = 128;      // one K step: 256 elements of a row
+constexpr int kScaleBytes = 16;     // a row's scale bytes of one panel (two K steps)
+
+struct MxArgs {
+    const uint8_t* a;
+    const uint8_t* b;
+    int64_t lda, ldb;               // bytes
+    const uint8_t* sa;
+    const uint8_t* sb;
+    int64_t psa, psb;               // bytes between scale panels
+    int m, n;
+    int steps;                      // K steps: ceil(k / 256)
+    int splits, steps_per;          // K splits of steps_per steps (even)
+    uint16_t* c;
+    int64_t ldc;
+    float* ws;                      // fp32 partials [splits, m, n], or null
+    int tiles_m, tiles_n, group_m;
+    int pair_store;                 // two adjacent outputs can be stored as one word
+    fp8_counters* ctr;
+};
+
+// Position of 16-byte chunk c (0..7) in the 128-byte LDS row r.  A fragment
+// read takes chunk c of 32 rows for the lower half wave and chunk c + 4 for
+// the upper: 16 lanes fill the 16 slots of a 256-byte line, 32 lanes the 32
+// slots of 512 bytes.  An involution in c.
+__device__ inline int swz32(int r, int c)
+{
+    return c ^ (((r >> 2) & 1) | ((r & 2) ^ ((r >> 3) & 2)) | ((r >> 1) & 4));
+}
+
+// Lane l's 16 bytes of K quarter q (64 elements: 32 for each half wave) of
+// row row0 + l % 32.
+__device__ inline v8i frag(const uint8_t* lds, int row0, int q)
+{
+    const int l = threadIdx.x & 63;
+    const int r = row0 + (l & 31);
+    const uint4 v = *reinterpret_cast<const uint4*>(lds + r * kRowBytes + swz32(r, 4 * (l >> 5) + q) * 16);
+    return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+}
+
+template <int Q>
+__device__ inline v16f mfma(const v8i& a, const v8i& b, const v16f& c, uint32_t ea, uint32_t eb)
+{
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, Q, (int)ea, Q, (int)eb);
+}
+
+// Linear workgroup id to (split, tile row, tile column): ids go to the XCDs
+// in turn, so XCD x takes a contiguous range of the tile order, which walks
+// group_m tile rows at a time.
+__device__ inline void item_of(const MxArgs& p, int bid, int& split, int& tm, int& tn)
+{
+    const int total = p.tiles_m * p.tiles_n * p.splits;
+    const int xcd = bid & 7, local = bid >> 3;
+    const int pid = xcd * (total >> 3) + min(xcd, total & 7) + local;
+    const int per_split = p.tiles_m * p.tiles_n;
+    split = pid / per_split;
+    const int t = pid - split * per_split;
+    const int in_group = p.group_m * p.tiles_n;
+    const int g = t / in_group;
+    const int first_m = g * p.group_m;
+    const int gsize = min(p.tiles_m - first_m, p.group_m);
+    const int r = t - g * in_group;
+    tm = first_m + r % gsize;
+    tn = r / gsize;
+}
+
+// Stores one wave's MF x 2 accumulators: rows row0 + 32 i + 8 (r / 4) +
+// 4 (lane / 32) + r % 4, columns col and col + 1 (col already the lane's).
+template <int MF>
+__device__ inline uint32_t store_out(const MxArgs& p, const v16f (&acc)[MF][2], int row0, int col, int split)
+{
+    const int lane = threadIdx.x & 63;
+    uint32_t nonfinite = 0;
+    if (col >= p.n) return 0;
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int row = row0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+            if (row >= p.m) continue;
+            const float lo = acc[i][0][r], hi = acc[i][1][r];
+            if (p.ws) {
+                float* w = p.ws + ((int64_t)split * p.m + row) * p.n + col;
+                w[0] = lo;
+                if (col + 1 < p.n) w[1] = hi;
+                continue;
+            }
+            const uint32_t h = gemm::pack_bf16(lo, hi);
+            uint16_t* c = p.c + row * p.ldc + col;
+            nonfinite += (h & 0x7F80u) == 0x7F80u;
+            if (p.pair_store && col + 1 < p.n) {
+                __builtin_nontemporal_store(h, reinterpret_cast<uint32_t*>(c));
+                nonfinite += (h & 0x7F800000u) == 0x7F800000u;
+            } else {
+                c[0] = (uint16_t)h;
+                if (col + 1 < p.n) {
+                    c[1] = (uint16_t)(h >> 16);
+                    nonfinite += (h & 0x7F800000u) == 0x7F800000u;
+                }
+            }
+        }
+    return nonfinite;
+}
+
+// ------------------------------------------------------------------ one tile per workgroup
+// WR x WC waves of MF x 2 fragments (32 MF x 64 outputs) each.  A ring of
+// STAGES K steps in LDS, filled by DMA STAGES - 1 steps ahead; one barrier a
+// step: past it every wave has read the step before, whose slot the next DMA
+// refills.  Rows of B lie permuted in each 64-row group (LDS row R holds row
+// 2 (R % 32) + R / 32), so that a lane ends up with two adjacent outputs of a
+// row and a half wave with 128 adjacent bytes.
+template <int WR, int WC, int MF, int STAGES>
+__global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
+{
+    constexpr int W = WR * WC;
+    constexpr int TM = 32 * MF * WR, TN = 64 * WC;
+    constexpr int kA = TM * kRowBytes, kB = TN * kRowBytes;
+    constexpr int kStage = kA + kB + (TM + TN) * kScaleBytes;
+    constexpr int kData = (TM + TN) / 8 / W;        // DMA instructions of a wave and step
+    constexpr int kScale = (TM + TN) / 64;          // over all waves
+    static_assert((TM + TN) / 8 % W == 0 && TM / 8 % W == 0, "whole DMA instructions");
+    static_assert(kScale <= W || kScale % W == 0, "scale DMA");
+    constexpr int kScalePer = (kScale + W - 1) / W;
+    constexpr int kPer = kData + kScalePer;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    int split, tm, tn;
+    item_of(p, blockIdx.x, split, tm, tn);
+    const int m0 = tm * TM, n0 = tn * TN;
+    const int kt0 = split * p.steps_per;
+    const int nt = min(p.steps, kt0 + p.steps_per) - kt0;
+    const int64_t rows_a = min(p.m - m0, TM), rows_b = min(p.n - n0, TN);
+    const v4u ra = gemm::make_rsrc(p.a + (int64_t)m0 * p.lda, (uint32_t)(rows_a * p.lda));
+    const v4u rb = gemm::make_rsrc(p.b + (int64_t)n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+    const uint32_t base = gemm::lds_addr(lds);
+
+    // K step t of this split into its ring slot: kPer instructions per wave
+    const auto fill = [&](int t) {
+        const bool live = t < nt;
+        const int slot = t % STAGES, kb = kt0 + t;
+        const uint32_t to = base + slot * kStage;
+        const int q = lane >> 3, pos = lane & 7;
+#pragma unroll
+        for (int j = 0; j < kData; ++j) {
+            const int R = 8 * (j * W + wave) + q;       // LDS row: A's, then B's
+            uint32_t off;
+            v4u rs;
+            if (8 * (j * W) < TM) {                     // uniform in j: TM is a multiple of 8 W
+                off = (uint32_t)(R * p.lda + 16 * swz32(R, pos));
+                rs = ra;
+            } else {
+                const int Rb = R - TM;
+                const int g = (Rb & ~63) + 2 * (Rb & 31) + ((Rb >> 5) & 1);
+                off = (uint32_t)(g * p.ldb + 16 * swz32(Rb, pos));
+                rs = rb;
+            }
+            rs.z = live ? rs.z : 0u;
+            gemm::dma16(to + 1024 * (j * W + wave), off + (uint32_t)kb * kRowBytes, rs);
+        }
+#pragma unroll
+        for (int j = 0; j < kScalePer; ++j) {
+            const int u = j * W + wave;                 // 64 rows of scales; past the last: a repeat of it
+            const int uu = min(u, kScale - 1);
+            const int64_t panel = kb >> 1;
+            const uint8_t* src;
+            uint32_t off, bytes;
+            if (uu < TM / 64) {
+                src = p.sa + panel * p.psa + (int64_t)m0 * kScaleBytes;
+                bytes = (uint32_t)rows_a * kScaleBytes;
+                off = (uint32_t)(64 * uu + lane) * kScaleBytes;
+            } else {
+                src = p.sb + panel * p.psb + (int64_t)n0 * kScaleBytes;
+                bytes = (uint32_t)rows_b * kScaleBytes;
+                off = (uint32_t)(64 * (uu - TM / 64) + 2 * (lane & 31) + (lane >> 5)) * kScaleBytes;
+            }
+            gemm::dma16(to + kA + kB + 1024 * uu, off, gemm::make_rsrc(src, live ? bytes : 0u));
+        }
+    };
+
+    v16f acc[MF][2];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    const int wm = (wave % WR) * 32 * MF, wn = (wave / WR) * 64;
+#pragma unroll
+    for (int t = 0; t < STAGES - 1; ++t) fill(t);
+    for (int t = 0; t < nt; ++t) {
+        // all but the newest STAGES - 2 steps have landed
+        if constexpr (kPer * (STAGES - 2) == 0)
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer * (STAGES - 2)) : "memory");
+        gemm::barrier_lds();
+        fill(t + STAGES - 1);
+        const uint8_t* st = lds + (t % STAGES) * kStage;
+        const uint8_t* la = st;
+        const uint8_t* lb = st + kA;
+        const uint8_t* ls = st + kA + kB + ((kt0 + t) & 1) * 8 + 4 * (lane >> 5);
+        uint32_t ea[MF], eb[2];
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            ea[i] = *reinterpret_cast<const uint32_t*>(ls + (wm + 32 * i + (lane & 31)) * kScaleBytes);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            eb[j] = *reinterpret_cast<const uint32_t*>(ls + (TM + wn + 32 * j + (lane & 31)) * kScaleBytes);
+        const auto quarter = [&](auto Q) {
+            constexpr int q = decltype(Q)::value;
+            v8i fa[MF], fb[2];
+#pragma unroll
+            for (int i = 0; i < MF; ++i) fa[i] = frag(la, wm + 32 * i, q);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) fb[j] = frag(lb, wn + 32 * j, q);
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma<q>(fa[i], fb[j], acc[i][j], ea[i], eb[j]);
+        };
+        quarter(std::integral_constant<int, 0>{});
+        quarter(std::integral_constant<int, 1>{});
+        quarter(std::integral_constant<int, 2>{});
+        quarter(std::integral_constant<int, 3>{});
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint32_t nonfinite = store_out<MF>(p, acc, m0 + wm, n0 + wn + 2 * (lane & 31), split);
+    if (!p.ws) flush_counters(p.ctr, 0, 0, 0, nonfinite);
+}
+
+template <int WR, int WC, int MF, int STAGES>
+hipError_t launch_tile(MxArgs p, hipStream_t stream)
+{
+    constexpr int TM = 32 * MF * WR, TN = 64 * WC;
+    constexpr int kLds = STAGES * ((TM + TN) * (kRowBytes + kScaleBytes));
+    p.tiles_m = (p.m + TM - 1) / TM;
+    p.tiles_n = (p.n + TN - 1) / TN;
+    p.group_m = 4;
+    const auto kernel = k_mx4_tile_gemm<WR, WC, MF, STAGES>;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(p.tiles_m * p.tiles_n * p.splits), dim3(64 * WR * WC), kLds, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k)
+{
+    (void)m;
+    (void)n;
+    (void)k;
+    return 0;
+}
+
+hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
+{
+    if (g.m == 0 || g.n == 0) return hipSuccess;
+    if (g.k == 0) return launch_zero_bf16(static_cast<uint16_t*>(g.c), (int)g.m, (int)g.n, g.ldc, stream);
+    MxArgs p;
+    p.a = g.a;
+    p.b = g.b;
+    p.lda = g.lda;
+    p.ldb = g.ldb;
+    p.sa = g.sa;
+    p.sb = g.sb;
+    p.psa = g.psa;
+    p.psb = g.psb;
+    p.m = (int)g.m;
+    p.n = (int)g.n;
+    p.steps = (int)((g.k + mx4::kRowAlign - 1) / mx4::kRowAlign);
+    p.splits = 1;
+    p.steps_per = p.steps + (p.steps & 1);
+    p.c = static_cast<uint16_t*>(g.c);
+    p.ldc = g.ldc;
+    p.ws = nullptr;
+    p.pair_store = g.ldc % 2 == 0 && (reinterpret_cast<uintptr_t>(g.c) & 3u) == 0;
+    p.ctr = g.ctr;
+    return launch_tile<2, 2, 2, 4>(p, stream);
+}
+
+}  // namespace fp8mi

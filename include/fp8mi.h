@@ -316,6 +316,61 @@ fp8_status fp8_requant_weights(const fp8_weight_cache* caches, const void* const
                                const fp8_dtype* master_dtypes, int32_t count,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------ 4-bit operands
+ * OCP microscaling FP4 (MXFP4): a row is cut into blocks of 32 consecutive
+ * elements; each element is an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives, codes 0..7 and 8..15) and each block has one E8M0 scale
+ * byte b that stands for 2^(b-127); 255 makes the whole block NaN.
+ * A quantized [rows, cols] tensor is
+ *   q   rows of 128 ceil(cols/256) bytes, ldq bytes apart: two codes a byte,
+ *       the even column in the low half, codes past `cols` 0;
+ *   s   ceil(cols/512) panels of [rows, 16] scale bytes, ps bytes apart
+ *       (ps >= 16 rows): byte 16 r + i of panel p is block 16 p + i of row r;
+ *       bytes of blocks past `cols` 127.  The scales of one K step of many
+ *       rows are one contiguous run.
+ * q and s are 16-byte aligned, ldq and ps multiples of 16.
+ *
+ * Quantize: per block, s = the smallest power of two with amax / s <= 6
+ * (amax over the finite elements; 1 when it is 0; at least 2^-126), then
+ * x / s on the E2M1 grid.
+ *   seed NULL   round to nearest, ties to the even code.
+ *   seed        DEVICE pointer to 64 bits: round stochastically.  The value v
+ *       between neighbours lo < v < hi goes up when
+ *       (v - lo) / (hi - lo) + r / 65536 >= 1, r the element's 16 random bits:
+ *         mix(v): v ^= v>>16; v *= 0x6A09E667; v ^= v>>15; v *= 0xBB67AE85; v ^= v>>16
+ *         mix(mix(row * 0x9E3779B1 + seed_lo) ^ ((col>>1) * 0x3C6EF373 + seed_hi))
+ *       (all mod 2^32), the low half for an even column, the high half for an
+ *       odd one.  Both copies use the same element's bits.
+ *   +-Inf -> +-6 (counted as saturated); a block that holds a NaN gets the
+ *   scale byte 255 and codes 0 (each NaN counted).  underflow counts non-zero
+ *   elements of other blocks whose code is +-0.  Counters follow q alone.
+ *   q_t, s_t    optional: the quantization of the transpose x^T [cols, rows]
+ *       (blocks of 32 rows of a column, with scales of their own).
+ * x as in fp8_quantize, bf16 or fp32; rows and cols below 2^31. */
+fp8_status fp8_mx4_quantize(const void* x, fp8_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                            uint8_t* q, int64_t ldq, uint8_t* s, int64_t ps,
+                            uint8_t* q_t, int64_t ldq_t, uint8_t* s_t, int64_t ps_t,
+                            const uint64_t* seed, fp8_counters* ctr, hipStream_t stream);
+
+/* y[r, c] = the value code and scale stand for, in bf16 or fp32 (exact but
+ * for values past the type's range, which become Inf). */
+fp8_status fp8_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t ps,
+                              int64_t rows, int64_t cols, void* y, fp8_dtype dtype, int64_t ldy,
+                              hipStream_t stream);
+
+/* y [m, n] bf16 = A B^T, A quantized [m, k], B quantized [n, k]: exact
+ * products, fp32 sums (K splits in a fixed order), one rounding to nearest
+ * even.  Codes past k are read: they have to be 0 in A or B, and no scale
+ * byte there 255 (as fp8_mx4_quantize leaves them).  lda, ldb below 2^22
+ * bytes, ldc below 2^21, m, n and k below 2^31; k = 0 writes zeros.
+ * workspace: fp8_mx4_mm_workspace_size() bytes, 16-byte aligned; without it
+ * K is not split (slower for short outputs).  ctr counts nonfinite_out. */
+size_t     fp8_mx4_mm_workspace_size(int64_t m, int64_t n, int64_t k);
+fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t psa,
+                      const uint8_t* b, int64_t ldb, const uint8_t* sb, int64_t psb,
+                      int64_t m, int64_t n, int64_t k, void* c_bf16, int64_t ldc,
+                      void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream);
+
 /* Zero a counter block on `stream` (a small fill kernel, safe to capture). */
 fp8_status fp8_counters_reset(fp8_counters* ctr, hipStream_t stream);
 

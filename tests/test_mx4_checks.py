@@ -1,0 +1,117 @@
+"""Refusals of the 4-bit entry points, on the CPU: the C ABI rejects bad
+arguments before it touches the device, the binding before it calls it."""
+import pytest
+import torch
+
+import fp8_scaled_matmul_amd as fm
+
+BAD = 0x1000        # non-null, aligned, never dereferenced: every call fails before
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import os
+    if not os.path.exists(fm.LIB_PATH):
+        from fp8_scaled_matmul_amd import build
+        build.build()
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(dtype=5), fm.FP8_ERR_INVALID_ARG),
+    (dict(rows=-1), fm.FP8_ERR_INVALID_ARG),
+    (dict(ld=10), fm.FP8_ERR_INVALID_ARG),
+    (dict(x=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(x=BAD + 1), fm.FP8_ERR_INVALID_ARG),
+    (dict(q=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(q=BAD + 8), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldq=255), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldq=264), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldq=128), fm.FP8_ERR_INVALID_ARG),
+    (dict(s=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(s=BAD + 4), fm.FP8_ERR_INVALID_ARG),
+    (dict(cols=513, ld=513, ldq=384, ps=16 * 63), fm.FP8_ERR_INVALID_ARG),
+    (dict(q_t=BAD), fm.FP8_ERR_INVALID_ARG),
+    (dict(s_t=BAD), fm.FP8_ERR_INVALID_ARG),
+    (dict(q_t=BAD, s_t=BAD, ldq_t=64), fm.FP8_ERR_INVALID_ARG),
+    (dict(seed=BAD + 4), fm.FP8_ERR_INVALID_ARG),
+    (dict(rows=1 << 31), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+])
+def test_quantize_rejects_before_device(args, code):
+    a = dict(x=BAD, dtype=fm.BF16, rows=64, cols=512, ld=513, q=BAD, ldq=256, s=BAD, ps=1024, q_t=None, ldq_t=0,
+             s_t=None, ps_t=0, seed=None, ctr=None)
+    a.update(args)
+    assert fm.fp8_mx4_quantize(*a.values(), None) == code, fm.lib().fp8_last_error()
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(dtype=3), fm.FP8_ERR_INVALID_ARG),
+    (dict(q=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(y=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldy=511), fm.FP8_ERR_INVALID_ARG),
+    (dict(y=BAD + 2, dtype=fm.FP32), fm.FP8_ERR_INVALID_ARG),
+])
+def test_dequantize_rejects_before_device(args, code):
+    a = dict(q=BAD, ldq=256, s=BAD, ps=1024, rows=64, cols=512, y=BAD, dtype=fm.BF16, ldy=512)
+    a.update(args)
+    assert fm.fp8_mx4_dequantize(*a.values(), None) == code, fm.lib().fp8_last_error()
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(m=-1), fm.FP8_ERR_INVALID_ARG),
+    (dict(a=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(b=BAD + 8), fm.FP8_ERR_INVALID_ARG),
+    (dict(sb=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(lda=128), fm.FP8_ERR_INVALID_ARG),
+    (dict(psb=16 * 47), fm.FP8_ERR_INVALID_ARG),
+    (dict(psb=16 * 48 + 8), fm.FP8_ERR_INVALID_ARG),
+    (dict(c=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(c=BAD + 1), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldc=47), fm.FP8_ERR_INVALID_ARG),
+    (dict(ws=BAD + 8), fm.FP8_ERR_INVALID_ARG),
+    (dict(lda=1 << 22), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+    (dict(ldc=1 << 21), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+    (dict(k=1 << 31), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+])
+def test_mm_rejects_before_device(args, code):
+    a = dict(a=BAD, lda=384, sa=BAD, psa=16 * 32, b=BAD, ldb=384, sb=BAD, psb=16 * 48, m=32, n=48, k=768, c=BAD,
+             ldc=48, ws=None, wsb=0, ctr=None)
+    a.update(args)
+    assert fm.fp8_mx4_mm(*a.values(), None) == code, fm.lib().fp8_last_error()
+
+
+def _mx4(rows, cols):
+    return fm.Mx4.empty(rows, cols, "cpu")
+
+
+def test_mx4_layout_is_checked():
+    q, s = torch.zeros(5, 256, dtype=torch.uint8), torch.zeros(1, 5, 16, dtype=torch.uint8)
+    assert fm.Mx4(q, s, 500).shape == (5, 500)
+    for bad in [(q.short(), s, 500), (q, s, 256), (q, s, 513), (q, s.reshape(5, 1, 16), 500),
+                (q.t().contiguous().t(), s, 500), (q, s.expand(1, 5, 16)[..., ::1].transpose(1, 2), 500)]:
+        with pytest.raises(ValueError):
+            fm.Mx4(*bad)
+
+
+def test_binding_rejects():
+    x = torch.zeros(8, 64, dtype=torch.bfloat16)
+    for kw in [dict(x=x.half()), dict(x=x[0]), dict(x=x.t()), dict(seed=torch.zeros(1)),
+               dict(seed=torch.zeros(2, dtype=torch.int64)), dict(out=_mx4(8, 65)), dict(out=x),
+               dict(out_t=_mx4(64, 8)), dict(want_t=True, out_t=_mx4(8, 64))]:
+        with pytest.raises(ValueError):
+            fm.mx4_quantize(**{"x": x, **kw})
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.mx4_quantize(x)
+    with pytest.raises(ValueError, match="out must"):
+        fm.mx4_dequantize(_mx4(8, 64), out=torch.zeros(8, 63))
+    with pytest.raises(ValueError, match="dtype"):
+        fm.mx4_dequantize(_mx4(8, 64), torch.float16)
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.mx4_dequantize(_mx4(8, 64))
+    with pytest.raises(ValueError, match="disagree"):
+        fm.mx4_mm(_mx4(8, 64), _mx4(8, 65))
+    with pytest.raises(ValueError, match="a must be an Mx4"):
+        fm.mx4_mm(x, _mx4(8, 64))
+    with pytest.raises(ValueError, match="out must"):
+        fm.mx4_mm(_mx4(8, 64), _mx4(9, 64), out=torch.zeros(8, 9))
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.mx4_mm(_mx4(8, 64), _mx4(9, 64))
