@@ -37,6 +37,7 @@ EXPORTED = [
     "fp8_quantize_scaled_mm_workspace_size", "fp8_quantize_scaled_mm",
     "fp8_requant_workspace_size", "fp8_requant_weights",
     "fp8_mx4_quantize", "fp8_mx4_dequantize", "fp8_mx4_mm_workspace_size", "fp8_mx4_mm",
+    "fp8_mx4_moe_workspace_size", "fp8_mx4_moe",
     "fp8_counters_reset", "fp8_debug_set_wait_limit",
 ]
 
@@ -45,6 +46,11 @@ class Fp8Error(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__(f"{_status_name(status)}: {detail}")
         self.status = status
+
+
+class Mx4Experts(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("eq", ctypes.c_int64),
+                ("ps", ctypes.c_int64), ("es", ctypes.c_int64)]
 
 
 class WeightCacheDesc(ctypes.Structure):
@@ -112,6 +118,11 @@ def lib():
         L.fp8_mx4_mm_workspace_size.argtypes = [i64, i64, i64]
         L.fp8_mx4_mm.restype = i32
         L.fp8_mx4_mm.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, sz, vp, vp]
+        L.fp8_mx4_moe_workspace_size.restype = sz
+        L.fp8_mx4_moe_workspace_size.argtypes = [i64] * 5
+        L.fp8_mx4_moe.restype = i32
+        L.fp8_mx4_moe.argtypes = [vp, i64, i64, i64, vp, i64, ctypes.POINTER(Mx4Experts), ctypes.POINTER(Mx4Experts),
+                                  i64, i64, i64, ctypes.c_int32, vp, i64, vp, vp, vp, sz, vp, vp]
         L.fp8_counters_reset.restype = i32
         L.fp8_counters_reset.argtypes = [vp, vp]
         L.fp8_debug_set_wait_limit.restype = ctypes.c_int32
@@ -189,6 +200,12 @@ def fp8_mx4_dequantize(q, ldq, s, ps, rows, cols, y, dtype, ldy, stream) -> int:
 
 def fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, workspace, workspace_bytes, ctr, stream) -> int:
     return lib().fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, workspace, workspace_bytes, ctr, stream)
+
+
+def fp8_mx4_moe(x, tokens, hidden, ldx, router, ldr, w1, w2, experts, inner, top_k, renormalize, y, ldy, ids, weights,
+                workspace, workspace_bytes, ctr, stream) -> int:
+    return lib().fp8_mx4_moe(x, tokens, hidden, ldx, router, ldr, w1, w2, experts, inner, top_k, renormalize, y, ldy,
+                             ids, weights, workspace, workspace_bytes, ctr, stream)
 
 
 def fp8_counters_reset(ctr, stream) -> int:
@@ -692,3 +709,63 @@ def mx4_mm(a: Mx4, b: Mx4, out=None, counters: Counters | None = None, workspace
                        workspace.numel() if workspace is not None else 0,
                        counters.ptr() if counters else None, _stream()))
     return c
+
+
+class MoeMx4:
+    """A mixture-of-experts layer with 4-bit weights, set up once: router
+    [experts, hidden] bf16, w1 Mx4 [experts, 2 inner, hidden] (gate rows, then
+    up rows), w2 Mx4 [experts, hidden, inner].  A call takes x [tokens <=
+    max_tokens, hidden] bf16 and returns (y bf16 [tokens, hidden], ids int32
+    and weights fp32 [tokens, top_k]).  renormalize: the chosen experts'
+    weights sum to 1 (else the softmax runs over all experts).  The tensors
+    are held by reference; their storage must stay where it is.  The layer
+    owns a workspace: one call at a time."""
+    MAX_TOKENS = 64
+
+    def __init__(self, router, w1: Mx4, w2: Mx4, top_k: int, max_tokens: int = MAX_TOKENS, renormalize: bool = True,
+                 counters: Counters | None = None):
+        torch = _torch()
+        _check_tensor(router, "router", (torch.bfloat16,), unit_col_stride=True)
+        experts, hidden = router.shape
+        for t, name in ((w1, "w1"), (w2, "w2")):
+            if not isinstance(t, Mx4) or t.q.dim() != 3:
+                raise ValueError(f"{name} must be an Mx4 of one matrix per expert")
+        inner = w2.cols
+        if w1.shape != (experts, 2 * inner, hidden) or w2.shape != (experts, hidden, inner):
+            raise ValueError(f"w1 must be [experts, 2 inner, hidden] and w2 [experts, hidden, inner] with experts, "
+                             f"hidden = {experts}, {hidden}; got {w1.shape} and {w2.shape}")
+        if not 1 <= top_k <= experts or not 1 <= max_tokens <= self.MAX_TOKENS:
+            raise ValueError(f"top_k must be 1 to {experts}, max_tokens 1 to {self.MAX_TOKENS}")
+        _check_devices(router, w1.q, w1.s, w2.q, w2.s, counters.buf if counters else None)
+        self.router, self.w1, self.w2, self.counters = router, w1, w2, counters
+        self.experts, self.hidden, self.inner, self.top_k = experts, hidden, inner, int(top_k)
+        self.max_tokens, self.renormalize = int(max_tokens), bool(renormalize)
+        wsb = lib().fp8_mx4_moe_workspace_size(self.max_tokens, experts, self.top_k, hidden, inner)
+        if wsb == 0:
+            raise ValueError("at most 512 experts, top_k 16, hidden and inner below 2^24")
+        self._ws = torch.zeros(wsb, dtype=torch.uint8, device=router.device)
+
+        def held(w):
+            return Mx4Experts(w.q.data_ptr(), w.s.data_ptr(), w.q.stride(1) if w.rows > 1 else w.q.shape[2],
+                              w.q.stride(0) if experts > 1 else 0,
+                              w.s.stride(1) if w.s.shape[1] > 1 else 16 * w.rows, w.s.stride(0) if experts > 1 else 0)
+
+        self._w1, self._w2 = held(w1), held(w2)
+
+    def __call__(self, x, out=None):
+        torch = _torch()
+        _check_tensor(x, "x", (torch.bfloat16,), unit_col_stride=True)
+        tokens = x.shape[0]
+        if x.shape[1] != self.hidden or tokens > self.max_tokens:
+            raise ValueError(f"x must be [at most {self.max_tokens}, {self.hidden}], got {tuple(x.shape)}")
+        if out is not None:
+            _check_tensor(out, "out", (torch.bfloat16,), (tokens, self.hidden), unit_col_stride=True)
+        _check_devices(x, self.router, out)
+        y = out if out is not None else torch.empty((tokens, self.hidden), dtype=torch.bfloat16, device=x.device)
+        ids = torch.empty((tokens, self.top_k), dtype=torch.int32, device=x.device)
+        weights = torch.empty((tokens, self.top_k), dtype=torch.float32, device=x.device)
+        check(lib().fp8_mx4_moe(x.data_ptr(), tokens, self.hidden, _ld(x), self.router.data_ptr(), _ld(self.router),
+                                self._w1, self._w2, self.experts, self.inner, self.top_k, self.renormalize,
+                                y.data_ptr(), _ld(y), ids.data_ptr(), weights.data_ptr(), self._ws.data_ptr(),
+                                self._ws.numel(), self.counters.ptr() if self.counters else None, _stream()))
+        return y, ids, weights

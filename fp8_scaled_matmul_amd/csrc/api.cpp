@@ -116,6 +116,10 @@ fp8_status check_quantize_args(const void* x, fp8_dtype dtype, int64_t rows, int
     return FP8_OK;
 }
 
+// Limits of the mixture-of-experts layer: a 64-bit mask of an expert's tokens,
+// 32-bit offsets inside an expert's row tile.
+constexpr int64_t kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxWidth = (int64_t)1 << 24;
+
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 // A quantized 4-bit operand [rows, cols].
@@ -611,6 +615,65 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
     g.ctr = ctr;
     hipError_t e = launch_mx4_gemm(g, stream);
     return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_mm launch");
+}
+
+size_t fp8_mx4_moe_workspace_size(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner)
+{
+    if (tokens <= 0 || tokens > kMoeMaxTokens || experts <= 0 || experts > kMoeMaxExperts || top_k <= 0 ||
+        top_k > kMoeMaxTopK || hidden <= 0 || hidden >= kMoeMaxWidth || inner <= 0 || inner >= kMoeMaxWidth)
+        return 0;
+    return mx4_moe_workspace(tokens, experts, top_k, hidden, inner);
+}
+
+fp8_status fp8_mx4_moe(const void* x, int64_t tokens, int64_t hidden, int64_t ldx, const void* router, int64_t ldr,
+                       const fp8_mx4_experts* w1, const fp8_mx4_experts* w2, int64_t experts, int64_t inner,
+                       int64_t top_k, int32_t renormalize, void* y, int64_t ldy, int32_t* ids, float* weights,
+                       void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream)
+{
+    if (experts < 1 || hidden < 1 || inner < 1 || tokens < 0 || top_k < 1 || top_k > experts)
+        return fail(FP8_ERR_INVALID_ARG, "moe: sizes are positive, top_k at most experts");
+    if (tokens > kMoeMaxTokens || experts > kMoeMaxExperts || top_k > kMoeMaxTopK || hidden >= kMoeMaxWidth ||
+        inner >= kMoeMaxWidth)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE,
+                    "moe: at most 64 tokens, 512 experts, top_k 16; hidden and inner below 2^24");
+    fp8_status st;
+    if ((st = check_2d(x, tokens, hidden, ldx, "x")) != FP8_OK) return st;
+    if ((st = check_2d(router, experts, hidden, ldr, "router")) != FP8_OK) return st;
+    if ((st = check_2d(y, tokens, hidden, ldy, "y")) != FP8_OK) return st;
+    if (!w1 || !w2) return fail(FP8_ERR_INVALID_ARG, "moe: null weights");
+    if ((st = check_mx4(w1->q, w1->ldq, w1->s, w1->ps, 2 * inner, hidden, "w1")) != FP8_OK) return st;
+    if ((st = check_mx4(w2->q, w2->ldq, w2->s, w2->ps, hidden, inner, "w2")) != FP8_OK) return st;
+    if ((w1->eq | w1->es | w2->eq | w2->es) % 16 != 0 || w1->eq < 0 || w1->es < 0 || w2->eq < 0 || w2->es < 0)
+        return fail(FP8_ERR_INVALID_ARG, "moe: experts lie multiples of 16 bytes apart");
+    if (misaligned(x, 2) || misaligned(router, 2) || misaligned(y, 2) || misaligned(ids, 4) || misaligned(weights, 4))
+        return fail(FP8_ERR_INVALID_ARG, "moe: misaligned pointer");
+    if (tokens == 0) return FP8_OK;
+    if (!ids || !weights) return fail(FP8_ERR_INVALID_ARG, "moe: null ids or weights");
+    if (!workspace || misaligned(workspace, 16) ||
+        workspace_bytes < mx4_moe_workspace(tokens, experts, top_k, hidden, inner))
+        return fail(FP8_ERR_INVALID_ARG, "moe: workspace smaller than fp8_mx4_moe_workspace_size() or misaligned");
+    if ((st = check_device()) != FP8_OK) return st;
+    Mx4MoeArgs g;
+    g.x = x;
+    g.tokens = tokens;
+    g.hidden = hidden;
+    g.ldx = ldx;
+    g.router = router;
+    g.ldr = ldr;
+    g.w1 = *w1;
+    g.w2 = *w2;
+    g.experts = experts;
+    g.inner = inner;
+    g.top_k = top_k;
+    g.renormalize = renormalize != 0;
+    g.y = y;
+    g.ldy = ldy;
+    g.ids = ids;
+    g.weights = weights;
+    g.ws = workspace;
+    g.ctr = ctr;
+    hipError_t e = launch_mx4_moe(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_moe launch");
 }
 
 fp8_status fp8_counters_reset(fp8_counters* ctr, hipStream_t stream)

@@ -180,6 +180,24 @@ struct Mx4GemmArgs {
 };
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream);
+// Mixture-of-experts layer with 4-bit weights (mx4_moe.hip).
+struct Mx4MoeArgs {
+    const void* x;
+    int64_t tokens, hidden, ldx;
+    const void* router;
+    int64_t ldr;
+    fp8_mx4_experts w1, w2;
+    int64_t experts, inner, top_k;
+    int renormalize;
+    void* y;
+    int64_t ldy;
+    int32_t* ids;
+    float* weights;
+    void* ws;
+    fp8_counters* ctr;
+};
+size_t mx4_moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner);
+hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream);
 // Pieces of gemm.hip that the 4-bit GEMM uses too: zeros (k = 0), and the
 // fixed-order sum of split-K partials.
 hipError_t launch_zero_bf16(uint16_t* c, int m, int n, int64_t ldc, hipStream_t stream);

@@ -371,6 +371,37 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
                       int64_t m, int64_t n, int64_t k, void* c_bf16, int64_t ldc,
                       void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream);
 
+/* A mixture-of-experts layer with 4-bit weights for 1 to 64 tokens (0 does
+ * nothing), as decoding calls it:
+ *   l[t, e] = sum x[t, c] router[e, c]     x [tokens, hidden], router [experts, hidden] bf16, sums in 64 bits
+ *   ids[t]  = the top_k largest l of a token in falling order, equal ones by the lower expert, NaN last
+ *   weights = exp(l - max) / sum exp(l - max), the sum over ids[t] (renormalize) or over all experts
+ *   y[t]    = sum over ids[t] of weight * W2[e] (silu(W1[e][:inner] x[t]) * (W1[e][inner:] x[t])), bf16
+ * w1 [experts, 2 inner, hidden], w2 [experts, hidden, inner].  x enters the
+ * products as it is (but for elements under 2^-13 of the largest of their
+ * block of 32, held to 2^-21 of that), the inner activations to 2^-12,
+ * sums are fp32 in an order that the sizes and the chosen experts alone set.
+ * A token whose x holds an Inf or NaN gets NaN in y.
+ * ids int32 and weights fp32 [tokens, top_k], contiguous.  top_k <= 16,
+ * experts <= 512; hidden, inner below 2^24; ldx, ldr, ldy in elements.
+ * workspace: fp8_mx4_moe_workspace_size() bytes (grows with tokens), 16-byte
+ * aligned, its first 256 bytes ZERO before the first call that uses it (each
+ * call leaves them zero), and no two calls at once on one workspace.
+ * ctr (may be NULL) counts nonfinite_out. */
+typedef struct {
+    const uint8_t* q;    /* [experts, rows, 128 ceil(cols/256)] */
+    const uint8_t* s;    /* [experts, ceil(cols/512), rows, 16] */
+    int64_t ldq, eq;     /* bytes between rows of codes, between experts' codes */
+    int64_t ps, es;      /* bytes between scale panels, between experts' scales */
+} fp8_mx4_experts;
+
+size_t     fp8_mx4_moe_workspace_size(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner);
+fp8_status fp8_mx4_moe(const void* x_bf16, int64_t tokens, int64_t hidden, int64_t ldx,
+                       const void* router_bf16, int64_t ldr, const fp8_mx4_experts* w1, const fp8_mx4_experts* w2,
+                       int64_t experts, int64_t inner, int64_t top_k, int32_t renormalize,
+                       void* y_bf16, int64_t ldy, int32_t* ids, float* weights,
+                       void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream);
+
 /* Zero a counter block on `stream` (a small fill kernel, safe to capture). */
 fp8_status fp8_counters_reset(fp8_counters* ctr, hipStream_t stream);
 

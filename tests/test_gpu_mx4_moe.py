@@ -1,0 +1,230 @@
+"""The mixture-of-experts layer with 4-bit weights against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import fp8_scaled_matmul_amd as fm
+from oracle import mx4
+
+pytestmark = pytest.mark.gpu
+
+
+def _experts(e, rows, cols, rng, std):
+    """Random codes and scales of e matrices: (Mx4 on the GPU, float64 values)."""
+    codes = rng.integers(0, 16, (e * rows, cols)).astype(np.uint8)
+    mid = 127 + int(np.floor(np.log2(std / 3)))
+    sb = rng.integers(mid - 2, mid + 2, (e * rows, -(-cols // 32))).astype(np.uint8)
+    q, s = mx4.pack(codes, sb)
+    s = np.ascontiguousarray(s.reshape(s.shape[0], e, rows, 16).transpose(1, 0, 2, 3))
+    held = fm.Mx4(torch.from_numpy(q.reshape(e, rows, -1)).cuda(), torch.from_numpy(s).cuda(), cols)
+    return held, mx4.values(codes, sb).reshape(e, rows, cols)
+
+
+class Layer:
+    def __init__(self, t, e, k, h, i, renormalize, seed=0, **kw):
+        rng = np.random.default_rng([t, e, k, h, i, seed])
+        self.rng, self.k, self.renormalize = rng, k, renormalize
+        self.w1, self.v1 = _experts(e, 2 * i, h, rng, h ** -0.5)
+        self.w2, self.v2 = _experts(e, h, i, rng, i ** -0.5)
+        self.router = torch.from_numpy(rng.standard_normal((e, h)) * h ** -0.5).bfloat16()
+        self.moe = fm.MoeMx4(self.router.cuda(), self.w1, self.w2, k, max_tokens=t, renormalize=renormalize, **kw)
+
+    def x(self, t, h, scale=1.0):
+        return torch.from_numpy(self.rng.standard_normal((t, h)) * scale).bfloat16()
+
+    def check(self, x, got):
+        """ids equal; weights within their fp32 roundings; y within what the
+        roundings of the formula's steps add up to."""
+        y, ids, weights = [v.cpu() for v in got]
+        xv, rv = x.double().numpy(), self.router.double().numpy()
+        want, wid, wp = mx4.moe(xv, rv, self.v1, self.v2, self.k, self.renormalize)
+        assert np.array_equal(ids.numpy(), wid)
+        e, h = rv.shape
+        i = self.v2.shape[2]
+        logits = xv @ rv.T
+        z = np.abs(np.take_along_axis(logits, wid, 1) - logits.max(1, keepdims=True))
+        # exponent argument, exp, the sum's additions and the quotient
+        # (a weight below fp32's smallest number is 0)
+        held = wp.astype(np.float32).astype(np.float64)
+        assert (np.abs(weights.double().numpy() - held) <= (z + 16 + e) * 2.0 ** -24 * wp).all()
+        blk = np.abs(np.pad(xv, ((0, 0), (0, -h % 32)))).reshape(len(xv), -1, 32).max(2).repeat(32, 1)[:, :h]
+        bound = 2.0 ** -8 * np.abs(want) + 2.0 ** -134
+        for t in range(len(xv)):
+            for j in range(self.k):
+                w1, w2 = self.v1[wid[t, j]], self.v2[wid[t, j]]
+                gu = w1 @ xv[t]
+                # fp32 sums of h terms (doubled for their order), x's small elements
+                d = np.abs(w1) @ (2 * h * 2.0 ** -24 * np.abs(xv[t]) + 2.0 ** -21 * blk[t])
+                g, u = gu[:i], gu[i:]
+                with np.errstate(over="ignore"):
+                    silu = g / (1 + np.exp(-g))
+                a = wp[t, j] * silu * u
+                # silu's slope is under 1.1; a dozen roundings besides
+                da = wp[t, j] * (1.1 * d[:i] * np.abs(u) + (np.abs(silu) + 1.1 * d[:i]) * d[i:])
+                da += (z[t, j] + 32 + e + np.abs(g)) * 2.0 ** -24 * np.abs(a)
+                # a's pieces, and fp32 sums of k i terms
+                ab = np.abs(np.pad(a, (0, -i % 32))).reshape(-1, 32).max(1).repeat(32)[:i]
+                da += 2.0 ** -12 * np.abs(a) + 2.0 ** -25 * ab + 2 * self.k * i * 2.0 ** -24 * np.abs(a)
+                bound[t] += np.abs(w2) @ da
+        err = np.abs(y.double().numpy() - want)
+        assert (err <= bound).all(), f"worst {np.max(err / bound):.3g} of the bound"
+
+
+SIZES = [(1, 1, 1, 1, 1), (1, 4, 1, 32, 32), (1, 64, 8, 256, 100), (2, 37, 3, 1000, 531), (3, 5, 5, 70, 33),
+         (7, 37, 3, 264, 65), (16, 8, 2, 520, 64), (17, 8, 2, 256, 257), (33, 20, 1, 96, 40), (64, 16, 4, 512, 300),
+         (64, 4, 4, 300, 128), (40, 130, 16, 264, 96), (5, 512, 10, 128, 64), (64, 100, 8, 64, 32)]
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("t,e,k,h,i", SIZES)
+def test_moe(t, e, k, h, i, renormalize):
+    m = Layer(t, e, k, h, i, renormalize)
+    x = m.x(t, h)
+    got = m.moe(x.cuda())
+    m.check(x, got)
+    # the same bits again, and fewer tokens through the same layer
+    assert all(torch.equal(a, b) for a, b in zip(got, m.moe(x.cuda())))
+    few = x[: t // 2 + 1]
+    m.check(few, m.moe(few.cuda()))
+    m.check(x, m.moe(x.cuda()))
+
+
+def test_moe_every_token_to_one_expert():
+    """64 tokens reach the same experts: four columns tiles of 16, and the
+    other experts none."""
+    m = Layer(64, 9, 2, 320, 96, True)
+    m.router[:] = 0
+    m.router[3] = 1
+    m.router[7] = 0.5
+    m.moe.router.copy_(m.router)
+    x = m.x(64, 320).abs()
+    got = m.moe(x.cuda())
+    assert (got[1].cpu() == torch.tensor([3, 7])).all()
+    m.check(x, got)
+
+
+def test_moe_ties_go_to_the_lower_expert():
+    m = Layer(4, 150, 6, 64, 32, True)
+    m.router[:] = m.router[:1]
+    m.router[100:] *= 2
+    m.moe.router.copy_(m.router)
+    x = m.x(4, 64)
+    got = m.moe(x.cuda())
+    m.check(x, got)
+    up = (x.double() @ m.router[0].double()) > 0
+    assert torch.equal(got[1].cpu()[:, 0], torch.where(up, 100, 0).int())
+    x[:] = 0                    # every logit 0
+    got = m.moe(x.cuda())
+    assert (got[1].cpu() == torch.arange(6)).all() and (got[0] == 0).all()
+    m.check(x, got)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-30, 1e4, 1e15])
+def test_moe_far_ranges(scale):
+    """Blocks at both ends of the range; outliers beside small elements."""
+    m = Layer(6, 12, 3, 300, 70, True)
+    x = m.x(6, 300, 1.0)
+    x[:, ::50] *= 1000
+    x[:, 1::50] *= 1e-6
+    m.router /= 64
+    m.moe.router.copy_(m.router)
+    if scale > 1:
+        m.router /= scale
+        m.moe.router.copy_(m.router)
+    x = (x.float() * scale).bfloat16()
+    m.check(x, m.moe(x.cuda()))
+
+
+def test_moe_nonfinite_rows():
+    """A token that holds an Inf or NaN is NaN throughout, valid ids all the
+    same; the other tokens are as without it, and the outputs are counted."""
+    ctr = fm.Counters()
+    m = Layer(20, 30, 4, 200, 96, True, counters=ctr)
+    x = m.x(20, 200)
+    want = [v.clone() for v in m.moe(x.cuda())]
+    assert ctr.read()["nonfinite_out"] == 0
+    bad = x.clone()
+    bad[3, 17] = float("nan")
+    bad[11, 199] = float("inf")
+    y, ids, weights = m.moe(bad.cuda())
+    ok = [t for t in range(20) if t not in (3, 11)]
+    assert torch.isnan(y[[3, 11]]).all() and ctr.read()["nonfinite_out"] == 400
+    assert torch.equal(y[ok], want[0][ok]) and torch.equal(ids[ok], want[1][ok])
+    assert ((ids >= 0) & (ids < 30)).all() and all(len(set(r.tolist())) == 4 for r in ids)
+    # a NaN block of one expert reaches the tokens that chose it, in its row alone
+    e, row = int(ids[0, 0]), 5
+    m.w2.s[e, 0, row, 1] = 255
+    y2, ids2, _ = m.moe(x.cuda())
+    hit = (want[1] == e).any(1)
+    nan = torch.isnan(y2)
+    assert torch.equal(nan[:, row], hit) and int(nan.sum()) == int(hit.sum())
+
+
+def test_moe_strides_and_outputs_given():
+    m = Layer(9, 20, 3, 200, 96, False)
+    x = m.x(9, 200)
+    want = m.moe(x.cuda())
+    for pitch in (203, 208):
+        wide = torch.zeros(9, pitch, dtype=torch.bfloat16, device="cuda")
+        wide[:, :200] = x.cuda()
+        buf = torch.full((9, pitch), 7.0, dtype=torch.bfloat16, device="cuda")
+        got = m.moe(wide[:, :200], out=buf[:, :200])
+        assert torch.equal(buf[:, :200], want[0]) and (buf[:, 200:] == 7).all()
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    # experts of a larger stack (a shard), rows of codes further apart
+    q1 = torch.zeros(22, 192, 144, dtype=torch.uint8, device="cuda")
+    q1[1:21, :, :128] = m.w1.q
+    s1 = torch.zeros(22, 1, 200, 16, dtype=torch.uint8, device="cuda")
+    s1[1:21, :, :192] = m.w1.s
+    w1 = fm.Mx4(q1[1:21, :, :128], s1[1:21, :, :192], 200)
+    got = fm.MoeMx4(m.router.cuda(), w1, m.w2, 3, max_tokens=9, renormalize=False)(x.cuda())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    y, ids, weights = m.moe(x[:0].cuda())
+    assert y.shape == (0, 200) and ids.shape == (0, 3) and weights.shape == (0, 3)
+
+
+def test_moe_on_another_stream_and_captured():
+    m = Layer(12, 40, 4, 256, 128, True)
+    x = m.x(12, 256).cuda()
+    want = [v.clone() for v in m.moe(x)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = m.moe(x)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = m.moe(x)
+    for i in range(4):
+        x.copy_(m.x(12, 256))
+        want = [v.clone() for v in m.moe(x)]
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_moe_is_what_quantize_and_product_give():
+    """The layer on weights that the library quantized, against the library's
+    own products, expert by expert, on activations that 4 bits hold exactly."""
+    t, e, h, i = 4, 3, 128, 64
+    rng = np.random.default_rng(1)
+    w1 = torch.from_numpy(rng.standard_normal((e, 2 * i, h))).bfloat16().cuda()
+    w2 = torch.from_numpy(rng.standard_normal((e, h, i))).bfloat16().cuda()
+    h1 = [fm.mx4_quantize(w)[0] for w in w1]
+    h2 = [fm.mx4_quantize(w)[0] for w in w2]
+    stack = lambda a, c: fm.Mx4(torch.stack([v.q for v in a]), torch.stack([v.s for v in a]), c)    # noqa: E731
+    x = torch.from_numpy(mx4.VALUES[rng.integers(0, 16, (t, h))]).bfloat16().cuda()
+    x[:, ::32] = 6
+    router = torch.from_numpy(rng.standard_normal((e, h)) / 16).bfloat16().cuda()
+    y, ids, weights = fm.MoeMx4(router, stack(h1, h), stack(h2, i), 1)(x)
+    xq, _ = fm.mx4_quantize(x)
+    for tok in range(t):
+        gu = fm.mx4_mm(xq, h1[ids[tok, 0]]).float()[tok]
+        a = torch.nn.functional.silu(gu[:i]) * gu[i:] * weights[tok, 0]
+        want = fm.mx4_dequantize(h2[ids[tok, 0]], torch.float32) @ a
+        size = fm.mx4_dequantize(h2[ids[tok, 0]], torch.float32).abs() @ a.abs()
+        # gate and up rounded to bf16 (silu's relative slope is at most 1 + |g|), y too, a to 2^-12
+        slope = 2 + gu[:i].abs().max()
+        assert ((y[tok].float() - want).abs() <= 2.0 ** -8 * (want.abs() + slope * size) + 2.0 ** -12 * size).all()

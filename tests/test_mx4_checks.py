@@ -115,3 +115,56 @@ def test_binding_rejects():
         fm.mx4_mm(_mx4(8, 64), _mx4(9, 64), out=torch.zeros(8, 9))
     with pytest.raises(ValueError, match="CUDA"):
         fm.mx4_mm(_mx4(8, 64), _mx4(9, 64))
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(tokens=-1), fm.FP8_ERR_INVALID_ARG),
+    (dict(top_k=0), fm.FP8_ERR_INVALID_ARG),
+    (dict(top_k=9), fm.FP8_ERR_INVALID_ARG),
+    (dict(experts=0), fm.FP8_ERR_INVALID_ARG),
+    (dict(inner=0), fm.FP8_ERR_INVALID_ARG),
+    (dict(x=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(x=BAD + 1), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldx=255), fm.FP8_ERR_INVALID_ARG),
+    (dict(router=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldr=255), fm.FP8_ERR_INVALID_ARG),
+    (dict(y=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(ldy=255), fm.FP8_ERR_INVALID_ARG),
+    (dict(ids=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(weights=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(w1=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(w1=(BAD, None, 128, 24576, 3072 * 2, 3072 * 2)), fm.FP8_ERR_INVALID_ARG),
+    (dict(w1=(BAD, BAD, 64, 24576, 6144, 6144)), fm.FP8_ERR_INVALID_ARG),
+    (dict(w2=(BAD, BAD, 128, 24584, 6144, 6144)), fm.FP8_ERR_INVALID_ARG),
+    (dict(w2=(BAD, BAD, 128, 24576, 6144, -16)), fm.FP8_ERR_INVALID_ARG),
+    (dict(ws=None), fm.FP8_ERR_INVALID_ARG),
+    (dict(ws=BAD + 8), fm.FP8_ERR_INVALID_ARG),
+    (dict(wsb=1024), fm.FP8_ERR_INVALID_ARG),
+    (dict(tokens=65), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+    (dict(experts=513), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+    (dict(experts=20, top_k=17), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+    (dict(hidden=1 << 24, ldx=1 << 24, ldr=1 << 24, ldy=1 << 24), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+])
+def test_moe_rejects_before_device(args, code):
+    held = (BAD, BAD, 128, 24576, 6144, 6144)
+    a = dict(x=BAD, tokens=4, hidden=256, ldx=256, router=BAD, ldr=256, w1=held, w2=held, experts=8, inner=96, top_k=2,
+             renormalize=1, y=BAD, ldy=256, ids=BAD, weights=BAD, ws=BAD, wsb=1 << 30, ctr=None)
+    a.update(args)
+    for w in ("w1", "w2"):
+        a[w] = fm.Mx4Experts(*a[w]) if a[w] else None
+    assert fm.fp8_mx4_moe(*a.values(), None) == code, fm.lib().fp8_last_error()
+
+
+def test_moe_binding_rejects():
+    e, h, i = 4, 64, 32
+    router = torch.zeros(e, h, dtype=torch.bfloat16)
+    stack = lambda r, c: fm.Mx4(torch.zeros(e, r, 128, dtype=torch.uint8),      # noqa: E731
+                                torch.zeros(e, 1, r, 16, dtype=torch.uint8), c)
+    w1, w2 = stack(2 * i, h), stack(h, i)
+    for bad in [(router.float(), w1, w2, 1), (router, _mx4(2 * i, h), w2, 1), (router, w2, w1, 1),
+                (router[:3], w1, w2, 1), (router, w1, w2, 0), (router, w1, w2, 5), (router, w1, w2, 1, 65),
+                (router, w1, w2, 1, 0), (router, w1.q, w2, 1)]:
+        with pytest.raises(ValueError):
+            fm.MoeMx4(*bad)
+    with pytest.raises(ValueError, match="CUDA"):
+        fm.MoeMx4(router, w1, w2, 2)
