@@ -275,6 +275,150 @@ hipError_t launch_tile(MxArgs p, hipStream_t stream)
     return hipGetLastError();
 }
 
+// ------------------------------------------------------------------ 256 x 256 tiles
+// 8 waves of 4 x 2 fragments (128 x 64 outputs, 128 accumulator registers).
+// A stage is 128 K (64 bytes of a row, two matrix instructions deep); a ring
+// of four, filled by DMA three stages ahead, and two panels of scales (512 K:
+// four stages) beside it.
+constexpr int kBig = 256, kBigThreads = 512;
+constexpr int kStageBytes = 2 * kBig * 64;      // A's 256 rows, then B's
+constexpr int kPanelBytes = 2 * kBig * kScaleBytes;
+constexpr int kBigLds = 4 * kStageBytes + 2 * kPanelBytes;
+
+// Position of 16-byte chunk c (0..3) in the 64-byte LDS row r: as for swz32,
+// 16 rows at one chunk fill the 16 slots of a 256-byte line and 32 rows with
+// two chunks the 32 of 512 bytes.  An involution in c.
+__device__ inline int swz64(int r, int c) { return c ^ ((((r >> 2) ^ (r >> 4)) & 1) | ((r >> 2) & 2)); }
+
+__global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
+{
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    int split, tm, tn;
+    item_of(p, blockIdx.x, split, tm, tn);
+    const int m0 = tm * kBig, n0 = tn * kBig;
+    const int st0 = 2 * split * p.steps_per;
+    const int nt = 2 * min(p.steps, (split + 1) * p.steps_per) - st0;      // even
+    const int64_t rows_a = min(p.m - m0, kBig), rows_b = min(p.n - n0, kBig);
+    const uint32_t base = gemm::lds_addr(lds);
+    const uint32_t scales = base + 4 * kStageBytes;
+
+    // This wave's DMA of a stage: 2 x 16 rows of A and of B, 1 KB each.
+    // Rows of B lie permuted as in the kernel above.
+    const v4u ra = gemm::make_rsrc(p.a + (int64_t)m0 * p.lda, (uint32_t)(rows_a * p.lda));
+    const v4u rb = gemm::make_rsrc(p.b + (int64_t)n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+    uint32_t va[2], vb[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int R = 32 * wave + 16 * j + (lane >> 2);
+        const int g = (R & ~63) + 2 * (R & 31) + ((R >> 5) & 1);
+        va[j] = (uint32_t)(R * p.lda + 16 * swz64(R, lane & 3));
+        vb[j] = (uint32_t)(g * p.ldb + 16 * swz64(R, lane & 3));
+    }
+    // Waves 0-3 bring the scales of 64 rows of A, 4-7 of B.
+    const uint8_t* sp = wave < 4 ? p.sa + (int64_t)m0 * kScaleBytes : p.sb + (int64_t)n0 * kScaleBytes;
+    const int64_t ps = wave < 4 ? p.psa : p.psb;
+    const uint32_t sbytes = (uint32_t)(wave < 4 ? rows_a : rows_b) * kScaleBytes;
+    const int sr = wave < 4 ? 64 * wave + lane : 64 * (wave - 4) + 2 * (lane & 31) + (lane >> 5);
+    const auto fill = [&](int t) {
+        const uint32_t to = base + (t & 3) * kStageBytes + 2048 * wave;
+        v4u a = ra, b = rb;
+        a.z = t < nt ? a.z : 0u;
+        b.z = t < nt ? b.z : 0u;
+        const uint32_t kb = (uint32_t)(st0 + t) * 64;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) gemm::dma16(to + 1024 * j, va[j] + kb, a);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) gemm::dma16(to + kBig * 64 + 1024 * j, vb[j] + kb, b);
+    };
+    const auto fill_scales = [&](int q) {       // panel q of this split
+        const bool live = 4 * q < nt;
+        gemm::dma16(scales + (q & 1) * kPanelBytes + 1024 * wave, (uint32_t)sr * kScaleBytes,
+                    gemm::make_rsrc(sp + (int64_t)(st0 / 4 + q) * ps, live ? sbytes : 0u));
+    };
+
+    v16f acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    const int wm = (wave & 1) * 128, wn = (wave >> 1) * 64;
+    fill_scales(0);
+    fill(0);
+    fill(1);
+    fill(2);
+    // This lane's row of a fragment and its chunk of the first matrix
+    // instruction (the second's lies 32 bytes across); the swizzle is the
+    // same in every fragment.
+    const int fr = lane & 31, half = lane >> 5;
+    const uint32_t at0 = (uint32_t)(fr * 64 + 16 * swz64(fr, half)), at1 = at0 ^ 32u;
+    const uint8_t* fa_at[2] = {lds + wm * 64 + at0, lds + wm * 64 + at1};
+    const uint8_t* fb_at[2] = {lds + (kBig + wn) * 64 + at0, lds + (kBig + wn) * 64 + at1};
+    const uint8_t* sa_at = lds + 4 * kStageBytes + (wm + fr) * kScaleBytes;
+    const uint8_t* sb_at = lds + 4 * kStageBytes + (kBig + wn + fr) * kScaleBytes;
+    for (int t = 0; t < nt; t += 2) {
+        const int ring = (t & 2) * kStageBytes, panel = (t & 4 ? kPanelBytes : 0) + 4 * (t & 2);
+        const auto stage = [&](auto J) {
+            constexpr int j = decltype(J)::value;
+            // stage t + j has landed: only the two after it are younger (and,
+            // at times, a panel of scales)
+            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+            gemm::barrier_lds();
+            if (j == 0 && (t & 2) == 0) fill_scales(t / 4 + 1);
+            fill(t + j + 3);
+            // block 2 kk + half of the stage: that byte of the panel's word j
+            uint32_t ea[4], eb[2];
+            v8i fa[2][4], fb[2][2];
+            const auto get = [](const uint8_t* from) {
+                const uint4 v = *reinterpret_cast<const uint4*>(from);
+                return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
+            };
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                eb[i] = *reinterpret_cast<const uint32_t*>(sb_at + panel + 512 * i + 4 * j) >> (8 * half);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ea[i] = *reinterpret_cast<const uint32_t*>(sa_at + panel + 512 * i + 4 * j) >> (8 * half);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) fb[kk][i] = get(fb_at[kk] + ring + j * kStageBytes + 2048 * i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fa[kk][i] = get(fa_at[kk] + ring + j * kStageBytes + 2048 * i);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) acc[i][n] = mfma<0>(fa[0][i], fb[0][n], acc[i][n], ea[i], eb[n]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) acc[i][n] = mfma<2>(fa[1][i], fb[1][n], acc[i][n], ea[i], eb[n]);
+        };
+        stage(std::integral_constant<int, 0>{});
+        stage(std::integral_constant<int, 1>{});
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const uint32_t nonfinite = store_out<4>(p, acc, m0 + wm, n0 + wn + 2 * (lane & 31), split);
+    if (!p.ws) flush_counters(p.ctr, 0, 0, 0, nonfinite);
+}
+
+hipError_t launch_big(MxArgs p, hipStream_t stream)
+{
+    p.tiles_m = (p.m + kBig - 1) / kBig;
+    p.tiles_n = (p.n + kBig - 1) / kBig;
+    p.group_m = 4;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_big_gemm),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_mx4_big_gemm, dim3(p.tiles_m * p.tiles_n * p.splits), dim3(kBigThreads), kBigLds, stream, p);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k)
@@ -308,6 +452,8 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
     p.ws = nullptr;
     p.pair_store = g.ldc % 2 == 0 && (reinterpret_cast<uintptr_t>(g.c) & 3u) == 0;
     p.ctr = g.ctr;
+    const int64_t big = ((g.m + kBig - 1) / kBig) * ((g.n + kBig - 1) / kBig);
+    if (big >= 192) return launch_big(p, stream);
     return launch_tile<2, 2, 2, 4>(p, stream);
 }
 

@@ -205,6 +205,19 @@ def test_mm_large(m, n, k):
     _check_mm(fm.mx4_mm(a, b), va, vb)
 
 
+@pytest.mark.parametrize("m,n,k", [(3400, 4100, 700), (4097, 3585, 1024), (6000, 2100, 130), (4096, 4096, 1300)])
+def test_mm_many_tiles(m, n, k):
+    """Enough output for the largest tiles: ragged edges, one to five panels
+    of scales, an odd pitch."""
+    a, va = _operand(m, k, 8)
+    b, vb = _operand(n, k, 9)
+    y = fm.mx4_mm(a, b)
+    _check_mm(y, va, vb)
+    buf = torch.full((m, n + 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    fm.mx4_mm(a, b, out=buf[:, :n])
+    assert torch.equal(buf[:, :n], y) and (buf[:, n:] == 7).all()
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_mm_scales_at_their_ends(m):
     """Scale bytes over the whole range, each product within bf16's range."""
