@@ -276,38 +276,69 @@ hipError_t launch_tile(MxArgs p, hipStream_t stream)
 }
 
 // ------------------------------------------------------------------ 256 x 256 tiles
-// 8 waves of 4 x 2 fragments (128 x 64 outputs, 128 accumulator registers).
-// A stage is 128 K (64 bytes of a row, two matrix instructions deep); a ring
-// of four, filled by DMA three stages ahead, and two panels of scales (512 K:
-// four stages) beside it.
+// 8 waves of 4 x 2 fragments (128 x 64 outputs, 128 accumulator registers), one
+// workgroup per CU, which walks its tiles.  A stage is 128 K (64 bytes of a
+// row, two matrix instructions deep); a ring of four in LDS, and three panels
+// of scales (512 K: four stages, or the two that end a K range) beside it.
+// The stages of all of a workgroup's tiles are one stream, filled by DMA four
+// ahead, so that a tile's first stages arrive while the one before is stored.
+// Fragments are read half a stage ahead of their products, which leaves one
+// barrier a stage: in its middle, once the whole of it has been read.
 constexpr int kBig = 256, kBigThreads = 512;
 constexpr int kStageBytes = 2 * kBig * 64;      // A's 256 rows, then B's
 constexpr int kPanelBytes = 2 * kBig * kScaleBytes;
-constexpr int kBigLds = 4 * kStageBytes + 2 * kPanelBytes;
+constexpr int kBigPanels = 3;
+constexpr int kBigLds = 4 * kStageBytes + kBigPanels * kPanelBytes;
+constexpr int kBigStores = 64;                  // of a tile, by a wave
 
 // Position of 16-byte chunk c (0..3) in the 64-byte LDS row r: as for swz32,
 // 16 rows at one chunk fill the 16 slots of a 256-byte line and 32 rows with
 // two chunks the 32 of 512 bytes.  An involution in c.
 __device__ inline int swz64(int r, int c) { return c ^ ((((r >> 2) ^ (r >> 4)) & 1) | ((r >> 2) & 2)); }
 
+// A tile and K split.
+struct BigItem {
+    int id;             // past the last: no tile
+    int split, m0, n0;
+    int st0, nt;        // its first stage and number of stages (even)
+};
+__device__ inline BigItem big_item(const MxArgs& p, int id)
+{
+    BigItem it;
+    it.id = id;
+    it.split = it.m0 = it.n0 = it.st0 = 0;
+    it.nt = 1 << 30;
+    if (id < p.tiles_m * p.tiles_n * p.splits) {
+        int tm, tn;
+        item_of(p, id, it.split, tm, tn);
+        it.m0 = tm * kBig;
+        it.n0 = tn * kBig;
+        it.st0 = 2 * it.split * p.steps_per;
+        it.nt = 2 * min(p.steps, (it.split + 1) * p.steps_per) - it.st0;
+    }
+    return it;
+}
+
+// Tracks the largest |bf16| stored, two packed maxima.
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+__device__ inline void track_max(us2& mx, uint32_t w)
+{
+    mx = __builtin_elementwise_max(mx, __builtin_bit_cast(us2, w & 0x7FFF7FFFu));
+}
+
 __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
 {
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    int split, tm, tn;
-    item_of(p, blockIdx.x, split, tm, tn);
-    const int m0 = tm * kBig, n0 = tn * kBig;
-    const int st0 = 2 * split * p.steps_per;
-    const int nt = 2 * min(p.steps, (split + 1) * p.steps_per) - st0;      // even
-    const int64_t rows_a = min(p.m - m0, kBig), rows_b = min(p.n - n0, kBig);
+    const int total = p.tiles_m * p.tiles_n * p.splits;
     const uint32_t base = gemm::lds_addr(lds);
     const uint32_t scales = base + 4 * kStageBytes;
 
-    // This wave's DMA of a stage: 2 x 16 rows of A and of B, 1 KB each.
-    // Rows of B lie permuted as in the kernel above.
-    const v4u ra = gemm::make_rsrc(p.a + (int64_t)m0 * p.lda, (uint32_t)(rows_a * p.lda));
-    const v4u rb = gemm::make_rsrc(p.b + (int64_t)n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
+    // ---- the stream of fills
+    // This wave's DMA of a stage: 2 x 16 rows of A and of B, 1 KB each.  Rows
+    // of B lie permuted as in the kernel above.  Waves 0-3 bring the scales
+    // of 64 rows of A, 4-7 of B.
     uint32_t va[2], vb[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -316,94 +347,176 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
         va[j] = (uint32_t)(R * p.lda + 16 * swz64(R, lane & 3));
         vb[j] = (uint32_t)(g * p.ldb + 16 * swz64(R, lane & 3));
     }
-    // Waves 0-3 bring the scales of 64 rows of A, 4-7 of B.
-    const uint8_t* sp = wave < 4 ? p.sa + (int64_t)m0 * kScaleBytes : p.sb + (int64_t)n0 * kScaleBytes;
+    const uint32_t vs = (uint32_t)(wave < 4 ? 64 * wave + lane : 64 * (wave - 4) + 2 * (lane & 31) + (lane >> 5)) * kScaleBytes;
     const int64_t ps = wave < 4 ? p.psa : p.psb;
-    const uint32_t sbytes = (uint32_t)(wave < 4 ? rows_a : rows_b) * kScaleBytes;
-    const int sr = wave < 4 ? 64 * wave + lane : 64 * (wave - 4) + 2 * (lane & 31) + (lane >> 5);
-    const auto fill = [&](int t) {
-        const uint32_t to = base + (t & 3) * kStageBytes + 2048 * wave;
-        v4u a = ra, b = rb;
-        a.z = t < nt ? a.z : 0u;
-        b.z = t < nt ? b.z : 0u;
-        const uint32_t kb = (uint32_t)(st0 + t) * 64;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) gemm::dma16(to + 1024 * j, va[j] + kb, a);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) gemm::dma16(to + kBig * 64 + 1024 * j, vb[j] + kb, b);
+    BigItem f = big_item(p, blockIdx.x);        // the item being filled, its next stage
+    int ft = 0, fslot = 0, fpanel = 0;          // ring positions of the next stage and panel
+    v4u ra, rb, rs;
+    const uint8_t* sp;
+    const auto describe = [&]() {
+        const bool live = f.id < total;
+        const int64_t rows_a = min(p.m - f.m0, kBig), rows_b = min(p.n - f.n0, kBig);
+        ra = gemm::make_rsrc(p.a + (int64_t)f.m0 * p.lda, live ? (uint32_t)(rows_a * p.lda) : 0u);
+        rb = gemm::make_rsrc(p.b + (int64_t)f.n0 * p.ldb, live ? (uint32_t)(rows_b * p.ldb) : 0u);
+        sp = (wave < 4 ? p.sa + (int64_t)f.m0 * kScaleBytes : p.sb + (int64_t)f.n0 * kScaleBytes) + (f.st0 / 4) * ps;
+        rs = gemm::make_rsrc(sp, live ? (uint32_t)(wave < 4 ? rows_a : rows_b) * kScaleBytes : 0u);
     };
-    const auto fill_scales = [&](int q) {       // panel q of this split
-        const bool live = 4 * q < nt;
-        gemm::dma16(scales + (q & 1) * kPanelBytes + 1024 * wave, (uint32_t)sr * kScaleBytes,
-                    gemm::make_rsrc(sp + (int64_t)(st0 / 4 + q) * ps, live ? sbytes : 0u));
+    describe();
+    // The next stage (4 instructions a wave; one more where it begins a panel).
+    const auto fill = [&]() {
+        if ((ft & 3) == 0) {
+            gemm::dma16(scales + fpanel * kPanelBytes + 1024 * wave, vs,
+                        gemm::make_rsrc(sp + (int64_t)(ft >> 2) * ps, rs.z));
+            fpanel = fpanel == kBigPanels - 1 ? 0 : fpanel + 1;
+        }
+        const uint32_t to = base + fslot * kStageBytes + 2048 * wave;
+        const uint32_t kb = (uint32_t)(f.st0 + ft) * 64;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) gemm::dma16(to + 1024 * j, va[j] + kb, ra);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) gemm::dma16(to + kBig * 64 + 1024 * j, vb[j] + kb, rb);
+        fslot = (fslot + 1) & 3;
+        if (++ft == f.nt) {
+            f = big_item(p, f.id + gridDim.x);
+            ft = 0;
+            describe();
+        }
     };
 
-    v16f acc[4][2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-
-    const int wm = (wave & 1) * 128, wn = (wave >> 1) * 64;
-    fill_scales(0);
-    fill(0);
-    fill(1);
-    fill(2);
+    // ---- the fragments
     // This lane's row of a fragment and its chunk of the first matrix
     // instruction (the second's lies 32 bytes across); the swizzle is the
     // same in every fragment.
+    const int wm = (wave & 1) * 128, wn = (wave >> 1) * 64;
     const int fr = lane & 31, half = lane >> 5;
     const uint32_t at0 = (uint32_t)(fr * 64 + 16 * swz64(fr, half)), at1 = at0 ^ 32u;
     const uint8_t* fa_at[2] = {lds + wm * 64 + at0, lds + wm * 64 + at1};
     const uint8_t* fb_at[2] = {lds + (kBig + wn) * 64 + at0, lds + (kBig + wn) * 64 + at1};
     const uint8_t* sa_at = lds + 4 * kStageBytes + (wm + fr) * kScaleBytes;
     const uint8_t* sb_at = lds + 4 * kStageBytes + (kBig + wn + fr) * kScaleBytes;
-    for (int t = 0; t < nt; t += 2) {
-        const int ring = (t & 2) * kStageBytes, panel = (t & 4 ? kPanelBytes : 0) + 4 * (t & 2);
-        const auto stage = [&](auto J) {
-            constexpr int j = decltype(J)::value;
-            // stage t + j has landed: only the two after it are younger (and,
-            // at times, a panel of scales)
-            asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-            gemm::barrier_lds();
-            if (j == 0 && (t & 2) == 0) fill_scales(t / 4 + 1);
-            fill(t + j + 3);
-            // block 2 kk + half of the stage: that byte of the panel's word j
-            uint32_t ea[4], eb[2];
-            v8i fa[2][4], fb[2][2];
-            const auto get = [](const uint8_t* from) {
-                const uint4 v = *reinterpret_cast<const uint4*>(from);
-                return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
-            };
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                eb[i] = *reinterpret_cast<const uint32_t*>(sb_at + panel + 512 * i + 4 * j) >> (8 * half);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                ea[i] = *reinterpret_cast<const uint32_t*>(sa_at + panel + 512 * i + 4 * j) >> (8 * half);
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) fb[kk][i] = get(fb_at[kk] + ring + j * kStageBytes + 2048 * i);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) fa[kk][i] = get(fa_at[kk] + ring + j * kStageBytes + 2048 * i);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) acc[i][n] = mfma<0>(fa[0][i], fb[0][n], acc[i][n], ea[i], eb[n]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int n = 0; n < 2; ++n) acc[i][n] = mfma<2>(fa[1][i], fb[1][n], acc[i][n], ea[i], eb[n]);
+    v8i fa[2][4], fb[2][2];
+    uint32_t ea[4], eb[2], na[4], nb[2];        // scale words of this stage, of the next
+    int slot = 0, panel = 0;                    // the ring position and panel of the next fragments
+    const auto read = [&](auto KK) {
+        constexpr int kk = decltype(KK)::value;
+        const auto get = [](const uint8_t* from) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from);
+            return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
         };
-        stage(std::integral_constant<int, 0>{});
-        stage(std::integral_constant<int, 1>{});
+        const int ring = slot * kStageBytes;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) fb[kk][i] = get(fb_at[kk] + ring + 2048 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fa[kk][i] = get(fa_at[kk] + ring + 2048 * i);
+    };
+    // block 2 kk + lane / 32 of stage t: that byte of the panel's word t % 4
+    const auto read_scales = [&](int t) {
+        const int at = panel * kPanelBytes + 4 * (t & 3);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) nb[i] = *reinterpret_cast<const uint32_t*>(sb_at + at + 512 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) na[i] = *reinterpret_cast<const uint32_t*>(sa_at + at + 512 * i);
+    };
+    const auto take_scales = [&]() {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) eb[i] = nb[i] >> (8 * half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ea[i] = na[i] >> (8 * half);
+    };
+
+    v16f acc[4][2];
+    // Matrix instructions lo .. hi - 1 of the 8 of a half stage.  What is
+    // written around a call stays on its side.
+    const auto products = [&](auto KK, int lo, int hi) {
+        constexpr int kk = decltype(KK)::value;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+            if (m >= lo && m < hi)
+                acc[m >> 1][m & 1] = mfma<2 * kk>(fa[kk][m >> 1], fb[kk][m & 1], acc[m >> 1][m & 1], ea[m >> 1], eb[m & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const auto clear = [&]() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    };
+    clear();
+
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) fill();
+    // the first stage and its scales (three stages and at most one panel are younger)
+    asm volatile("s_waitcnt vmcnt(12)" ::: "memory");
+    gemm::barrier_lds();
+    read(std::integral_constant<int, 0>{});
+    read_scales(0);
+    uint32_t nonfinite = 0;
+    int stored = 3;                             // stages since the last tile's stores, up to 3
+    for (BigItem it = big_item(p, blockIdx.x); it.id < total; it = big_item(p, it.id + gridDim.x)) {
+        for (int t = 0; t < it.nt; ++t) {
+            // the stage's second half is read under the first's products
+            take_scales();
+            products(std::integral_constant<int, 0>{}, 0, 2);
+            read(std::integral_constant<int, 1>{});
+            products(std::integral_constant<int, 0>{}, 2, 8);
+            // The next stage has landed: the two after it are younger.  So are
+            // a tile's stores to the three stages that were filled before them.
+            if (stored < 3) {
+                static_assert(kBigStores + 8 >= 63, "stores and fills younger than the stage");
+                asm volatile("s_waitcnt vmcnt(63)" ::: "memory");
+                ++stored;
+            } else {
+                asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+            }
+            // past this every wave has read the whole stage: its slot is free
+            gemm::barrier_lds();
+            products(std::integral_constant<int, 1>{}, 0, 2);
+            slot = (slot + 1) & 3;
+            const int next = t + 1 == it.nt ? 0 : t + 1;
+            if ((next & 3) == 0) panel = panel == kBigPanels - 1 ? 0 : panel + 1;
+            read(std::integral_constant<int, 0>{});
+            read_scales(next);
+            fill();
+            products(std::integral_constant<int, 1>{}, 2, 8);
+        }
+        if (!p.ws && p.pair_store) {
+            // 64 stores of two adjacent outputs, those out of range dropped
+            const int64_t rows_c = min(p.m - it.m0, kBig);
+            const __amdgpu_buffer_rsrc_t rc = gemm::make_store_rsrc(
+                p.c + (int64_t)it.m0 * p.ldc, (uint32_t)(((rows_c - 1) * p.ldc + p.n) * 2));
+            const int col = it.n0 + wn + 2 * fr;
+            const uint32_t at = col < p.n ? (uint32_t)((wm + 4 * half) * p.ldc + col) * 2 : gemm::kOutOfRange;
+            us2 mx = us2{0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const uint32_t h = gemm::pack_bf16(acc[i][0][r], acc[i][1][r]);
+                    track_max(mx, h);
+                    __builtin_amdgcn_raw_buffer_store_b32(h, rc, (int)(at + (uint32_t)(32 * i + 8 * (r >> 2) + (r & 3)) * (uint32_t)p.ldc * 2),
+                                                          0, 2);
+                }
+            stored = 0;
+            if (p.ctr && (mx.x >= 0x7F80u || mx.y >= 0x7F80u)) {
+                // the outputs past the edges are zeros
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const uint32_t h = gemm::pack_bf16(acc[i][0][r], acc[i][1][r]);
+                        nonfinite += ((h & 0x7F80u) == 0x7F80u) + ((h & 0x7F800000u) == 0x7F800000u);
+                    }
+            }
+        } else {
+            nonfinite += store_out<4>(p, acc, it.m0 + wm, it.n0 + wn + 2 * fr, it.split);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        clear();
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const uint32_t nonfinite = store_out<4>(p, acc, m0 + wm, n0 + wn + 2 * (lane & 31), split);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // the fills past the end
     if (!p.ws) flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
@@ -412,10 +525,12 @@ hipError_t launch_big(MxArgs p, hipStream_t stream)
     p.tiles_m = (p.m + kBig - 1) / kBig;
     p.tiles_n = (p.n + kBig - 1) / kBig;
     p.group_m = 4;
+    p.pair_store = p.pair_store && p.n % 2 == 0;
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_big_gemm),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_mx4_big_gemm, dim3(p.tiles_m * p.tiles_n * p.splits), dim3(kBigThreads), kBigLds, stream, p);
+    const int grid = std::min(p.tiles_m * p.tiles_n * p.splits, gemm_num_cus());
+    hipLaunchKernelGGL(k_mx4_big_gemm, dim3(grid), dim3(kBigThreads), kBigLds, stream, p);
     return hipGetLastError();
 }
 
