@@ -294,7 +294,7 @@ constexpr int kBigStores = 64;                  // of a tile, by a wave
 // Position of 16-byte chunk c (0..3) in the 64-byte LDS row r: as for swz32,
 // 16 rows at one chunk fill the 16 slots of a 256-byte line and 32 rows with
 // two chunks the 32 of 512 bytes.  An involution in c.
-__device__ inline int swz64(int r, int c) { return c ^ ((((r >> 2) ^ (r >> 4)) & 1) | ((r >> 2) & 2)); }
+__device__ inline int swz64(int r, int c) { return c ^ (((r >> 2) & 1) | (((r >> 1) ^ (r >> 2) ^ (r >> 3)) & 1) << 1); }
 
 // A tile and K split.
 struct BigItem {
@@ -473,14 +473,14 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
             }
             // past this every wave has read the whole stage: its slot is free
             gemm::barrier_lds();
-            products(std::integral_constant<int, 1>{}, 0, 2);
+            products(std::integral_constant<int, 1>{}, 0, 4);
+            fill();
             slot = (slot + 1) & 3;
             const int next = t + 1 == it.nt ? 0 : t + 1;
             if ((next & 3) == 0) panel = panel == kBigPanels - 1 ? 0 : panel + 1;
             read(std::integral_constant<int, 0>{});
             read_scales(next);
-            fill();
-            products(std::integral_constant<int, 1>{}, 2, 8);
+            products(std::integral_constant<int, 1>{}, 4, 8);
         }
         if (!p.ws && p.pair_store) {
             // 64 stores of two adjacent outputs, those out of range dropped
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
                     const uint32_t h = gemm::pack_bf16(acc[i][0][r], acc[i][1][r]);
                     track_max(mx, h);
                     __builtin_amdgcn_raw_buffer_store_b32(h, rc, (int)(at + (uint32_t)(32 * i + 8 * (r >> 2) + (r & 3)) * (uint32_t)p.ldc * 2),
-                                                          0, 2);
+                                                          0, 0);
                 }
             stored = 0;
             if (p.ctr && (mx.x >= 0x7F80u || mx.y >= 0x7F80u)) {
