@@ -10,16 +10,21 @@
 //
 // What bounds it is the read of the chosen experts' codes, half a byte a
 // weight, each read once; so the weights go from memory to the registers of
-// v_mfma_scale_f32_16x16x128_f8f6f4 as they lie (16 rows of weights by up to
-// 16 tokens), with no decoding.  The activations are the instruction's E4M3
-// operand: a block of 32 values is the sum of pieces, each E4M3 (4 bits) with
-// a power of two scale of its own, every next piece's 2^-4 of the one before
-// and holding what the last left.  Two pieces hold a bf16 x exactly, but for
-// elements under 2^-13 of their block's largest, which are off by at most
-// 2^-21 of that; three hold the fp32 intermediate a to 2^-12 of itself (or
-// 2^-25 of the block's largest), a sixteenth of the output's own rounding.
-// Sums are fp32, in an order that only the sizes and the chosen experts set:
-// no atomics on values.
+// v_mfma_scale_f32_16x16x128_f8f6f4 as they lie (16 rows of weights by 16
+// columns of activations), with no decoding.  The activations are the
+// instruction's E4M3 operand: a block of 32 values is the sum of pieces, each
+// E4M3 (4 bits) with a power of two scale of its own, every next piece's 2^-4
+// of the one before and holding what the last left.  Two pieces hold a bf16 x
+// exactly, but for elements under 2^-13 of their block's largest, which are
+// off by at most 2^-21 of that; three hold the fp32 intermediate a to 2^-14
+// of itself (or 2^-25 of the block's largest), far under the output's own
+// rounding.  A column is one piece of one token, so that the few tokens of an
+// expert share the 16 columns with their pieces; the columns of a token are
+// added at the end.  Sums are fp32, in an order that only the sizes and the
+// chosen experts set: no atomics on values.
+//
+// Three launches: the router, which also lists the reached experts and their
+// tokens; up; down.
 #include <algorithm>
 
 #include "device_common.h"
@@ -35,19 +40,31 @@ using gemm::v4f;
 using gemm::v8i;
 typedef double v4d __attribute__((ext_vector_type(4)));
 
-constexpr int kUnit = 256;          // K elements of a row read at a time: two matrix instructions
+constexpr int kUnit = 256;          // K elements of a row of codes: rows are padded to whole units
 constexpr int kXPieces = 2, kAPieces = 3;
-constexpr int kRouteThreads = 512;
-constexpr int kUpThreads = 256;
-constexpr int kDownThreads = 1024;
+constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;
 
+// A reached expert, the mask of its tokens, and where they lie among all
+// chosen (token, expert) pairs in order of the experts, then of the tokens:
+// places off, off + 1, ..
+struct MoeReached {
+    int32_t expert, off;
+    uint64_t mask;
+};
+// The second layer takes an expert's tokens 16 / 3 at a time (a column each
+// piece): the first 5 of the mask, from place off on.
+constexpr int kDownTokens = 16 / kAPieces;
+using MoeGroup = MoeReached;
+
+// Workspace.  What workgroups of one launch hand to each other goes through
+// agent-scope atomics.
 struct MoeArgs {
     const uint16_t* x;
     int64_t ldx;
     const uint16_t* router;
     int64_t ldr;
     int tokens, experts, top_k, hidden, inner, renormalize;
-    int hp, ip;                     // hidden, inner in whole units
+    int hp, ip;                     // hidden, inner in whole panels of 512
     const uint8_t* q1;
     const uint8_t* s1;
     int64_t ldq1, eq1, ps1, es1;    // bytes between rows, experts, scale panels, experts' scales
@@ -58,17 +75,28 @@ struct MoeArgs {
     int64_t ldy;
     int32_t* ids;
     float* weights;
-    // workspace
-    uint32_t* arrived;              // [4]: router tiles done, of 16 tokens each; zero between calls
-    double* logits;                 // [tokens, experts]
-    uint8_t* xq;                    // [tokens, 2, hp]
-    uint8_t* xs;                    // [tokens, hp / 32]
-    uint8_t* aq;                    // [tokens top_k, 3, ip]
-    uint8_t* as;                    // [tokens top_k, ip / 32]
+    uint32_t* arrived;              // [5] router workgroups done: of each 16 tokens, and token tiles; zero between calls
+    double* logits;                 // [splits, tokens, experts] partial sums
+    uint8_t* xq;                    // [tokens, 2, hp] pieces
+    uint8_t* xs;                    // [tokens, 2, hp / 32] their scale bytes
+    int32_t* count;                 // [2] reached experts, groups of their tokens
+    MoeReached* reached;            // [min(tokens top_k, experts)], by expert
+    MoeGroup* groups;               // [max_groups()], by expert
+    float* prob;                    // [tokens top_k] the weight at each place
+    uint8_t* aq;                    // [tokens top_k, 3, ip] pieces at each place
+    uint8_t* as;                    // [tokens top_k, 3, ip / 32]
     fp8_counters* ctr;
-    int tiles_e, tiles_t;           // router tiles
-    int by_pair;                    // a slot is a (token, rank) pair, else an expert
+    float* part;                    // [shares, tokens, hidden] partial sums of y
+    uint32_t* arrived_rows;         // [row blocks of y] workgroups done; zero between calls
+    int tiles_e, tiles_t, splits;   // router tiles of 16 x 16, K splits
+    int shares;                     // workgroups that share a row block of y
+    int max_groups;                 // most groups there can be
 };
+
+template <typename T>
+__device__ inline void agent_store(T* p, T v) { __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <typename T>
+__device__ inline T agent_load(const T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
 // ------------------------------------------------------------------ pieces
 // E8M0 byte of the first piece's scale of a block with that amax: v / s in
@@ -104,20 +132,62 @@ __device__ inline void to_pieces(const float x[4], float inv, uint32_t out[P])
 __device__ inline float inv_scale(uint32_t b) { return __builtin_bit_cast(float, (254u - b) << 23); }
 
 // ------------------------------------------------------------------ matrix instruction
-__device__ inline v8i weights_of(const uint4& v) { return v8i{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0}; }
-__device__ inline v8i codes_of(const uint4& a, const uint4& b)
+// One unit (256 K) of a lane's row of weights, and of its column.  16 rows x
+// 16 columns x 128 K an instruction: lane l holds 32 weights of row l % 16, K
+// 32 (l / 16) on; of column l % 16 the codes of K 16 (l / 16) on and of K 64 +
+// 16 (l / 16) on; and both scale bytes of K block l / 16.
+struct UnitW {
+    uint4 q[2];
+};
+struct UnitX {
+    uint4 q[2][2];
+};
+template <typename T>
+__device__ inline T load_at(const uint8_t* base, uint32_t off)
 {
-    return v8i{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    return *reinterpret_cast<const T*>(base + off);
 }
-// 16 rows of weights x 16 tokens x 128 K.  Lane l holds 32 weights of row
-// l % 16, K 32 (l / 16) on; of token l % 16 the codes of K 16 (l / 16) on and
-// of K 64 + 16 (l / 16) on; the scale bytes of both for K block l / 16.
-__device__ inline v4f mma(const v8i& w, const v8i& x, const v4f& c, uint32_t sw, uint32_t sx)
+// base uniform; off: the lane's row (column), 16 (l / 16) bytes in.
+__device__ inline void load_w(UnitW& o, const uint8_t* base, uint32_t off)
 {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 4, 0, 0, (int)sw, 0, (int)sx);
+    o.q[0] = load_at<uint4>(base, off);
+    o.q[1] = load_at<uint4>(base + 64, off);
+}
+__device__ inline void load_x(UnitX& o, const uint8_t* base, uint32_t off)
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) o.q[k][h] = load_at<uint4>(base + 128 * k + 64 * h, off);
+}
+// sw, sx: the unit's 8 scale bytes.
+__device__ inline void unit_mma(v4f& acc, const UnitW& w, const UnitX& x, const uint2& sw, const uint2& sx)
+{
+    const int sh = 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const v8i a = v8i{(int)w.q[k].x, (int)w.q[k].y, (int)w.q[k].z, (int)w.q[k].w, 0, 0, 0, 0};
+        const v8i b = v8i{(int)x.q[k][0].x, (int)x.q[k][0].y, (int)x.q[k][0].z, (int)x.q[k][0].w,
+                          (int)x.q[k][1].x, (int)x.q[k][1].y, (int)x.q[k][1].z, (int)x.q[k][1].w};
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, (int)((k ? sw.y : sw.x) >> sh), 0,
+                                                               (int)((k ? sx.y : sx.x) >> sh));
+    }
 }
 
+// A neighbour's value within 16 lanes.
+template <int CTRL>
+__device__ inline float dpp_f(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+constexpr int kDppXor1 = 0xB1, kDppNext1 = 0x101, kDppNext2 = 0x102;    // lanes l ^ 1, l + 1, l + 2
+
 // ------------------------------------------------------------------ router
+constexpr int kRouteThreads = 512;
+constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kChunk = 32;          // K of 8 fp64 matrix instructions
+constexpr int kRouteDepth = 4;      // chunks read at a time
+
 // Eight elements of a row from column c on, zeros past the end.
 template <bool VEC>
 __device__ inline uint4 row8(const uint16_t* row, int c, int cols)
@@ -135,6 +205,38 @@ __device__ inline uint4 row8(const uint16_t* row, int c, int cols)
     return v;
 }
 
+// One wave: 512 columns of a token to pieces.
+template <bool VEC>
+__device__ inline void cut_x(const MoeArgs& p, int item)
+{
+    const int lane = threadIdx.x & 63;
+    const int panels = (p.hp + mx4::kPanel - 1) / mx4::kPanel;
+    const int t = item / panels, c = (item - t * panels) * mx4::kPanel + 8 * lane;
+    if (t >= p.tokens || c >= p.hp) return;
+    const uint4 v = row8<VEC>(p.x + t * p.ldx, c, p.hidden);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) amax = max(amax, max(w[j] & 0x7FFF0000u, (w[j] << 16) & 0x7FFF0000u));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, 64));
+    amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, 64));
+    const bool finite = amax < 0x7F800000u;
+    const uint32_t b = finite ? piece_byte(amax) : 255u;
+    uint32_t o[2][kXPieces];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float f[4] = {bf16_lo(w[2 * h]), bf16_hi(w[2 * h]), bf16_lo(w[2 * h + 1]), bf16_hi(w[2 * h + 1])};
+        to_pieces<kXPieces>(f, inv_scale(finite ? b : 127u), o[h]);
+    }
+#pragma unroll
+    for (int i = 0; i < kXPieces; ++i) {
+        *reinterpret_cast<uint2*>(p.xq + (int64_t)(t * kXPieces + i) * p.hp + c) =
+            finite ? uint2{o[0][i], o[1][i]} : uint2{0, 0};
+        if ((lane & 3) == 0)
+            p.xs[(int64_t)(t * kXPieces + i) * (p.hp / 32) + c / 32] = (uint8_t)(finite ? b - 4 * i : 255u);
+    }
+}
+
 // fp64 as an unsigned key of the same order; NaN lowest, +0 and -0 alike
 __device__ inline uint64_t key_of(double v)
 {
@@ -143,61 +245,85 @@ __device__ inline uint64_t key_of(double v)
     return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
 
-__device__ inline double logit_at(const MoeArgs& p, int t, int e)
+// The largest value of the wave's lanes, in every lane.
+__device__ inline uint32_t max_of_wave(uint32_t v)
 {
-    return __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p.logits) + (int64_t)t * p.experts + e,
-                                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    const auto step = [](uint32_t a, int moved) { return max(a, (uint32_t)moved); };
+    v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));      // l ^ 1
+    v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));      // l ^ 2
+    v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, true));     // 4, then 8 across of 16
+    v = step(v, __builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max((uint32_t)a[0], (uint32_t)a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// One wave: the top_k experts of token t and their weights.
-constexpr int kMaxExperts = 512;
+// One wave: the top_k experts of token t and their weights.  Lane l holds
+// experts l, l + 64, ..
 __device__ inline void select(const MoeArgs& p, int t)
 {
     const int lane = threadIdx.x & 63;
     constexpr int kPer = kMaxExperts / 64;
     uint64_t key[kPer];
     double l[kPer];
+    const int64_t split = (int64_t)p.tokens * p.experts;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         const int e = 64 * j + lane;
-        key[j] = 0;
         l[j] = 0;
-        if (64 * j < p.experts && e < p.experts) {
-            l[j] = logit_at(p, t, e);
-            key[j] = key_of(l[j]);
+        if (64 * j < p.experts) {
+            const uint64_t* at = reinterpret_cast<const uint64_t*>(p.logits) + (int64_t)t * p.experts + min(e, p.experts - 1);
+            uint64_t part[8];
+            for (int s0 = 0; s0 < p.splits; s0 += 8) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s) part[s] = s0 + s < p.splits ? agent_load(at + (s0 + s) * split) : 0;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) l[j] += __builtin_bit_cast(double, part[s]);
+            }
         }
+        key[j] = key_of(l[j]);
     }
-    uint32_t taken = 0;
+    uint32_t open = 0;                  // which of its experts are not taken
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) open |= (uint32_t)(64 * j + lane < p.experts) << j;
     double top = 0, mine = 0;           // lane r keeps rank r's
     int id = 0;
     for (int r = 0; r < p.top_k; ++r) {
         uint64_t best = 0;
-        int at = -1;
+        int at = kPer;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (64 * j + lane < p.experts && !(taken >> j & 1) && (at < 0 || key[j] > best)) {
+        for (int j = kPer - 1; j >= 0; --j)
+            if (64 * j < p.experts && (open >> j & 1) && (at == kPer || key[j] >= best)) {
                 best = key[j];
                 at = j;
             }
-        int e = at < 0 ? 0x7FFFFFFF : 64 * at + lane;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            const uint64_t ob = __shfl_xor(best, off, 64);
-            const int oe = __shfl_xor(e, off, 64);
-            const bool take = oe != 0x7FFFFFFF && (e == 0x7FFFFFFF || ob > best || (ob == best && oe < e));
-            best = take ? ob : best;
-            e = take ? oe : e;
+        const int e = 64 * at + lane;
+        // the lanes that hold the largest: by the high words, the low words,
+        // the expert
+        const uint32_t hi = at < kPer ? (uint32_t)(best >> 32) : 0u, lo = (uint32_t)best;
+        const uint32_t top_hi = max_of_wave(hi);
+        uint64_t who = __ballot(at < kPer && hi == top_hi);
+        if (__builtin_popcountll(who) > 1) {
+            const bool in = who >> lane & 1;
+            const uint32_t top_lo = max_of_wave(in ? lo : 0u);
+            const bool still = in && lo == top_lo;
+            const uint32_t first = ~max_of_wave(still ? ~(uint32_t)e : 0u);
+            who = __ballot(still && (uint32_t)e == first);
         }
-        const int owner = e & 63, slot = e >> 6;
-        double v = 0;
+        const int owner = __builtin_ctzll(who);
+        double v = l[0];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) v = j == slot ? l[j] : v;
-        v = __shfl(v, owner, 64);
-        if (lane == owner) taken |= 1u << slot;
+        for (int j = 1; j < kPer; ++j) v = j == at ? l[j] : v;
+        const uint64_t vb = __builtin_bit_cast(uint64_t, v);
+        v = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)vb, owner) |
+                                           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(vb >> 32), owner) << 32);
+        const int chosen = __builtin_amdgcn_readlane(e, owner);
+        if (lane == owner) open &= ~(1u << at);
         if (r == 0) top = v;
         if (lane == r) {
             mine = v;
-            id = e;
+            id = chosen;
         }
     }
     const float z = lane < p.top_k ? expf((float)(mine - top)) : 0.0f;
@@ -211,65 +337,137 @@ __device__ inline void select(const MoeArgs& p, int t)
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
     if (lane < p.top_k) {
-        p.ids[t * p.top_k + lane] = id;
-        p.weights[t * p.top_k + lane] = z / sum;
+        agent_store(p.ids + t * p.top_k + lane, id);
+        agent_store(p.weights + t * p.top_k + lane, z / sum);
     }
 }
 
-// Workgroups below tiles_e tiles_t take 16 tokens x 16 experts of the logits,
-// K over their waves; the last of a token tile's to arrive selects.  The
-// others cut x into pieces, 512 columns of a token a wave.
+// Adds this workgroup to a count of `all`, after its stores have completed.
+// True in the last of them, which leaves the count zero.
+__device__ inline bool last_of(uint32_t* count, uint32_t all)
+{
+    __shared__ int s_last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s_last = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == all;
+        if (s_last) agent_store(count, 0u);
+    }
+    __syncthreads();
+    return s_last;
+}
+
+// The reached experts in order, and each one's tokens in order.
+__device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off)
+{
+    __shared__ int s_n[kRouteWaves], s_groups[kRouteWaves], s_active[kRouteWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    static_assert(kRouteThreads >= kMaxExperts && kMaxTokens * kMaxTopK <= 2 * kRouteThreads, "a thread each");
+    mask[threadIdx.x] = 0;
+    __syncthreads();
+    int e[2];
+    float w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int pair = threadIdx.x + i * kRouteThreads;
+        e[i] = -1;
+        w[i] = 0;
+        if (pair < p.tokens * p.top_k) {
+            e[i] = min(max(agent_load(p.ids + pair), 0), p.experts - 1);
+            w[i] = agent_load(p.weights + pair);
+            atomicOr(&mask[e[i]], 1ull << (pair / p.top_k));
+        }
+    }
+    __syncthreads();
+    const int n = __builtin_popcountll(mask[threadIdx.x]);
+    const uint64_t here = __ballot(n > 0);
+    const int groups = (n + kDownTokens - 1) / kDownTokens;
+    int before = n, first = groups;     // inclusive sums over the wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(before, d, 64), og = __shfl_up(first, d, 64);
+        before += lane >= d ? o : 0;
+        first += lane >= d ? og : 0;
+    }
+    if (lane == 63) {
+        s_n[wave] = before;
+        s_groups[wave] = first;
+        s_active[wave] = __builtin_popcountll(here);
+    }
+    __syncthreads();
+    int at = before - n, active = 0;
+    first -= groups;
+#pragma unroll
+    for (int i = 0; i < kRouteWaves; ++i) {
+        at += i < wave ? s_n[i] : 0;
+        first += i < wave ? s_groups[i] : 0;
+        active += i < wave ? s_active[i] : 0;
+    }
+    off[threadIdx.x] = at;
+    if (n > 0)
+        p.reached[active + __builtin_popcountll(here & ((1ull << lane) - 1))] =
+            MoeReached{(int)threadIdx.x, at, mask[threadIdx.x]};
+    uint64_t left = mask[threadIdx.x];
+    for (int g = 0; g < groups; ++g) {
+        p.groups[first + g] = MoeGroup{(int)threadIdx.x, at + kDownTokens * g, left};
+        for (int j = 0; j < kDownTokens; ++j) left &= left - 1;
+    }
+    if (threadIdx.x == kRouteThreads - 1) {
+        p.count[0] = active + __builtin_popcountll(here);
+        p.count[1] = first + groups;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (e[i] >= 0) {
+            const int t = (threadIdx.x + i * kRouteThreads) / p.top_k;
+            const int to = off[e[i]] + __builtin_popcountll(mask[e[i]] & ((1ull << t) - 1));
+            p.prob[to] = w[i];
+        }
+}
+
+// Workgroups below tiles_e tiles_t splits take 16 tokens x 16 experts of the
+// logits and a share of K, which their waves split.  The last of 16 tokens to
+// arrive selects, the last of those lists the reached experts.  The others
+// cut x into pieces.  fp64 sums: products of bf16 are exact in fp64, so that
+// the chosen experts do not hang on the order of a sum.
 template <bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
 {
-    constexpr int kWaves = kRouteThreads / 64;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nroute = p.tiles_e * p.tiles_t;
+    const int nroute = p.tiles_e * p.tiles_t * p.splits;
     if ((int)blockIdx.x >= nroute) {
-        const int panels = (p.hp + mx4::kPanel - 1) / mx4::kPanel;
-        const int item = ((int)blockIdx.x - nroute) * kWaves + wave;
-        const int t = item / panels, c = (item - t * panels) * mx4::kPanel + 8 * lane;
-        if (t >= p.tokens || c >= p.hp) return;
-        const uint4 v = row8<VEC>(p.x + t * p.ldx, c, p.hidden);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t amax = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) amax = max(amax, max(w[j] & 0x7FFF0000u, (w[j] << 16) & 0x7FFF0000u));
-        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, 64));
-        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, 64));
-        const bool finite = amax < 0x7F800000u;
-        const uint32_t b = finite ? piece_byte(amax) : 255u;
-        uint8_t* q = p.xq + (int64_t)t * kXPieces * p.hp + c;
-        uint32_t o[2][kXPieces];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float f[4] = {bf16_lo(w[2 * h]), bf16_hi(w[2 * h]), bf16_lo(w[2 * h + 1]), bf16_hi(w[2 * h + 1])};
-            to_pieces<kXPieces>(f, inv_scale(finite ? b : 127u), o[h]);
-        }
-#pragma unroll
-        for (int i = 0; i < kXPieces; ++i)
-            *reinterpret_cast<uint2*>(q + (int64_t)i * p.hp) = finite ? uint2{o[0][i], o[1][i]} : uint2{0, 0};
-        if ((lane & 3) == 0) p.xs[(int64_t)t * (p.hp / 32) + c / 32] = (uint8_t)b;
+        cut_x<VEC>(p, ((int)blockIdx.x - nroute) * kRouteWaves + wave);
         return;
     }
-
-    __shared__ double red[kWaves][256];
-    __shared__ int s_last;
-    const int tt = blockIdx.x / p.tiles_e, te = blockIdx.x - tt * p.tiles_e;
+    __shared__ __attribute__((aligned(16))) double red[kRouteWaves][256];
+    static_assert(sizeof(red) >= kMaxExperts * (sizeof(uint64_t) + sizeof(int)), "the lists' masks and places");
+    const int tt = blockIdx.x / (p.tiles_e * p.splits), rest = blockIdx.x - tt * p.tiles_e * p.splits;
+    const int split = rest / p.tiles_e, te = rest - split * p.tiles_e;
     const int t = min(16 * tt + (lane & 15), p.tokens - 1), e = min(16 * te + (lane & 15), p.experts - 1);
     const uint16_t* xr = p.x + t * p.ldx;
     const uint16_t* rr = p.router + e * p.ldr;
     v4d acc = {0, 0, 0, 0};
-    const int chunks = (p.hidden + 31) / 32;
-    for (int c = wave; c < chunks; c += kWaves) {
-        const uint4 a = row8<VEC>(rr, 32 * c + 8 * (lane >> 4), p.hidden);
-        const uint4 b = row8<VEC>(xr, 32 * c + 8 * (lane >> 4), p.hidden);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    const int chunks = (p.hidden + kChunk - 1) / kChunk;
+    const int stride = kRouteWaves * p.splits;
+    for (int c0 = split * kRouteWaves + wave; c0 < chunks; c0 += kRouteDepth * stride) {
+        uint4 a[kRouteDepth], b[kRouteDepth];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)bf16_lo(aw[j]), (double)bf16_lo(bw[j]), acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)bf16_hi(aw[j]), (double)bf16_hi(bw[j]), acc, 0, 0, 0);
+        for (int d = 0; d < kRouteDepth; ++d) {
+            const int c = kChunk * (c0 + d * stride) + 8 * (lane >> 4);
+            a[d] = row8<VEC>(rr, c, p.hidden);
+            b[d] = row8<VEC>(xr, c, p.hidden);
+        }
+#pragma unroll
+        for (int d = 0; d < kRouteDepth; ++d) {
+            if (c0 + d * stride >= chunks) break;
+            const uint32_t aw[4] = {a[d].x, a[d].y, a[d].z, a[d].w}, bw[4] = {b[d].x, b[d].y, b[d].z, b[d].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)bf16_lo(aw[j]), (double)bf16_lo(bw[j]), acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)bf16_hi(aw[j]), (double)bf16_hi(bw[j]), acc, 0, 0, 0);
+            }
         }
     }
     // register i of lane l: expert 4 i + l / 16, token l % 16
@@ -279,286 +477,360 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
     if (threadIdx.x < 256) {
         double s = red[0][threadIdx.x];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) s += red[w][threadIdx.x];
+        for (int w = 1; w < kRouteWaves; ++w) s += red[w][threadIdx.x];
         const int oe = 16 * te + (threadIdx.x >> 4), ot = 16 * tt + (threadIdx.x & 15);
-        // agent-scope stores and loads need no write-back of the L2s between them
         if (oe < p.experts && ot < p.tokens)
-            __hip_atomic_store(reinterpret_cast<uint64_t*>(p.logits) + (int64_t)ot * p.experts + oe,
-                               __builtin_bit_cast(uint64_t, s), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            agent_store(reinterpret_cast<uint64_t*>(p.logits) + ((int64_t)split * p.tokens + ot) * p.experts + oe,
+                        __builtin_bit_cast(uint64_t, s));
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // the stores have completed
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        const uint32_t n = __hip_atomic_fetch_add(p.arrived + tt, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = n + 1 == (uint32_t)p.tiles_e;
-        if (s_last) __hip_atomic_store(p.arrived + tt, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    for (int i = wave; i < 16; i += kWaves)
+    if (!last_of(p.arrived + tt, (uint32_t)(p.tiles_e * p.splits))) return;
+    for (int i = wave; i < 16; i += kRouteWaves)
         if (16 * tt + i < p.tokens) select(p, 16 * tt + i);
+    if (!last_of(p.arrived + kMaxTokens / 16, (uint32_t)p.tiles_t)) return;
+    unsigned long long* mask = reinterpret_cast<unsigned long long*>(&red[0][0]);
+    list_reached(p, mask, reinterpret_cast<int*>(mask + kMaxExperts));
+}
+
+// Lists that an earlier launch wrote, at uniform places: read through the
+// scalar cache, beside the vector reads and not in their order.
+template <typename T>
+__device__ inline T listed(const T* list, int i)
+{
+    return ((const __attribute__((address_space(4))) T*)list)[i];
+}
+// What the lists hold, within their bounds whatever is there: a workspace
+// that was not zeroed makes wrong results, not wild reads.
+__device__ inline int reached_count(const MoeArgs& p)
+{
+    return min(max(listed(p.count, 0), 0), min(p.tokens * p.top_k, p.experts));
+}
+__device__ inline int group_count(const MoeArgs& p)
+{
+    return reached_count(p) > 0 ? min(max(listed(p.count, 1), 1), p.max_groups) : 0;
+}
+__device__ inline MoeReached reached_at(const MoeArgs& p, const MoeReached* list, int i)
+{
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(list + i);
+    MoeReached r;
+    r.expert = min(max((int)listed(words, 0), 0), p.experts - 1);
+    r.mask = ((uint64_t)listed(words, 2) | (uint64_t)listed(words, 3) << 32) & (~0ull >> (64 - p.tokens));
+    r.mask = r.mask ? r.mask : 1ull;
+    r.off = min(max((int)listed(words, 1), 0), p.tokens * p.top_k - __builtin_popcountll(r.mask));
+    return r;
+}
+// The c-th token of a mask.
+__device__ inline int token_of(uint64_t mask, int c)
+{
+    for (int j = 0; j < c; ++j) mask &= mask - 1;
+    return __builtin_ctzll(mask);
 }
 
 // ------------------------------------------------------------------ up
-// One unit (256 K) of R tiles of 16 weight rows against 16 tokens.
-struct RowPtr {
-    const uint8_t* q;       // this lane's row of codes, 16 (l / 16) bytes in
-    const uint8_t* s;       // its first panel's scale bytes
-};
-
-template <int P>
-struct UnitX {
-    uint4 q[2][P][2];
-    uint2 s;
-};
-// x: this lane's token, 16 (l / 16) bytes in; piece bytes apart.
-template <int P>
-__device__ inline void load_x(UnitX<P>& o, const uint8_t* q, int64_t piece, const uint8_t* s, int u)
-{
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const uint8_t* a = q + i * piece + u * kUnit + 128 * k;
-            o.q[k][i][0] = *reinterpret_cast<const uint4*>(a);
-            o.q[k][i][1] = *reinterpret_cast<const uint4*>(a + 64);
-        }
-    o.s = *reinterpret_cast<const uint2*>(s + 8 * u);
-}
-struct UnitW {
-    uint4 q[2];
-    uint2 s;
-};
-__device__ inline void load_w(UnitW& o, const RowPtr& r, int64_t ps, int u)
-{
-    o.q[0] = *reinterpret_cast<const uint4*>(r.q + u * 128);
-    o.q[1] = *reinterpret_cast<const uint4*>(r.q + u * 128 + 64);
-    o.s = *reinterpret_cast<const uint2*>(r.s + (u >> 1) * ps + 8 * (u & 1));
-}
-template <int P>
-__device__ inline void unit_mma(v4f& acc, const UnitW& w, const UnitX<P>& x)
-{
-    const int sh = 8 * ((threadIdx.x & 63) >> 4);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t sw = (k ? w.s.y : w.s.x) >> sh, sx = (k ? x.s.y : x.s.x) >> sh;
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-            acc = mma(weights_of(w.q[k]), codes_of(x.q[k][i][0], x.q[k][i][1]), acc, sw, sx - 4 * i);
-    }
-}
-
-__device__ inline uint64_t tokens_of(const MoeArgs& p, int e, int& rank)
-{
-    const int lane = threadIdx.x & 63;
-    bool has = false;
-    rank = 0;
-    if (lane < p.tokens)
-        for (int j = 0; j < p.top_k; ++j)
-            if (p.ids[lane * p.top_k + j] == e) {
-                has = true;
-                rank = j;
-            }
-    return __ballot(has);
-}
+constexpr int kUpThreads = 256;
+constexpr int kUpWaves = kUpThreads / 64;
+constexpr int kUpTokens = 16 / kXPieces;    // of 16 columns
 
 // A workgroup takes an expert's 32 gate rows and the 32 up rows of the same
-// outputs, K over its waves.
-__global__ void __launch_bounds__(kUpThreads) k_moe_up(MoeArgs p)
+// outputs, K over its waves, for up to 16 tokens at a time (two tiles of
+// columns).  Codes of x past the last unit are zeros, so that a wave may
+// read the last unit's weights again in the place of one past it.
+__global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
 {
-    constexpr int kWaves = kUpThreads / 64;
-    __shared__ v4f red[kWaves][4][64];
-    __shared__ int s_pair[64];
+    __shared__ v4f red[2][kUpWaves][4][32];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = (p.inner + 31) / 32;
     const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
-    const int e = p.by_pair ? __builtin_amdgcn_readfirstlane(p.ids[slot]) : slot;
-    if ((uint32_t)e >= (uint32_t)p.experts) return;     // no selection: the workspace was not zeroed
-    int rank;
-    const uint64_t mask = tokens_of(p, e, rank);
-    // an expert's first pair stands for all of its tokens
-    if (mask == 0 || (p.by_pair && __builtin_ctzll(mask) != slot / p.top_k)) return;
-    if (wave == 0 && (mask >> lane & 1))
-        s_pair[__builtin_popcountll(mask & ((1ull << lane) - 1))] = lane * p.top_k + rank;
-    __syncthreads();
-    const int n = __builtin_popcountll(mask);
+    const MoeReached at = reached_at(p, p.reached, slot);
+    if (slot >= reached_count(p)) return;
+    const int e = at.expert, off = at.off;
+    const int n = __builtin_popcountll(at.mask);
     const int c16 = lane & 15, q = lane >> 4;
 
-    RowPtr w[4];
+    // gate rows; up rows lie `inner` rows on
+    const uint8_t* wq = p.q1 + e * p.eq1 + 32 * tile * p.ldq1;
+    const uint8_t* ws = p.s1 + e * p.es1 + 32 * tile * 16;
+    uint32_t woff[2], soff[2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int row = min(32 * tile + 16 * (r & 1) + c16, p.inner - 1) + (r >> 1) * p.inner;
-        w[r].q = p.q1 + e * p.eq1 + row * p.ldq1 + 16 * q;
-        w[r].s = p.s1 + e * p.es1 + row * 16;
+    for (int h = 0; h < 2; ++h) {
+        const int row = min(16 * h + c16, p.inner - 1 - 32 * tile);
+        woff[h] = (uint32_t)(row * p.ldq1 + 16 * q);
+        soff[h] = (uint32_t)(row * 16);
     }
-    const int units = p.hp / kUnit;
-    for (int c0 = 0; c0 < n; c0 += 16) {
-        const int pair = s_pair[min(c0 + c16, n - 1)];
-        const int t = pair / p.top_k;
-        const uint8_t* xq = p.xq + (int64_t)t * kXPieces * p.hp + 16 * q;
-        const uint8_t* xs = p.xs + (int64_t)t * (p.hp / 32);
-        v4f acc[4] = {};
-        for (int u = wave; u < units; u += kWaves) {
-            UnitW uw[4];
-            UnitX<kXPieces> ux;
+    const int units = (p.hidden + kUnit - 1) / kUnit;
+    for (int c0 = 0; c0 < n; c0 += 2 * kUpTokens) {
+        const int cols = kXPieces * (n - c0);
+        const bool two = cols > 16;
+        uint32_t xrow[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) load_w(uw[r], w[r], p.ps1, u);
-            load_x(ux, xq, p.hp, xs, u);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) unit_mma(acc[r], uw[r], ux);
+        for (int h = 0; h < 2; ++h) {
+            const int col = min(16 * h + c16, cols - 1);
+            xrow[h] = (uint32_t)(token_of(at.mask, c0 + col / kXPieces) * kXPieces + col % kXPieces);
         }
+        // token r of tile h (r = lane / 8), of whose column tile this wave ends with
+        const int c = c0 + wave * kUpTokens + (lane >> 3);
+        const float prob = p.prob[off + min(c, n - 1)];
+        v4f acc[2][4] = {};
+        for (int u = wave; u < units; u += kUpWaves) {
+            UnitW w[4];
+            uint2 sw[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int64_t far = (r >> 1) * (int64_t)p.inner;
+                sw[r] = load_at<uint2>(ws + far * 16 + (u >> 1) * p.ps1 + 8 * (u & 1), soff[r & 1]);
+                load_w(w[r], wq + far * p.ldq1 + u * 128, woff[r & 1]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (h == 0 || two) {
+                    UnitX x;
+                    const uint2 sx = load_at<uint2>(p.xs + 8 * u, xrow[h] * (uint32_t)(p.hp / 32));
+                    load_x(x, p.xq + u * kUnit, xrow[h] * (uint32_t)p.hp + 16 * q);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) unit_mma(acc[h][r], w[r], x, sw[r], sx);
+                }
+        }
+        if (c0 > 0) __syncthreads();
+        // the pieces of a token are neighbours
+        static_assert(kXPieces == 2, "one exchange");
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (h == 0 || two)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    v4f s;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[i] = acc[h][r][i] + dpp_f<kDppXor1>(acc[h][r][i]);
+                    if ((c16 & 1) == 0) red[h][wave][r][8 * q + (c16 >> 1)] = s;
+                }
         __syncthreads();
+        // wave h: the tokens of tile h; lane: token lane / 8 of it, 16 r +
+        // 4 qq + i of the 32 outputs
+        if (wave > 1 || c0 + wave * kUpTokens >= n) continue;
+        const int r = (lane >> 2) & 1, qq = lane & 3;
+        v4f g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave][r][lane] = acc[r];
-        __syncthreads();
-        if (wave != 0) continue;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int o = 1; o < kWaves; ++o) acc[r] += red[o][r][lane];
-        // lane: token c16, outputs 32 tile + 16 r + 4 q + i
-        const float prob = p.weights[pair];
-        float a[2][4];
+        for (int w = 0; w < kUpWaves; ++w) {
+            g += red[wave][w][r][8 * qq + (lane >> 3)];
+            u += red[wave][w][r + 2][8 * qq + (lane >> 3)];
+        }
+        float a[4];
         uint32_t amax = 0;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int i = 0; i < 4; ++i) {
+            const float v = prob * (g[i] / (1.0f + expf(-g[i])) * u[i]);
+            a[i] = 32 * tile + 16 * r + 4 * qq + i < p.inner ? v : 0.0f;
+            amax = max(amax, __builtin_bit_cast(uint32_t, a[i]) & 0x7FFFFFFFu);
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float g = acc[r][i], u = acc[r + 2][i];
-                const float v = prob * (g / (1.0f + expf(-g)) * u);
-                a[r][i] = 32 * tile + 16 * r + 4 * q + i < p.inner ? v : 0.0f;
-                amax = max(amax, __builtin_bit_cast(uint32_t, a[r][i]) & 0x7FFFFFFFu);
-            }
-        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 16, 64));
-        amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32, 64));
+        for (int d = 1; d < 8; d <<= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d, 64));
         const bool finite = amax < 0x7F800000u;
         const uint32_t b = finite ? piece_byte(amax) : 255u;
-        if (c0 + c16 >= n) continue;
-        uint8_t* out = p.aq + (int64_t)pair * kAPieces * p.ip + 32 * tile + 4 * q;
+        uint32_t o[kAPieces];
+        to_pieces<kAPieces>(a, inv_scale(finite ? b : 127u), o);
+        if (c >= n) continue;
+        uint8_t* aq = p.aq + (int64_t)(off + c) * kAPieces * p.ip;
+        uint8_t* as = p.as + (int64_t)(off + c) * kAPieces * (p.ip / 32);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            uint32_t o[kAPieces];
-            to_pieces<kAPieces>(a[r], inv_scale(finite ? b : 127u), o);
-#pragma unroll
-            for (int i = 0; i < kAPieces; ++i)
-                *reinterpret_cast<uint32_t*>(out + (int64_t)i * p.ip + 16 * r) = finite ? o[i] : 0u;
+        for (int i = 0; i < kAPieces; ++i) {
+            *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + 32 * tile + 16 * r + 4 * qq) = finite ? o[i] : 0u;
+            if ((lane & 7) == 0) as[i * (p.ip / 32) + tile] = (uint8_t)(finite ? b - 4 * i : 255u);
         }
-        uint8_t* os = p.as + (int64_t)pair * (p.ip / 32);
-        if (q == 0) os[tile] = (uint8_t)b;
-        // zeros to the end of the last unit
+        // zeros to the end of the last panel
         if (tile == tiles - 1)
-            for (int c = 32 * tiles; c < p.ip; c += 32) {
+            for (int z = 32 * tiles; z < p.ip; z += 32)
 #pragma unroll
-                for (int i = 0; i < kAPieces; ++i)
-                    *reinterpret_cast<uint2*>(p.aq + ((int64_t)pair * kAPieces + i) * p.ip + c + 8 * q) = uint2{0, 0};
-                if (q == 0) os[c / 32] = 127;
-            }
+                for (int i = 0; i < kAPieces; ++i) {
+                    *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + z + 4 * (lane & 7)) = 0u;
+                    if ((lane & 7) == 0) as[i * (p.ip / 32) + z / 32] = 127;
+                }
     }
 }
 
 // ------------------------------------------------------------------ down
-// A workgroup takes 16 rows of y for every token.  Its waves share the reached
-// experts (and their K where those are few) in a fixed order, each with sums
-// of its own in LDS, which are added in wave order at the end.
-__global__ void __launch_bounds__(kDownThreads) k_moe_down(MoeArgs p)
+constexpr int kDownThreads = 256;
+constexpr int kDownWaves = kDownThreads / 64;
+constexpr int kDownRows = 32;
+constexpr int kMaxShares = 8;
+#ifndef FP8MI_DOWN_STEPS
+#define FP8MI_DOWN_STEPS 2
+#endif
+
+// `shares` workgroups take the same 32 rows of y for every token.  Their waves
+// share the steps (up to five tokens of an expert, a panel of K: two units) in
+// a fixed order, each with sums of its own in LDS, which are added in wave
+// order at the end, and over the workgroups by the last of them to arrive.  A
+// step's weights are read two steps ahead and its columns one: reads come back
+// in order, so the columns of the next step are asked for before the weights
+// of the one after it, and no read hangs on a branch (past the end the last
+// step's are read again).
+__global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
 {
-    constexpr int kWaves = kDownThreads / 64;
-    extern __shared__ __attribute__((aligned(16))) float ysum[];     // [waves, tokens, 16]
-    __shared__ unsigned long long s_mask[kMaxExperts];
-    __shared__ int16_t s_expert[kMaxExperts];
-    __shared__ int32_t s_ids[64 * 16];
-    __shared__ int s_count[kMaxExperts / 64];
+    extern __shared__ __attribute__((aligned(16))) float ysum[];     // [waves, tokens, 32]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row0 = 16 * blockIdx.x;
-    const int pairs = p.tokens * p.top_k;
-    if ((int)threadIdx.x < p.experts) s_mask[threadIdx.x] = 0;
-    for (int i = threadIdx.x; i < kWaves * p.tokens * 16; i += kDownThreads) ysum[i] = 0.0f;
-    __syncthreads();
-    if ((int)threadIdx.x < pairs) {
-        const int e = p.ids[threadIdx.x];
-        s_ids[threadIdx.x] = e;
-        if ((uint32_t)e < (uint32_t)p.experts) atomicOr(&s_mask[e], 1ull << (threadIdx.x / p.top_k));
-    }
-    __syncthreads();
-    // the reached experts in order
-    const bool reached = (int)threadIdx.x < p.experts && s_mask[threadIdx.x] != 0;
-    const uint64_t here = __ballot(reached);
-    if (wave < kMaxExperts / 64 && lane == 0) s_count[wave] = __builtin_popcountll(here);
-    __syncthreads();
-    int before = 0, active = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 64; ++i) {
-        before += i < wave ? s_count[i] : 0;
-        active += s_count[i];
-    }
-    if (reached) s_expert[before + __builtin_popcountll(here & ((1ull << lane) - 1))] = (int16_t)threadIdx.x;
-    __syncthreads();
+    const int block = blockIdx.x / p.shares, share = blockIdx.x - block * p.shares;
+    const int row0 = kDownRows * block;
+    const int groups = group_count(p);
 
     const int c16 = lane & 15, q = lane >> 4;
-    const int row = min(row0 + c16, p.hidden - 1);
-    const int units = p.ip / kUnit;
-    const int per = active >= 2 * kWaves ? units : 1;      // units of an item
-    const int chunks = (units + per - 1) / per;
-    float* mine = ysum + wave * p.tokens * 16;
-    for (int item = wave; item < active * chunks; item += kWaves) {
-        const int at = item / chunks, u0 = (item - at * chunks) * per, u1 = min(units, u0 + per);
-        const int e = s_expert[at];
-        const uint64_t mask = s_mask[e];
-        const int n = __builtin_popcountll(mask);
-        RowPtr w;
-        w.q = p.q2 + e * p.eq2 + row * p.ldq2 + 16 * q;
-        w.s = p.s2 + e * p.es2 + row * 16;
-        uint64_t left = mask;
-        for (int c0 = 0; c0 < n; c0 += 16) {
-            // column c: the c-th token of the mask that is left, or its last
-            uint64_t m = left;
-            const int skip = min(c16, n - c0 - 1);
-            for (int j = 0; j < skip; ++j) m &= m - 1;
-            const int t = __builtin_ctzll(m);
-            int pair = 0;
-            for (int j = 0; j < p.top_k; ++j)
-                if (s_ids[t * p.top_k + j] == e) pair = t * p.top_k + j;
-            for (int j = 0; j < 16; ++j) left &= left - 1;
-            const uint8_t* aq = p.aq + (int64_t)pair * kAPieces * p.ip + 16 * q;
-            const uint8_t* as = p.as + (int64_t)pair * (p.ip / 32);
-            v4f acc = {0, 0, 0, 0};
-            for (int u = u0; u < u1; ++u) {
-                UnitW uw;
-                UnitX<kAPieces> ux;
-                load_w(uw, w, p.ps2, u);
-                load_x(ux, aq, p.ip, as, u);
-                unit_mma(acc, uw, ux);
-            }
-            if (c0 + c16 < n) {
-                v4f* s = reinterpret_cast<v4f*>(mine + t * 16 + 4 * q);
-                *s += acc;
-            }
+    uint32_t woff[2], soff[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int row = min(16 * h + c16, p.hidden - 1 - row0);
+        woff[h] = (uint32_t)(row * p.ldq2 + 16 * q);
+        soff[h] = (uint32_t)(row * 16);
+    }
+    const int units = (p.inner + kUnit - 1) / kUnit, panels = p.ip / mx4::kPanel;
+    const int steps = groups * panels;
+    float* mine = ysum + wave * p.tokens * kDownRows;
+
+    struct At {
+        int e, row, n, panel;       // row: of the first token's first piece; n tokens
+        uint64_t mask;
+    };
+    const auto at_step = [&](int i) {
+        At a;
+        i = min(i, steps - 1);
+        const int g = i / panels;
+        a.panel = i - g * panels;
+        const MoeReached r = reached_at(p, p.groups, g);
+        a.mask = r.mask;
+        a.e = r.expert;
+        a.row = kAPieces * r.off;
+        a.n = min(__builtin_popcountll(r.mask), kDownTokens);
+        return a;
+    };
+    struct W {
+        UnitW u[2][2];
+        uint4 s[2];
+    };
+    struct X {
+        UnitX u[2];
+        uint4 s;
+    };
+    const auto get_w = [&](W& w, const At& a) {
+        const uint8_t* base = p.q2 + a.e * p.eq2 + row0 * p.ldq2;
+        const uint8_t* sbase = p.s2 + a.e * p.es2 + a.panel * p.ps2 + row0 * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            w.s[h] = load_at<uint4>(sbase, soff[h]);
+            // past the last unit its weights again, against zeros
+            load_w(w.u[h][0], base + 256 * a.panel, woff[h]);
+            load_w(w.u[h][1], base + 128 * min(2 * a.panel + 1, units - 1), woff[h]);
         }
+    };
+    const auto get_x = [&](X& x, const At& a) {
+        const uint8_t* base = p.aq + (int64_t)a.row * p.ip + mx4::kPanel * a.panel;
+        const uint8_t* sbase = p.as + (int64_t)a.row * (p.ip / 32) + 16 * a.panel;
+        const uint32_t col = (uint32_t)min(c16, kAPieces * a.n - 1);
+        x.s = load_at<uint4>(sbase, col * (uint32_t)(p.ip / 32));
+        load_x(x.u[0], base, col * (uint32_t)p.ip + 16 * q);
+        load_x(x.u[1], base + kUnit, col * (uint32_t)p.ip + 16 * q);
+    };
+    // 32 rows x the tokens of 15 columns, added to this wave's sums
+    const auto compute = [&](const W& w, const X& x, const At& a, bool live) {
+        static_assert(kAPieces == 3, "two neighbours");
+        const int c = c16 / kAPieces;
+        const bool mine_to_add = live && c16 % kAPieces == 0 && c < a.n;
+        v4f* to = reinterpret_cast<v4f*>(mine + token_of(a.mask, min(c, a.n - 1)) * kDownRows + 4 * q);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            v4f acc = {0, 0, 0, 0};
+            unit_mma(acc, w.u[h][0], x.u[0], uint2{w.s[h].x, w.s[h].y}, uint2{x.s.x, x.s.y});
+            unit_mma(acc, w.u[h][1], x.u[1], uint2{w.s[h].z, w.s[h].w}, uint2{x.s.z, x.s.w});
+            v4f sum;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = acc[i] + (dpp_f<kDppNext1>(acc[i]) + dpp_f<kDppNext2>(acc[i]));
+            if (mine_to_add) to[4 * h] += sum;
+        }
+    };
+
+    const int first = share * kDownWaves + wave, stride = p.shares * kDownWaves;
+    W w0, w1;
+    X x0, x1;
+    At a0, a1;
+    if (first < steps) {
+        a0 = at_step(first);
+        a1 = at_step(first + stride);
+        get_w(w0, a0);
+        get_x(x0, a0);
+        get_w(w1, a1);
+    }
+    for (int i = lane; i < p.tokens * kDownRows; i += 64) mine[i] = 0.0f;
+    for (int i = first; i < steps; i += 2 * stride) {
+        get_x(x1, a1);
+        compute(w0, x0, a0, true);
+        a0 = at_step(i + 2 * stride);
+        get_w(w0, a0);
+        get_x(x0, a0);
+        compute(w1, x1, a1, i + stride < steps);
+        a1 = at_step(i + 3 * stride);
+        get_w(w1, a1);
     }
     __syncthreads();
     uint32_t nonfinite = 0;
-    for (int i = threadIdx.x; i < p.tokens * 16; i += kDownThreads) {
-        const int t = i >> 4, r = row0 + (i & 15);
+    const int rows = min(p.hidden - row0, kDownRows);
+    const auto put = [&](int t, int r, float v) {
+        const uint16_t h = gemm::to_bf16(v);
+        nonfinite += (h & 0x7F80u) == 0x7F80u;
+        p.y[t * p.ldy + row0 + r] = h;
+    };
+    for (int i = threadIdx.x; i < p.tokens * kDownRows; i += kDownThreads) {
+        const int t = i / kDownRows, r = i % kDownRows;
         float s = ysum[i];
-        for (int w = 1; w < kWaves; ++w) s += ysum[w * p.tokens * 16 + i];
-        if (r < p.hidden) {
-            const uint16_t h = gemm::to_bf16(s);
-            nonfinite += (h & 0x7F80u) == 0x7F80u;
-            p.y[t * p.ldy + r] = h;
+#pragma unroll
+        for (int w = 1; w < kDownWaves; ++w) s += ysum[w * p.tokens * kDownRows + i];
+        if (r >= rows) continue;
+        if (p.shares == 1)
+            put(t, r, s);
+        else
+            agent_store(p.part + ((int64_t)share * p.tokens + t) * p.hidden + row0 + r, s);
+    }
+    if (p.shares > 1) {
+        if (!last_of(p.arrived_rows + block, (uint32_t)p.shares)) return;
+        for (int i = threadIdx.x; i < p.tokens * kDownRows; i += kDownThreads) {
+            const int t = i / kDownRows, r = i % kDownRows;
+            if (r >= rows) continue;
+            const float* from = p.part + (int64_t)t * p.hidden + row0 + r;
+            float v[kMaxShares];
+#pragma unroll
+            for (int j = 0; j < kMaxShares; ++j)
+                v[j] = j < p.shares ? agent_load(from + (int64_t)j * p.tokens * p.hidden) : 0.0f;
+            float s = v[0];
+#pragma unroll
+            for (int j = 1; j < kMaxShares; ++j) s += v[j];
+            put(t, r, s);
         }
     }
     flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
+// Workgroups that share a row block of y: enough for two on each of 256 CUs,
+// where there is work for them.
+int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
+{
+    const int64_t blocks = (hidden + kDownRows - 1) / kDownRows;
+    const int64_t steps = std::min<int64_t>(tokens * top_k, 128) * ((inner + mx4::kPanel - 1) / mx4::kPanel);
+    return (int)std::clamp<int64_t>(std::min((512 + blocks - 1) / blocks, steps / (FP8MI_DOWN_STEPS * kDownWaves)), 1, kMaxShares);
+}
+
+// K splits of the router: two rounds of reads a workgroup at most, and few
+// enough partial sums.
+int route_splits(int64_t hidden)
+{
+    const int64_t chunks = (hidden + kChunk - 1) / kChunk;
+    return (int)std::clamp<int64_t>((chunks + 2 * kRouteWaves - 1) / (2 * kRouteWaves), 1, 8);
+}
+
 struct MoeLayout {
-    size_t logits, xq, xs, aq, as, total;
+    size_t arrived_rows, zeroed, logits, xq, xs, count, reached, groups, prob, aq, as, part, total;
+    int64_t max_groups;
 };
 MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner)
 {
     const auto up = [](int64_t v, int64_t a) { return (v + a - 1) / a * a; };
-    const int64_t hp = up(hidden, kUnit), ip = up(inner, kUnit);
+    const int64_t hp = up(hidden, mx4::kPanel), ip = up(inner, mx4::kPanel), pairs = tokens * top_k;
     MoeLayout m;
     int64_t at = 256;                                       // arrival counts
     const auto take = [&](int64_t bytes) {
@@ -566,11 +838,20 @@ MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hid
         at = up(at + bytes, 256);
         return (size_t)o;
     };
-    m.logits = take(tokens * experts * 8);
+    m.arrived_rows = take((hidden + kDownRows - 1) / kDownRows * 4);
+    m.zeroed = (size_t)at;
+    m.logits = take(route_splits(hidden) * tokens * experts * 8);
     m.xq = take(tokens * kXPieces * hp);
-    m.xs = take(tokens * (hp / 32));
-    m.aq = take(tokens * top_k * kAPieces * ip);
-    m.as = take(tokens * top_k * (ip / 32));
+    m.xs = take(tokens * kXPieces * (hp / 32));
+    m.count = take(4);
+    m.reached = take(std::min(pairs, experts) * (int64_t)sizeof(MoeReached));
+    // an expert's last group may be short
+    m.max_groups = std::min(pairs, std::min(pairs, experts) + pairs / kDownTokens);
+    m.groups = take(m.max_groups * (int64_t)sizeof(MoeGroup));
+    m.prob = take(pairs * 4);
+    m.aq = take(pairs * kAPieces * ip);
+    m.as = take(pairs * kAPieces * (ip / 32));
+    m.part = take(kMaxShares * tokens * hidden * 4);
     m.total = (size_t)at;
     return m;
 }
@@ -598,8 +879,8 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     p.hidden = (int)g.hidden;
     p.inner = (int)g.inner;
     p.renormalize = g.renormalize;
-    p.hp = (int)((g.hidden + kUnit - 1) / kUnit * kUnit);
-    p.ip = (int)((g.inner + kUnit - 1) / kUnit * kUnit);
+    p.hp = (int)((g.hidden + mx4::kPanel - 1) / mx4::kPanel * mx4::kPanel);
+    p.ip = (int)((g.inner + mx4::kPanel - 1) / mx4::kPanel * mx4::kPanel);
     p.q1 = g.w1.q;
     p.s1 = g.w1.s;
     p.ldq1 = g.w1.ldq;
@@ -620,31 +901,36 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     p.logits = reinterpret_cast<double*>(ws + m.logits);
     p.xq = ws + m.xq;
     p.xs = ws + m.xs;
+    p.count = reinterpret_cast<int32_t*>(ws + m.count);
+    p.reached = reinterpret_cast<MoeReached*>(ws + m.reached);
+    p.groups = reinterpret_cast<MoeGroup*>(ws + m.groups);
+    p.max_groups = (int)m.max_groups;
+    p.prob = reinterpret_cast<float*>(ws + m.prob);
+    p.part = reinterpret_cast<float*>(ws + m.part);
+    p.arrived_rows = reinterpret_cast<uint32_t*>(ws + m.arrived_rows);
+    p.shares = down_shares(g.tokens, g.top_k, g.hidden, g.inner);
     p.aq = ws + m.aq;
     p.as = ws + m.as;
     p.ctr = g.ctr;
     p.tiles_e = (p.experts + 15) / 16;
     p.tiles_t = (p.tokens + 15) / 16;
-    p.by_pair = p.tokens * p.top_k <= p.experts;
+    p.splits = route_splits(p.hidden);
 
     const auto al16 = [](const void* v) { return (reinterpret_cast<uintptr_t>(v) & 15u) == 0; };
     const bool vec = p.hidden % 8 == 0 && p.ldx % 8 == 0 && p.ldr % 8 == 0 && al16(g.x) && al16(g.router);
     const int items = p.tokens * ((p.hp + mx4::kPanel - 1) / mx4::kPanel);
-    const int route = p.tiles_e * p.tiles_t + (items + kRouteThreads / 64 - 1) / (kRouteThreads / 64);
+    const int route = p.tiles_e * p.tiles_t * p.splits + (items + kRouteWaves - 1) / kRouteWaves;
     if (vec)
         hipLaunchKernelGGL((k_moe_route<true>), dim3(route), dim3(kRouteThreads), 0, stream, p);
     else
         hipLaunchKernelGGL((k_moe_route<false>), dim3(route), dim3(kRouteThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int slots = p.by_pair ? p.tokens * p.top_k : p.experts;
+    const int slots = std::min(p.tokens * p.top_k, p.experts);
     hipLaunchKernelGGL(k_moe_up, dim3(slots * ((p.inner + 31) / 32)), dim3(kUpThreads), 0, stream, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int lds = kDownThreads / 64 * p.tokens * 64;
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_moe_down), hipFuncAttributeMaxDynamicSharedMemorySize,
-                            kDownThreads / 64 * 64 * 64);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_moe_down, dim3((p.hidden + 15) / 16), dim3(kDownThreads), lds, stream, p);
+    const int lds = kDownWaves * p.tokens * kDownRows * 4;
+    hipLaunchKernelGGL(k_moe_down, dim3((p.hidden + kDownRows - 1) / kDownRows * p.shares), dim3(kDownThreads), lds, stream, p);
     return hipGetLastError();
 }
 

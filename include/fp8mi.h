@@ -385,8 +385,9 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
  * ids int32 and weights fp32 [tokens, top_k], contiguous.  top_k <= 16,
  * experts <= 512; hidden, inner below 2^24; ldx, ldr, ldy in elements.
  * workspace: fp8_mx4_moe_workspace_size() bytes (grows with tokens), 16-byte
- * aligned, its first 256 bytes ZERO before the first call that uses it (each
- * call leaves them zero), and no two calls at once on one workspace.
+ * aligned, ZERO before its first call and before one with other sizes than
+ * tokens (it begins with counts that each call leaves zero), and no two calls
+ * at once on one workspace.
  * ctr (may be NULL) counts nonfinite_out. */
 typedef struct {
     const uint8_t* q;    /* [experts, rows, 128 ceil(cols/256)] */
