@@ -183,10 +183,11 @@ __device__ inline float dpp_f(float v)
 constexpr int kDppXor1 = 0xB1, kDppNext1 = 0x101, kDppNext2 = 0x102;    // lanes l ^ 1, l + 1, l + 2
 
 // ------------------------------------------------------------------ router
-constexpr int kRouteThreads = 512;
+constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / 64;
+constexpr int kMaxSplits = 8;
 constexpr int kChunk = 32;          // K of 8 fp64 matrix instructions
-constexpr int kRouteDepth = 4;      // chunks read at a time
+constexpr int kRouteDepth = 2;      // chunks read at a time
 
 // Eight elements of a row from column c on, zeros past the end.
 template <bool VEC>
@@ -237,10 +238,11 @@ __device__ inline void cut_x(const MoeArgs& p, int item)
     }
 }
 
-// fp64 as an unsigned key of the same order; NaN lowest, +0 and -0 alike
+// fp64 as an unsigned key over 1 of the same order; NaN lowest, +0 and -0
+// alike
 __device__ inline uint64_t key_of(double v)
 {
-    if (v != v) return 0;
+    if (v != v) return 1;
     const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
     return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
@@ -259,51 +261,52 @@ __device__ inline uint32_t max_of_wave(uint32_t v)
     return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-// One wave: the top_k experts of token t and their weights.  Lane l holds
-// experts l, l + 64, ..
-__device__ inline void select(const MoeArgs& p, int t)
+// One wave: the top_k experts of token t and their weights, to `ids` and
+// `weights` too.  Lane l holds experts l, l + 64, .. up to 64 N.
+template <int N>
+__device__ inline void select(const MoeArgs& p, int t, int* ids, float* weights)
 {
     const int lane = threadIdx.x & 63;
-    constexpr int kPer = kMaxExperts / 64;
-    uint64_t key[kPer];
-    double l[kPer];
     const int64_t split = (int64_t)p.tokens * p.experts;
+    const uint64_t* at = reinterpret_cast<const uint64_t*>(p.logits) + (int64_t)t * p.experts;
+    double l[N];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int e = 64 * j + lane;
-        l[j] = 0;
-        if (64 * j < p.experts) {
-            const uint64_t* at = reinterpret_cast<const uint64_t*>(p.logits) + (int64_t)t * p.experts + min(e, p.experts - 1);
-            uint64_t part[8];
-            for (int s0 = 0; s0 < p.splits; s0 += 8) {
+    for (int j = 0; j < N; ++j) l[j] = 0;
+    constexpr int kAtOnce = kMaxSplits / N;
+    for (int s0 = 0; s0 < p.splits; s0 += kAtOnce) {
+        uint64_t part[N][kAtOnce];
 #pragma unroll
-                for (int s = 0; s < 8; ++s) part[s] = s0 + s < p.splits ? agent_load(at + (s0 + s) * split) : 0;
+        for (int j = 0; j < N; ++j)
 #pragma unroll
-                for (int s = 0; s < 8; ++s) l[j] += __builtin_bit_cast(double, part[s]);
-            }
-        }
-        key[j] = key_of(l[j]);
+            for (int s = 0; s < kAtOnce; ++s)
+                part[j][s] = s0 + s < p.splits ? agent_load(at + (s0 + s) * split + min(64 * j + lane, p.experts - 1)) : 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int s = 0; s < kAtOnce; ++s) l[j] += __builtin_bit_cast(double, part[j][s]);
     }
-    uint32_t open = 0;                  // which of its experts are not taken
+    uint64_t key[N];                    // 0: none, or taken
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) open |= (uint32_t)(64 * j + lane < p.experts) << j;
+    for (int j = 0; j < N; ++j) key[j] = 64 * j + lane < p.experts ? key_of(l[j]) : 0;
     double top = 0, mine = 0;           // lane r keeps rank r's
     int id = 0;
     for (int r = 0; r < p.top_k; ++r) {
-        uint64_t best = 0;
-        int at = kPer;
+        uint64_t best = key[0];
+        double v = l[0];
+        int at = 0;
 #pragma unroll
-        for (int j = kPer - 1; j >= 0; --j)
-            if (64 * j < p.experts && (open >> j & 1) && (at == kPer || key[j] >= best)) {
-                best = key[j];
-                at = j;
-            }
+        for (int j = 1; j < N; ++j) {
+            const bool more = key[j] > best;
+            best = more ? key[j] : best;
+            v = more ? l[j] : v;
+            at = more ? j : at;
+        }
         const int e = 64 * at + lane;
-        // the lanes that hold the largest: by the high words, the low words,
-        // the expert
-        const uint32_t hi = at < kPer ? (uint32_t)(best >> 32) : 0u, lo = (uint32_t)best;
+        // the lanes that hold the largest: by the high words; where those are
+        // alike by the low words, then the expert
+        const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
         const uint32_t top_hi = max_of_wave(hi);
-        uint64_t who = __ballot(at < kPer && hi == top_hi);
+        uint64_t who = __ballot(hi == top_hi);
         if (__builtin_popcountll(who) > 1) {
             const bool in = who >> lane & 1;
             const uint32_t top_lo = max_of_wave(in ? lo : 0u);
@@ -312,14 +315,12 @@ __device__ inline void select(const MoeArgs& p, int t)
             who = __ballot(still && (uint32_t)e == first);
         }
         const int owner = __builtin_ctzll(who);
-        double v = l[0];
-#pragma unroll
-        for (int j = 1; j < kPer; ++j) v = j == at ? l[j] : v;
         const uint64_t vb = __builtin_bit_cast(uint64_t, v);
         v = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)vb, owner) |
                                            (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(vb >> 32), owner) << 32);
         const int chosen = __builtin_amdgcn_readlane(e, owner);
-        if (lane == owner) open &= ~(1u << at);
+#pragma unroll
+        for (int j = 0; j < N; ++j) key[j] = lane == owner && j == at ? 0 : key[j];
         if (r == 0) top = v;
         if (lane == r) {
             mine = v;
@@ -331,14 +332,16 @@ __device__ inline void select(const MoeArgs& p, int t)
     if (!p.renormalize) {
         sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (64 * j + lane < p.experts) sum += expf((float)(l[j] - top));
+        for (int j = 0; j < N; ++j) sum += 64 * j + lane < p.experts ? expf((float)(l[j] - top)) : 0.0f;
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
     if (lane < p.top_k) {
-        agent_store(p.ids + t * p.top_k + lane, id);
-        agent_store(p.weights + t * p.top_k + lane, z / sum);
+        const int i = t * p.top_k + lane;
+        agent_store(p.ids + i, id);
+        agent_store(p.weights + i, z / sum);
+        ids[i] = id;
+        weights[i] = z / sum;
     }
 }
 
@@ -357,27 +360,18 @@ __device__ inline bool last_of(uint32_t* count, uint32_t all)
     return s_last;
 }
 
-// The reached experts in order, and each one's tokens in order.
-__device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off)
+// The reached experts in order, and each one's tokens in order.  ids and
+// weights: of every pair.
+__device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off, const int* ids, const float* weights)
 {
     __shared__ int s_n[kRouteWaves], s_groups[kRouteWaves], s_active[kRouteWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    static_assert(kRouteThreads >= kMaxExperts && kMaxTokens * kMaxTopK <= 2 * kRouteThreads, "a thread each");
+    static_assert(kRouteThreads >= kMaxExperts && kRouteThreads >= kMaxTokens * kMaxTopK, "a thread each");
     mask[threadIdx.x] = 0;
     __syncthreads();
-    int e[2];
-    float w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int pair = threadIdx.x + i * kRouteThreads;
-        e[i] = -1;
-        w[i] = 0;
-        if (pair < p.tokens * p.top_k) {
-            e[i] = min(max(agent_load(p.ids + pair), 0), p.experts - 1);
-            w[i] = agent_load(p.weights + pair);
-            atomicOr(&mask[e[i]], 1ull << (pair / p.top_k));
-        }
-    }
+    const int t = threadIdx.x / p.top_k;
+    const int e = t < p.tokens ? min(max(ids[threadIdx.x], 0), p.experts - 1) : -1;
+    if (e >= 0) atomicOr(&mask[e], 1ull << t);
     __syncthreads();
     const int n = __builtin_popcountll(mask[threadIdx.x]);
     const uint64_t here = __ballot(n > 0);
@@ -417,13 +411,7 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
         p.count[1] = first + groups;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (e[i] >= 0) {
-            const int t = (threadIdx.x + i * kRouteThreads) / p.top_k;
-            const int to = off[e[i]] + __builtin_popcountll(mask[e[i]] & ((1ull << t) - 1));
-            p.prob[to] = w[i];
-        }
+    if (e >= 0) p.prob[off[e] + __builtin_popcountll(mask[e] & ((1ull << t) - 1))] = weights[threadIdx.x];
 }
 
 // Workgroups below tiles_e tiles_t splits take 16 tokens x 16 experts of the
@@ -442,7 +430,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
         return;
     }
     __shared__ __attribute__((aligned(16))) double red[kRouteWaves][256];
-    static_assert(sizeof(red) >= kMaxExperts * (sizeof(uint64_t) + sizeof(int)), "the lists' masks and places");
+    __shared__ int s_ids[kMaxTokens * kMaxTopK];
+    __shared__ float s_weights[kMaxTokens * kMaxTopK];
+    static_assert(sizeof(red) >= kRouteThreads * (sizeof(uint64_t) + sizeof(int)), "the lists' masks and places");
     const int tt = blockIdx.x / (p.tiles_e * p.splits), rest = blockIdx.x - tt * p.tiles_e * p.splits;
     const int split = rest / p.tiles_e, te = rest - split * p.tiles_e;
     const int t = min(16 * tt + (lane & 15), p.tokens - 1), e = min(16 * te + (lane & 15), p.experts - 1);
@@ -484,11 +474,28 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
                         __builtin_bit_cast(uint64_t, s));
     }
     if (!last_of(p.arrived + tt, (uint32_t)(p.tiles_e * p.splits))) return;
-    for (int i = wave; i < 16; i += kRouteWaves)
-        if (16 * tt + i < p.tokens) select(p, 16 * tt + i);
-    if (!last_of(p.arrived + kMaxTokens / 16, (uint32_t)p.tiles_t)) return;
+    static_assert(kRouteWaves == 16, "a wave each token");
+    if (16 * tt + wave < p.tokens) {
+        const int at = 16 * tt + wave;
+        if (p.experts <= 64)
+            select<1>(p, at, s_ids, s_weights);
+        else if (p.experts <= 128)
+            select<2>(p, at, s_ids, s_weights);
+        else if (p.experts <= 256)
+            select<4>(p, at, s_ids, s_weights);
+        else
+            select<8>(p, at, s_ids, s_weights);
+    }
+    if (p.tiles_t > 1) {
+        if (!last_of(p.arrived + kMaxTokens / 16, (uint32_t)p.tiles_t)) return;
+        if ((int)threadIdx.x < p.tokens * p.top_k) {
+            s_ids[threadIdx.x] = agent_load(p.ids + threadIdx.x);
+            s_weights[threadIdx.x] = agent_load(p.weights + threadIdx.x);
+        }
+    }
+    __syncthreads();
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(&red[0][0]);
-    list_reached(p, mask, reinterpret_cast<int*>(mask + kMaxExperts));
+    list_reached(p, mask, reinterpret_cast<int*>(mask + kRouteThreads), s_ids, s_weights);
 }
 
 // Lists that an earlier launch wrote, at uniform places: read through the
@@ -652,9 +659,6 @@ constexpr int kDownThreads = 256;
 constexpr int kDownWaves = kDownThreads / 64;
 constexpr int kDownRows = 32;
 constexpr int kMaxShares = 8;
-#ifndef FP8MI_DOWN_STEPS
-#define FP8MI_DOWN_STEPS 2
-#endif
 
 // `shares` workgroups take the same 32 rows of y for every token.  Their waves
 // share the steps (up to five tokens of an expert, a panel of K: two units) in
@@ -746,26 +750,28 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
         }
     };
 
-    const int first = share * kDownWaves + wave, stride = p.shares * kDownWaves;
+    // this wave's steps, neighbours in memory
+    const int who = share * kDownWaves + wave, all = p.shares * kDownWaves;
+    const int first = (int)((int64_t)steps * who / all), end = (int)((int64_t)steps * (who + 1) / all);
     W w0, w1;
     X x0, x1;
     At a0, a1;
-    if (first < steps) {
+    if (first < end) {
         a0 = at_step(first);
-        a1 = at_step(first + stride);
+        a1 = at_step(first + 1);
         get_w(w0, a0);
         get_x(x0, a0);
         get_w(w1, a1);
     }
     for (int i = lane; i < p.tokens * kDownRows; i += 64) mine[i] = 0.0f;
-    for (int i = first; i < steps; i += 2 * stride) {
+    for (int i = first; i < end; i += 2) {
         get_x(x1, a1);
         compute(w0, x0, a0, true);
-        a0 = at_step(i + 2 * stride);
+        a0 = at_step(i + 2);
         get_w(w0, a0);
         get_x(x0, a0);
-        compute(w1, x1, a1, i + stride < steps);
-        a1 = at_step(i + 3 * stride);
+        compute(w1, x1, a1, i + 1 < end);
+        a1 = at_step(i + 3);
         get_w(w1, a1);
     }
     __syncthreads();
@@ -789,30 +795,44 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
     }
     if (p.shares > 1) {
         if (!last_of(p.arrived_rows + block, (uint32_t)p.shares)) return;
-        for (int i = threadIdx.x; i < p.tokens * kDownRows; i += kDownThreads) {
-            const int t = i / kDownRows, r = i % kDownRows;
-            if (r >= rows) continue;
-            const float* from = p.part + (int64_t)t * p.hidden + row0 + r;
-            float v[kMaxShares];
+        // all reads of 8 outputs a thread (of 64 tokens) in flight at once
+        constexpr int kAt = kMaxTokens * kDownRows / kDownThreads;
+        const int r = threadIdx.x % kDownRows, t0 = threadIdx.x / kDownRows;
+        constexpr int kApart = kDownThreads / kDownRows;
+        const float* from = p.part + row0 + min(r, rows - 1);
+        float v[kAt];
 #pragma unroll
-            for (int j = 0; j < kMaxShares; ++j)
-                v[j] = j < p.shares ? agent_load(from + (int64_t)j * p.tokens * p.hidden) : 0.0f;
-            float s = v[0];
+        for (int i = 0; i < kAt; ++i) v[i] = 0.0f;
+        for (int j0 = 0; j0 < p.shares; j0 += 4) {
+            float w[kAt][4];
 #pragma unroll
-            for (int j = 1; j < kMaxShares; ++j) s += v[j];
-            put(t, r, s);
+            for (int i = 0; i < kAt; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (t0 + kApart * i < p.tokens && j0 + j < p.shares)
+                        w[i][j] = agent_load(from + ((int64_t)(j0 + j) * p.tokens + t0 + kApart * i) * p.hidden);
+                    else
+                        w[i][j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kAt; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i] += w[i][j];
         }
+#pragma unroll
+        for (int i = 0; i < kAt; ++i)
+            if (t0 + kApart * i < p.tokens && r < rows) put(t0 + kApart * i, r, v[i]);
     }
     flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
-// Workgroups that share a row block of y: enough for two on each of 256 CUs,
-// where there is work for them.
+// Workgroups that share a row block of y: enough for one on each of 256 CUs,
+// of two steps a wave at least.  (64 tokens, 128 experts of 4096 x 1024: 197
+// us with 2, 202 with 4, 213 with 8.)
 int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
 {
     const int64_t blocks = (hidden + kDownRows - 1) / kDownRows;
-    const int64_t steps = std::min<int64_t>(tokens * top_k, 128) * ((inner + mx4::kPanel - 1) / mx4::kPanel);
-    return (int)std::clamp<int64_t>(std::min((512 + blocks - 1) / blocks, steps / (FP8MI_DOWN_STEPS * kDownWaves)), 1, kMaxShares);
+    const int64_t steps = tokens * top_k * ((inner + mx4::kPanel - 1) / mx4::kPanel);
+    return (int)std::clamp<int64_t>(std::min((256 + blocks - 1) / blocks, steps / (2 * kDownWaves)), 1, kMaxShares);
 }
 
 // K splits of the router: two rounds of reads a workgroup at most, and few
@@ -820,7 +840,7 @@ int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
 int route_splits(int64_t hidden)
 {
     const int64_t chunks = (hidden + kChunk - 1) / kChunk;
-    return (int)std::clamp<int64_t>((chunks + 2 * kRouteWaves - 1) / (2 * kRouteWaves), 1, 8);
+    return (int)std::clamp<int64_t>((chunks + 2 * kRouteWaves - 1) / (2 * kRouteWaves), 1, kMaxSplits);
 }
 
 struct MoeLayout {
