@@ -36,7 +36,7 @@ EXPORTED = [
     "fp8_scaled_mm_workspace_size", "fp8_scaled_mm",
     "fp8_quantize_scaled_mm_workspace_size", "fp8_quantize_scaled_mm",
     "fp8_requant_workspace_size", "fp8_requant_weights",
-    "fp8_mx4_quantize", "fp8_mx4_dequantize", "fp8_mx4_mm_workspace_size", "fp8_mx4_mm",
+    "fp8_mx4_quantize", "fp8_mx4_dequantize", "fp8_mx4_mm",
     "fp8_mx4_moe_workspace_size", "fp8_mx4_moe",
     "fp8_counters_reset", "fp8_debug_set_wait_limit",
 ]
@@ -114,10 +114,8 @@ def lib():
         L.fp8_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp]
         L.fp8_mx4_dequantize.restype = i32
         L.fp8_mx4_dequantize.argtypes = [vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]
-        L.fp8_mx4_mm_workspace_size.restype = sz
-        L.fp8_mx4_mm_workspace_size.argtypes = [i64, i64, i64]
         L.fp8_mx4_mm.restype = i32
-        L.fp8_mx4_mm.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, sz, vp, vp]
+        L.fp8_mx4_mm.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, vp]
         L.fp8_mx4_moe_workspace_size.restype = sz
         L.fp8_mx4_moe_workspace_size.argtypes = [i64] * 5
         L.fp8_mx4_moe.restype = i32
@@ -198,8 +196,8 @@ def fp8_mx4_dequantize(q, ldq, s, ps, rows, cols, y, dtype, ldy, stream) -> int:
     return lib().fp8_mx4_dequantize(q, ldq, s, ps, rows, cols, y, dtype, ldy, stream)
 
 
-def fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, workspace, workspace_bytes, ctr, stream) -> int:
-    return lib().fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, workspace, workspace_bytes, ctr, stream)
+def fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, ctr, stream) -> int:
+    return lib().fp8_mx4_mm(a, lda, sa, psa, b, ldb, sb, psb, m, n, k, c, ldc, ctr, stream)
 
 
 def fp8_mx4_moe(x, tokens, hidden, ldx, router, ldr, w1, w2, experts, inner, top_k, renormalize, y, ldy, ids, weights,
@@ -681,10 +679,8 @@ def mx4_dequantize(a: Mx4, dtype=None, out=None):
     return y
 
 
-def mx4_mm(a: Mx4, b: Mx4, out=None, counters: Counters | None = None, workspace=None):
-    """y = A B^T of two quantized operands a [m, k] and b [n, k], bf16 [m, n].
-    workspace: optional uint8 device tensor of at least
-    fp8_mx4_mm_workspace_size(m, n, k) bytes (allocated per call when None)."""
+def mx4_mm(a: Mx4, b: Mx4, out=None, counters: Counters | None = None):
+    """y = A B^T of two quantized operands a [m, k] and b [n, k], bf16 [m, n]."""
     torch = _torch()
     _check_mx4(a, "a")
     _check_mx4(b, "b")
@@ -694,20 +690,10 @@ def mx4_mm(a: Mx4, b: Mx4, out=None, counters: Counters | None = None, workspace
         raise ValueError("a and b disagree on k")
     if out is not None:
         _check_tensor(out, "out", (torch.bfloat16,), (m, n), unit_col_stride=True)
-    if workspace is not None:
-        _check_tensor(workspace, "workspace", (torch.uint8,), contiguous=True)
-    _check_devices(a.q, a.s, b.q, b.s, out, workspace, counters.buf if counters else None)
+    _check_devices(a.q, a.s, b.q, b.s, out, counters.buf if counters else None)
     c = out if out is not None else torch.empty((m, n), dtype=torch.bfloat16, device=a.q.device)
-    L = lib()
-    wsb = L.fp8_mx4_mm_workspace_size(m, n, k)
-    if workspace is None:
-        if wsb:
-            workspace = torch.empty(wsb, dtype=torch.uint8, device=c.device)
-    elif workspace.numel() < wsb:
-        raise ValueError(f"workspace needs {wsb} bytes, got {workspace.numel()}")
-    check(L.fp8_mx4_mm(*a._args(), *b._args(), m, n, k, c.data_ptr(), _ld(c), _ptr(workspace),
-                       workspace.numel() if workspace is not None else 0,
-                       counters.ptr() if counters else None, _stream()))
+    check(lib().fp8_mx4_mm(*a._args(), *b._args(), m, n, k, c.data_ptr(), _ld(c),
+                           counters.ptr() if counters else None, _stream()))
     return c
 
 

@@ -574,22 +574,15 @@ fp8_status fp8_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, i
     return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_dequantize launch");
 }
 
-size_t fp8_mx4_mm_workspace_size(int64_t m, int64_t n, int64_t k)
-{
-    if (m <= 0 || n <= 0 || k <= 0) return 0;
-    return mx4_gemm_workspace(m, n, k);
-}
-
 fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t psa, const uint8_t* b, int64_t ldb,
                       const uint8_t* sb, int64_t psb, int64_t m, int64_t n, int64_t k, void* c_bf16, int64_t ldc,
-                      void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream)
+                      fp8_counters* ctr, hipStream_t stream)
 {
     fp8_status st;
     if ((st = check_mx4(a, lda, sa, psa, m, k, "a")) != FP8_OK) return st;
     if ((st = check_mx4(b, ldb, sb, psb, n, k, "b")) != FP8_OK) return st;
     if ((st = check_2d(c_bf16, m, n, ldc, "c")) != FP8_OK) return st;
     if (misaligned(c_bf16, 2)) return fail(FP8_ERR_INVALID_ARG, "c must be 2-byte aligned");
-    if (misaligned(workspace, 16)) return fail(FP8_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
     // byte offsets inside one 256-row operand or output tile are 32-bit
     if (m > 0 && n > 0 && (lda >= ((int64_t)1 << 22) || ldb >= ((int64_t)1 << 22) || ldc >= ((int64_t)1 << 21)))
         return fail(FP8_ERR_UNSUPPORTED_SHAPE, "lda, ldb must be below 2^22 and ldc below 2^21");
@@ -610,8 +603,6 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
     g.k = k;
     g.c = c_bf16;
     g.ldc = ldc;
-    g.ws = static_cast<float*>(workspace);
-    g.ws_bytes = workspace ? workspace_bytes : 0;
     g.ctr = ctr;
     hipError_t e = launch_mx4_gemm(g, stream);
     return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_mm launch");

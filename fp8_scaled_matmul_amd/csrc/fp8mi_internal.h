@@ -174,11 +174,8 @@ struct Mx4GemmArgs {
     int64_t m, n, k;
     void* c;
     int64_t ldc;
-    float* ws;              // split-K partials, or nullptr
-    size_t ws_bytes;
     fp8_counters* ctr;
 };
-size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream);
 // Mixture-of-experts layer with 4-bit weights (mx4_moe.hip).
 struct Mx4MoeArgs {
@@ -198,10 +195,7 @@ struct Mx4MoeArgs {
 };
 size_t mx4_moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner);
 hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream);
-// Pieces of gemm.hip that the 4-bit GEMM uses too: zeros (k = 0), and the
-// fixed-order sum of split-K partials.
+// Zeros (k = 0), in gemm.hip.
 hipError_t launch_zero_bf16(uint16_t* c, int m, int n, int64_t ldc, hipStream_t stream);
-hipError_t launch_splitk_sum(const float* ws, int splits, int m, int n, uint16_t* c, int64_t ldc, fp8_counters* ctr,
-                             hipStream_t stream);
 
 }  // namespace fp8mi

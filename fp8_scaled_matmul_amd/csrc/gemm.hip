@@ -942,24 +942,6 @@ hipError_t launch_zero_bf16(uint16_t* c, int m, int n, int64_t ldc, hipStream_t 
     return hipGetLastError();
 }
 
-hipError_t launch_splitk_sum(const float* ws, int splits, int m, int n, uint16_t* c, int64_t ldc, fp8_counters* ctr,
-                             hipStream_t stream)
-{
-    KArgs p{};
-    p.ws = const_cast<float*>(ws);
-    p.splits = splits;
-    p.m = m;
-    p.n = n;
-    p.c = c;
-    GemmArgs g{};
-    g.m = m;
-    g.n = n;
-    g.c = c;
-    g.ldc = ldc;
-    g.ctr = ctr;
-    return launch_reduce(p, g, 0.0f, stream);
-}
-
 int gemm_num_cus()
 {
     static int n = 0;

@@ -38,10 +38,8 @@ struct MxArgs {
     int64_t psa, psb;               // bytes between scale panels
     int m, n;
     int steps;                      // K steps: ceil(k / 256)
-    int splits, steps_per;          // K splits of steps_per steps (even)
     uint16_t* c;
     int64_t ldc;
-    float* ws;                      // fp32 partials [splits, m, n], or null
     int tiles_m, tiles_n, group_m;
     int pair_store;                 // two adjacent outputs can be stored as one word
     fp8_counters* ctr;
@@ -72,17 +70,14 @@ __device__ inline v16f mfma(const v8i& a, const v8i& b, const v16f& c, uint32_t 
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, Q, (int)ea, Q, (int)eb);
 }
 
-// Linear workgroup id to (split, tile row, tile column): ids go to the XCDs
-// in turn, so XCD x takes a contiguous range of the tile order, which walks
-// group_m tile rows at a time.
-__device__ inline void item_of(const MxArgs& p, int bid, int& split, int& tm, int& tn)
+// Linear workgroup id to (tile row, tile column): ids go to the XCDs in turn,
+// so XCD x takes a contiguous range of the tile order, which walks group_m
+// tile rows at a time.
+__device__ inline void item_of(const MxArgs& p, int bid, int& tm, int& tn)
 {
-    const int total = p.tiles_m * p.tiles_n * p.splits;
+    const int total = p.tiles_m * p.tiles_n;
     const int xcd = bid & 7, local = bid >> 3;
-    const int pid = xcd * (total >> 3) + min(xcd, total & 7) + local;
-    const int per_split = p.tiles_m * p.tiles_n;
-    split = pid / per_split;
-    const int t = pid - split * per_split;
+    const int t = xcd * (total >> 3) + min(xcd, total & 7) + local;
     const int in_group = p.group_m * p.tiles_n;
     const int g = t / in_group;
     const int first_m = g * p.group_m;
@@ -95,7 +90,7 @@ __device__ inline void item_of(const MxArgs& p, int bid, int& split, int& tm, in
 // Stores one wave's MF x 2 accumulators: rows row0 + 32 i + 8 (r / 4) +
 // 4 (lane / 32) + r % 4, columns col and col + 1 (col already the lane's).
 template <int MF>
-__device__ inline uint32_t store_out(const MxArgs& p, const v16f (&acc)[MF][2], int row0, int col, int split)
+__device__ inline uint32_t store_out(const MxArgs& p, const v16f (&acc)[MF][2], int row0, int col)
 {
     const int lane = threadIdx.x & 63;
     uint32_t nonfinite = 0;
@@ -107,12 +102,6 @@ __device__ inline uint32_t store_out(const MxArgs& p, const v16f (&acc)[MF][2], 
             const int row = row0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
             if (row >= p.m) continue;
             const float lo = acc[i][0][r], hi = acc[i][1][r];
-            if (p.ws) {
-                float* w = p.ws + ((int64_t)split * p.m + row) * p.n + col;
-                w[0] = lo;
-                if (col + 1 < p.n) w[1] = hi;
-                continue;
-            }
             const uint32_t h = gemm::pack_bf16(lo, hi);
             uint16_t* c = p.c + row * p.ldc + col;
             nonfinite += (h & 0x7F80u) == 0x7F80u;
@@ -154,20 +143,19 @@ __global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    int split, tm, tn;
-    item_of(p, blockIdx.x, split, tm, tn);
+    int tm, tn;
+    item_of(p, blockIdx.x, tm, tn);
     const int m0 = tm * TM, n0 = tn * TN;
-    const int kt0 = split * p.steps_per;
-    const int nt = min(p.steps, kt0 + p.steps_per) - kt0;
+    const int nt = p.steps;
     const int64_t rows_a = min(p.m - m0, TM), rows_b = min(p.n - n0, TN);
     const v4u ra = gemm::make_rsrc(p.a + (int64_t)m0 * p.lda, (uint32_t)(rows_a * p.lda));
     const v4u rb = gemm::make_rsrc(p.b + (int64_t)n0 * p.ldb, (uint32_t)(rows_b * p.ldb));
     const uint32_t base = gemm::lds_addr(lds);
 
-    // K step t of this split into its ring slot: kPer instructions per wave
+    // K step t into its ring slot: kPer instructions per wave
     const auto fill = [&](int t) {
         const bool live = t < nt;
-        const int slot = t % STAGES, kb = kt0 + t;
+        const int slot = t % STAGES;
         const uint32_t to = base + slot * kStage;
         const int q = lane >> 3, pos = lane & 7;
 #pragma unroll
@@ -185,13 +173,13 @@ __global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
                 rs = rb;
             }
             rs.z = live ? rs.z : 0u;
-            gemm::dma16(to + 1024 * (j * W + wave), off + (uint32_t)kb * kRowBytes, rs);
+            gemm::dma16(to + 1024 * (j * W + wave), off + (uint32_t)t * kRowBytes, rs);
         }
 #pragma unroll
         for (int j = 0; j < kScalePer; ++j) {
             const int u = j * W + wave;                 // 64 rows of scales; past the last: a repeat of it
             const int uu = min(u, kScale - 1);
-            const int64_t panel = kb >> 1;
+            const int64_t panel = t >> 1;
             const uint8_t* src;
             uint32_t off, bytes;
             if (uu < TM / 64) {
@@ -229,7 +217,7 @@ __global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
         const uint8_t* st = lds + (t % STAGES) * kStage;
         const uint8_t* la = st;
         const uint8_t* lb = st + kA;
-        const uint8_t* ls = st + kA + kB + ((kt0 + t) & 1) * 8 + 4 * (lane >> 5);
+        const uint8_t* ls = st + kA + kB + (t & 1) * 8 + 4 * (lane >> 5);
         uint32_t ea[MF], eb[2];
 #pragma unroll
         for (int i = 0; i < MF; ++i)
@@ -255,8 +243,8 @@ __global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
         quarter(std::integral_constant<int, 3>{});
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const uint32_t nonfinite = store_out<MF>(p, acc, m0 + wm, n0 + wn + 2 * (lane & 31), split);
-    if (!p.ws) flush_counters(p.ctr, 0, 0, 0, nonfinite);
+    const uint32_t nonfinite = store_out<MF>(p, acc, m0 + wm, n0 + wn + 2 * (lane & 31));
+    flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
 template <int WR, int WC, int MF, int STAGES>
@@ -271,7 +259,7 @@ hipError_t launch_tile(MxArgs p, hipStream_t stream)
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(p.tiles_m * p.tiles_n * p.splits), dim3(64 * WR * WC), kLds, stream, p);
+    hipLaunchKernelGGL(kernel, dim3(p.tiles_m * p.tiles_n), dim3(64 * WR * WC), kLds, stream, p);
     return hipGetLastError();
 }
 
@@ -296,25 +284,18 @@ constexpr int kBigStores = 64;                  // of a tile, by a wave
 // two chunks the 32 of 512 bytes.  An involution in c.
 __device__ inline int swz64(int r, int c) { return c ^ (((r >> 2) & 1) | (((r >> 1) ^ (r >> 2) ^ (r >> 3)) & 1) << 1); }
 
-// A tile and K split.
-struct BigItem {
+struct BigTile {
     int id;             // past the last: no tile
-    int split, m0, n0;
-    int st0, nt;        // its first stage and number of stages (even)
+    int m0, n0;
 };
-__device__ inline BigItem big_item(const MxArgs& p, int id)
+__device__ inline BigTile big_tile(const MxArgs& p, int id)
 {
-    BigItem it;
-    it.id = id;
-    it.split = it.m0 = it.n0 = it.st0 = 0;
-    it.nt = 1 << 30;
-    if (id < p.tiles_m * p.tiles_n * p.splits) {
+    BigTile it{id, 0, 0};
+    if (id < p.tiles_m * p.tiles_n) {
         int tm, tn;
-        item_of(p, id, it.split, tm, tn);
+        item_of(p, id, tm, tn);
         it.m0 = tm * kBig;
         it.n0 = tn * kBig;
-        it.st0 = 2 * it.split * p.steps_per;
-        it.nt = 2 * min(p.steps, (it.split + 1) * p.steps_per) - it.st0;
     }
     return it;
 }
@@ -331,7 +312,8 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    const int total = p.tiles_m * p.tiles_n * p.splits;
+    const int total = p.tiles_m * p.tiles_n;
+    const int nt = 2 * p.steps;         // stages of a tile
     const uint32_t base = gemm::lds_addr(lds);
     const uint32_t scales = base + 4 * kStageBytes;
 
@@ -349,7 +331,7 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
     }
     const uint32_t vs = (uint32_t)(wave < 4 ? 64 * wave + lane : 64 * (wave - 4) + 2 * (lane & 31) + (lane >> 5)) * kScaleBytes;
     const int64_t ps = wave < 4 ? p.psa : p.psb;
-    BigItem f = big_item(p, blockIdx.x);        // the item being filled, its next stage
+    BigTile f = big_tile(p, blockIdx.x);        // the tile being filled, its next stage
     int ft = 0, fslot = 0, fpanel = 0;          // ring positions of the next stage and panel
     v4u ra, rb, rs;
     const uint8_t* sp;
@@ -358,7 +340,7 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
         const int64_t rows_a = min(p.m - f.m0, kBig), rows_b = min(p.n - f.n0, kBig);
         ra = gemm::make_rsrc(p.a + (int64_t)f.m0 * p.lda, live ? (uint32_t)(rows_a * p.lda) : 0u);
         rb = gemm::make_rsrc(p.b + (int64_t)f.n0 * p.ldb, live ? (uint32_t)(rows_b * p.ldb) : 0u);
-        sp = (wave < 4 ? p.sa + (int64_t)f.m0 * kScaleBytes : p.sb + (int64_t)f.n0 * kScaleBytes) + (f.st0 / 4) * ps;
+        sp = (wave < 4 ? p.sa + (int64_t)f.m0 * kScaleBytes : p.sb + (int64_t)f.n0 * kScaleBytes);
         rs = gemm::make_rsrc(sp, live ? (uint32_t)(wave < 4 ? rows_a : rows_b) * kScaleBytes : 0u);
     };
     describe();
@@ -370,14 +352,14 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
             fpanel = fpanel == kBigPanels - 1 ? 0 : fpanel + 1;
         }
         const uint32_t to = base + fslot * kStageBytes + 2048 * wave;
-        const uint32_t kb = (uint32_t)(f.st0 + ft) * 64;
+        const uint32_t kb = (uint32_t)ft * 64;
 #pragma unroll
         for (int j = 0; j < 2; ++j) gemm::dma16(to + 1024 * j, va[j] + kb, ra);
 #pragma unroll
         for (int j = 0; j < 2; ++j) gemm::dma16(to + kBig * 64 + 1024 * j, vb[j] + kb, rb);
         fslot = (fslot + 1) & 3;
-        if (++ft == f.nt) {
-            f = big_item(p, f.id + gridDim.x);
+        if (++ft == nt && f.id < total) {
+            f = big_tile(p, f.id + gridDim.x);
             ft = 0;
             describe();
         }
@@ -455,8 +437,8 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
     read_scales(0);
     uint32_t nonfinite = 0;
     int stored = 3;                             // stages since the last tile's stores, up to 3
-    for (BigItem it = big_item(p, blockIdx.x); it.id < total; it = big_item(p, it.id + gridDim.x)) {
-        for (int t = 0; t < it.nt; ++t) {
+    for (BigTile it = big_tile(p, blockIdx.x); it.id < total; it = big_tile(p, it.id + gridDim.x)) {
+        for (int t = 0; t < nt; ++t) {
             // the stage's second half is read under the first's products
             take_scales();
             products(std::integral_constant<int, 0>{}, 0, 2);
@@ -476,13 +458,13 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
             products(std::integral_constant<int, 1>{}, 0, 4);
             fill();
             slot = (slot + 1) & 3;
-            const int next = t + 1 == it.nt ? 0 : t + 1;
+            const int next = t + 1 == nt ? 0 : t + 1;
             if ((next & 3) == 0) panel = panel == kBigPanels - 1 ? 0 : panel + 1;
             read(std::integral_constant<int, 0>{});
             read_scales(next);
             products(std::integral_constant<int, 1>{}, 4, 8);
         }
-        if (!p.ws && p.pair_store) {
+        if (p.pair_store) {
             // 64 stores of two adjacent outputs, those out of range dropped
             const int64_t rows_c = min(p.m - it.m0, kBig);
             const __amdgpu_buffer_rsrc_t rc = gemm::make_store_rsrc(
@@ -511,13 +493,13 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
                     }
             }
         } else {
-            nonfinite += store_out<4>(p, acc, it.m0 + wm, it.n0 + wn + 2 * fr, it.split);
+            nonfinite += store_out<4>(p, acc, it.m0 + wm, it.n0 + wn + 2 * fr);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
         clear();
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");    // the fills past the end
-    if (!p.ws) flush_counters(p.ctr, 0, 0, 0, nonfinite);
+    flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
 hipError_t launch_big(MxArgs p, hipStream_t stream)
@@ -529,20 +511,153 @@ hipError_t launch_big(MxArgs p, hipStream_t stream)
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_big_gemm),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
     if (e != hipSuccess) return e;
-    const int grid = std::min(p.tiles_m * p.tiles_n * p.splits, gemm_num_cus());
+    const int grid = std::min(p.tiles_m * p.tiles_n, gemm_num_cus());
     hipLaunchKernelGGL(k_mx4_big_gemm, dim3(grid), dim3(kBigThreads), kBigLds, stream, p);
     return hipGetLastError();
 }
 
-}  // namespace
+// ------------------------------------------------------------------ straight from memory
+// Few outputs, where the read of B (a weight) or the mere latency counts: a
+// workgroup takes 16 CT rows of A by 16 RT rows of B, its KW waves share K,
+// and the operands go from memory to the registers of
+// v_mfma_scale_f32_16x16x128 (B's rows as the instruction's rows, A's as its
+// columns): no LDS but for the waves' sums at the end, which are added in
+// order.  A step is U units of 256 K; the next one is read under this one's
+// products.
+struct Unit {
+    uint4 q[2];         // K 32 (l / 16) on of either 128
+};
 
-size_t mx4_gemm_workspace(int64_t m, int64_t n, int64_t k)
+template <int RT, int CT, int KW, int U>
+__global__ void __launch_bounds__(64 * KW) k_mx4_direct_gemm(MxArgs p)
 {
-    (void)m;
-    (void)n;
-    (void)k;
-    return 0;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    v4f* red = reinterpret_cast<v4f*>(lds);     // [KW, RT CT, 64]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c16 = lane & 15, q = lane >> 4;
+    int tm, tn;
+    item_of(p, blockIdx.x, tm, tn);
+    const int m0 = tm * 16 * CT, n0 = tn * 16 * RT;
+
+    // operands 0 .. RT - 1: B's rows, then A's
+    constexpr int F = RT + CT;
+    uint32_t at[F], sat[F];
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+        const int row = f < RT ? min(16 * f + c16, p.n - 1 - n0) : min(16 * (f - RT) + c16, p.m - 1 - m0);
+        at[f] = (uint32_t)(row * (f < RT ? p.ldb : p.lda) + 16 * q);
+        sat[f] = (uint32_t)(row * kScaleBytes);
+    }
+    const uint8_t* b = p.b + (int64_t)n0 * p.ldb;
+    const uint8_t* a = p.a + (int64_t)m0 * p.lda;
+    const uint8_t* sb = p.sb + (int64_t)n0 * kScaleBytes;
+    const uint8_t* sa = p.sa + (int64_t)m0 * kScaleBytes;
+    struct Step {
+        Unit u[U][F];
+        uint2 s[U][F];
+    };
+    const int steps = (p.steps + U - 1) / U;
+    const int first = steps * wave / KW, end = steps * (wave + 1) / KW;
+    const auto get = [&](Step& x, int i) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            // past the end the last unit again, not used
+            const int u = min(min(i, end - 1) * U + k, p.steps - 1);
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const uint8_t* from = (f < RT ? b : a) + 128 * u;
+                const uint8_t* sfrom = (f < RT ? sb + (u >> 1) * p.psb : sa + (u >> 1) * p.psa) + 8 * (u & 1);
+                x.s[k][f] = *reinterpret_cast<const uint2*>(sfrom + sat[f]);
+                x.u[k][f].q[0] = *reinterpret_cast<const uint4*>(from + at[f]);
+                x.u[k][f].q[1] = *reinterpret_cast<const uint4*>(from + 64 + at[f]);
+            }
+        }
+    };
+    v4f acc[RT][CT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[r][c] = v4f{0, 0, 0, 0};
+    const auto products = [&](const Step& x, int i) {
+        const int sh = 8 * q;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (i >= end || i * U + k >= p.steps) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                v8i v[F];
+                uint32_t e[F];
+#pragma unroll
+                for (int f = 0; f < F; ++f) {
+                    const uint4 w = x.u[k][f].q[h];
+                    v[f] = v8i{(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+                    e[f] = (h ? x.s[k][f].y : x.s[k][f].x) >> sh;
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        acc[r][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v[r], v[RT + c], acc[r][c], 4, 4, 0,
+                                                                                     (int)e[r], 0, (int)e[RT + c]);
+            }
+        }
+    };
+    Step x0, x1;
+    if (first < end) {
+        get(x0, first);
+        for (int i = first; i < end; i += 2) {
+            get(x1, i + 1);
+            products(x0, i);
+            get(x0, i + 2);
+            products(x1, i + 1);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) red[(wave * RT * CT + r * CT + c) * 64 + lane] = acc[r][c];
+    __syncthreads();
+    uint32_t nonfinite = 0;
+    for (int i = threadIdx.x; i < RT * CT * 64; i += 64 * KW) {
+        v4f s = red[i];
+#pragma unroll
+        for (int w = 1; w < KW; ++w) s += red[w * RT * CT * 64 + i];
+        const int l = i & 63, c = (i >> 6) % CT, r = (i >> 6) / CT;
+        const int row = m0 + 16 * c + (l & 15), col = n0 + 16 * r + 4 * (l >> 4);
+        if (row >= p.m || col >= p.n) continue;
+        const uint32_t lo = gemm::pack_bf16(s[0], s[1]), hi = gemm::pack_bf16(s[2], s[3]);
+        uint16_t* to = p.c + row * p.ldc + col;
+        if (p.pair_store && col + 3 < p.n) {
+            reinterpret_cast<uint32_t*>(to)[0] = lo;
+            reinterpret_cast<uint32_t*>(to)[1] = hi;
+            nonfinite += ((lo & 0x7F80u) == 0x7F80u) + ((lo & 0x7F800000u) == 0x7F800000u) +
+                         ((hi & 0x7F80u) == 0x7F80u) + ((hi & 0x7F800000u) == 0x7F800000u);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col + j < p.n) {
+                    const uint16_t h = (uint16_t)((j < 2 ? lo : hi) >> (16 * (j & 1)));
+                    to[j] = h;
+                    nonfinite += (h & 0x7F80u) == 0x7F80u;
+                }
+        }
+    }
+    flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
+
+template <int RT, int CT, int KW, int U>
+hipError_t launch_direct(MxArgs p, hipStream_t stream)
+{
+    p.tiles_m = (p.m + 16 * CT - 1) / (16 * CT);
+    p.tiles_n = (p.n + 16 * RT - 1) / (16 * RT);
+    p.group_m = 4;
+    const int lds = KW * RT * CT * 1024;
+    hipLaunchKernelGGL((k_mx4_direct_gemm<RT, CT, KW, U>), dim3(p.tiles_m * p.tiles_n), dim3(64 * KW), lds, stream, p);
+    return hipGetLastError();
+}
+
+}  // namespace
 
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
 {
@@ -560,16 +675,28 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
     p.m = (int)g.m;
     p.n = (int)g.n;
     p.steps = (int)((g.k + mx4::kRowAlign - 1) / mx4::kRowAlign);
-    p.splits = 1;
-    p.steps_per = p.steps + (p.steps & 1);
     p.c = static_cast<uint16_t*>(g.c);
     p.ldc = g.ldc;
-    p.ws = nullptr;
     p.pair_store = g.ldc % 2 == 0 && (reinterpret_cast<uintptr_t>(g.c) & 3u) == 0;
     p.ctr = g.ctr;
-    const int64_t big = ((g.m + kBig - 1) / kBig) * ((g.n + kBig - 1) / kBig);
-    if (big >= 192) return launch_big(p, stream);
-    return launch_tile<2, 2, 2, 4>(p, stream);
+    // The largest tile that still leaves most of the 256 CUs a workgroup, and
+    // is not mostly past the end of A: what is read falls with the tile's
+    // size, what is idle grows.  Either side of a border, us (weights from
+    // memory, kernels back to back):
+    //   1 x 8192 x 8192      16 x 16: 10.7   16 x 32: 10.1   32 x 32: 10.8
+    //   128 x 512 x 512      16 x 16: 2.9    16 x 32: 3.2    32 x 32: 3.6
+    //   256 x 1024 x 1024    16 x 32: 6.6    32 x 32: 5.1    64 x 32: 7.1
+    //   333 x 1000 x 1568    32 x 32: 8.9    64 x 32: 7.2    64 x 64: 8.6
+    //   512 x 2048 x 2048    64 x 32: 12.3   64 x 64: 9.4    128 x 128: 12.3
+    //   1024 x 4096 x 4096   64 x 64: 42.1   128 x 128: 19.2   256 x 256: 29.2
+    const auto enough = [&](int64_t tm, int64_t tn) { return ((g.m + tm - 1) / tm) * ((g.n + tn - 1) / tn) >= 192; };
+    if (enough(256, 256)) return launch_big(p, stream);
+    if (g.m > 64 && enough(128, 128)) return launch_tile<2, 2, 2, 4>(p, stream);
+    if (g.m > 32 && enough(64, 64)) return launch_direct<4, 4, 2, 1>(p, stream);
+    if (g.m > 32 && enough(64, 32)) return launch_direct<2, 4, 4, 1>(p, stream);
+    if (g.m > 16 && enough(32, 32)) return launch_direct<2, 2, 4, 2>(p, stream);
+    if (enough(16, 32)) return launch_direct<2, 1, 4, 2>(p, stream);
+    return launch_direct<1, 1, 4, 2>(p, stream);
 }
 
 }  // namespace fp8mi

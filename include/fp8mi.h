@@ -359,17 +359,15 @@ fp8_status fp8_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, i
                               hipStream_t stream);
 
 /* y [m, n] bf16 = A B^T, A quantized [m, k], B quantized [n, k]: exact
- * products, fp32 sums (K splits in a fixed order), one rounding to nearest
- * even.  Codes past k are read: they have to be 0 in A or B, and no scale
+ * products, fp32 sums in an order that the sizes alone set, one rounding to
+ * nearest even.  Codes past k are read: they have to be 0 in A or B, and no scale
  * byte there 255 (as fp8_mx4_quantize leaves them).  lda, ldb below 2^22
  * bytes, ldc below 2^21, m, n and k below 2^31; k = 0 writes zeros.
- * workspace: fp8_mx4_mm_workspace_size() bytes, 16-byte aligned; without it
- * K is not split (slower for short outputs).  ctr counts nonfinite_out. */
-size_t     fp8_mx4_mm_workspace_size(int64_t m, int64_t n, int64_t k);
+ * ctr (may be NULL) counts nonfinite_out. */
 fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t psa,
                       const uint8_t* b, int64_t ldb, const uint8_t* sb, int64_t psb,
                       int64_t m, int64_t n, int64_t k, void* c_bf16, int64_t ldc,
-                      void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream);
+                      fp8_counters* ctr, hipStream_t stream);
 
 /* A mixture-of-experts layer with 4-bit weights for 1 to 64 tokens (0 does
  * nothing), as decoding calls it:

@@ -67,14 +67,13 @@ def test_dequantize_rejects_before_device(args, code):
     (dict(c=None), fm.FP8_ERR_INVALID_ARG),
     (dict(c=BAD + 1), fm.FP8_ERR_INVALID_ARG),
     (dict(ldc=47), fm.FP8_ERR_INVALID_ARG),
-    (dict(ws=BAD + 8), fm.FP8_ERR_INVALID_ARG),
     (dict(lda=1 << 22), fm.FP8_ERR_UNSUPPORTED_SHAPE),
     (dict(ldc=1 << 21), fm.FP8_ERR_UNSUPPORTED_SHAPE),
     (dict(k=1 << 31), fm.FP8_ERR_UNSUPPORTED_SHAPE),
 ])
 def test_mm_rejects_before_device(args, code):
     a = dict(a=BAD, lda=384, sa=BAD, psa=16 * 32, b=BAD, ldb=384, sb=BAD, psb=16 * 48, m=32, n=48, k=768, c=BAD,
-             ldc=48, ws=None, wsb=0, ctr=None)
+             ldc=48, ctr=None)
     a.update(args)
     assert fm.fp8_mx4_mm(*a.values(), None) == code, fm.lib().fp8_last_error()
 
