@@ -535,8 +535,8 @@ fp8_status fp8_mx4_quantize(const void* x, fp8_dtype dtype, int64_t rows, int64_
     if (q_t && (st = check_mx4(q_t, ldq_t, s_t, ps_t, cols, rows, "q_t")) != FP8_OK) return st;
     if (misaligned(x, dtype == FP8_IN_BF16 ? 2 : 4)) return fail(FP8_ERR_INVALID_ARG, "x: misaligned");
     if (misaligned(seed, 8)) return fail(FP8_ERR_INVALID_ARG, "seed: must be 8-byte aligned");
-    // one workgroup per 256 x 128 tile or 16 rows x 512 columns
-    if (cdiv(rows, 512) * cdiv(cols, 512) >= ((int64_t)1 << 27))
+    // one workgroup per 128 x 128 tile or 16 rows x 512 columns
+    if (cdiv(rows, 512) * cdiv(cols, 512) >= ((int64_t)1 << 26))
         return fail(FP8_ERR_UNSUPPORTED_SHAPE, "tensor too large");
     if ((st = check_device()) != FP8_OK) return st;
     Mx4QuantArgs a;

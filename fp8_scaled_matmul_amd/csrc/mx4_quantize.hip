@@ -26,6 +26,10 @@ namespace {
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+// The same 16 bytes wherever an element may lie: one access of any alignment.
+typedef uint32_t u4x2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u4x4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f4x4 __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr uint32_t kNonFinite = 0x7F800000u;
 constexpr uint32_t kNanKey = 0xFFFFFFFFu;   // the key of a block that holds a NaN
@@ -114,9 +118,8 @@ struct Row8 {
     }
 };
 
-// Elements col .. col + 7 of a row, zeros past the matrix.  VEC: rows start
-// on 16-byte boundaries and cols % 8 == 0.
-template <int DT, bool VEC>
+// Elements col .. col + 7 of a row, zeros past the matrix.
+template <int DT>
 __device__ inline Row8<DT> load8(const Mx4Args& p, int64_t row, int64_t col)
 {
     Row8<DT> r;
@@ -125,11 +128,9 @@ __device__ inline Row8<DT> load8(const Mx4Args& p, int64_t row, int64_t col)
     if (row >= p.rows) return r;
     if constexpr (DT == 0) {
         const uint16_t* x = static_cast<const uint16_t*>(p.x) + row * p.ld + col;
-        if constexpr (VEC) {
-            if (col < p.cols) {
-                const u4 v = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x));
-                r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-            }
+        if (col + 8 <= p.cols) {
+            const u4 v = __builtin_nontemporal_load(reinterpret_cast<const u4x2*>(x));
+            r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
         } else {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -137,13 +138,11 @@ __device__ inline Row8<DT> load8(const Mx4Args& p, int64_t row, int64_t col)
         }
     } else {
         const uint32_t* x = static_cast<const uint32_t*>(p.x) + row * p.ld + col;
-        if constexpr (VEC) {
-            if (col < p.cols) {
-                const u4 v = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x));
-                const u4 u = __builtin_nontemporal_load(reinterpret_cast<const u4*>(x) + 1);
-                r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-                r.w[4] = u.x; r.w[5] = u.y; r.w[6] = u.z; r.w[7] = u.w;
-            }
+        if (col + 8 <= p.cols) {
+            const u4 v = __builtin_nontemporal_load(reinterpret_cast<const u4x4*>(x));
+            const u4 u = __builtin_nontemporal_load(reinterpret_cast<const u4x4*>(x + 4));
+            r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+            r.w[4] = u.x; r.w[5] = u.y; r.w[6] = u.z; r.w[7] = u.w;
         } else {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -201,7 +200,7 @@ constexpr int kRowsPerWave = 4;
 // A wave takes 512 columns of kRowsPerWave rows, 8 columns a lane, every load
 // first: 16 blocks a row, whose codes are 256 and whose scales 16 adjacent
 // bytes.
-template <int DT, bool SR, bool COUNT, bool VEC>
+template <int DT, bool SR, bool COUNT>
 __global__ void __launch_bounds__(kRowThreads) k_mx4_rows(Mx4Args p)
 {
     const int lane = threadIdx.x & 63;
@@ -214,7 +213,7 @@ __global__ void __launch_bounds__(kRowThreads) k_mx4_rows(Mx4Args p)
     if (row0 < p.rows) {
         Row8<DT> r[kRowsPerWave];
 #pragma unroll
-        for (int j = 0; j < kRowsPerWave; ++j) r[j] = load8<DT, VEC>(p, row0 + j, col);
+        for (int j = 0; j < kRowsPerWave; ++j) r[j] = load8<DT>(p, row0 + j, col);
         uint32_t seed_lo = 0, pk[4];
         if constexpr (SR) {
             const uint64_t seed = *p.seed;
@@ -259,34 +258,37 @@ __global__ void __launch_bounds__(kRowThreads) k_mx4_rows(Mx4Args p)
 }
 
 // ------------------------------------------------------------------ both directions
-constexpr int kTileThreads = 512;
-constexpr int kTileRows = 256, kTileCols = 128;
+constexpr int kTileThreads = 256;
+constexpr int kTileRows = 128, kTileCols = 128;
 
-// A workgroup of 8 waves takes 256 x 128 elements, a wave 32 rows: lane
+// A workgroup of 4 waves takes 128 x 128 elements, a wave 32 rows: lane
 // (c8, rq) holds rows 8 rq .. + 7 of columns 8 c8 .. + 7.  Row codes go
 // straight out, 64 adjacent bytes a row; transposed ones (4 bytes a lane and
-// column) meet in LDS, so that a column's 256 codes leave as 128 adjacent
-// bytes.  16-byte chunk w of a column's 128 bytes lies at chunk w ^ (c8 & 7):
-// the 16 lanes of one rq then write to 32 banks and not to 4.
-template <int DT, bool SR, bool COUNT, bool VEC>
+// column) meet in LDS, so that a column's 128 codes leave as 64 adjacent
+// bytes.  In LDS column 8 c8 + c is the 64 bytes from 64 (16 c + c8) on, and
+// wave w's 16 bytes of it lie at chunk w ^ (c8 / 4): the lanes of a wave then
+// write to all 64 banks.
+template <int DT, bool SR, bool COUNT>
 __global__ void __launch_bounds__(kTileThreads) k_mx4_tile(Mx4Args p)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t codes[kTileCols * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t scales[kTileCols * 8];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kTileCols * 64];
+    __shared__ __attribute__((aligned(16))) uint8_t scales[kTileCols * 4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c8 = lane & 15, rq = lane >> 4;
-    // neighbouring tiles of a row on one XCD, whose L2 then joins their lines
+    // neighbouring tiles on one XCD, two rows of tiles abreast, whose L2 then
+    // joins their lines
     const int total = (int)gridDim.x;
     const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
     const int tile = xcd * (total >> 3) + min(xcd, total & 7) + at;
-    const int64_t tr = tile / p.tiles_c, tc = tile - tr * p.tiles_c;
+    const int64_t pair = tile / (2 * p.tiles_c), in = tile - pair * 2 * p.tiles_c;
+    const int64_t tr = 2 * pair + (in & 1), tc = in >> 1;
     const int64_t row0 = tr * kTileRows + wave * 32 + rq * 8;
     const int64_t col0 = tc * kTileCols, col = col0 + c8 * 8;
 
     Row8<DT> r[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = load8<DT, VEC>(p, row0 + j, col);
+    for (int j = 0; j < 8; ++j) r[j] = load8<DT>(p, row0 + j, col);
     uint32_t h[8][4];
     if constexpr (SR) {
         const uint64_t seed = *p.seed;
@@ -396,26 +398,27 @@ __global__ void __launch_bounds__(kTileThreads) k_mx4_tile(Mx4Args p)
         }
         w = byte == 255u ? 0u : w;
         const int lc = c8 * 8 + c;
-        *reinterpret_cast<uint32_t*>(codes + lc * 128 + ((wave ^ (c8 & 7)) * 16) + rq * 4) = w;
-        if (rq == 0) scales[lc * 8 + wave] = (uint8_t)byte;
+        *reinterpret_cast<uint32_t*>(codes + (16 * c + c8) * 64 + ((wave ^ (c8 >> 2)) * 16) + rq * 4) = w;
+        if (rq == 0) scales[lc * 4 + wave] = (uint8_t)byte;
     }
     __syncthreads();
     const int64_t padded_t = (p.rows + mx4::kRowAlign - 1) & ~(int64_t)(mx4::kRowAlign - 1);
     if (tr * kTileRows < padded_t) {
 #pragma unroll
-        for (int i = 0; i < kTileCols * 8 / kTileThreads; ++i) {
+        for (int i = 0; i < kTileCols * 4 / kTileThreads; ++i) {
             const int t = i * kTileThreads + threadIdx.x;
-            const int lc = t >> 3, ch = t & 7;
+            const int lc = t >> 2, ch = t & 3;
             if (col0 + lc < p.cols) {
-                const u4 v = *reinterpret_cast<const u4*>(codes + lc * 128 + ((ch ^ ((lc >> 3) & 7)) * 16));
+                const int at = 16 * (lc & 7) + (lc >> 3);
+                const u4 v = *reinterpret_cast<const u4*>(codes + at * 64 + ((ch ^ (lc >> 5)) * 16));
                 __builtin_nontemporal_store(
                     v, reinterpret_cast<u4*>(p.qt + (col0 + lc) * p.ldqt + tr * (kTileRows / 2) + ch * 16));
             }
         }
     }
     if (threadIdx.x < kTileCols && col0 + (int)threadIdx.x < p.cols)
-        *reinterpret_cast<u2*>(p.st + (tr >> 1) * p.stps + (col0 + threadIdx.x) * 16 + (tr & 1) * 8) =
-            *reinterpret_cast<const u2*>(scales + threadIdx.x * 8);
+        *reinterpret_cast<uint32_t*>(p.st + (tr >> 2) * p.stps + (col0 + threadIdx.x) * 16 + (tr & 3) * 4) =
+            *reinterpret_cast<const uint32_t*>(scales + threadIdx.x * 4);
     if constexpr (COUNT) flush_counters_block(p.ctr, sat, und, nan);
 }
 
@@ -431,65 +434,78 @@ struct Mx4DeqArgs {
     int panels;
 };
 
-// A wave writes 512 columns of kRowsPerWave rows, 8 columns a lane.
-template <int DT, bool VEC>
+// A wave writes 512 columns of kRowsPerWave rows.  bf16: 8 columns a lane;
+// fp32: 4 columns a lane of either half, so that the lanes' 16 bytes are
+// adjacent in both (two halves of 8 columns a lane: 2.8 TB/s, not 5).
+template <int DT>
 __global__ void __launch_bounds__(kRowThreads) k_mx4_dequantize(Mx4DeqArgs p)
 {
+    constexpr int kParts = DT == 0 ? 1 : 2;
+    constexpr int kCols = 8 / kParts;           // of a lane and part
     const int lane = threadIdx.x & 63;
     const int64_t item = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t group = item / p.panels;
     const int panel = (int)(item - group * p.panels);
     const int64_t row0 = group * kRowsPerWave;
-    const int64_t col = (int64_t)panel * mx4::kPanel + 8 * lane;
-    if (row0 >= p.rows || col >= p.cols) return;
-    uint32_t w[kRowsPerWave], b[kRowsPerWave];
+    if (row0 >= p.rows) return;
+    uint32_t w[kRowsPerWave][kParts], b[kRowsPerWave][kParts];
 #pragma unroll
     for (int j = 0; j < kRowsPerWave; ++j) {
         const int64_t row = min(row0 + j, p.rows - 1);
-        w[j] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p.q + row * p.ldq + (col >> 1)));
-        b[j] = p.s[panel * p.sps + row * 16 + (lane >> 2)];
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+            // rows of codes end on 128 bytes, panels of scales on 16
+            const int64_t in = 64 * kCols * h + kCols * lane;
+            const int64_t col = min((int64_t)panel * mx4::kPanel + in, (p.cols - 1) & ~(int64_t)(kCols - 1));
+            const uint8_t* q = p.q + row * p.ldq + (col >> 1);
+            if constexpr (DT == 0)
+                w[j][h] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(q));
+            else
+                w[j][h] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(q));
+            b[j][h] = p.s[panel * p.sps + row * 16 + (in >> 5)];
+        }
     }
 #pragma unroll
     for (int j = 0; j < kRowsPerWave; ++j) {
         const int64_t row = row0 + j;
         if (row >= p.rows) break;
-        const float s = mx4::scale_float(b[j]);
-        if constexpr (DT == 0) {
-            uint32_t v[4];
-            v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 0));
-            v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 1));
-            v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 2));
-            v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j], s, 3));
-            uint16_t* y = static_cast<uint16_t*>(p.y) + row * p.ldy + col;
-            if constexpr (VEC) {
-                __builtin_nontemporal_store((u4{v[0], v[1], v[2], v[3]}), reinterpret_cast<u4*>(y));
-            } else {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (col + c < p.cols) y[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
-            }
-        } else {
-            mx4::v2f v[4];
-            v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 0);
-            v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 1);
-            v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 2);
-            v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j], s, 3);
-            float* y = static_cast<float*>(p.y) + row * p.ldy + col;
-            if constexpr (VEC) {
-                typedef float f4 __attribute__((ext_vector_type(4)));
-                __builtin_nontemporal_store((f4{v[0][0], v[0][1], v[1][0], v[1][1]}), reinterpret_cast<f4*>(y));
-                __builtin_nontemporal_store((f4{v[2][0], v[2][1], v[3][0], v[3][1]}), reinterpret_cast<f4*>(y) + 1);
-            } else {
+        for (int h = 0; h < kParts; ++h) {
+            const int64_t col = (int64_t)panel * mx4::kPanel + 64 * kCols * h + kCols * lane;
+            const float s = mx4::scale_float(b[j][h]);
+            if constexpr (DT == 0) {
+                uint32_t v[4];
+                v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][h], s, 0));
+                v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][h], s, 1));
+                v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][h], s, 2));
+                v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[j][h], s, 3));
+                uint16_t* y = static_cast<uint16_t*>(p.y) + row * p.ldy + col;
+                if (col + 8 <= p.cols) {
+                    __builtin_nontemporal_store((u4x2{v[0], v[1], v[2], v[3]}), reinterpret_cast<u4x2*>(y));
+                } else {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    if (col + c < p.cols) y[c] = v[c >> 1][c & 1];
+                    for (int c = 0; c < 8; ++c)
+                        if (col + c < p.cols) y[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+                }
+            } else {
+                const mx4::v2f lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j][h], s, 0);
+                const mx4::v2f hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[j][h], s, 1);
+                const float v[4] = {lo[0], lo[1], hi[0], hi[1]};
+                float* y = static_cast<float*>(p.y) + row * p.ldy + col;
+                if (col + 4 <= p.cols) {
+                    __builtin_nontemporal_store((f4x4{v[0], v[1], v[2], v[3]}), reinterpret_cast<f4x4*>(y));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (col + c < p.cols) y[c] = v[c];
+                }
             }
         }
     }
 }
 
 template <int DT, bool SR, bool COUNT>
-hipError_t launch_dir(const Mx4Args& p, bool vec, hipStream_t stream)
+hipError_t launch_dir(const Mx4Args& p, hipStream_t stream)
 {
     Mx4Args a = p;
     if (p.qt) {
@@ -498,19 +514,13 @@ hipError_t launch_dir(const Mx4Args& p, bool vec, hipStream_t stream)
         a.tiles_c = (int)((p.cols + mx4::kPanel - 1) / mx4::kPanel) * (mx4::kPanel / kTileCols);
         const int64_t tiles_r = (p.rows + mx4::kPanel - 1) / mx4::kPanel * (mx4::kPanel / kTileRows);
         const dim3 grid((unsigned)(a.tiles_c * tiles_r));
-        if (vec)
-            hipLaunchKernelGGL((k_mx4_tile<DT, SR, COUNT, true>), grid, dim3(kTileThreads), 0, stream, a);
-        else
-            hipLaunchKernelGGL((k_mx4_tile<DT, SR, COUNT, false>), grid, dim3(kTileThreads), 0, stream, a);
+        hipLaunchKernelGGL((k_mx4_tile<DT, SR, COUNT>), grid, dim3(kTileThreads), 0, stream, a);
         return hipGetLastError();
     }
     a.tiles_c = (int)((p.cols + mx4::kPanel - 1) / mx4::kPanel);
     const int64_t items = (p.rows + kRowsPerWave - 1) / kRowsPerWave * a.tiles_c;
     const dim3 grid((unsigned)((items + kRowThreads / 64 - 1) / (kRowThreads / 64)));
-    if (vec)
-        hipLaunchKernelGGL((k_mx4_rows<DT, SR, COUNT, true>), grid, dim3(kRowThreads), 0, stream, a);
-    else
-        hipLaunchKernelGGL((k_mx4_rows<DT, SR, COUNT, false>), grid, dim3(kRowThreads), 0, stream, a);
+    hipLaunchKernelGGL((k_mx4_rows<DT, SR, COUNT>), grid, dim3(kRowThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -535,14 +545,12 @@ hipError_t launch_mx4_quantize(const Mx4QuantArgs& g, hipStream_t stream)
     p.seed = g.seed;
     p.ctr = g.ctr;
     p.tiles_c = 0;
-    const int64_t size = g.dtype == FP8_IN_BF16 ? 2 : 4;
-    const bool vec = (reinterpret_cast<uintptr_t>(g.x) & 15u) == 0 && (g.ld * size) % 16 == 0 && g.cols % 8 == 0;
     if (g.dtype == FP8_IN_BF16) {
-        if (g.seed) return g.ctr ? launch_dir<0, true, true>(p, vec, stream) : launch_dir<0, true, false>(p, vec, stream);
-        return g.ctr ? launch_dir<0, false, true>(p, vec, stream) : launch_dir<0, false, false>(p, vec, stream);
+        if (g.seed) return g.ctr ? launch_dir<0, true, true>(p, stream) : launch_dir<0, true, false>(p, stream);
+        return g.ctr ? launch_dir<0, false, true>(p, stream) : launch_dir<0, false, false>(p, stream);
     }
-    if (g.seed) return g.ctr ? launch_dir<1, true, true>(p, vec, stream) : launch_dir<1, true, false>(p, vec, stream);
-    return g.ctr ? launch_dir<1, false, true>(p, vec, stream) : launch_dir<1, false, false>(p, vec, stream);
+    if (g.seed) return g.ctr ? launch_dir<1, true, true>(p, stream) : launch_dir<1, true, false>(p, stream);
+    return g.ctr ? launch_dir<1, false, true>(p, stream) : launch_dir<1, false, false>(p, stream);
 }
 
 hipError_t launch_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t sps, int64_t rows,
@@ -552,19 +560,10 @@ hipError_t launch_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s
     Mx4DeqArgs p{q, ldq, s, sps, rows, cols, y, ldy, (int)((cols + mx4::kPanel - 1) / mx4::kPanel)};
     const int64_t items = (rows + kRowsPerWave - 1) / kRowsPerWave * p.panels;
     const dim3 grid((unsigned)((items + kRowThreads / 64 - 1) / (kRowThreads / 64)));
-    const int64_t size = dtype == FP8_IN_BF16 ? 2 : 4;
-    const bool vec = (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && (ldy * size) % 16 == 0 && cols % 8 == 0;
-    if (dtype == FP8_IN_BF16) {
-        if (vec)
-            hipLaunchKernelGGL((k_mx4_dequantize<0, true>), grid, dim3(kRowThreads), 0, stream, p);
-        else
-            hipLaunchKernelGGL((k_mx4_dequantize<0, false>), grid, dim3(kRowThreads), 0, stream, p);
-    } else {
-        if (vec)
-            hipLaunchKernelGGL((k_mx4_dequantize<1, true>), grid, dim3(kRowThreads), 0, stream, p);
-        else
-            hipLaunchKernelGGL((k_mx4_dequantize<1, false>), grid, dim3(kRowThreads), 0, stream, p);
-    }
+    if (dtype == FP8_IN_BF16)
+        hipLaunchKernelGGL((k_mx4_dequantize<0>), grid, dim3(kRowThreads), 0, stream, p);
+    else
+        hipLaunchKernelGGL((k_mx4_dequantize<1>), grid, dim3(kRowThreads), 0, stream, p);
     return hipGetLastError();
 }
 
