@@ -216,15 +216,19 @@ def _torch():
     return torch
 
 
+_raw_stream = None
+
+
 def _stream():
     """The current HIP stream of the current device, as an integer handle.
     torch's raw-stream query is used when it exists (it skips building a
     Stream object, about 3 us per call on the host)."""
+    global _raw_stream
     torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dtype_code(t) -> int:
@@ -569,11 +573,6 @@ def requant_weights(caches: list[WeightCache], masters: list) -> None:
 
 
 # ---------------------------------------------------------------- 4-bit operands
-def mx4_shapes(rows: int, cols: int) -> tuple[tuple[int, int], tuple[int, int, int]]:
-    """Shapes of the codes and the scale bytes of a quantized [rows, cols]."""
-    return (rows, 128 * -(-cols // 256)), (-(-cols // 512), rows, 16)
-
-
 class Mx4:
     """A tensor [..., rows, cols] in OCP microscaling FP4: `q` uint8 codes
     [..., rows, 128 ceil(cols/256)] (two to a byte, the even column in the low
@@ -581,29 +580,35 @@ class Mx4:
     16] (one for 32 elements of a row, 127 past cols).  Rows of q and panels
     of s may lie further apart, by multiples of 16 bytes.  One leading
     dimension (experts) is taken by MoeMx4."""
-    __slots__ = ("q", "s", "cols")
+    __slots__ = ("q", "s", "cols", "_held")
 
     def __init__(self, q, s, cols: int):
         torch = _torch()
-        if q.dtype != torch.uint8 or s.dtype != torch.uint8:
+        if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
             raise ValueError(f"q and s must be torch.uint8, got {q.dtype} and {s.dtype}")
         cols = int(cols)
-        if q.dim() not in (2, 3) or cols < 0 or q.shape[-1] != 128 * -(-cols // 256):
+        nq, ns = q.shape, s.shape
+        if len(nq) not in (2, 3) or cols < 0 or nq[-1] != 128 * -(-cols // 256):
             raise ValueError(f"q of {cols} columns must have shape [..., rows, {128 * -(-cols // 256)}], "
-                             f"got {tuple(q.shape)}")
-        want = (*q.shape[:-2], -(-cols // 512), q.shape[-2], 16)
-        if tuple(s.shape) != want:
-            raise ValueError(f"s must have shape {want}, got {tuple(s.shape)}")
-        if q.numel() and (q.stride(-1) != 1 or s.stride(-1) != 1 or (s.shape[-2] > 1 and s.stride(-2) != 16)):
+                             f"got {tuple(nq)}")
+        rows, panels = nq[-2], -(-cols // 512)
+        if ns[-3:] != (panels, rows, 16) or ns[:-3] != nq[:-2]:
+            raise ValueError(f"s must have shape {(*nq[:-2], panels, rows, 16)}, got {tuple(ns)}")
+        lq, ls = q.stride(), s.stride()
+        if (lq[-1] != 1 or ls[-1] != 1 or (rows > 1 and ls[-2] != 16)) and q.numel():
             raise ValueError("the bytes of a row of q and of a panel of s must be adjacent")
         self.q, self.s, self.cols = q, s, cols
+        self._held = (lq[-2] if rows > 1 else max(nq[-1], 16), ls[-3] if panels > 1 else 16 * rows)
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):
         torch = _torch()
-        nq, ns = mx4_shapes(rows, cols)
-        return cls(torch.empty(nq, dtype=torch.uint8, device=device),
-                   torch.empty(ns, dtype=torch.uint8, device=device), cols)
+        row, panels = 128 * -(-cols // 256), -(-cols // 512)
+        a = object.__new__(cls)
+        a.q = torch.empty_strided((rows, row), (row, 1), dtype=torch.uint8, device=device)
+        a.s = torch.empty_strided((panels, rows, 16), (16 * rows, 16, 1), dtype=torch.uint8, device=device)
+        a.cols, a._held = cols, (max(row, 16), 16 * rows)
+        return a
 
     @property
     def rows(self) -> int:
@@ -615,19 +620,17 @@ class Mx4:
 
     def _args(self):
         """data pointer and distance of the rows of codes, of the scale panels."""
-        q, s = self.q, self.s
-        rows = q.shape[-2]
-        ldq = q.stride(-2) if rows > 1 else max(q.shape[-1], 16)
-        ps = s.stride(-3) if s.shape[-3] > 1 else 16 * rows
-        return q.data_ptr(), ldq, s.data_ptr(), ps
+        row, panel = self._held
+        return self.q.data_ptr(), row, self.s.data_ptr(), panel
 
 
 def _check_mx4(t, name, rows=None, cols=None):
     if not isinstance(t, Mx4):
         raise ValueError(f"{name} must be an Mx4, got {type(t).__name__}")
-    if t.q.dim() != 2:
+    shape = t.q.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a matrix, got shape {t.shape}")
-    if (rows is not None and t.rows != rows) or (cols is not None and t.cols != cols):
+    if (rows is not None and shape[0] != rows) or (cols is not None and t.cols != cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {t.shape}")
 
 
@@ -648,15 +651,16 @@ def mx4_quantize(x, want_t: bool = False, seed=None, counters: Counters | None =
         if not want_t:
             raise ValueError("out_t given without want_t=True")
         _check_mx4(out_t, "out_t", cols, rows)
-    _check_devices(x, seed, out and out.q, out and out.s, out_t and out_t.q, out_t and out_t.s,
-                   counters.buf if counters else None)
+    if out is None and out_t is None and counters is None:
+        _check_devices(x, seed)
+    else:
+        _check_devices(x, seed, out and out.q, out and out.s, out_t and out_t.q, out_t and out_t.s,
+                       counters.buf if counters else None)
     q = out if out is not None else Mx4.empty(rows, cols, x.device)
     qt = None
     if want_t:
         qt = out_t if out_t is not None else Mx4.empty(cols, rows, x.device)
-    t_args = qt._args() if qt is not None else (None, 0, None, 0)
-    if rows == 0 or cols == 0:
-        t_args = (None, 0, None, 0)
+    t_args = qt._args() if qt is not None and rows > 0 and cols > 0 else (None, 0, None, 0)
     check(lib().fp8_mx4_quantize(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), *q._args(), *t_args,
                                  _ptr(seed), counters.ptr() if counters else None, _stream()))
     return q, qt
@@ -674,7 +678,8 @@ def mx4_dequantize(a: Mx4, dtype=None, out=None):
     elif dtype not in (None, torch.bfloat16, torch.float32):
         raise ValueError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
     _check_devices(a.q, a.s, out)
-    y = out if out is not None else torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=a.q.device)
+    y = out if out is not None else torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype or torch.bfloat16,
+                                                        device=a.q.device)
     check(lib().fp8_mx4_dequantize(*a._args(), rows, cols, y.data_ptr(), _dtype_code(y), _ld(y), _stream()))
     return y
 
@@ -691,7 +696,7 @@ def mx4_mm(a: Mx4, b: Mx4, out=None, counters: Counters | None = None):
     if out is not None:
         _check_tensor(out, "out", (torch.bfloat16,), (m, n), unit_col_stride=True)
     _check_devices(a.q, a.s, b.q, b.s, out, counters.buf if counters else None)
-    c = out if out is not None else torch.empty((m, n), dtype=torch.bfloat16, device=a.q.device)
+    c = out if out is not None else torch.empty_strided((m, n), (max(n, 1), 1), dtype=torch.bfloat16, device=a.q.device)
     check(lib().fp8_mx4_mm(*a._args(), *b._args(), m, n, k, c.data_ptr(), _ld(c),
                            counters.ptr() if counters else None, _stream()))
     return c
@@ -747,9 +752,10 @@ class MoeMx4:
         if out is not None:
             _check_tensor(out, "out", (torch.bfloat16,), (tokens, self.hidden), unit_col_stride=True)
         _check_devices(x, self.router, out)
-        y = out if out is not None else torch.empty((tokens, self.hidden), dtype=torch.bfloat16, device=x.device)
-        ids = torch.empty((tokens, self.top_k), dtype=torch.int32, device=x.device)
-        weights = torch.empty((tokens, self.top_k), dtype=torch.float32, device=x.device)
+        new, device, k = torch.empty_strided, x.device, self.top_k
+        y = out if out is not None else new((tokens, self.hidden), (self.hidden, 1), dtype=torch.bfloat16, device=device)
+        ids = new((tokens, k), (k, 1), dtype=torch.int32, device=device)
+        weights = new((tokens, k), (k, 1), dtype=torch.float32, device=device)
         check(lib().fp8_mx4_moe(x.data_ptr(), tokens, self.hidden, _ld(x), self.router.data_ptr(), _ld(self.router),
                                 self._w1, self._w2, self.experts, self.inner, self.top_k, self.renormalize,
                                 y.data_ptr(), _ld(y), ids.data_ptr(), weights.data_ptr(), self._ws.data_ptr(),
