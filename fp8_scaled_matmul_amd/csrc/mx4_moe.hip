@@ -835,12 +835,12 @@ int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
     return (int)std::clamp<int64_t>(std::min((256 + blocks - 1) / blocks, steps / (2 * kDownWaves)), 1, kMaxShares);
 }
 
-// K splits of the router: two rounds of reads a workgroup at most, and few
-// enough partial sums.
+// K splits of the router: one round of reads a wave, in up to 8 (1 token, 64
+// experts of 2048: 1 us less than with two rounds).
 int route_splits(int64_t hidden)
 {
     const int64_t chunks = (hidden + kChunk - 1) / kChunk;
-    return (int)std::clamp<int64_t>((chunks + 2 * kRouteWaves - 1) / (2 * kRouteWaves), 1, kMaxSplits);
+    return (int)std::clamp<int64_t>((chunks + kRouteWaves - 1) / kRouteWaves, 1, kMaxSplits);
 }
 
 struct MoeLayout {
