@@ -216,6 +216,24 @@ def _torch():
     return torch
 
 
+_ext_module = None
+
+
+def _ext():
+    """The extension module for calls that are all in order: it returns None
+    for any other, and the code here takes those."""
+    global _ext_module
+    if _ext_module is None:
+        _torch()        # its libraries come first
+        try:
+            from . import _fp8mi_torch
+        except ImportError as e:
+            raise RuntimeError("_fp8mi_torch.so does not load: build it with "
+                               "`python -m fp8_scaled_matmul_amd.build`") from e
+        _ext_module = _fp8mi_torch
+    return _ext_module
+
+
 _raw_stream = None
 
 
@@ -583,6 +601,10 @@ class Mx4:
     __slots__ = ("q", "s", "cols", "_held")
 
     def __init__(self, q, s, cols: int):
+        held = _ext().mx4_held(q, s, cols)
+        if held is not None:
+            self.q, self.s, self.cols, self._held = q, s, cols, held
+            return
         torch = _torch()
         if q.dtype is not torch.uint8 or s.dtype is not torch.uint8:
             raise ValueError(f"q and s must be torch.uint8, got {q.dtype} and {s.dtype}")
@@ -599,6 +621,13 @@ class Mx4:
             raise ValueError("the bytes of a row of q and of a panel of s must be adjacent")
         self.q, self.s, self.cols = q, s, cols
         self._held = (lq[-2] if rows > 1 else max(nq[-1], 16), ls[-3] if panels > 1 else 16 * rows)
+
+    @classmethod
+    def _of(cls, q, s, rows: int, cols: int):
+        """Of codes and scales that were allocated for it."""
+        a = object.__new__(cls)
+        a.q, a.s, a.cols, a._held = q, s, cols, (128 * -(-cols // 256), 16 * rows)
+        return a
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda"):
@@ -640,6 +669,13 @@ def mx4_quantize(x, want_t: bool = False, seed=None, counters: Counters | None =
     None rounds to nearest even; an int64 device tensor of one element rounds
     stochastically with the bits it draws (a captured graph reads it anew at
     each replay)."""
+    if out is None and out_t is None and counters is None:
+        r = _ext().mx4_quantize(x, bool(want_t), seed)
+        if r is not None:
+            if type(r) is int:
+                check(r)
+            rows, cols = x.shape
+            return Mx4._of(r[0], r[1], rows, cols), Mx4._of(r[2], r[3], cols, rows) if want_t else None
     torch = _torch()
     _check_tensor(x, "x", (torch.bfloat16, torch.float32), unit_col_stride=True)
     rows, cols = x.shape
@@ -651,11 +687,8 @@ def mx4_quantize(x, want_t: bool = False, seed=None, counters: Counters | None =
         if not want_t:
             raise ValueError("out_t given without want_t=True")
         _check_mx4(out_t, "out_t", cols, rows)
-    if out is None and out_t is None and counters is None:
-        _check_devices(x, seed)
-    else:
-        _check_devices(x, seed, out and out.q, out and out.s, out_t and out_t.q, out_t and out_t.s,
-                       counters.buf if counters else None)
+    _check_devices(x, seed, out and out.q, out and out.s, out_t and out_t.q, out_t and out_t.s,
+                   counters.buf if counters else None)
     q = out if out is not None else Mx4.empty(rows, cols, x.device)
     qt = None
     if want_t:
@@ -670,6 +703,12 @@ def mx4_dequantize(a: Mx4, dtype=None, out=None):
     """The values of a quantized matrix, in bf16 (the default) or fp32."""
     torch = _torch()
     _check_mx4(a, "a")
+    if out is None and dtype in (None, torch.bfloat16, torch.float32):
+        y = _ext().mx4_dequantize(a.q, a.s, a._held, a.cols, dtype is torch.float32)
+        if y is not None:
+            if type(y) is int:
+                check(y)
+            return y
     rows, cols = a.shape
     if out is not None:
         _check_tensor(out, "out", (torch.bfloat16, torch.float32), (rows, cols), unit_col_stride=True)
@@ -686,9 +725,15 @@ def mx4_dequantize(a: Mx4, dtype=None, out=None):
 
 def mx4_mm(a: Mx4, b: Mx4, out=None, counters: Counters | None = None):
     """y = A B^T of two quantized operands a [m, k] and b [n, k], bf16 [m, n]."""
-    torch = _torch()
     _check_mx4(a, "a")
     _check_mx4(b, "b")
+    if out is None and counters is None:
+        c = _ext().mx4_mm(a.q, a.s, a._held, a.cols, b.q, b.s, b._held, b.cols)
+        if c is not None:
+            if type(c) is int:
+                check(c)
+            return c
+    torch = _torch()
     m, k = a.shape
     n = b.rows
     if b.cols != k:
@@ -742,8 +787,16 @@ class MoeMx4:
                               w.s.stride(1) if w.s.shape[1] > 1 else 16 * w.rows, w.s.stride(0) if experts > 1 else 0)
 
         self._w1, self._w2 = held(w1), held(w2)
+        self._plan = (self.router, self._ws, ctypes.addressof(self._w1), ctypes.addressof(self._w2), experts, inner,
+                      self.top_k, int(self.renormalize), self.max_tokens)
 
     def __call__(self, x, out=None):
+        if out is None and self.counters is None:
+            r = _ext().mx4_moe(x, *self._plan)
+            if r is not None:
+                if type(r) is int:
+                    check(r)
+                return r
         torch = _torch()
         _check_tensor(x, "x", (torch.bfloat16,), unit_col_stride=True)
         tokens = x.shape[0]
@@ -753,7 +806,8 @@ class MoeMx4:
             _check_tensor(out, "out", (torch.bfloat16,), (tokens, self.hidden), unit_col_stride=True)
         _check_devices(x, self.router, out)
         new, device, k = torch.empty_strided, x.device, self.top_k
-        y = out if out is not None else new((tokens, self.hidden), (self.hidden, 1), dtype=torch.bfloat16, device=device)
+        y = out if out is not None else new((tokens, self.hidden), (self.hidden, 1), dtype=torch.bfloat16,
+                                            device=device)
         ids = new((tokens, k), (k, 1), dtype=torch.int32, device=device)
         weights = new((tokens, k), (k, 1), dtype=torch.float32, device=device)
         check(lib().fp8_mx4_moe(x.data_ptr(), tokens, self.hidden, _ld(x), self.router.data_ptr(), _ld(self.router),

@@ -1,4 +1,5 @@
-"""Build the HIP library libfp8mi.so in-tree for gfx950 with hipcc.
+"""Build the HIP library libfp8mi.so in-tree for gfx950 with hipcc, and the
+extension module _fp8mi_torch.so that calls it with torch tensors.
 
 Usage: python -m fp8_scaled_matmul_amd.build   (or call build()).
 """
@@ -8,12 +9,14 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8mi.so")
+BINDING = os.path.join(PKG, "_fp8mi_torch.so")
 
 SOURCES = ["quantize.hip", "gemm.hip", "gemm_persistent.hip", "gemm_astat.hip", "mx4_quantize.hip", "mx4_gemm.hip",
            "mx4_moe.hip", "api.cpp"]
@@ -49,18 +52,44 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every HIP/C++ source and link libfp8mi.so (always rebuilds)."""
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(_compile, SOURCES))
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
+def _compile_binding() -> str:
+    import torch
+    os.makedirs(BUILD, exist_ok=True)
+    obj = os.path.join(BUILD, "binding.cpp.o")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    rocm = os.path.dirname(os.path.dirname(HIPCC))
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.join(ROOT, "include"),
+           "-isystem", inc, "-isystem", os.path.join(rocm, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link(cmd: list, out: str) -> None:
+    tmp = out + ".tmp"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    os.replace(tmp, out)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every HIP/C++ source and link libfp8mi.so and the extension
+    module (always rebuilds)."""
+    import torch
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding)
+        objs = list(ex.map(_compile, SOURCES))
+        binding = binding.result()
+    _link([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs], LIB)
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _link(["g++", "-shared", "-fPIC", binding, "-L", PKG, "-l:libfp8mi.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"], BINDING)
     if verbose:
-        print("built", LIB)
+        print("built", LIB, BINDING)
     return LIB
 
 

@@ -344,3 +344,20 @@ def test_linear_gradients_against_formula_and_differences():
         step[r, 3] = 1.0
         d = ((dy * ((x + step) @ w.T)).sum() - (dy * ((x - step) @ w.T)).sum()) / 2
         assert abs(dx[r, 3] - d) <= 2.0 ** -8 * abs(d) + 1e-6
+
+
+def test_same_results_with_and_without_outputs_given():
+    """The calls that the extension module takes whole and those the Python
+    code takes give the same, parameters that require gradients among them."""
+    x = torch.nn.Parameter(_x(100, 300).cuda())
+    seed = torch.tensor([3], dtype=torch.int64, device="cuda")
+    for sd in (None, seed):
+        q, qt = fm.mx4_quantize(x, want_t=True, seed=sd)
+        o, ot = fm.mx4_quantize(x, want_t=True, seed=sd, out=fm.Mx4.empty(100, 300), out_t=fm.Mx4.empty(300, 100))
+        assert all(torch.equal(a, b) for a, b in ((q.q, o.q), (q.s, o.s), (qt.q, ot.q), (qt.s, ot.s)))
+        assert fm.mx4_quantize(x, seed=sd)[1] is None and not q.q.requires_grad
+    for dtype in (torch.bfloat16, torch.float32):
+        y = torch.empty(100, 300, dtype=dtype, device="cuda")
+        assert torch.equal(fm.mx4_dequantize(q, dtype), fm.mx4_dequantize(q, out=y))
+    y = torch.empty(100, 100, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(fm.mx4_mm(q, q), fm.mx4_mm(q, q, out=y))

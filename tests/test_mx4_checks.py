@@ -167,3 +167,30 @@ def test_moe_binding_rejects():
             fm.MoeMx4(*bad)
     with pytest.raises(ValueError, match="CUDA"):
         fm.MoeMx4(router, w1, w2, 2)
+
+
+def test_extension_leaves_other_calls_to_python():
+    """Calls that are not all in order get None from the extension module, so
+    that the Python code refuses or handles them."""
+    ext = fm._ext()
+    x = torch.zeros(8, 64, dtype=torch.bfloat16)
+    q, s = torch.zeros(5, 256, dtype=torch.uint8), torch.zeros(1, 5, 16, dtype=torch.uint8)
+    assert ext.mx4_held(q, s, 500) == (256, 80)
+    wide = torch.zeros(5, 300, dtype=torch.uint8)[:, :256]
+    assert ext.mx4_held(wide, s, 500) == (300, 80)
+    for args in [(q.short(), s, 500), (q, s, 256), (q, s, 513), (q, s[0], 500), (q, s, 500.0), (q, None, 500),
+                 (q[0], s, 500), (q, s.expand(2, 5, 16), 500), (q, s), (q[:0], s[:, :0], 500)]:
+        assert ext.mx4_held(*args) is None
+    for args in [(x, False, None), (None, False, None), (x[0], False, None), (x, False, 5), (x,)]:
+        assert ext.mx4_quantize(*args) is None
+    a = _mx4(8, 64)
+    assert ext.mx4_dequantize(a.q, a.s, a._held, a.cols, False) is None
+    assert ext.mx4_mm(a.q, a.s, a._held, a.cols, a.q, a.s, a._held, a.cols) is None
+    assert ext.mx4_mm(a.q, a.s, a._held, a.cols, a.q, a.s, a._held, 65) is None
+    assert ext.mx4_moe(x, x, a.q, 0, 0, 8, 32, 1, 0, 8) is None
+
+
+def test_extension_passes_errors_of_its_arguments_on():
+    a = _mx4(8, 64)
+    with pytest.raises(OverflowError):
+        fm._ext().mx4_held(a.q, a.s, 1 << 70)
