@@ -364,7 +364,7 @@ __device__ inline bool last_of(uint32_t* count, uint32_t all)
 // weights: of every pair.
 __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off, const int* ids, const float* weights)
 {
-    __shared__ int s_n[kRouteWaves], s_groups[kRouteWaves], s_active[kRouteWaves];
+    __shared__ int s_sum[kRouteWaves], s_active[kRouteWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     static_assert(kRouteThreads >= kMaxExperts && kRouteThreads >= kMaxTokens * kMaxTopK, "a thread each");
     mask[threadIdx.x] = 0;
@@ -376,27 +376,29 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
     const int n = __builtin_popcountll(mask[threadIdx.x]);
     const uint64_t here = __ballot(n > 0);
     const int groups = (n + kDownTokens - 1) / kDownTokens;
-    int before = n, first = groups;     // inclusive sums over the wave
+    // inclusive sums over the wave, of both at once (n and its sum under 2^16)
+    const int both = n | groups << 16;
+    int sum = both;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(before, d, 64), og = __shfl_up(first, d, 64);
-        before += lane >= d ? o : 0;
-        first += lane >= d ? og : 0;
+        const int o = __shfl_up(sum, d, 64);
+        sum += lane >= d ? o : 0;
     }
     if (lane == 63) {
-        s_n[wave] = before;
-        s_groups[wave] = first;
+        s_sum[wave] = sum;
         s_active[wave] = __builtin_popcountll(here);
     }
     __syncthreads();
-    int at = before - n, active = 0;
-    first -= groups;
-#pragma unroll
-    for (int i = 0; i < kRouteWaves; ++i) {
-        at += i < wave ? s_n[i] : 0;
-        first += i < wave ? s_groups[i] : 0;
+    sum -= both;
+    int active = 0, total = 0, all = 0;
+    const int waves = (p.experts + 63) / 64;
+    for (int i = 0; i < waves; ++i) {
+        sum += i < wave ? s_sum[i] : 0;
         active += i < wave ? s_active[i] : 0;
+        total += s_active[i];
+        all += s_sum[i];
     }
+    const int at = sum & 0xFFFF, first = sum >> 16;
     off[threadIdx.x] = at;
     if (n > 0)
         p.reached[active + __builtin_popcountll(here & ((1ull << lane) - 1))] =
@@ -406,9 +408,9 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
         p.groups[first + g] = MoeGroup{(int)threadIdx.x, at + kDownTokens * g, left};
         for (int j = 0; j < kDownTokens; ++j) left &= left - 1;
     }
-    if (threadIdx.x == kRouteThreads - 1) {
-        p.count[0] = active + __builtin_popcountll(here);
-        p.count[1] = first + groups;
+    if (threadIdx.x == 0) {
+        p.count[0] = total;
+        p.count[1] = all >> 16;
     }
     __syncthreads();
     if (e >= 0) p.prob[off[e] + __builtin_popcountll(mask[e] & ((1ull << t) - 1))] = weights[threadIdx.x];
@@ -666,8 +668,7 @@ constexpr int kMaxShares = 8;
 // order at the end, and over the workgroups by the last of them to arrive.  A
 // step's weights are read two steps ahead and its columns one: reads come back
 // in order, so the columns of the next step are asked for before the weights
-// of the one after it, and no read hangs on a branch (past the end the last
-// step's are read again).
+// of the one after it, and no read in the loop hangs on a branch.
 __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float ysum[];     // [waves, tokens, 32]
@@ -693,16 +694,23 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
         int e, row, n, panel;       // row: of the first token's first piece; n tokens
         uint64_t mask;
     };
-    const auto at_step = [&](int i) {
-        At a;
+    struct Entry {
+        MoeReached r;
+        int panel;
+    };
+    // what the list holds for step i, then what it means
+    const auto entry = [&](int i) {
         i = min(i, steps - 1);
         const int g = i / panels;
-        a.panel = i - g * panels;
-        const MoeReached r = reached_at(p, p.groups, g);
-        a.mask = r.mask;
-        a.e = r.expert;
-        a.row = kAPieces * r.off;
-        a.n = min(__builtin_popcountll(r.mask), kDownTokens);
+        return Entry{reached_at(p, p.groups, g), i - g * panels};
+    };
+    const auto at_step = [&](const Entry& x) {
+        At a;
+        a.panel = x.panel;
+        a.mask = x.r.mask;
+        a.e = x.r.expert;
+        a.row = kAPieces * x.r.off;
+        a.n = min(__builtin_popcountll(x.r.mask), kDownTokens);
         return a;
     };
     struct W {
@@ -733,10 +741,10 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
         load_x(x.u[1], base + kUnit, col * (uint32_t)p.ip + 16 * q);
     };
     // 32 rows x the tokens of 15 columns, added to this wave's sums
-    const auto compute = [&](const W& w, const X& x, const At& a, bool live) {
+    const auto compute = [&](const W& w, const X& x, const At& a) {
         static_assert(kAPieces == 3, "two neighbours");
         const int c = c16 / kAPieces;
-        const bool mine_to_add = live && c16 % kAPieces == 0 && c < a.n;
+        const bool mine_to_add = c16 % kAPieces == 0 && c < a.n;
         v4f* to = reinterpret_cast<v4f*>(mine + token_of(a.mask, min(c, a.n - 1)) * kDownRows + 4 * q);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -757,22 +765,32 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
     X x0, x1;
     At a0, a1;
     if (first < end) {
-        a0 = at_step(first);
-        a1 = at_step(first + 1);
+        const Entry e0 = entry(first), e1 = entry(first + 1);
+        a0 = at_step(e0);
+        a1 = at_step(e1);
         get_w(w0, a0);
         get_x(x0, a0);
         get_w(w1, a1);
     }
     for (int i = lane; i < p.tokens * kDownRows; i += 64) mine[i] = 0.0f;
-    for (int i = first; i < end; i += 2) {
-        get_x(x1, a1);
-        compute(w0, x0, a0, true);
-        a0 = at_step(i + 2);
-        get_w(w0, a0);
-        get_x(x0, a0);
-        compute(w1, x1, a1, i + 1 < end);
-        a1 = at_step(i + 3);
-        get_w(w1, a1);
+    if (first < end) {
+        int i = first;
+        for (; i + 2 < end; i += 2) {
+            get_x(x1, a1);
+            const Entry e0 = entry(i + 2);
+            compute(w0, x0, a0);
+            a0 = at_step(e0);
+            get_w(w0, a0);
+            get_x(x0, a0);
+            const Entry e1 = entry(i + 3);
+            compute(w1, x1, a1);
+            a1 = at_step(e1);
+            get_w(w1, a1);
+        }
+        const bool two = i + 1 < end;
+        if (two) get_x(x1, a1);
+        compute(w0, x0, a0);
+        if (two) compute(w1, x1, a1);
     }
     __syncthreads();
     uint32_t nonfinite = 0;
@@ -835,12 +853,13 @@ int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
     return (int)std::clamp<int64_t>(std::min((256 + blocks - 1) / blocks, steps / (2 * kDownWaves)), 1, kMaxShares);
 }
 
-// K splits of the router: one round of reads a wave, in up to 8 (1 token, 64
-// experts of 2048: 1 us less than with two rounds).
-int route_splits(int64_t hidden)
+// K splits of the router: one round of reads a wave, as far as the partial sums
+// of 16 tokens, which one workgroup reads, stay under 64 KB (64 tokens, 128
+// experts of 4096: 4 splits, the launch 2 us shorter than with 8).
+int route_splits(int64_t tokens, int64_t experts, int64_t hidden)
 {
-    const int64_t chunks = (hidden + kChunk - 1) / kChunk;
-    return (int)std::clamp<int64_t>((chunks + kRouteWaves - 1) / kRouteWaves, 1, kMaxSplits);
+    const int64_t chunks = (hidden + kChunk - 1) / kChunk, bytes = std::min<int64_t>(tokens, 16) * experts * 8;
+    return (int)std::clamp<int64_t>(std::min((chunks + kRouteWaves - 1) / kRouteWaves, 65536 / bytes), 1, kMaxSplits);
 }
 
 struct MoeLayout {
@@ -860,7 +879,7 @@ MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hid
     };
     m.arrived_rows = take((hidden + kDownRows - 1) / kDownRows * 4);
     m.zeroed = (size_t)at;
-    m.logits = take(route_splits(hidden) * tokens * experts * 8);
+    m.logits = take(route_splits(tokens, experts, hidden) * tokens * experts * 8);
     m.xq = take(tokens * kXPieces * hp);
     m.xs = take(tokens * kXPieces * (hp / 32));
     m.count = take(4);
@@ -934,7 +953,7 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     p.ctr = g.ctr;
     p.tiles_e = (p.experts + 15) / 16;
     p.tiles_t = (p.tokens + 15) / 16;
-    p.splits = route_splits(p.hidden);
+    p.splits = route_splits(g.tokens, g.experts, g.hidden);
 
     const auto al16 = [](const void* v) { return (reinterpret_cast<uintptr_t>(v) & 15u) == 0; };
     const bool vec = p.hidden % 8 == 0 && p.ldx % 8 == 0 && p.ldr % 8 == 0 && al16(g.x) && al16(g.router);
