@@ -285,48 +285,61 @@ __device__ inline void select(const MoeArgs& p, int t, int* ids, float* weights)
 #pragma unroll
             for (int s = 0; s < kAtOnce; ++s) l[j] += __builtin_bit_cast(double, part[j][s]);
     }
-    uint64_t key[N];                    // 0: none, or taken
+    // a lane's own in falling order (equal ones as they come); key 0: none, or taken
+    uint32_t hi[N], lo[N], slot[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) key[j] = 64 * j + lane < p.experts ? key_of(l[j]) : 0;
-    double top = 0, mine = 0;           // lane r keeps rank r's
-    int id = 0;
-    for (int r = 0; r < p.top_k; ++r) {
-        uint64_t best = key[0];
-        double v = l[0];
-        int at = 0;
+    for (int j = 0; j < N; ++j) {
+        const uint64_t key = 64 * j + lane < p.experts ? key_of(l[j]) : 0;
+        hi[j] = (uint32_t)(key >> 32);
+        lo[j] = (uint32_t)key;
+        slot[j] = j;
+    }
 #pragma unroll
-        for (int j = 1; j < N; ++j) {
-            const bool more = key[j] > best;
-            best = more ? key[j] : best;
-            v = more ? l[j] : v;
-            at = more ? j : at;
+    for (int i = N - 1; i > 0; --i)
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+            const uint64_t x = (uint64_t)hi[j] << 32 | lo[j], y = (uint64_t)hi[j + 1] << 32 | lo[j + 1];
+            const bool swap = y > x;
+            const uint32_t h = hi[j], w = lo[j], k = slot[j];
+            hi[j] = swap ? hi[j + 1] : h;
+            lo[j] = swap ? lo[j + 1] : w;
+            slot[j] = swap ? slot[j + 1] : k;
+            hi[j + 1] = swap ? h : hi[j + 1];
+            lo[j + 1] = swap ? w : lo[j + 1];
+            slot[j + 1] = swap ? k : slot[j + 1];
         }
-        const int e = 64 * at + lane;
+    int id = 0;                         // lane r: rank r's
+    for (int r = 0; r < p.top_k; ++r) {
         // the lanes that hold the largest: by the high words; where those are
         // alike by the low words, then the expert
-        const uint32_t hi = (uint32_t)(best >> 32), lo = (uint32_t)best;
-        const uint32_t top_hi = max_of_wave(hi);
-        uint64_t who = __ballot(hi == top_hi);
-        if (__builtin_popcountll(who) > 1) {
+        const uint32_t top_hi = max_of_wave(hi[0]);
+        uint64_t who = __ballot(hi[0] == top_hi);
+        const uint32_t e = 64 * slot[0] + lane;
+        if (who & (who - 1)) {
             const bool in = who >> lane & 1;
-            const uint32_t top_lo = max_of_wave(in ? lo : 0u);
-            const bool still = in && lo == top_lo;
-            const uint32_t first = ~max_of_wave(still ? ~(uint32_t)e : 0u);
-            who = __ballot(still && (uint32_t)e == first);
+            const uint32_t top_lo = max_of_wave(in ? lo[0] : 0u);
+            const bool still = in && lo[0] == top_lo;
+            const uint32_t first = ~max_of_wave(still ? ~e : 0u);
+            who = __ballot(still && e == first);
         }
         const int owner = __builtin_ctzll(who);
-        const uint64_t vb = __builtin_bit_cast(uint64_t, v);
-        v = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)vb, owner) |
-                                           (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(vb >> 32), owner) << 32);
-        const int chosen = __builtin_amdgcn_readlane(e, owner);
+        const int chosen = __builtin_amdgcn_readlane((int)e, owner);
+        id = lane == r ? chosen : id;
+        const bool took = lane == owner;
 #pragma unroll
-        for (int j = 0; j < N; ++j) key[j] = lane == owner && j == at ? 0 : key[j];
-        if (r == 0) top = v;
-        if (lane == r) {
-            mine = v;
-            id = chosen;
+        for (int j = 0; j < N; ++j) {
+            hi[j] = took ? (j + 1 < N ? hi[j + 1] : 0u) : hi[j];
+            lo[j] = took ? (j + 1 < N ? lo[j + 1] : 0u) : lo[j];
+            slot[j] = took ? (j + 1 < N ? slot[j + 1] : 0u) : slot[j];
         }
     }
+    double mine = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const double v = __shfl(l[j], id & 63, 64);
+        mine = id >> 6 == j ? v : mine;
+    }
+    const double top = __shfl(mine, 0, 64);
     const float z = lane < p.top_k ? expf((float)(mine - top)) : 0.0f;
     float sum = z;
     if (!p.renormalize) {
