@@ -688,10 +688,18 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
     //   256 x 1024 x 1024    16 x 32: 6.6    32 x 32: 5.1    64 x 32: 7.1
     //   333 x 1000 x 1568    32 x 32: 8.9    64 x 32: 7.2    64 x 64: 8.6
     //   512 x 2048 x 2048    64 x 32: 12.3   64 x 64: 9.4    128 x 128: 12.3
-    //   1024 x 4096 x 4096   64 x 64: 42.1   128 x 128: 19.2   256 x 256: 29.2
+    //   1024 x 4096 x 4096   64 x 64: 41.9   128 x 128: 17.1   256 x 256: 28.9
+    //   4096 x 2048 x 7168   (128 of 256 x 256)   128 x 128: 38.5   256 x 256: 50.0
+    //   2048 x 7168 x 2048   (224 of 256 x 256)   128 x 128: 25.7   256 x 256: 23.9
     const auto enough = [&](int64_t tm, int64_t tn) { return ((g.m + tm - 1) / tm) * ((g.n + tn - 1) / tn) >= 192; };
     if (enough(256, 256)) return launch_big(p, stream);
-    if (g.m > 64 && enough(128, 128)) return launch_tile<2, 2, 2, 4>(p, stream);
+    if (g.m > 64 && enough(128, 128)) {
+        // One tile a CU: three stages (108 KB of LDS); more: two, and two
+        // workgroups a CU.  512 x 8192 x 4096 (256 tiles): 16.6 and 19.8 us;
+        // 1100 x 4096 x 4096 (288): 28.5 and 20.3 us.
+        const int64_t tiles = ((g.m + 127) / 128) * ((g.n + 127) / 128);
+        return tiles <= gemm_num_cus() ? launch_tile<4, 2, 1, 3>(p, stream) : launch_tile<4, 2, 1, 2>(p, stream);
+    }
     if (g.m > 32 && enough(64, 64)) return launch_direct<4, 4, 2, 1>(p, stream);
     if (g.m > 32 && enough(64, 32)) return launch_direct<2, 4, 4, 1>(p, stream);
     if (g.m > 16 && enough(32, 32)) return launch_direct<2, 2, 4, 2>(p, stream);

@@ -217,6 +217,20 @@ def test_mm_many_tiles(m, n, k):
     assert torch.equal(buf[:, :n], y) and (buf[:, n:] == 7).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(1900, 2000, 700), (1536, 2048, 256), (2000, 1600, 31), (3000, 2600, 1300),
+                                   (2900, 1537, 256)])
+def test_mm_some_tiles(m, n, k):
+    """About one and two middle-sized tiles a CU: fewer steps than the ring
+    has stages, ragged edges, an odd pitch."""
+    a, va = _operand(m, k, 10)
+    b, vb = _operand(n, k, 11)
+    y = fm.mx4_mm(a, b)
+    _check_mm(y, va, vb)
+    buf = torch.full((m, n + 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    fm.mx4_mm(a, b, out=buf[:, :n])
+    assert torch.equal(buf[:, :n], y) and (buf[:, n:] == 7).all()
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_mm_scales_at_their_ends(m):
     """Scale bytes over the whole range, each product within bf16's range."""
