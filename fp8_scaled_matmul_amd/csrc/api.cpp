@@ -634,6 +634,8 @@ fp8_status fp8_mx4_moe(const void* x, int64_t tokens, int64_t hidden, int64_t ld
     if (!w1 || !w2) return fail(FP8_ERR_INVALID_ARG, "moe: null weights");
     if ((st = check_mx4(w1->q, w1->ldq, w1->s, w1->ps, 2 * inner, hidden, "w1")) != FP8_OK) return st;
     if ((st = check_mx4(w2->q, w2->ldq, w2->s, w2->ps, hidden, inner, "w2")) != FP8_OK) return st;
+    if (w1->ldq >= kMoeMaxWidth * 4 || w2->ldq >= kMoeMaxWidth * 4)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "moe: rows of codes lie less than 2^26 bytes apart");
     if ((w1->eq | w1->es | w2->eq | w2->es) % 16 != 0 || w1->eq < 0 || w1->es < 0 || w2->eq < 0 || w2->es < 0)
         return fail(FP8_ERR_INVALID_ARG, "moe: experts lie multiples of 16 bytes apart");
     if (misaligned(x, 2) || misaligned(router, 2) || misaligned(y, 2) || misaligned(ids, 4) || misaligned(weights, 4))

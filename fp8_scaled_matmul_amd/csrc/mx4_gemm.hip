@@ -6,10 +6,16 @@
 // v_mfma_scale_f32_32x32x64_f8f6f4 computes exactly that sum for a 32 x 32
 // tile and 64 K: lane l holds 32 consecutive elements (16 bytes) of row l % 32
 // of each operand and the byte of its own block's scale, so the scales cost no
-// arithmetic and the products are exact before the fp32 sum.  The instruction
-// runs at twice the FP8 rate (about 10 PFLOP/s for the chip), which leaves
-// the feeding of operands from L2 as the bound of the large products.
+// arithmetic and the products are exact before the fp32 sum.  At the nominal
+// clock the instruction does about 10 PFLOP/s on the chip; on random codes,
+// fed from registers alone, 6.0 to 6.7 (power holds the clock near 1.6 GHz).
+//
+// Three kernels: 256 x 256 tiles where the output has enough of them, 128 x
+// 128 tiles, and small tiles straight from memory where outputs are few.  The
+// first two are bound by what L2 delivers to a CU, about 20 bytes a clock
+// (41 to 45 GB/s at the nominal one), which falls with the clock.
 #include <algorithm>
+#include <atomic>
 
 #include "device_common.h"
 #include "fp8mi_internal.h"
@@ -123,7 +129,8 @@ __device__ inline uint32_t store_out(const MxArgs& p, const v16f (&acc)[MF][2], 
 // WR x WC waves of MF x 2 fragments (32 MF x 64 outputs) each.  A ring of
 // STAGES K steps in LDS, filled by DMA STAGES - 1 steps ahead; one barrier a
 // step: past it every wave has read the step before, whose slot the next DMA
-// refills.  Rows of B lie permuted in each 64-row group (LDS row R holds row
+// refills.  1024 x 4096 x 4096, one tile a CU: 15.7 us; its operands alone,
+// 576 KB a CU, take 12.8 at what L2 delivers.  Rows of B lie permuted in each 64-row group (LDS row R holds row
 // 2 (R % 32) + R / 32), so that a lane ends up with two adjacent outputs of a
 // row and a half wave with 128 adjacent bytes.
 template <int WR, int WC, int MF, int STAGES>
@@ -247,6 +254,22 @@ __global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
     flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
+// A kernel's LDS limit, raised once a device.
+struct LdsLimit {
+    std::atomic<uint64_t> done{0};
+    hipError_t raise(const void* kernel, int bytes)
+    {
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return e;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+        e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
+
 template <int WR, int WC, int MF, int STAGES>
 hipError_t launch_tile(MxArgs p, hipStream_t stream)
 {
@@ -256,8 +279,8 @@ hipError_t launch_tile(MxArgs p, hipStream_t stream)
     p.tiles_n = (p.n + TN - 1) / TN;
     p.group_m = 4;
     const auto kernel = k_mx4_tile_gemm<WR, WC, MF, STAGES>;
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), kLds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(p.tiles_m * p.tiles_n), dim3(64 * WR * WC), kLds, stream, p);
     return hipGetLastError();
@@ -272,6 +295,10 @@ hipError_t launch_tile(MxArgs p, hipStream_t stream)
 // ahead, so that a tile's first stages arrive while the one before is stored.
 // Fragments are read half a stage ahead of their products, which leaves one
 // barrier a stage: in its middle, once the whole of it has been read.
+// 16384 x 8192 x 7168: 465 us, 4.1 PFLOP/s, matrix units busy 55 % of the time
+// at 1.76 GHz; zeros for operands, which take little power, 350 us: the 34 KB of
+// a stage at 44 GB/s a CU.  (One tile a workgroup: 522 us; reads and products of
+// a stage not overlapped: 587 us on random operands.)
 constexpr int kBig = 256, kBigThreads = 512;
 constexpr int kStageBytes = 2 * kBig * 64;      // A's 256 rows, then B's
 constexpr int kPanelBytes = 2 * kBig * kScaleBytes;
@@ -329,7 +356,8 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
         va[j] = (uint32_t)(R * p.lda + 16 * swz64(R, lane & 3));
         vb[j] = (uint32_t)(g * p.ldb + 16 * swz64(R, lane & 3));
     }
-    const uint32_t vs = (uint32_t)(wave < 4 ? 64 * wave + lane : 64 * (wave - 4) + 2 * (lane & 31) + (lane >> 5)) * kScaleBytes;
+    const int scale_row = wave < 4 ? 64 * wave + lane : 64 * (wave - 4) + 2 * (lane & 31) + (lane >> 5);
+    const uint32_t vs = (uint32_t)scale_row * kScaleBytes;
     const int64_t ps = wave < 4 ? p.psa : p.psb;
     BigTile f = big_tile(p, blockIdx.x);        // the tile being filled, its next stage
     int ft = 0, fslot = 0, fpanel = 0;          // ring positions of the next stage and panel
@@ -415,7 +443,8 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
 #pragma unroll
         for (int m = 0; m < 8; ++m)
             if (m >= lo && m < hi)
-                acc[m >> 1][m & 1] = mfma<2 * kk>(fa[kk][m >> 1], fb[kk][m & 1], acc[m >> 1][m & 1], ea[m >> 1], eb[m & 1]);
+                acc[m >> 1][m & 1] =
+                    mfma<2 * kk>(fa[kk][m >> 1], fb[kk][m & 1], acc[m >> 1][m & 1], ea[m >> 1], eb[m & 1]);
         __builtin_amdgcn_sched_barrier(0);
     };
     const auto clear = [&]() {
@@ -478,8 +507,8 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
                 for (int r = 0; r < 16; ++r) {
                     const uint32_t h = gemm::pack_bf16(acc[i][0][r], acc[i][1][r]);
                     track_max(mx, h);
-                    __builtin_amdgcn_raw_buffer_store_b32(h, rc, (int)(at + (uint32_t)(32 * i + 8 * (r >> 2) + (r & 3)) * (uint32_t)p.ldc * 2),
-                                                          0, 0);
+                    const uint32_t down = (uint32_t)(32 * i + 8 * (r >> 2) + (r & 3)) * (uint32_t)p.ldc * 2;
+                    __builtin_amdgcn_raw_buffer_store_b32(h, rc, (int)(at + down), 0, 0);
                 }
             stored = 0;
             if (p.ctr && (mx.x >= 0x7F80u || mx.y >= 0x7F80u)) {
@@ -508,8 +537,8 @@ hipError_t launch_big(MxArgs p, hipStream_t stream)
     p.tiles_n = (p.n + kBig - 1) / kBig;
     p.group_m = 4;
     p.pair_store = p.pair_store && p.n % 2 == 0;
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k_mx4_big_gemm),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, kBigLds);
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_mx4_big_gemm), kBigLds);
     if (e != hipSuccess) return e;
     const int grid = std::min(p.tiles_m * p.tiles_n, gemm_num_cus());
     hipLaunchKernelGGL(k_mx4_big_gemm, dim3(grid), dim3(kBigThreads), kBigLds, stream, p);
@@ -523,7 +552,8 @@ hipError_t launch_big(MxArgs p, hipStream_t stream)
 // v_mfma_scale_f32_16x16x128 (B's rows as the instruction's rows, A's as its
 // columns): no LDS but for the waves' sums at the end, which are added in
 // order.  A step is U units of 256 K; the next one is read under this one's
-// products.
+// products.  1 x 8192 x 8192: 8.5 us, 4.2 TB/s; 333 x 1000 x 1568: 7 us, which
+// is latency (a launch alone takes 2.2).
 struct Unit {
     uint4 q[2];         // K 32 (l / 16) on of either 128
 };

