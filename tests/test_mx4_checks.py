@@ -132,7 +132,7 @@ def test_binding_rejects():
     (dict(ids=None), fm.FP8_ERR_INVALID_ARG),
     (dict(weights=None), fm.FP8_ERR_INVALID_ARG),
     (dict(w1=None), fm.FP8_ERR_INVALID_ARG),
-    (dict(w1=(BAD, None, 128, 24576, 3072 * 2, 3072 * 2)), fm.FP8_ERR_INVALID_ARG),
+    (dict(w1=(BAD, None, 128, 24576, 6144, 6144)), fm.FP8_ERR_INVALID_ARG),
     (dict(w1=(BAD, BAD, 64, 24576, 6144, 6144)), fm.FP8_ERR_INVALID_ARG),
     (dict(w2=(BAD, BAD, 128, 24584, 6144, 6144)), fm.FP8_ERR_INVALID_ARG),
     (dict(w2=(BAD, BAD, 128, 24576, 6144, -16)), fm.FP8_ERR_INVALID_ARG),
