@@ -709,32 +709,53 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
     p.ldc = g.ldc;
     p.pair_store = g.ldc % 2 == 0 && (reinterpret_cast<uintptr_t>(g.c) & 3u) == 0;
     p.ctr = g.ctr;
-    // The largest tile that still leaves most of the 256 CUs a workgroup, and
-    // is not mostly past the end of A: what is read falls with the tile's
-    // size, what is idle grows.  Either side of a border, us (weights from
-    // memory, kernels back to back):
-    //   1 x 8192 x 8192      16 x 16: 10.7   16 x 32: 10.1   32 x 32: 10.8
-    //   128 x 512 x 512      16 x 16: 2.9    16 x 32: 3.2    32 x 32: 3.6
-    //   256 x 1024 x 1024    16 x 32: 6.6    32 x 32: 5.1    64 x 32: 7.1
-    //   333 x 1000 x 1568    32 x 32: 8.9    64 x 32: 7.2    64 x 64: 8.6
-    //   512 x 2048 x 2048    64 x 32: 12.3   64 x 64: 9.4    128 x 128: 12.3
-    //   1024 x 4096 x 4096   64 x 64: 41.9   128 x 128: 17.1   256 x 256: 28.9
-    //   4096 x 2048 x 7168   (128 of 256 x 256)   128 x 128: 38.5   256 x 256: 50.0
-    //   2048 x 7168 x 2048   (224 of 256 x 256)   128 x 128: 25.7   256 x 256: 23.9
-    const auto enough = [&](int64_t tm, int64_t tn) { return ((g.m + tm - 1) / tm) * ((g.n + tn - 1) / tn) >= 192; };
-    if (enough(256, 256)) return launch_big(p, stream);
-    if (g.m > 64 && enough(128, 128)) {
+    // The tile with the least to bring to the busiest CU: its rows of A and B
+    // times the tiles that fall to one CU, where a row costs the tiles that
+    // share it through LDS about 0.55 (128 x 128) and 0.65 (256 x 256) of what
+    // it costs those that read it straight.  Measured, us (weights from memory,
+    // kernels back to back), the chosen one first:
+    //   1 x 8192 x 8192      16 x 32: 10.1    16 x 16: 10.7    32 x 32: 10.8
+    //   12 x 16000 x 3000    16 x 64: 10.0    16 x 32: 12.4    64 x 64: 9.8
+    //   128 x 512 x 512      16 x 16: 2.9     16 x 32: 3.2     32 x 32: 3.6
+    //   100 x 700 x 16384    16 x 32: 15.8    16 x 16: 20.4    32 x 32: 20.3
+    //   500 x 300 x 4096     32 x 32: 7.9     16 x 32: 10.8    64 x 32: 9.9
+    //   333 x 1000 x 1568    64 x 32: 7.2     32 x 32: 8.9     64 x 64: 8.6
+    //   2000 x 300 x 1000    64 x 64: 6.7     64 x 32: 11.5    128 x 128: 7.7
+    //   1500 x 1500 x 8192   128 x 128: 26.0  64 x 64: 69.5
+    //   4096 x 2048 x 7168   128 x 128: 38.5  256 x 256: 50.0
+    //   3000 x 3000 x 512    256 x 256: 11.7  128 x 128: 13.6
+    const int64_t cus = gemm_num_cus();
+    static constexpr struct {
+        int tm, tn;
+        double row;
+    } kTiles[] = {{16, 16, 1.0}, {16, 32, 1.0},     {16, 64, 1.0},     {32, 32, 1.0},
+                  {64, 32, 1.0}, {64, 64, 1.0}, {128, 128, 0.55}, {256, 256, 0.65}};
+    int best = 0;
+    double least = 0.0;
+    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+        const int64_t tiles = ((g.m + kTiles[i].tm - 1) / kTiles[i].tm) * ((g.n + kTiles[i].tn - 1) / kTiles[i].tn);
+        const double cost = (double)((tiles + cus - 1) / cus) * (kTiles[i].tm + kTiles[i].tn) * kTiles[i].row;
+        if (i == 0 || cost < least) {
+            best = i;
+            least = cost;
+        }
+    }
+    switch (best) {
+    case 0: return launch_direct<1, 1, 4, 2>(p, stream);
+    case 1: return launch_direct<2, 1, 4, 2>(p, stream);
+    case 2: return launch_direct<4, 1, 4, 1>(p, stream);
+    case 3: return launch_direct<2, 2, 4, 2>(p, stream);
+    case 4: return launch_direct<2, 4, 4, 1>(p, stream);
+    case 5: return launch_direct<4, 4, 2, 1>(p, stream);
+    case 6: {
         // One tile a CU: three stages (108 KB of LDS); more: two, and two
         // workgroups a CU.  512 x 8192 x 4096 (256 tiles): 16.6 and 19.8 us;
         // 1100 x 4096 x 4096 (288): 28.5 and 20.3 us.
         const int64_t tiles = ((g.m + 127) / 128) * ((g.n + 127) / 128);
-        return tiles <= gemm_num_cus() ? launch_tile<4, 2, 1, 3>(p, stream) : launch_tile<4, 2, 1, 2>(p, stream);
+        return tiles <= cus ? launch_tile<4, 2, 1, 3>(p, stream) : launch_tile<4, 2, 1, 2>(p, stream);
     }
-    if (g.m > 32 && enough(64, 64)) return launch_direct<4, 4, 2, 1>(p, stream);
-    if (g.m > 32 && enough(64, 32)) return launch_direct<2, 4, 4, 1>(p, stream);
-    if (g.m > 16 && enough(32, 32)) return launch_direct<2, 2, 4, 2>(p, stream);
-    if (enough(16, 32)) return launch_direct<2, 1, 4, 2>(p, stream);
-    return launch_direct<1, 1, 4, 2>(p, stream);
+    default: return launch_big(p, stream);
+    }
 }
 
 }  // namespace fp8mi

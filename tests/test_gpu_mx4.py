@@ -231,6 +231,19 @@ def test_mm_some_tiles(m, n, k):
     assert torch.equal(buf[:, :n], y) and (buf[:, n:] == 7).all()
 
 
+@pytest.mark.parametrize("m,n,k", [(12, 16000, 300), (9, 12345, 96), (3000, 50, 800), (2000, 300, 1000), (500, 300, 1040),
+                                   (100, 700, 9000), (1500, 1500, 256), (16, 64, 33), (1300, 1300, 511)])
+def test_mm_every_shape_of_tile(m, n, k):
+    """Few rows or columns, long and short K: the tiles that such products take."""
+    a, va = _operand(m, k, 12)
+    b, vb = _operand(n, k, 13)
+    y = fm.mx4_mm(a, b)
+    _check_mm(y, va, vb)
+    buf = torch.full((m, n + 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    fm.mx4_mm(a, b, out=buf[:, :n])
+    assert torch.equal(buf[:, :n], y) and (buf[:, n:] == 7).all()
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_mm_scales_at_their_ends(m):
     """Scale bytes over the whole range, each product within bf16's range."""
