@@ -44,17 +44,17 @@ constexpr int kUnit = 256;          // K elements of a row of codes: rows are pa
 constexpr int kXPieces = 2, kAPieces = 3;
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;
 
-// A reached expert, the mask of its tokens, and where they lie among all
-// chosen (token, expert) pairs in order of the experts, then of the tokens:
-// places off, off + 1, ..
-struct MoeReached {
+// Some tokens of an expert: the first ones of the mask, which lie among all
+// chosen (token, expert) pairs, in order of the experts, then of the tokens,
+// at places off, off + 1, ..  The first layer takes an expert's tokens 16 at a
+// time (two tiles of columns, a column each piece), the second 5 (one tile).
+struct MoeGroup {
     int32_t expert, off;
     uint64_t mask;
 };
-// The second layer takes an expert's tokens 16 / 3 at a time (a column each
-// piece): the first 5 of the mask, from place off on.
+constexpr int kUpTokens = 16 / kXPieces;    // of a tile of 16 columns
+constexpr int kUpGroup = 2 * kUpTokens;
 constexpr int kDownTokens = 16 / kAPieces;
-using MoeGroup = MoeReached;
 
 // Workspace.  What workgroups of one launch hand to each other goes through
 // agent-scope atomics.
@@ -79,9 +79,9 @@ struct MoeArgs {
     double* logits;                 // [splits, tokens, experts] partial sums
     uint8_t* xq;                    // [tokens, 2, hp] pieces
     uint8_t* xs;                    // [tokens, 2, hp / 32] their scale bytes
-    int32_t* count;                 // [2] reached experts, groups of their tokens
-    MoeReached* reached;            // [min(tokens top_k, experts)], by expert
-    MoeGroup* groups;               // [max_groups()], by expert
+    int32_t* count;                 // [2] groups of the first layer, of the second
+    MoeGroup* up_groups;            // [max_groups(kUpGroup)], by expert
+    MoeGroup* groups;               // [max_groups(kDownTokens)], by expert
     float* prob;                    // [tokens top_k] the weight at each place
     uint8_t* aq;                    // [tokens top_k, 3, ip] pieces at each place
     uint8_t* as;                    // [tokens top_k, 3, ip / 32]
@@ -90,7 +90,7 @@ struct MoeArgs {
     uint32_t* arrived_rows;         // [row blocks of y] workgroups done; zero between calls
     int tiles_e, tiles_t, splits;   // router tiles of 16 x 16, K splits
     int shares;                     // workgroups that share a row block of y
-    int max_groups;                 // most groups there can be
+    int max_up_groups, max_groups;  // most groups there can be
 };
 
 template <typename T>
@@ -374,12 +374,12 @@ __device__ inline bool last_of(uint32_t* count, uint32_t all)
     return s_last;
 }
 
-// The reached experts in order, and each one's tokens in order.  ids and
+// The groups of the reached experts in order.  ids and
 // weights: of every pair.
 __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off, const int* ids,
                                     const float* weights)
 {
-    __shared__ int s_sum[kRouteWaves], s_active[kRouteWaves];
+    __shared__ uint32_t s_sum[kRouteWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     static_assert(kRouteThreads >= kMaxExperts && kRouteThreads >= kMaxTokens * kMaxTopK, "a thread each");
     mask[threadIdx.x] = 0;
@@ -389,43 +389,39 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
     if (e >= 0) atomicOr(&mask[e], 1ull << t);
     __syncthreads();
     const int n = __builtin_popcountll(mask[threadIdx.x]);
-    const uint64_t here = __ballot(n > 0);
-    const int groups = (n + kDownTokens - 1) / kDownTokens;
-    // inclusive sums over the wave, of both at once (n and its sum under 2^16)
-    const int both = n | groups << 16;
-    int sum = both;
+    const int groups = (n + kDownTokens - 1) / kDownTokens, up_groups = (n + kUpGroup - 1) / kUpGroup;
+    // inclusive sums over the wave, of all three at once: at most 1024 pairs,
+    // which makes at most 717 and 576 groups
+    const uint32_t all = (uint32_t)(n | groups << 11 | up_groups << 21);
+    uint32_t sum = all;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(sum, d, 64);
+        const uint32_t o = (uint32_t)__shfl_up((int)sum, d, 64);
         sum += lane >= d ? o : 0;
     }
-    if (lane == 63) {
-        s_sum[wave] = sum;
-        s_active[wave] = __builtin_popcountll(here);
-    }
+    if (lane == 63) s_sum[wave] = sum;
     __syncthreads();
-    sum -= both;
-    int active = 0, total = 0, all = 0;
+    sum -= all;
+    uint32_t total = 0;
     const int waves = (p.experts + 63) / 64;
     for (int i = 0; i < waves; ++i) {
-        sum += i < wave ? s_sum[i] : 0;
-        active += i < wave ? s_active[i] : 0;
-        total += s_active[i];
-        all += s_sum[i];
+        sum += i < wave ? s_sum[i] : 0u;
+        total += s_sum[i];
     }
-    const int at = sum & 0xFFFF, first = sum >> 16;
+    const int at = sum & 0x7FF, first = (sum >> 11) & 0x3FF, first_up = sum >> 21;
     off[threadIdx.x] = at;
-    if (n > 0)
-        p.reached[active + __builtin_popcountll(here & ((1ull << lane) - 1))] =
-            MoeReached{(int)threadIdx.x, at, mask[threadIdx.x]};
-    uint64_t left = mask[threadIdx.x];
-    for (int g = 0; g < groups; ++g) {
-        p.groups[first + g] = MoeGroup{(int)threadIdx.x, at + kDownTokens * g, left};
-        for (int j = 0; j < kDownTokens; ++j) left &= left - 1;
-    }
+    const auto list = [&](MoeGroup* to, int count, int size) {
+        uint64_t left = mask[threadIdx.x];
+        for (int g = 0; g < count; ++g) {
+            to[g] = MoeGroup{(int)threadIdx.x, at + size * g, left};
+            for (int j = 0; j < size; ++j) left &= left - 1;
+        }
+    };
+    list(p.up_groups + first_up, up_groups, kUpGroup);
+    list(p.groups + first, groups, kDownTokens);
     if (threadIdx.x == 0) {
-        p.count[0] = total;
-        p.count[1] = all >> 16;
+        p.count[0] = total >> 21;
+        p.count[1] = (total >> 11) & 0x3FF;
     }
     __syncthreads();
     if (e >= 0) p.prob[off[e] + __builtin_popcountll(mask[e] & ((1ull << t) - 1))] = weights[threadIdx.x];
@@ -526,18 +522,12 @@ __device__ inline T listed(const T* list, int i)
 }
 // What the lists hold, within their bounds whatever is there: a workspace
 // that was not zeroed makes wrong results, not wild reads.
-__device__ inline int reached_count(const MoeArgs& p)
-{
-    return min(max(listed(p.count, 0), 0), min(p.tokens * p.top_k, p.experts));
-}
-__device__ inline int group_count(const MoeArgs& p)
-{
-    return reached_count(p) > 0 ? min(max(listed(p.count, 1), 1), p.max_groups) : 0;
-}
-__device__ inline MoeReached reached_at(const MoeArgs& p, const MoeReached* list, int i)
+__device__ inline int up_group_count(const MoeArgs& p) { return min(max(listed(p.count, 0), 0), p.max_up_groups); }
+__device__ inline int group_count(const MoeArgs& p) { return min(max(listed(p.count, 1), 0), p.max_groups); }
+__device__ inline MoeGroup group_at(const MoeArgs& p, const MoeGroup* list, int i)
 {
     const uint32_t* words = reinterpret_cast<const uint32_t*>(list + i);
-    MoeReached r;
+    MoeGroup r;
     r.expert = min(max((int)listed(words, 0), 0), p.experts - 1);
     r.mask = ((uint64_t)listed(words, 2) | (uint64_t)listed(words, 3) << 32) & (~0ull >> (64 - p.tokens));
     r.mask = r.mask ? r.mask : 1ull;
@@ -554,10 +544,9 @@ __device__ inline int token_of(uint64_t mask, int c)
 // ------------------------------------------------------------------ up
 constexpr int kUpThreads = 256;
 constexpr int kUpWaves = kUpThreads / 64;
-constexpr int kUpTokens = 16 / kXPieces;    // of 16 columns
 
 // A workgroup takes an expert's 32 gate rows and the 32 up rows of the same
-// outputs, K over its waves, for up to 16 tokens at a time (two tiles of
+// outputs, K over its waves, for a group of up to 16 tokens (two tiles of
 // columns).  64 tokens, 128 experts of 4096 x 1024: 101 us, 5.6 TB/s; one
 // token, 8 experts of 2048 x 1408: 9.4 us for 24.5 MB.  (64 tokens: 137 us with
 // 8 waves a workgroup, 107 with 2, 109 with the next unit's weights read ahead.)
@@ -567,11 +556,11 @@ __global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = (p.inner + 31) / 32;
-    const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
-    const MoeReached at = reached_at(p, p.reached, slot);
-    if (slot >= reached_count(p)) return;
+    const int group = blockIdx.x / tiles, tile = blockIdx.x - group * tiles;
+    const MoeGroup at = group_at(p, p.up_groups, group);
+    if (group >= up_group_count(p)) return;
     const int e = at.expert, off = at.off;
-    const int n = __builtin_popcountll(at.mask);
+    const int n = min(__builtin_popcountll(at.mask), kUpGroup);
     const int c16 = lane & 15, q = lane >> 4;
 
     // gate rows; up rows lie `inner` rows on
@@ -585,93 +574,90 @@ __global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
         soff[h] = (uint32_t)(row * 16);
     }
     const int units = (p.hidden + kUnit - 1) / kUnit;
-    for (int c0 = 0; c0 < n; c0 += 2 * kUpTokens) {
-        const int cols = kXPieces * (n - c0);
-        const bool two = cols > 16;
-        uint32_t xrow[2];
+    const int cols = kXPieces * n;
+    const bool two = cols > 16;
+    uint32_t xrow[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int col = min(16 * h + c16, cols - 1);
-            xrow[h] = (uint32_t)(token_of(at.mask, c0 + col / kXPieces) * kXPieces + col % kXPieces);
+    for (int h = 0; h < 2; ++h) {
+        const int col = min(16 * h + c16, cols - 1);
+        xrow[h] = (uint32_t)(token_of(at.mask, col / kXPieces) * kXPieces + col % kXPieces);
+    }
+    // token r of tile h (r = lane / 8), of whose column tile this wave ends with
+    const int c = wave * kUpTokens + (lane >> 3);
+    const float prob = p.prob[off + min(c, n - 1)];
+    v4f acc[2][4] = {};
+    for (int u = wave; u < units; u += kUpWaves) {
+        UnitW w[4];
+        uint2 sw[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t far = (r >> 1) * (int64_t)p.inner;
+            sw[r] = load_at<uint2>(ws + far * 16 + (u >> 1) * p.ps1 + 8 * (u & 1), soff[r & 1]);
+            load_w(w[r], wq + far * p.ldq1 + u * 128, woff[r & 1]);
         }
-        // token r of tile h (r = lane / 8), of whose column tile this wave ends with
-        const int c = c0 + wave * kUpTokens + (lane >> 3);
-        const float prob = p.prob[off + min(c, n - 1)];
-        v4f acc[2][4] = {};
-        for (int u = wave; u < units; u += kUpWaves) {
-            UnitW w[4];
-            uint2 sw[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int64_t far = (r >> 1) * (int64_t)p.inner;
-                sw[r] = load_at<uint2>(ws + far * 16 + (u >> 1) * p.ps1 + 8 * (u & 1), soff[r & 1]);
-                load_w(w[r], wq + far * p.ldq1 + u * 128, woff[r & 1]);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (h == 0 || two) {
-                    UnitX x;
-                    const uint2 sx = load_at<uint2>(p.xs + 8 * u, xrow[h] * (uint32_t)(p.hp / 32));
-                    load_x(x, p.xq + u * kUnit, xrow[h] * (uint32_t)p.hp + 16 * q);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) unit_mma(acc[h][r], w[r], x, sw[r], sx);
-                }
-        }
-        if (c0 > 0) __syncthreads();
-        // the pieces of a token are neighbours
-        static_assert(kXPieces == 2, "one exchange");
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (h == 0 || two)
+            if (h == 0 || two) {
+                UnitX x;
+                const uint2 sx = load_at<uint2>(p.xs + 8 * u, xrow[h] * (uint32_t)(p.hp / 32));
+                load_x(x, p.xq + u * kUnit, xrow[h] * (uint32_t)p.hp + 16 * q);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    v4f s;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] = acc[h][r][i] + dpp_f<kDppXor1>(acc[h][r][i]);
-                    if ((c16 & 1) == 0) red[h][wave][r][8 * q + (c16 >> 1)] = s;
-                }
-        __syncthreads();
-        // wave h: the tokens of tile h; lane: token lane / 8 of it, 16 r +
-        // 4 qq + i of the 32 outputs
-        if (wave > 1 || c0 + wave * kUpTokens >= n) continue;
-        const int r = (lane >> 2) & 1, qq = lane & 3;
-        v4f g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < kUpWaves; ++w) {
-            g += red[wave][w][r][8 * qq + (lane >> 3)];
-            u += red[wave][w][r + 2][8 * qq + (lane >> 3)];
-        }
-        float a[4];
-        uint32_t amax = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float v = prob * (g[i] / (1.0f + expf(-g[i])) * u[i]);
-            a[i] = 32 * tile + 16 * r + 4 * qq + i < p.inner ? v : 0.0f;
-            amax = max(amax, __builtin_bit_cast(uint32_t, a[i]) & 0x7FFFFFFFu);
-        }
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d, 64));
-        const bool finite = amax < 0x7F800000u;
-        const uint32_t b = finite ? piece_byte(amax) : 255u;
-        uint32_t o[kAPieces];
-        to_pieces<kAPieces>(a, inv_scale(finite ? b : 127u), o);
-        if (c >= n) continue;
-        uint8_t* aq = p.aq + (int64_t)(off + c) * kAPieces * p.ip;
-        uint8_t* as = p.as + (int64_t)(off + c) * kAPieces * (p.ip / 32);
-#pragma unroll
-        for (int i = 0; i < kAPieces; ++i) {
-            *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + 32 * tile + 16 * r + 4 * qq) = finite ? o[i] : 0u;
-            if ((lane & 7) == 0) as[i * (p.ip / 32) + tile] = (uint8_t)(finite ? b - 4 * i : 255u);
-        }
-        // zeros to the end of the last panel
-        if (tile == tiles - 1)
-            for (int z = 32 * tiles; z < p.ip; z += 32)
-#pragma unroll
-                for (int i = 0; i < kAPieces; ++i) {
-                    *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + z + 4 * (lane & 7)) = 0u;
-                    if ((lane & 7) == 0) as[i * (p.ip / 32) + z / 32] = 127;
-                }
+                for (int r = 0; r < 4; ++r) unit_mma(acc[h][r], w[r], x, sw[r], sx);
+            }
     }
+    // the pieces of a token are neighbours
+    static_assert(kXPieces == 2, "one exchange");
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (h == 0 || two)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                v4f s;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = acc[h][r][i] + dpp_f<kDppXor1>(acc[h][r][i]);
+                if ((c16 & 1) == 0) red[h][wave][r][8 * q + (c16 >> 1)] = s;
+            }
+    __syncthreads();
+    // wave h: the tokens of tile h; lane: token lane / 8 of it, 16 r +
+    // 4 qq + i of the 32 outputs
+    if (wave > 1 || wave * kUpTokens >= n) return;
+    const int r = (lane >> 2) & 1, qq = lane & 3;
+    v4f g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kUpWaves; ++w) {
+        g += red[wave][w][r][8 * qq + (lane >> 3)];
+        u += red[wave][w][r + 2][8 * qq + (lane >> 3)];
+    }
+    float a[4];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float v = prob * (g[i] / (1.0f + expf(-g[i])) * u[i]);
+        a[i] = 32 * tile + 16 * r + 4 * qq + i < p.inner ? v : 0.0f;
+        amax = max(amax, __builtin_bit_cast(uint32_t, a[i]) & 0x7FFFFFFFu);
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d, 64));
+    const bool finite = amax < 0x7F800000u;
+    const uint32_t b = finite ? piece_byte(amax) : 255u;
+    uint32_t o[kAPieces];
+    to_pieces<kAPieces>(a, inv_scale(finite ? b : 127u), o);
+    if (c >= n) return;
+    uint8_t* aq = p.aq + (int64_t)(off + c) * kAPieces * p.ip;
+    uint8_t* as = p.as + (int64_t)(off + c) * kAPieces * (p.ip / 32);
+#pragma unroll
+    for (int i = 0; i < kAPieces; ++i) {
+        *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + 32 * tile + 16 * r + 4 * qq) = finite ? o[i] : 0u;
+        if ((lane & 7) == 0) as[i * (p.ip / 32) + tile] = (uint8_t)(finite ? b - 4 * i : 255u);
+    }
+    // zeros to the end of the last panel
+    if (tile == tiles - 1)
+        for (int z = 32 * tiles; z < p.ip; z += 32)
+#pragma unroll
+            for (int i = 0; i < kAPieces; ++i) {
+                *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + z + 4 * (lane & 7)) = 0u;
+                if ((lane & 7) == 0) as[i * (p.ip / 32) + z / 32] = 127;
+            }
 }
 
 // ------------------------------------------------------------------ down
@@ -717,14 +703,14 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
         uint64_t mask;
     };
     struct Entry {
-        MoeReached r;
+        MoeGroup r;
         int panel;
     };
     // what the list holds for step i, then what it means
     const auto entry = [&](int i) {
         i = min(i, steps - 1);
         const int g = i / panels;
-        return Entry{reached_at(p, p.groups, g), i - g * panels};
+        return Entry{group_at(p, p.groups, g), i - g * panels};
     };
     const auto at_step = [&](const Entry& x) {
         At a;
@@ -885,8 +871,8 @@ int route_splits(int64_t tokens, int64_t experts, int64_t hidden)
 }
 
 struct MoeLayout {
-    size_t arrived_rows, zeroed, logits, xq, xs, count, reached, groups, prob, aq, as, part, total;
-    int64_t max_groups;
+    size_t arrived_rows, logits, xq, xs, count, up_groups, groups, prob, aq, as, part, total;
+    int64_t max_up_groups, max_groups;
 };
 MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner)
 {
@@ -900,14 +886,15 @@ MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hid
         return (size_t)o;
     };
     m.arrived_rows = take((hidden + kDownRows - 1) / kDownRows * 4);
-    m.zeroed = (size_t)at;
     m.logits = take(route_splits(tokens, experts, hidden) * tokens * experts * 8);
     m.xq = take(tokens * kXPieces * hp);
     m.xs = take(tokens * kXPieces * (hp / 32));
-    m.count = take(4);
-    m.reached = take(std::min(pairs, experts) * (int64_t)sizeof(MoeReached));
+    m.count = take(8);
     // an expert's last group may be short
-    m.max_groups = std::min(pairs, std::min(pairs, experts) + pairs / kDownTokens);
+    const auto most = [&](int64_t size) { return std::min(pairs, std::min(pairs, experts) + pairs / size); };
+    m.max_up_groups = most(kUpGroup);
+    m.max_groups = most(kDownTokens);
+    m.up_groups = take(m.max_up_groups * (int64_t)sizeof(MoeGroup));
     m.groups = take(m.max_groups * (int64_t)sizeof(MoeGroup));
     m.prob = take(pairs * 4);
     m.aq = take(pairs * kAPieces * ip);
@@ -963,7 +950,8 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     p.xq = ws + m.xq;
     p.xs = ws + m.xs;
     p.count = reinterpret_cast<int32_t*>(ws + m.count);
-    p.reached = reinterpret_cast<MoeReached*>(ws + m.reached);
+    p.up_groups = reinterpret_cast<MoeGroup*>(ws + m.up_groups);
+    p.max_up_groups = (int)m.max_up_groups;
     p.groups = reinterpret_cast<MoeGroup*>(ws + m.groups);
     p.max_groups = (int)m.max_groups;
     p.prob = reinterpret_cast<float*>(ws + m.prob);
@@ -987,8 +975,7 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
         hipLaunchKernelGGL((k_moe_route<false>), dim3(route), dim3(kRouteThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int slots = std::min(p.tokens * p.top_k, p.experts);
-    hipLaunchKernelGGL(k_moe_up, dim3(slots * ((p.inner + 31) / 32)), dim3(kUpThreads), 0, stream, p);
+    hipLaunchKernelGGL(k_moe_up, dim3(p.max_up_groups * ((p.inner + 31) / 32)), dim3(kUpThreads), 0, stream, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const int lds = kDownWaves * p.tokens * kDownRows * 4;
     const int blocks = (p.hidden + kDownRows - 1) / kDownRows;
