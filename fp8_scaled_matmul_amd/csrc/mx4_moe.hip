@@ -189,32 +189,30 @@ constexpr int kMaxSplits = 8;
 constexpr int kChunk = 32;          // K of 8 fp64 matrix instructions
 constexpr int kRouteDepth = 2;      // chunks read at a time
 
-// Eight elements of a row from column c on, zeros past the end.
-template <bool VEC>
-__device__ inline uint4 row8(const uint16_t* row, int c, int cols)
+// Eight elements of a row from column c on, zeros past the end: 16 bytes
+// wherever an element may lie.  `whole` (uniform): no lane's are past the end.
+typedef uint32_t u4x2 __attribute__((ext_vector_type(4), aligned(2)));
+__device__ inline uint4 row8(const uint16_t* row, int c, int cols, bool whole)
 {
-    uint4 v = uint4{0, 0, 0, 0};
-    if constexpr (VEC) {
-        if (c < cols) v = *reinterpret_cast<const uint4*>(row + c);
-    } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (c + j < cols) w[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
-        v = uint4{w[0], w[1], w[2], w[3]};
+    if (whole || c + 8 <= cols) {
+        const u4x2 v = *reinterpret_cast<const u4x2*>(row + c);
+        return uint4{v.x, v.y, v.z, v.w};
     }
-    return v;
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+        if (c + j < cols) w[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+    return uint4{w[0], w[1], w[2], w[3]};
 }
 
 // One wave: 512 columns of a token to pieces.
-template <bool VEC>
 __device__ inline void cut_x(const MoeArgs& p, int item)
 {
     const int lane = threadIdx.x & 63;
     const int panels = (p.hp + mx4::kPanel - 1) / mx4::kPanel;
     const int t = item / panels, c = (item - t * panels) * mx4::kPanel + 8 * lane;
     if (t >= p.tokens || c >= p.hp) return;
-    const uint4 v = row8<VEC>(p.x + t * p.ldx, c, p.hidden);
+    const uint4 v = row8(p.x + t * p.ldx, c, p.hidden, c - 8 * lane + mx4::kPanel <= p.hidden);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t amax = 0;
 #pragma unroll
@@ -376,7 +374,7 @@ __device__ inline bool last_of(uint32_t* count, uint32_t all)
 
 // The groups of the reached experts in order.  ids and
 // weights: of every pair.
-__device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, int* off, const int* ids,
+__device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, uint32_t* off, const int* ids,
                                     const float* weights)
 {
     __shared__ uint32_t s_sum[kRouteWaves];
@@ -408,23 +406,22 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
         sum += i < wave ? s_sum[i] : 0u;
         total += s_sum[i];
     }
-    const int at = sum & 0x7FF, first = (sum >> 11) & 0x3FF, first_up = sum >> 21;
-    off[threadIdx.x] = at;
-    const auto list = [&](MoeGroup* to, int count, int size) {
-        uint64_t left = mask[threadIdx.x];
-        for (int g = 0; g < count; ++g) {
-            to[g] = MoeGroup{(int)threadIdx.x, at + size * g, left};
-            for (int j = 0; j < size; ++j) left &= left - 1;
-        }
-    };
-    list(p.up_groups + first_up, up_groups, kUpGroup);
-    list(p.groups + first, groups, kDownTokens);
+    off[threadIdx.x] = sum;
     if (threadIdx.x == 0) {
         p.count[0] = total >> 21;
         p.count[1] = (total >> 11) & 0x3FF;
     }
     __syncthreads();
-    if (e >= 0) p.prob[off[e] + __builtin_popcountll(mask[e] & ((1ull << t) - 1))] = weights[threadIdx.x];
+    if (e < 0) return;
+    // each pair to its place; those that begin a group write it
+    const uint64_t before = mask[e] & ((1ull << t) - 1);
+    const int nth = __builtin_popcountll(before);
+    const uint32_t sums = off[e];
+    const int at = (int)(sums & 0x7FF) + nth;
+    p.prob[at] = weights[threadIdx.x];
+    const MoeGroup group{e, at, mask[e] ^ before};
+    if (nth % kDownTokens == 0) p.groups[((sums >> 11) & 0x3FF) + nth / kDownTokens] = group;
+    if (nth % kUpGroup == 0) p.up_groups[(sums >> 21) + nth / kUpGroup] = group;
 }
 
 // Workgroups below tiles_e tiles_t splits take 16 tokens x 16 experts of the
@@ -434,20 +431,19 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
 // the chosen experts do not hang on the order of a sum.  One token, 64 experts
 // of 2048: 7.6 us, of which the logits 3.7, their way to one workgroup 0.6, the
 // selection 2.0 and the lists 1.3; 64 tokens, 128 experts of 4096: 14 us.
-template <bool VEC>
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
 {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nroute = p.tiles_e * p.tiles_t * p.splits;
     if ((int)blockIdx.x >= nroute) {
-        cut_x<VEC>(p, ((int)blockIdx.x - nroute) * kRouteWaves + wave);
+        cut_x(p, ((int)blockIdx.x - nroute) * kRouteWaves + wave);
         return;
     }
     __shared__ __attribute__((aligned(16))) double red[kRouteWaves][256];
     __shared__ int s_ids[kMaxTokens * kMaxTopK];
     __shared__ float s_weights[kMaxTokens * kMaxTopK];
-    static_assert(sizeof(red) >= kRouteThreads * (sizeof(uint64_t) + sizeof(int)), "the lists' masks and places");
+    static_assert(sizeof(red) >= kRouteThreads * (sizeof(uint64_t) + sizeof(uint32_t)), "the lists' masks and places");
     const int tt = blockIdx.x / (p.tiles_e * p.splits), rest = blockIdx.x - tt * p.tiles_e * p.splits;
     const int split = rest / p.tiles_e, te = rest - split * p.tiles_e;
     const int t = min(16 * tt + (lane & 15), p.tokens - 1), e = min(16 * te + (lane & 15), p.experts - 1);
@@ -460,9 +456,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
         uint4 a[kRouteDepth], b[kRouteDepth];
 #pragma unroll
         for (int d = 0; d < kRouteDepth; ++d) {
-            const int c = kChunk * (c0 + d * stride) + 8 * (lane >> 4);
-            a[d] = row8<VEC>(rr, c, p.hidden);
-            b[d] = row8<VEC>(xr, c, p.hidden);
+            const int from = kChunk * (c0 + d * stride), c = from + 8 * (lane >> 4);
+            const bool whole = from + kChunk <= p.hidden;
+            a[d] = row8(rr, c, p.hidden, whole);
+            b[d] = row8(xr, c, p.hidden, whole);
         }
 #pragma unroll
         for (int d = 0; d < kRouteDepth; ++d) {
@@ -510,7 +507,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
     }
     __syncthreads();
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(&red[0][0]);
-    list_reached(p, mask, reinterpret_cast<int*>(mask + kRouteThreads), s_ids, s_weights);
+    list_reached(p, mask, reinterpret_cast<uint32_t*>(mask + kRouteThreads), s_ids, s_weights);
 }
 
 // Lists that an earlier launch wrote, at uniform places: read through the
@@ -965,14 +962,9 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     p.tiles_t = (p.tokens + 15) / 16;
     p.splits = route_splits(g.tokens, g.experts, g.hidden);
 
-    const auto al16 = [](const void* v) { return (reinterpret_cast<uintptr_t>(v) & 15u) == 0; };
-    const bool vec = p.hidden % 8 == 0 && p.ldx % 8 == 0 && p.ldr % 8 == 0 && al16(g.x) && al16(g.router);
     const int items = p.tokens * ((p.hp + mx4::kPanel - 1) / mx4::kPanel);
     const int route = p.tiles_e * p.tiles_t * p.splits + (items + kRouteWaves - 1) / kRouteWaves;
-    if (vec)
-        hipLaunchKernelGGL((k_moe_route<true>), dim3(route), dim3(kRouteThreads), 0, stream, p);
-    else
-        hipLaunchKernelGGL((k_moe_route<false>), dim3(route), dim3(kRouteThreads), 0, stream, p);
+    hipLaunchKernelGGL(k_moe_route, dim3(route), dim3(kRouteThreads), 0, stream, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_moe_up, dim3(p.max_up_groups * ((p.inner + 31) / 32)), dim3(kUpThreads), 0, stream, p);
