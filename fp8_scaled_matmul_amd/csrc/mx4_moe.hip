@@ -407,21 +407,26 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
         total += s_sum[i];
     }
     off[threadIdx.x] = sum;
+    // sums: of expert e; left: its tokens from the nth on
+    const auto list = [&](uint32_t sums, int e, int nth, uint64_t left) {
+        const MoeGroup group{e, (int)(sums & 0x7FF) + nth, left};
+        if (nth % kDownTokens == 0) p.groups[((sums >> 11) & 0x3FF) + nth / kDownTokens] = group;
+        if (nth % kUpGroup == 0) p.up_groups[(sums >> 21) + nth / kUpGroup] = group;
+    };
+    if (n) list(sum, threadIdx.x, 0, mask[threadIdx.x]);
     if (threadIdx.x == 0) {
         p.count[0] = total >> 21;
         p.count[1] = (total >> 11) & 0x3FF;
     }
     __syncthreads();
     if (e < 0) return;
-    // each pair to its place; those that begin a group write it
+    // each pair to its place; those that begin a further group write it (the
+    // first ones are on their way before the wait: 0.5 us of one token's 26)
     const uint64_t before = mask[e] & ((1ull << t) - 1);
     const int nth = __builtin_popcountll(before);
     const uint32_t sums = off[e];
-    const int at = (int)(sums & 0x7FF) + nth;
-    p.prob[at] = weights[threadIdx.x];
-    const MoeGroup group{e, at, mask[e] ^ before};
-    if (nth % kDownTokens == 0) p.groups[((sums >> 11) & 0x3FF) + nth / kDownTokens] = group;
-    if (nth % kUpGroup == 0) p.up_groups[(sums >> 21) + nth / kUpGroup] = group;
+    p.prob[(sums & 0x7FF) + nth] = weights[threadIdx.x];
+    if (nth) list(sums, e, nth, mask[e] ^ before);
 }
 
 // Workgroups below tiles_e tiles_t splits take 16 tokens x 16 experts of the
