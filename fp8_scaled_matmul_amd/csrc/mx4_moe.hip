@@ -189,20 +189,31 @@ constexpr int kMaxSplits = 8;
 constexpr int kChunk = 32;          // K of 8 fp64 matrix instructions
 constexpr int kRouteDepth = 2;      // chunks read at a time
 
-// Eight elements of a row from column c on, zeros past the end: 16 bytes
-// wherever an element may lie.  `whole` (uniform): no lane's are past the end.
+// Eight elements of a row from column c on (a multiple of 8), in two steps, so
+// that several reads are on their way at once: read8 takes 16 bytes, wherever
+// an element may lie, and where the row ends before c + 8 its last eight;
+// trim8 moves those to their places, zeros past the end.
 typedef uint32_t u4x2 __attribute__((ext_vector_type(4), aligned(2)));
-__device__ inline uint4 row8(const uint16_t* row, int c, int cols, bool whole)
+__device__ inline uint4 read8(const uint16_t* row, int c, int cols)
 {
-    if (whole || c + 8 <= cols) {
-        const u4x2 v = *reinterpret_cast<const u4x2*>(row + c);
+    if (cols >= 8) {
+        const u4x2 v = *reinterpret_cast<const u4x2*>(row + min(c, cols - 8));
         return uint4{v.x, v.y, v.z, v.w};
     }
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 7; ++j)
-        if (c + j < cols) w[j >> 1] |= (uint32_t)row[c + j] << (16 * (j & 1));
+        if (j < cols) w[j >> 1] |= (uint32_t)row[j] << (16 * (j & 1));
     return uint4{w[0], w[1], w[2], w[3]};
+}
+__device__ inline uint4 trim8(uint4 v, int c, int cols)
+{
+    const int past = c - min(c, max(cols - 8, 0));
+    if (past & 1)
+        v = uint4{v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16};
+    if (past & 2) v = uint4{v.y, v.z, v.w, 0};
+    if (past & 4) v = uint4{v.z, v.w, 0, 0};
+    return past >= 8 ? uint4{0, 0, 0, 0} : v;
 }
 
 // One wave: 512 columns of a token to pieces.
@@ -212,7 +223,7 @@ __device__ inline void cut_x(const MoeArgs& p, int item)
     const int panels = (p.hp + mx4::kPanel - 1) / mx4::kPanel;
     const int t = item / panels, c = (item - t * panels) * mx4::kPanel + 8 * lane;
     if (t >= p.tokens || c >= p.hp) return;
-    const uint4 v = row8(p.x + t * p.ldx, c, p.hidden, c - 8 * lane + mx4::kPanel <= p.hidden);
+    const uint4 v = trim8(read8(p.x + t * p.ldx, c, p.hidden), c, p.hidden);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t amax = 0;
 #pragma unroll
@@ -462,13 +473,18 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
 #pragma unroll
         for (int d = 0; d < kRouteDepth; ++d) {
             const int from = kChunk * (c0 + d * stride), c = from + 8 * (lane >> 4);
-            const bool whole = from + kChunk <= p.hidden;
-            a[d] = row8(rr, c, p.hidden, whole);
-            b[d] = row8(xr, c, p.hidden, whole);
+            if (from >= p.hidden) break;
+            a[d] = read8(rr, c, p.hidden);
+            b[d] = read8(xr, c, p.hidden);
         }
 #pragma unroll
         for (int d = 0; d < kRouteDepth; ++d) {
-            if (c0 + d * stride >= chunks) break;
+            const int from = kChunk * (c0 + d * stride);
+            if (from >= p.hidden) break;
+            if (from + kChunk > p.hidden) {
+                a[d] = trim8(a[d], from + 8 * (lane >> 4), p.hidden);
+                b[d] = trim8(b[d], from + 8 * (lane >> 4), p.hidden);
+            }
             const uint32_t aw[4] = {a[d].x, a[d].y, a[d].z, a[d].w}, bw[4] = {b[d].x, b[d].y, b[d].z, b[d].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
