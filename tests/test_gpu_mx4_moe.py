@@ -89,6 +89,18 @@ def test_moe(t, e, k, h, i, renormalize):
     m.check(x, m.moe(x.cuda()))
 
 
+@pytest.mark.parametrize("h", [2, 7, 9, 11, 39, 46, 61, 516, 525, 1031])
+def test_moe_row_ends(h):
+    """Rows of x and router that end anywhere in a read of eight, and rows
+    shorter than one, their elements after other rows' (NaN there)."""
+    m = Layer(20, 18, 3, h, 40, True)
+    x = m.x(20, h)
+    m.check(x, m.moe(x.cuda()))
+    wide = torch.full((20, h + 3), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 1:-2] = x.cuda()
+    m.check(x, m.moe(wide[:, 1:-2]))
+
+
 def test_moe_every_token_to_one_expert():
     """64 tokens reach the same experts: four columns tiles of 16, and the
     other experts none."""
