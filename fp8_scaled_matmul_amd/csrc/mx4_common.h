@@ -11,6 +11,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fp8mi.h"
 
 namespace fp8mi {
@@ -98,6 +100,22 @@ __device__ inline uint32_t cast8_sr(const float x[8], const uint32_t se[4], cons
     };
     return (join(a) & 0x0F0F0F0Fu) | (join(b) & 0xF0F0F0F0u);
 }
+
+// A kernel's LDS limit, raised once a device.
+struct LdsLimit {
+    std::atomic<uint64_t> done{0};
+    hipError_t raise(const void* kernel, int bytes)
+    {
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return e;
+        const uint64_t bit = 1ull << (dev & 63);
+        if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+        e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
 
 }  // namespace mx4
 }  // namespace fp8mi

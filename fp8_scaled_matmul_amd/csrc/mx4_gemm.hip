@@ -15,7 +15,6 @@
 // first two are bound by what L2 delivers to a CU, about 20 bytes a clock
 // (41 to 45 GB/s at the nominal one), which falls with the clock.
 #include <algorithm>
-#include <atomic>
 
 #include "device_common.h"
 #include "fp8mi_internal.h"
@@ -254,22 +253,6 @@ __global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
     flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
-// A kernel's LDS limit, raised once a device.
-struct LdsLimit {
-    std::atomic<uint64_t> done{0};
-    hipError_t raise(const void* kernel, int bytes)
-    {
-        int dev = 0;
-        hipError_t e = hipGetDevice(&dev);
-        if (e != hipSuccess) return e;
-        const uint64_t bit = 1ull << (dev & 63);
-        if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-        e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-        return e;
-    }
-};
-
 template <int WR, int WC, int MF, int STAGES>
 hipError_t launch_tile(MxArgs p, hipStream_t stream)
 {
@@ -279,7 +262,7 @@ hipError_t launch_tile(MxArgs p, hipStream_t stream)
     p.tiles_n = (p.n + TN - 1) / TN;
     p.group_m = 4;
     const auto kernel = k_mx4_tile_gemm<WR, WC, MF, STAGES>;
-    static LdsLimit limit;
+    static mx4::LdsLimit limit;
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), kLds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(kernel, dim3(p.tiles_m * p.tiles_n), dim3(64 * WR * WC), kLds, stream, p);
@@ -537,7 +520,7 @@ hipError_t launch_big(MxArgs p, hipStream_t stream)
     p.tiles_n = (p.n + kBig - 1) / kBig;
     p.group_m = 4;
     p.pair_store = p.pair_store && p.n % 2 == 0;
-    static LdsLimit limit;
+    static mx4::LdsLimit limit;
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(k_mx4_big_gemm), kBigLds);
     if (e != hipSuccess) return e;
     const int grid = std::min(p.tiles_m * p.tiles_n, gemm_num_cus());

@@ -9,19 +9,20 @@
 //   y[t]     = sum over e in E(t) of W2[e] a[t, e]
 //
 // What bounds it is the read of the chosen experts' codes, half a byte a
-// weight, each read once; so the weights go from memory to the registers of
-// v_mfma_scale_f32_16x16x128_f8f6f4 as they lie (16 rows of weights by 16
-// columns of activations), with no decoding.  The activations are the
-// instruction's E4M3 operand: a block of 32 values is the sum of pieces, each
-// E4M3 (4 bits) with a power of two scale of its own, every next piece's 2^-4
-// of the one before and holding what the last left.  Two pieces hold a bf16 x
-// exactly, but for elements under 2^-13 of their block's largest, which are
-// off by at most 2^-21 of that; three hold the fp32 intermediate a to 2^-14
-// of itself (or 2^-25 of the block's largest), far under the output's own
-// rounding.  A column is one piece of one token, so that the few tokens of an
-// expert share the 16 columns with their pieces; the columns of a token are
-// added at the end.  Sums are fp32, in an order that only the sizes and the
-// chosen experts set: no atomics on values.
+// weight, each read once; so the weights go from memory to registers as they
+// lie and are decoded there, two to an instruction, to bf16, which holds code
+// times scale exactly.  The products are v_mfma_f32_16x16x32_bf16's: 16 rows
+// of weights by 16 columns of activations, exact products, fp32 sums.  A
+// column of the first layer is a token's x as it is.  The second layer's
+// activations are fp32 numbers, each the exact sum of three bf16 pieces of 8
+// bits; a column there is one piece of one token, and the columns of a token
+// are added at the end.  (E4M3 pieces and undecoded weights through
+// v_mfma_scale_f32_16x16x128_f8f6f4 take no decoding, but that instruction adds
+// the products of neighbouring elements aligned to the largest of them
+// and drops what lies 2^-13 below it: measured, errors of 2^-18 of the summed
+// sizes for normal data and 2^-13 at worst, against 2^-22 with bf16 operands.)
+// Sums are in an order that only the sizes and the chosen experts set: no
+// atomics on values.
 //
 // Three launches: the router, which also lists the reached experts and their
 // tokens; up; down.
@@ -37,24 +38,23 @@ namespace fp8mi {
 namespace {
 
 using gemm::v4f;
-using gemm::v8i;
 typedef double v4d __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kUnit = 256;          // K elements of a row of codes: rows are padded to whole units
-constexpr int kXPieces = 2, kAPieces = 3;
+constexpr int kPieces = 3;          // bf16 numbers that add up to an fp32 one
 constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;
 
 // Some tokens of an expert: the first ones of the mask, which lie among all
 // chosen (token, expert) pairs, in order of the experts, then of the tokens,
 // at places off, off + 1, ..  The first layer takes an expert's tokens 16 at a
-// time (two tiles of columns, a column each piece), the second 5 (one tile).
+// time, the second 5 (a column each piece).
 struct MoeGroup {
     int32_t expert, off;
     uint64_t mask;
 };
-constexpr int kUpTokens = 16 / kXPieces;    // of a tile of 16 columns
-constexpr int kUpGroup = 2 * kUpTokens;
-constexpr int kDownTokens = 16 / kAPieces;
+constexpr int kUpTokens = 16;
+constexpr int kDownTokens = 16 / kPieces;
 
 // Workspace.  What workgroups of one launch hand to each other goes through
 // agent-scope atomics.
@@ -77,14 +77,12 @@ struct MoeArgs {
     float* weights;
     uint32_t* arrived;              // [5] router workgroups done: of each 16 tokens, and token tiles; zero between calls
     double* logits;                 // [splits, tokens, experts] partial sums
-    uint8_t* xq;                    // [tokens, 2, hp] pieces
-    uint8_t* xs;                    // [tokens, 2, hp / 32] their scale bytes
+    uint16_t* xq;                   // [tokens, hp] x in the order of place_of, zeros past hidden
     int32_t* count;                 // [2] groups of the first layer, of the second
-    MoeGroup* up_groups;            // [max_groups(kUpGroup)], by expert
+    MoeGroup* up_groups;            // [max_groups(kUpTokens)], by expert
     MoeGroup* groups;               // [max_groups(kDownTokens)], by expert
     float* prob;                    // [tokens top_k] the weight at each place
-    uint8_t* aq;                    // [tokens top_k, 3, ip] pieces at each place
-    uint8_t* as;                    // [tokens top_k, 3, ip / 32]
+    uint16_t* aq;                   // [tokens top_k, 3, ip] pieces at each place, in the order of place_of
     fp8_counters* ctr;
     float* part;                    // [shares, tokens, hidden] partial sums of y
     uint32_t* arrived_rows;         // [row blocks of y] workgroups done; zero between calls
@@ -98,50 +96,21 @@ __device__ inline void agent_store(T* p, T v) { __hip_atomic_store(p, v, __ATOMI
 template <typename T>
 __device__ inline T agent_load(const T* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 
-// ------------------------------------------------------------------ pieces
-// E8M0 byte of the first piece's scale of a block with that amax: v / s in
-// [128, 256).  At least 2^-119, so that the third piece's byte is a number.
-__device__ inline uint32_t piece_byte(uint32_t amax_bits)
-{
-    return (uint32_t)max((int)(amax_bits >> 23) - 7, 8);
-}
-
-// Four values to a word of E4M3 codes for each piece; inv = 1 / s.
-template <int P>
-__device__ inline void to_pieces(const float x[4], float inv, uint32_t out[P])
-{
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = x[i] * inv;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
-        out[p] = (uint32_t)w;
-        if (p + 1 < P) {
-            // what is left is exact: both terms are multiples of the code's last place
-            v[0] = 16.0f * (v[0] - __builtin_amdgcn_cvt_f32_fp8(w, 0));
-            v[1] = 16.0f * (v[1] - __builtin_amdgcn_cvt_f32_fp8(w, 1));
-            v[2] = 16.0f * (v[2] - __builtin_amdgcn_cvt_f32_fp8(w, 2));
-            v[3] = 16.0f * (v[3] - __builtin_amdgcn_cvt_f32_fp8(w, 3));
-        }
-    }
-}
-
-// The reciprocal of the scale of byte b, 8 <= b <= 247.
-__device__ inline float inv_scale(uint32_t b) { return __builtin_bit_cast(float, (254u - b) << 23); }
-
 // ------------------------------------------------------------------ matrix instruction
 // One unit (256 K) of a lane's row of weights, and of its column.  16 rows x
-// 16 columns x 128 K an instruction: lane l holds 32 weights of row l % 16, K
-// 32 (l / 16) on; of column l % 16 the codes of K 16 (l / 16) on and of K 64 +
-// 16 (l / 16) on; and both scale bytes of K block l / 16.
+// 16 columns x 128 K in four instructions: lane l holds 32 weights of row
+// l % 16, K 32 (l / 16) on, one scale block, 8 of them an instruction, and the
+// same K of column l % 16.  The columns' memory has each 128 elements in the
+// order in which the instructions take them.
 struct UnitW {
     uint4 q[2];
 };
 struct UnitX {
-    uint4 q[2][2];
+    uint4 q[2][4];
 };
+// Where element k of a column lies; eight from a multiple of eight on stay together.
+__device__ inline int place_of(int k) { return (k & ~127) | (k & 24) << 2 | (k & 96) >> 2 | (k & 7); }
+
 template <typename T>
 __device__ inline T load_at(const uint8_t* base, uint32_t off)
 {
@@ -153,24 +122,35 @@ __device__ inline void load_w(UnitW& o, const uint8_t* base, uint32_t off)
     o.q[0] = load_at<uint4>(base, off);
     o.q[1] = load_at<uint4>(base + 64, off);
 }
-__device__ inline void load_x(UnitX& o, const uint8_t* base, uint32_t off)
+__device__ inline void load_x(UnitX& o, const uint16_t* base, uint32_t off)
 {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) o.q[k][h] = load_at<uint4>(base + 128 * k + 64 * h, off);
+        for (int j = 0; j < 4; ++j)
+            o.q[k][j] = load_at<uint4>(reinterpret_cast<const uint8_t*>(base) + 256 * k + 64 * j, off);
 }
-// sw, sx: the unit's 8 scale bytes.
-__device__ inline void unit_mma(v4f& acc, const UnitW& w, const UnitX& x, const uint2& sw, const uint2& sx)
+// Eight weights, times their scale.
+__device__ inline v8bf decode8(uint32_t w, float s)
+{
+    const uint4 v = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+    return __builtin_bit_cast(v8bf, v);
+}
+// sw: the unit's 8 scale bytes.
+__device__ inline void unit_mma(v4f& acc, const UnitW& w, const UnitX& x, const uint2& sw)
 {
     const int sh = 8 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const v8i a = v8i{(int)w.q[k].x, (int)w.q[k].y, (int)w.q[k].z, (int)w.q[k].w, 0, 0, 0, 0};
-        const v8i b = v8i{(int)x.q[k][0].x, (int)x.q[k][0].y, (int)x.q[k][0].z, (int)x.q[k][0].w,
-                          (int)x.q[k][1].x, (int)x.q[k][1].y, (int)x.q[k][1].z, (int)x.q[k][1].w};
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, (int)((k ? sw.y : sw.x) >> sh), 0,
-                                                               (int)((k ? sx.y : sx.x) >> sh));
+        const float s = mx4::scale_float(((k ? sw.y : sw.x) >> sh) & 255u);
+        const uint32_t q[4] = {w.q[k].x, w.q[k].y, w.q[k].z, w.q[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode8(q[j], s), __builtin_bit_cast(v8bf, x.q[k][j]), acc, 0, 0,
+                                                          0);
     }
 }
 
@@ -180,7 +160,7 @@ __device__ inline float dpp_f(float v)
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
-constexpr int kDppXor1 = 0xB1, kDppNext1 = 0x101, kDppNext2 = 0x102;    // lanes l ^ 1, l + 1, l + 2
+constexpr int kDppNext1 = 0x101, kDppNext2 = 0x102;     // lanes l + 1, l + 2
 
 // ------------------------------------------------------------------ router
 constexpr int kRouteThreads = 1024;
@@ -216,35 +196,23 @@ __device__ inline uint4 trim8(uint4 v, int c, int cols)
     return past >= 8 ? uint4{0, 0, 0, 0} : v;
 }
 
-// One wave: 512 columns of a token to pieces.
-__device__ inline void cut_x(const MoeArgs& p, int item)
+// One wave: 512 columns of a token to their places.  A block of 32 that holds
+// an Inf or NaN becomes NaN.
+__device__ inline void place_x(const MoeArgs& p, int item)
 {
     const int lane = threadIdx.x & 63;
     const int panels = (p.hp + mx4::kPanel - 1) / mx4::kPanel;
     const int t = item / panels, c = (item - t * panels) * mx4::kPanel + 8 * lane;
     if (t >= p.tokens || c >= p.hp) return;
-    const uint4 v = trim8(read8(p.x + t * p.ldx, c, p.hidden), c, p.hidden);
+    uint4 v = trim8(read8(p.x + t * p.ldx, c, p.hidden), c, p.hidden);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t amax = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) amax = max(amax, max(w[j] & 0x7FFF0000u, (w[j] << 16) & 0x7FFF0000u));
     amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1, 64));
     amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2, 64));
-    const bool finite = amax < 0x7F800000u;
-    const uint32_t b = finite ? piece_byte(amax) : 255u;
-    uint32_t o[2][kXPieces];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float f[4] = {bf16_lo(w[2 * h]), bf16_hi(w[2 * h]), bf16_lo(w[2 * h + 1]), bf16_hi(w[2 * h + 1])};
-        to_pieces<kXPieces>(f, inv_scale(finite ? b : 127u), o[h]);
-    }
-#pragma unroll
-    for (int i = 0; i < kXPieces; ++i) {
-        *reinterpret_cast<uint2*>(p.xq + (int64_t)(t * kXPieces + i) * p.hp + c) =
-            finite ? uint2{o[0][i], o[1][i]} : uint2{0, 0};
-        if ((lane & 3) == 0)
-            p.xs[(int64_t)(t * kXPieces + i) * (p.hp / 32) + c / 32] = (uint8_t)(finite ? b - 4 * i : 255u);
-    }
+    if (amax >= 0x7F800000u) v = uint4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+    *reinterpret_cast<uint4*>(p.xq + (int64_t)t * p.hp + place_of(c)) = v;
 }
 
 // fp64 as an unsigned key over 1 of the same order; NaN lowest, +0 and -0
@@ -398,7 +366,7 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
     if (e >= 0) atomicOr(&mask[e], 1ull << t);
     __syncthreads();
     const int n = __builtin_popcountll(mask[threadIdx.x]);
-    const int groups = (n + kDownTokens - 1) / kDownTokens, up_groups = (n + kUpGroup - 1) / kUpGroup;
+    const int groups = (n + kDownTokens - 1) / kDownTokens, up_groups = (n + kUpTokens - 1) / kUpTokens;
     // inclusive sums over the wave, of all three at once: at most 1024 pairs,
     // which makes at most 717 and 576 groups
     const uint32_t all = (uint32_t)(n | groups << 11 | up_groups << 21);
@@ -422,7 +390,7 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
     const auto list = [&](uint32_t sums, int e, int nth, uint64_t left) {
         const MoeGroup group{e, (int)(sums & 0x7FF) + nth, left};
         if (nth % kDownTokens == 0) p.groups[((sums >> 11) & 0x3FF) + nth / kDownTokens] = group;
-        if (nth % kUpGroup == 0) p.up_groups[(sums >> 21) + nth / kUpGroup] = group;
+        if (nth % kUpTokens == 0) p.up_groups[(sums >> 21) + nth / kUpTokens] = group;
     };
     if (n) list(sum, threadIdx.x, 0, mask[threadIdx.x]);
     if (threadIdx.x == 0) {
@@ -443,7 +411,7 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
 // Workgroups below tiles_e tiles_t splits take 16 tokens x 16 experts of the
 // logits and a share of K, which their waves split.  The last of 16 tokens to
 // arrive selects, the last of those lists the reached experts.  The others
-// cut x into pieces.  fp64 sums: products of bf16 are exact in fp64, so that
+// bring x to its places.  fp64 sums: products of bf16 are exact in fp64, so that
 // the chosen experts do not hang on the order of a sum.  One token, 64 experts
 // of 2048: 7.6 us, of which the logits 3.7, their way to one workgroup 0.6, the
 // selection 2.0 and the lists 1.3; 64 tokens, 128 experts of 4096: 14 us.
@@ -453,7 +421,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nroute = p.tiles_e * p.tiles_t * p.splits;
     if ((int)blockIdx.x >= nroute) {
-        cut_x(p, ((int)blockIdx.x - nroute) * kRouteWaves + wave);
+        place_x(p, ((int)blockIdx.x - nroute) * kRouteWaves + wave);
         return;
     }
     __shared__ __attribute__((aligned(16))) double red[kRouteWaves][256];
@@ -563,14 +531,30 @@ __device__ inline int token_of(uint64_t mask, int c)
 constexpr int kUpThreads = 256;
 constexpr int kUpWaves = kUpThreads / 64;
 
+// v as three bf16 numbers, in the high halves of words: 8 bits of it each, so
+// that they add up to v (an fp32 number has 24; bits under 2^-133 are lost).
+// Inf and NaN stand in the first alone.
+__device__ inline void split(float v, uint32_t& a, uint32_t& b, uint32_t& c)
+{
+    const auto top = [](float f) { return __builtin_bit_cast(uint32_t, f) & 0xFFFF0000u; };
+    const auto val = [](uint32_t w) { return __builtin_bit_cast(float, w); };
+    const bool finite = (__builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu) < 0x7F800000u;
+    a = finite ? top(v) : v != v ? 0x7FC00000u : __builtin_bit_cast(uint32_t, v);
+    const float r = finite ? v - val(a) : 0.0f;
+    b = top(r);
+    c = top(r - val(b));
+}
+
 // A workgroup takes an expert's 32 gate rows and the 32 up rows of the same
-// outputs, K over its waves, for a group of up to 16 tokens (two tiles of
-// columns).  64 tokens, 128 experts of 4096 x 1024: 101 us, 5.6 TB/s; one
-// token, 8 experts of 2048 x 1408: 9.4 us for 24.5 MB.  (64 tokens: 137 us with
-// 8 waves a workgroup, 107 with 2, 109 with the next unit's weights read ahead.)
+// outputs, K over its waves, for a group of up to 16 tokens, a column each.
+// 64 tokens, 128 experts of 4096 x 1024: 106 us, 5.4 TB/s; one token, 8 experts
+// of 2048 x 1408: 9.7 us for 24.5 MB.  (64 tokens, the whole layer, 203 us: 201
+// with 8 waves a workgroup, 205 with 2, 214 with the next unit's weights read
+// ahead; without the barrier below the compiler puts half of the reads off
+// until others have arrived: 212.)
 __global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
 {
-    __shared__ v4f red[2][kUpWaves][4][32];
+    __shared__ v4f red[kUpWaves][4][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = (p.inner + 31) / 32;
@@ -578,7 +562,7 @@ __global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
     const MoeGroup at = group_at(p, p.up_groups, group);
     if (group >= up_group_count(p)) return;
     const int e = at.expert, off = at.off;
-    const int n = min(__builtin_popcountll(at.mask), kUpGroup);
+    const int n = min(__builtin_popcountll(at.mask), kUpTokens);
     const int c16 = lane & 15, q = lane >> 4;
 
     // gate rows; up rows lie `inner` rows on
@@ -592,18 +576,10 @@ __global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
         soff[h] = (uint32_t)(row * 16);
     }
     const int units = (p.hidden + kUnit - 1) / kUnit;
-    const int cols = kXPieces * n;
-    const bool two = cols > 16;
-    uint32_t xrow[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int col = min(16 * h + c16, cols - 1);
-        xrow[h] = (uint32_t)(token_of(at.mask, col / kXPieces) * kXPieces + col % kXPieces);
-    }
-    // token r of tile h (r = lane / 8), of whose column tile this wave ends with
-    const int c = wave * kUpTokens + (lane >> 3);
-    const float prob = p.prob[off + min(c, n - 1)];
-    v4f acc[2][4] = {};
+    const int c = min(c16, n - 1);
+    const uint32_t xoff = (uint32_t)(token_of(at.mask, c) * p.hp) * 2 + 16 * q;
+    const float prob = p.prob[off + c];
+    v4f acc[4] = {};
     for (int u = wave; u < units; u += kUpWaves) {
         UnitW w[4];
         uint2 sw[4];
@@ -613,91 +589,62 @@ __global__ void __launch_bounds__(kUpThreads, 3) k_moe_up(MoeArgs p)
             sw[r] = load_at<uint2>(ws + far * 16 + (u >> 1) * p.ps1 + 8 * (u & 1), soff[r & 1]);
             load_w(w[r], wq + far * p.ldq1 + u * 128, woff[r & 1]);
         }
+        UnitX x;
+        load_x(x, p.xq + u * kUnit, xoff);
+        __builtin_amdgcn_sched_barrier(0);      // every read of the unit on its way first
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (h == 0 || two) {
-                UnitX x;
-                const uint2 sx = load_at<uint2>(p.xs + 8 * u, xrow[h] * (uint32_t)(p.hp / 32));
-                load_x(x, p.xq + u * kUnit, xrow[h] * (uint32_t)p.hp + 16 * q);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) unit_mma(acc[h][r], w[r], x, sw[r], sx);
-            }
+        for (int r = 0; r < 4; ++r) unit_mma(acc[r], w[r], x, sw[r]);
     }
-    // the pieces of a token are neighbours
-    static_assert(kXPieces == 2, "one exchange");
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (h == 0 || two)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                v4f s;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = acc[h][r][i] + dpp_f<kDppXor1>(acc[h][r][i]);
-                if ((c16 & 1) == 0) red[h][wave][r][8 * q + (c16 >> 1)] = s;
-            }
+    for (int r = 0; r < 4; ++r) red[wave][r][lane] = acc[r];
     __syncthreads();
-    // wave h: the tokens of tile h; lane: token lane / 8 of it, 16 r +
-    // 4 qq + i of the 32 outputs
-    if (wave > 1 || wave * kUpTokens >= n) return;
-    const int r = (lane >> 2) & 1, qq = lane & 3;
+    // wave r: 16 r + 4 q + i of the 32 outputs, token c16
+    if (wave > 1 || c16 >= n) return;
     v4f g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < kUpWaves; ++w) {
-        g += red[wave][w][r][8 * qq + (lane >> 3)];
-        u += red[wave][w][r + 2][8 * qq + (lane >> 3)];
+        g += red[w][wave][lane];
+        u += red[w][wave + 2][lane];
     }
-    float a[4];
-    uint32_t amax = 0;
+    uint32_t o[kPieces][4];
+    const int k = 16 * wave + 4 * q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float v = prob * (g[i] / (1.0f + expf(-g[i])) * u[i]);
-        a[i] = 32 * tile + 16 * r + 4 * qq + i < p.inner ? v : 0.0f;
-        amax = max(amax, __builtin_bit_cast(uint32_t, a[i]) & 0x7FFFFFFFu);
+        split(32 * tile + k + i < p.inner ? v : 0.0f, o[0][i], o[1][i], o[2][i]);
     }
+    uint16_t* aq = p.aq + (int64_t)(off + c) * kPieces * p.ip;
 #pragma unroll
-    for (int d = 1; d < 8; d <<= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, d, 64));
-    const bool finite = amax < 0x7F800000u;
-    const uint32_t b = finite ? piece_byte(amax) : 255u;
-    uint32_t o[kAPieces];
-    to_pieces<kAPieces>(a, inv_scale(finite ? b : 127u), o);
-    if (c >= n) return;
-    uint8_t* aq = p.aq + (int64_t)(off + c) * kAPieces * p.ip;
-    uint8_t* as = p.as + (int64_t)(off + c) * kAPieces * (p.ip / 32);
-#pragma unroll
-    for (int i = 0; i < kAPieces; ++i) {
-        *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + 32 * tile + 16 * r + 4 * qq) = finite ? o[i] : 0u;
-        if ((lane & 7) == 0) as[i * (p.ip / 32) + tile] = (uint8_t)(finite ? b - 4 * i : 255u);
-    }
+    for (int i = 0; i < kPieces; ++i)
+        *reinterpret_cast<uint2*>(aq + (int64_t)i * p.ip + place_of(32 * tile + k)) =
+            uint2{o[i][0] >> 16 | o[i][1], o[i][2] >> 16 | o[i][3]};
     // zeros to the end of the last panel
     if (tile == tiles - 1)
         for (int z = 32 * tiles; z < p.ip; z += 32)
 #pragma unroll
-            for (int i = 0; i < kAPieces; ++i) {
-                *reinterpret_cast<uint32_t*>(aq + (int64_t)i * p.ip + z + 4 * (lane & 7)) = 0u;
-                if ((lane & 7) == 0) as[i * (p.ip / 32) + z / 32] = 127;
-            }
+            for (int i = 0; i < kPieces; ++i)
+                *reinterpret_cast<uint2*>(aq + (int64_t)i * p.ip + place_of(z + k)) = uint2{0, 0};
 }
 
 // ------------------------------------------------------------------ down
 constexpr int kDownThreads = 256;
 constexpr int kDownWaves = kDownThreads / 64;
-constexpr int kDownRows = 32;
 constexpr int kMaxShares = 8;
 
-// `shares` workgroups take the same 32 rows of y for every token.  Their waves
-// share the steps (up to five tokens of an expert, a panel of K: two units) in
-// a fixed order, each with sums of its own in LDS, which are added in wave
-// order at the end, and over the workgroups by the last of them to arrive.  A
-// step's weights are read two steps ahead and its columns one: reads come back
-// in order, so the columns of the next step are asked for before the weights
-// of the one after it, and no read in the loop hangs on a branch.  64 tokens,
-// 128 experts of 4096 x 1024: 71 us, 4.0 TB/s, of which 18 us are the columns
-// (from L2); one token, 8 experts of 2048 x 1408: 9 us for 12.2 MB.  (16 rows a
-// workgroup: 97 us; workgroups whose waves share the columns through L1, 128
-// rows: 100.)
+// `shares` workgroups take the same 16 R rows of y for every token.  Their waves
+// share the steps (up to five tokens of an expert, a unit of K) in a fixed
+// order, each with sums of its own in LDS, which are added in wave order at the
+// end, and over the workgroups by the last of them to arrive.  A step's weights
+// are read two steps ahead and its columns one: reads come back in order, so
+// the columns of the next step are asked for before the weights of the one
+// after it, and no read in the loop hangs on a branch.
+// 64 tokens, 128 experts of 4096 x 1024: 80 us, 3.6 TB/s, of which 19 us are the
+// columns (from L2); one token, 8 experts of 2048 x 1408: 9 us for 12.2 MB.
+template <int R>
 __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
 {
-    extern __shared__ __attribute__((aligned(16))) float ysum[];     // [waves, tokens, 32]
+    constexpr int kDownRows = 16 * R;
+    extern __shared__ __attribute__((aligned(16))) float ysum[];     // [waves, tokens, 16 R]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int block = blockIdx.x / p.shares, share = blockIdx.x - block * p.shares;
@@ -705,78 +652,67 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
     const int groups = group_count(p);
 
     const int c16 = lane & 15, q = lane >> 4;
-    uint32_t woff[2], soff[2];
+    uint32_t woff[R], soff[R];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < R; ++h) {
         const int row = min(16 * h + c16, p.hidden - 1 - row0);
         woff[h] = (uint32_t)(row * p.ldq2 + 16 * q);
         soff[h] = (uint32_t)(row * 16);
     }
-    const int units = (p.inner + kUnit - 1) / kUnit, panels = p.ip / mx4::kPanel;
-    const int steps = groups * panels;
+    const int units = (p.inner + kUnit - 1) / kUnit;
+    const int steps = groups * units;
     float* mine = ysum + wave * p.tokens * kDownRows;
 
     struct At {
-        int e, row, n, panel;       // row: of the first token's first piece; n tokens
+        int e, row, n, unit;        // row: of the first token's first piece; n tokens
         uint64_t mask;
     };
     struct Entry {
         MoeGroup r;
-        int panel;
+        int unit;
     };
     // what the list holds for step i, then what it means
     const auto entry = [&](int i) {
         i = min(i, steps - 1);
-        const int g = i / panels;
-        return Entry{group_at(p, p.groups, g), i - g * panels};
+        const int g = i / units;
+        return Entry{group_at(p, p.groups, g), i - g * units};
     };
     const auto at_step = [&](const Entry& x) {
         At a;
-        a.panel = x.panel;
+        a.unit = x.unit;
         a.mask = x.r.mask;
         a.e = x.r.expert;
-        a.row = kAPieces * x.r.off;
+        a.row = kPieces * x.r.off;
         a.n = min(__builtin_popcountll(x.r.mask), kDownTokens);
         return a;
     };
     struct W {
-        UnitW u[2][2];
-        uint4 s[2];
-    };
-    struct X {
-        UnitX u[2];
-        uint4 s;
+        UnitW u[R];
+        uint2 s[R];
     };
     const auto get_w = [&](W& w, const At& a) {
-        const uint8_t* base = p.q2 + a.e * p.eq2 + row0 * p.ldq2;
-        const uint8_t* sbase = p.s2 + a.e * p.es2 + a.panel * p.ps2 + row0 * 16;
+        const uint8_t* base = p.q2 + a.e * p.eq2 + row0 * p.ldq2 + 128 * a.unit;
+        const uint8_t* sbase = p.s2 + a.e * p.es2 + (a.unit >> 1) * p.ps2 + row0 * 16 + 8 * (a.unit & 1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            w.s[h] = load_at<uint4>(sbase, soff[h]);
-            // past the last unit its weights again, against zeros
-            load_w(w.u[h][0], base + 256 * a.panel, woff[h]);
-            load_w(w.u[h][1], base + 128 * min(2 * a.panel + 1, units - 1), woff[h]);
+        for (int h = 0; h < R; ++h) {
+            w.s[h] = load_at<uint2>(sbase, soff[h]);
+            load_w(w.u[h], base, woff[h]);
         }
     };
-    const auto get_x = [&](X& x, const At& a) {
-        const uint8_t* base = p.aq + (int64_t)a.row * p.ip + mx4::kPanel * a.panel;
-        const uint8_t* sbase = p.as + (int64_t)a.row * (p.ip / 32) + 16 * a.panel;
-        const uint32_t col = (uint32_t)min(c16, kAPieces * a.n - 1);
-        x.s = load_at<uint4>(sbase, col * (uint32_t)(p.ip / 32));
-        load_x(x.u[0], base, col * (uint32_t)p.ip + 16 * q);
-        load_x(x.u[1], base + kUnit, col * (uint32_t)p.ip + 16 * q);
+    const auto get_x = [&](UnitX& x, const At& a) {
+        const uint32_t col = (uint32_t)min(c16, kPieces * a.n - 1);
+        load_x(x, p.aq + (int64_t)a.row * p.ip + kUnit * a.unit, col * (uint32_t)p.ip * 2 + 16 * q);
     };
-    // 32 rows x the tokens of 15 columns, added to this wave's sums
-    const auto compute = [&](const W& w, const X& x, const At& a) {
-        static_assert(kAPieces == 3, "two neighbours");
-        const int c = c16 / kAPieces;
-        const bool mine_to_add = c16 % kAPieces == 0 && c < a.n;
+    // 16 R rows x the tokens of 15 columns, added to this wave's sums
+    const auto compute = [&](const W& w, const UnitX& x, const At& a) {
+        static_assert(kPieces == 3, "two neighbours");
+        const int c = c16 / kPieces;
+        const bool mine_to_add = c16 % kPieces == 0 && c < a.n;
         v4f* to = reinterpret_cast<v4f*>(mine + token_of(a.mask, min(c, a.n - 1)) * kDownRows + 4 * q);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < R; ++h) {
             v4f acc = {0, 0, 0, 0};
-            unit_mma(acc, w.u[h][0], x.u[0], uint2{w.s[h].x, w.s[h].y}, uint2{x.s.x, x.s.y});
-            unit_mma(acc, w.u[h][1], x.u[1], uint2{w.s[h].z, w.s[h].w}, uint2{x.s.z, x.s.w});
+            unit_mma(acc, w.u[h], x, w.s[h]);
             v4f sum;
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[i] = acc[i] + (dpp_f<kDppNext1>(acc[i]) + dpp_f<kDppNext2>(acc[i]));
@@ -788,7 +724,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
     const int who = share * kDownWaves + wave, all = p.shares * kDownWaves;
     const int first = (int)((int64_t)steps * who / all), end = (int)((int64_t)steps * (who + 1) / all);
     W w0, w1;
-    X x0, x1;
+    UnitX x0, x1;
     At a0, a1;
     if (first < end) {
         const Entry e0 = entry(first), e1 = entry(first + 1);
@@ -869,13 +805,27 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
     flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
-// Workgroups that share a row block of y: enough for one on each of 256 CUs,
-// of two steps a wave at least.  (64 tokens, 128 experts of 4096 x 1024: 197
-// us with 2, 202 with 4, 213 with 8.)
-int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
+// Rows of y a workgroup takes: 64, which halves the reads of the columns, from 64
+// wave steps of such a workgroup a CU on.  The layer, us, the chosen one first:
+//   1 token, 8 of 64 experts of 2048 x 1408      32: 26.4    64: 29.5
+//   64 tokens, 4 of 64 of 1024 x 700             32: 41.5    64: 49.1
+//   8 tokens, 8 of 128 of 4096 x 1024            64: 83.5    32: 86.7
+//   64 tokens, 8 of 128 of 4096 x 1024           64: 203     32: 217
+constexpr int kDownRowsFew = 32, kDownRowsMany = 64;
+int down_rows(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
 {
-    const int64_t blocks = (hidden + kDownRows - 1) / kDownRows;
-    const int64_t steps = tokens * top_k * ((inner + mx4::kPanel - 1) / mx4::kPanel);
+    const int64_t steps = tokens * top_k * ((inner + kUnit - 1) / kUnit) * ((hidden + 63) / 64);
+    return steps < 64 * 256 ? kDownRowsFew : kDownRowsMany;
+}
+
+// Workgroups that share a row block of y: enough for one on each of 256 CUs,
+// of two steps a wave at least.  (64 tokens, 128 experts of 4096 x 1024: 213
+// us with 3, 197 with 4, 203 with 8; one token of 2048 x 1408: 26.6 with 4, 28.2
+// with 8.)
+int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner, int64_t rows)
+{
+    const int64_t blocks = (hidden + rows - 1) / rows;
+    const int64_t steps = tokens * top_k * ((inner + kUnit - 1) / kUnit);
     return (int)std::clamp<int64_t>(std::min((256 + blocks - 1) / blocks, steps / (2 * kDownWaves)), 1, kMaxShares);
 }
 
@@ -889,7 +839,7 @@ int route_splits(int64_t tokens, int64_t experts, int64_t hidden)
 }
 
 struct MoeLayout {
-    size_t arrived_rows, logits, xq, xs, count, up_groups, groups, prob, aq, as, part, total;
+    size_t arrived_rows, logits, xq, count, up_groups, groups, prob, aq, part, total;
     int64_t max_up_groups, max_groups;
 };
 MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner)
@@ -903,20 +853,18 @@ MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hid
         at = up(at + bytes, 256);
         return (size_t)o;
     };
-    m.arrived_rows = take((hidden + kDownRows - 1) / kDownRows * 4);
+    m.arrived_rows = take((hidden + kDownRowsFew - 1) / kDownRowsFew * 4);
     m.logits = take(route_splits(tokens, experts, hidden) * tokens * experts * 8);
-    m.xq = take(tokens * kXPieces * hp);
-    m.xs = take(tokens * kXPieces * (hp / 32));
+    m.xq = take(tokens * hp * 2);
     m.count = take(8);
     // an expert's last group may be short
     const auto most = [&](int64_t size) { return std::min(pairs, std::min(pairs, experts) + pairs / size); };
-    m.max_up_groups = most(kUpGroup);
+    m.max_up_groups = most(kUpTokens);
     m.max_groups = most(kDownTokens);
     m.up_groups = take(m.max_up_groups * (int64_t)sizeof(MoeGroup));
     m.groups = take(m.max_groups * (int64_t)sizeof(MoeGroup));
     m.prob = take(pairs * 4);
-    m.aq = take(pairs * kAPieces * ip);
-    m.as = take(pairs * kAPieces * (ip / 32));
+    m.aq = take(pairs * kPieces * ip * 2);
     m.part = take(kMaxShares * tokens * hidden * 4);
     m.total = (size_t)at;
     return m;
@@ -965,8 +913,7 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     p.weights = g.weights;
     p.arrived = reinterpret_cast<uint32_t*>(ws);
     p.logits = reinterpret_cast<double*>(ws + m.logits);
-    p.xq = ws + m.xq;
-    p.xs = ws + m.xs;
+    p.xq = reinterpret_cast<uint16_t*>(ws + m.xq);
     p.count = reinterpret_cast<int32_t*>(ws + m.count);
     p.up_groups = reinterpret_cast<MoeGroup*>(ws + m.up_groups);
     p.max_up_groups = (int)m.max_up_groups;
@@ -975,9 +922,9 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     p.prob = reinterpret_cast<float*>(ws + m.prob);
     p.part = reinterpret_cast<float*>(ws + m.part);
     p.arrived_rows = reinterpret_cast<uint32_t*>(ws + m.arrived_rows);
-    p.shares = down_shares(g.tokens, g.top_k, g.hidden, g.inner);
-    p.aq = ws + m.aq;
-    p.as = ws + m.as;
+    const int rows = down_rows(g.tokens, g.top_k, g.hidden, g.inner);
+    p.shares = down_shares(g.tokens, g.top_k, g.hidden, g.inner, rows);
+    p.aq = reinterpret_cast<uint16_t*>(ws + m.aq);
     p.ctr = g.ctr;
     p.tiles_e = (p.experts + 15) / 16;
     p.tiles_t = (p.tokens + 15) / 16;
@@ -990,9 +937,15 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(k_moe_up, dim3(p.max_up_groups * ((p.inner + 31) / 32)), dim3(kUpThreads), 0, stream, p);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int lds = kDownWaves * p.tokens * kDownRows * 4;
-    const int blocks = (p.hidden + kDownRows - 1) / kDownRows;
-    hipLaunchKernelGGL(k_moe_down, dim3(blocks * p.shares), dim3(kDownThreads), lds, stream, p);
+    const int lds = kDownWaves * p.tokens * rows * 4;
+    const int blocks = (p.hidden + rows - 1) / rows;
+    const auto kernel = rows == kDownRowsFew ? k_moe_down<kDownRowsFew / 16> : k_moe_down<kDownRowsMany / 16>;
+    if (rows == kDownRowsMany) {
+        static mx4::LdsLimit limit;
+        e = limit.raise(reinterpret_cast<const void*>(kernel), kDownWaves * kMaxTokens * kDownRowsMany * 4);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, dim3(blocks * p.shares), dim3(kDownThreads), lds, stream, p);
     return hipGetLastError();
 }
 

@@ -240,3 +240,74 @@ def test_moe_is_what_quantize_and_product_give():
         # gate and up rounded to bf16 (silu's relative slope is at most 1 + |g|), y too, a to 2^-12
         slope = 2 + gu[:i].abs().max()
         assert ((y[tok].float() - want).abs() <= 2.0 ** -8 * (want.abs() + slope * size) + 2.0 ** -12 * size).all()
+
+
+def test_moe_inner_activations_keep_their_precision():
+    """Outputs that are differences of nearly equal inner activations show the
+    precision those are held to: fp32."""
+    t, h, i = 3, 256, 64
+    rng = np.random.default_rng(19)
+
+    def held(codes):        # every scale 1
+        q, s = mx4.pack(codes, np.full((codes.shape[0], -(-codes.shape[1] // 32)), 127, np.uint8))
+        return fm.Mx4(torch.from_numpy(q[None]).cuda(), torch.from_numpy(s[None]).cuda(), codes.shape[1])
+
+    # g = x[0]; u = x[0] + a little that differs, of blocks of its own: both exact in fp32
+    c1 = np.zeros((2 * i, h), np.uint8)
+    c1[:, 0] = 2
+    c1[i:, 32] = rng.integers(0, 16, i)
+    c1[i:, 64] = rng.integers(0, 16, i)
+    c2 = np.zeros((h, i), np.uint8)
+    for r in range(h):
+        c2[r, rng.choice(i, 2, replace=False)] = 2, 10      # 1, -1
+    x = np.zeros((t, h))
+    x[:, 0] = 1.75, 3.125, 0.8125
+    x[:, 32] = 1.25 * 2.0 ** -12
+    x[:, 64] = 1.625 * 2.0 ** -14
+    layer = fm.MoeMx4(torch.ones(1, h, dtype=torch.bfloat16, device="cuda"), held(c1), held(c2), 1, max_tokens=t)
+    y = layer(torch.from_numpy(x).bfloat16().cuda())[0].cpu().double().numpy()
+    gu = x @ mx4.VALUES[c1].T
+    a = gu[:, :i] / (1 + np.exp(-gu[:, :i])) * gu[:, i:]
+    # exp, sum, quotient and two products in fp32 (four units in the last place for exp and quotient)
+    da = 12 * 2.0 ** -23 * np.abs(a)
+    w2 = mx4.VALUES[c2]
+    want = a @ w2.T
+    bound = 2.0 ** -8 * np.abs(want) + da @ np.abs(w2).T + 2.0 ** -24 * np.abs(a) @ np.abs(w2).T
+    assert (np.abs(y - want) <= bound).all(), np.max(np.abs(y - want) / bound)
+
+
+def test_moe_sums_of_far_apart_terms_keep_their_precision():
+    """A sum's terms of very different size beside each other: what the small
+    ones add up to shows once the large ones cancel.  Both layers, bounds of
+    fp32 sums."""
+    t, h, i = 16, 512, 512
+    rng = np.random.default_rng(23)
+
+    def held(codes):
+        q, s = mx4.pack(codes, np.full((codes.shape[0], -(-codes.shape[1] // 32)), 127, np.uint8))
+        return fm.Mx4(torch.from_numpy(q[None]).cuda(), torch.from_numpy(s[None]).cuda(), codes.shape[1])
+
+    # every fourth element of x is large, in pairs that the weights 1 and -1 cancel exactly
+    x = rng.standard_normal((t, h))
+    x[:, ::8] = 192.0 * (1 + rng.integers(0, 4, (t, h // 8)))
+    x[:, 4::8] = x[:, ::8]
+    c1 = rng.integers(0, 16, (2 * i, h)).astype(np.uint8)
+    c1[:, ::8], c1[:, 4::8] = 2, 10
+    xb = torch.from_numpy(x).bfloat16()
+    xv = xb.double().numpy()
+    c2 = rng.integers(0, 16, (h, i)).astype(np.uint8)
+    layer = fm.MoeMx4(torch.ones(1, h, dtype=torch.bfloat16, device="cuda"), held(c1), held(c2), 1, max_tokens=t)
+    y = layer(xb.cuda())[0].cpu().double().numpy()
+    w1, w2 = mx4.VALUES[c1], mx4.VALUES[c2]
+    gu, size = xv @ w1.T, np.abs(xv) @ np.abs(w1).T
+    # an instruction's sum of 32 products is off by 2^-22 of their sizes at most (measured), 16 of them and three more
+    # sums of waves by 2^-24 of the sizes so far each
+    d = (2.0 ** -22 + 19 * 2.0 ** -24) * size
+    g, u, dg, du = gu[:, :i], gu[:, i:], d[:, :i], d[:, i:]
+    silu = g / (1 + np.exp(-g))
+    a = silu * u
+    da = 1.1 * dg * np.abs(u) + (np.abs(silu) + 1.1 * dg) * du + (12 + np.abs(g)) * 2.0 ** -23 * np.abs(a)
+    want, ysize = a @ w2.T, np.abs(a) @ np.abs(w2).T
+    # the rounding of y, its sums; the errors of a are independent, so that five deviations of their sum bound it
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -22 + 40 * 2.0 ** -24) * ysize + 5 * np.sqrt((da ** 2) @ (w2 ** 2).T)
+    assert (np.abs(y - want) <= bound).all(), np.max(np.abs(y - want) / bound)
