@@ -495,11 +495,12 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
                 }
             stored = 0;
             if (p.ctr && (mx.x >= 0x7F80u || mx.y >= 0x7F80u)) {
-                // the outputs past the edges are zeros
+                // past the edges a NaN scale of the other operand makes NaN, too
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
+                        if (col >= p.n || wm + 4 * half + 32 * i + 8 * (r >> 2) + (r & 3) >= rows_c) continue;
                         const uint32_t h = gemm::pack_bf16(acc[i][0][r], acc[i][1][r]);
                         nonfinite += ((h & 0x7F80u) == 0x7F80u) + ((h & 0x7F800000u) == 0x7F800000u);
                     }

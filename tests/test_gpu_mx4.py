@@ -388,3 +388,24 @@ def test_same_results_with_and_without_outputs_given():
         assert torch.equal(fm.mx4_dequantize(q, dtype), fm.mx4_dequantize(q, out=y))
     y = torch.empty(100, 100, dtype=torch.bfloat16, device="cuda")
     assert torch.equal(fm.mx4_mm(q, q), fm.mx4_mm(q, q, out=y))
+
+
+@pytest.mark.parametrize("m,n,k", [(1500, 1500, 512), (1300, 1202, 40), (3000, 3000, 512), (2998, 3002, 300),
+                                   (3001, 2999, 512)])
+def test_mm_counts_only_the_outputs_there_are(m, n, k):
+    """NaN blocks of either operand reach the places past the edges of a tile
+    too; those are no outputs.  Ragged products of the 128 x 128 and the 256 x
+    256 tile, even and odd n."""
+    a, _ = _operand(m, k, 14)
+    b, _ = _operand(n, k, 15)
+    ctr = fm.Counters()
+    assert torch.isfinite(fm.mx4_mm(a, b, counters=ctr)).all() and ctr.read()["nonfinite_out"] == 0
+    nan = torch.zeros(m, n, dtype=torch.bool)
+    for rows, cols in (((), (n - 1, 5)), ((0, m - 1), ()), ((m // 2,), (n // 3,))):
+        a.s[0, list(rows), 0] = 255
+        b.s[0, list(cols), (k - 1) // 32 % 16] = 255
+        nan[list(rows)] = True
+        nan[:, list(cols)] = True
+        ctr = fm.Counters()
+        y = fm.mx4_mm(a, b, counters=ctr)
+        assert torch.equal(torch.isnan(y).cpu(), nan) and ctr.read()["nonfinite_out"] == int(nan.sum())
