@@ -832,10 +832,11 @@ int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner, in
 // K splits of the router: one round of reads a wave, as far as the partial sums
 // of 16 tokens, which one workgroup reads, stay under 64 KB (64 tokens, 128
 // experts of 4096: 4 splits, the launch 2 us shorter than with 8).
+constexpr int64_t kSplitBytes = 65536;
 int route_splits(int64_t tokens, int64_t experts, int64_t hidden)
 {
     const int64_t chunks = (hidden + kChunk - 1) / kChunk, bytes = std::min<int64_t>(tokens, 16) * experts * 8;
-    return (int)std::clamp<int64_t>(std::min((chunks + kRouteWaves - 1) / kRouteWaves, 65536 / bytes), 1, kMaxSplits);
+    return (int)std::clamp<int64_t>(std::min((chunks + kRouteWaves - 1) / kRouteWaves, kSplitBytes / bytes), 1, kMaxSplits);
 }
 
 struct MoeLayout {
@@ -854,7 +855,8 @@ MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hid
         return (size_t)o;
     };
     m.arrived_rows = take((hidden + kDownRowsFew - 1) / kDownRowsFew * 4);
-    m.logits = take(route_splits(tokens, experts, hidden) * tokens * experts * 8);
+    // fewer tokens may take more splits, in as many bytes
+    m.logits = take(std::max<int64_t>(kSplitBytes, route_splits(tokens, experts, hidden) * tokens * experts * 8));
     m.xq = take(tokens * hp * 2);
     m.count = take(8);
     // an expert's last group may be short

@@ -311,3 +311,12 @@ def test_moe_sums_of_far_apart_terms_keep_their_precision():
     # the rounding of y, its sums; the errors of a are independent, so that five deviations of their sum bound it
     bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -22 + 40 * 2.0 ** -24) * ysize + 5 * np.sqrt((da ** 2) @ (w2 ** 2).T)
     assert (np.abs(y - want) <= bound).all(), np.max(np.abs(y - want) / bound)
+
+
+@pytest.mark.parametrize("most,t,e,k,h,i", [(9, 8, 512, 1, 520, 64), (11, 10, 400, 2, 600, 512)])
+def test_moe_fewer_tokens_through_a_layer_for_more(most, t, e, k, h, i):
+    """Where fewer tokens take more splits of the router's sums."""
+    m = Layer(most, e, k, h, i, True)
+    for n in (t, most):
+        x = m.x(n, h)
+        m.check(x, m.moe(x.cuda()))

@@ -196,3 +196,14 @@ def test_extension_passes_errors_of_its_arguments_on():
     a = _mx4(8, 64)
     with pytest.raises(OverflowError):
         fm._ext().mx4_held(a.q, a.s, 1 << 70)
+
+
+def test_moe_workspace_grows_with_tokens():
+    """A workspace for some tokens serves every call of fewer."""
+    import random
+    rng = random.Random(3)
+    sizes = [(512, 1, 520, 64), (400, 2, 600, 512), (1, 1, 1, 1), (512, 16, 9000, 64), (300, 3, 4100, 32)]
+    sizes += [(rng.randint(1, 512), 1, rng.randint(1, 9000), rng.randint(1, 3000)) for _ in range(300)]
+    for experts, top_k, hidden, inner in sizes:
+        size = [fm.lib().fp8_mx4_moe_workspace_size(t, experts, top_k, hidden, inner) for t in range(1, 65)]
+        assert size[0] > 0 and all(a <= b for a, b in zip(size, size[1:])), (experts, top_k, hidden, inner)
