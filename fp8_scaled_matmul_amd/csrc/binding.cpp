@@ -42,6 +42,15 @@ at::Tensor fresh(at::IntArrayRef size, at::IntArrayRef stride, at::ScalarType dt
 template <typename T>
 T* data(const at::Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
+// Other threads may run Python while this one allocates and enqueues: a launch
+// waits where a queue is full.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    Unlocked() = default;
+    Unlocked(const Unlocked&) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 hipStream_t stream() { return c10::hip::getCurrentHIPStream().stream(); }
 
 // Arguments are of the Python code's making; a failed conversion raises.
@@ -109,13 +118,18 @@ PyObject* mx4_quantize(PyObject*, PyObject* const* args, Py_ssize_t n)
     const int64_t rows = x->size(0), cols = x->size(1);
     const bool want_t = args[1] == Py_True;
     at::AutoDispatchBelowADInplaceOrView guard;
-    Codes c = fresh_codes(rows, cols, *x), t;
-    if (want_t) t = fresh_codes(cols, rows, *x);
-    const fp8_status st = fp8_mx4_quantize(x->data_ptr(), bf16 ? FP8_IN_BF16 : FP8_IN_FP32, rows, cols, ld,
-                                           data<uint8_t>(c.q), c.ldq, data<uint8_t>(c.s), c.ps,
-                                           want_t ? data<uint8_t>(t.q) : nullptr, t.ldq,
-                                           want_t ? data<uint8_t>(t.s) : nullptr, t.ps,
-                                           seed ? data<const uint64_t>(*seed) : nullptr, nullptr, stream());
+    Codes c, t;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        c = fresh_codes(rows, cols, *x);
+        if (want_t) t = fresh_codes(cols, rows, *x);
+        st = fp8_mx4_quantize(x->data_ptr(), bf16 ? FP8_IN_BF16 : FP8_IN_FP32, rows, cols, ld,
+                              data<uint8_t>(c.q), c.ldq, data<uint8_t>(c.s), c.ps,
+                              want_t ? data<uint8_t>(t.q) : nullptr, t.ldq,
+                              want_t ? data<uint8_t>(t.s) : nullptr, t.ps,
+                              seed ? data<const uint64_t>(*seed) : nullptr, nullptr, stream());
+    }
     if (st != FP8_OK) return PyLong_FromLong(st);
     PyObject* out = PyTuple_New(want_t ? 4 : 2);
     if (!out) return nullptr;
@@ -163,9 +177,14 @@ PyObject* mx4_dequantize(PyObject*, PyObject* const* args, Py_ssize_t n)
     const bool fp32 = args[4] == Py_True;
     const int64_t rows = a.q->size(0);
     at::AutoDispatchBelowADInplaceOrView guard;
-    at::Tensor y = fresh({rows, a.cols}, {a.cols, 1}, fp32 ? at::kFloat : at::kBFloat16, *a.q);
-    const fp8_status st = fp8_mx4_dequantize(data<const uint8_t>(*a.q), a.ldq, data<const uint8_t>(*a.s), a.ps, rows,
-                                             a.cols, y.data_ptr(), fp32 ? FP8_IN_FP32 : FP8_IN_BF16, a.cols, stream());
+    at::Tensor y;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        y = fresh({rows, a.cols}, {a.cols, 1}, fp32 ? at::kFloat : at::kBFloat16, *a.q);
+        st = fp8_mx4_dequantize(data<const uint8_t>(*a.q), a.ldq, data<const uint8_t>(*a.s), a.ps, rows,
+                                a.cols, y.data_ptr(), fp32 ? FP8_IN_FP32 : FP8_IN_BF16, a.cols, stream());
+    }
     if (st != FP8_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(std::move(y));
     END_HANDLE_TH_ERRORS
@@ -182,10 +201,15 @@ PyObject* mx4_mm(PyObject*, PyObject* const* args, Py_ssize_t n)
     }
     const int64_t rows = a.q->size(0), cols = b.q->size(0);
     at::AutoDispatchBelowADInplaceOrView guard;
-    at::Tensor y = fresh({rows, cols}, {cols, 1}, at::kBFloat16, *a.q);
-    const fp8_status st = fp8_mx4_mm(data<const uint8_t>(*a.q), a.ldq, data<const uint8_t>(*a.s), a.ps,
-                                     data<const uint8_t>(*b.q), b.ldq, data<const uint8_t>(*b.s), b.ps, rows, cols,
-                                     a.cols, y.data_ptr(), cols, nullptr, stream());
+    at::Tensor y;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        y = fresh({rows, cols}, {cols, 1}, at::kBFloat16, *a.q);
+        st = fp8_mx4_mm(data<const uint8_t>(*a.q), a.ldq, data<const uint8_t>(*a.s), a.ps,
+                        data<const uint8_t>(*b.q), b.ldq, data<const uint8_t>(*b.s), b.ps, rows, cols,
+                        a.cols, y.data_ptr(), cols, nullptr, stream());
+    }
     if (st != FP8_OK) return PyLong_FromLong(st);
     return THPVariable_Wrap(std::move(y));
     END_HANDLE_TH_ERRORS
@@ -207,14 +231,19 @@ PyObject* mx4_moe(PyObject*, PyObject* const* args, Py_ssize_t n)
         !here(*ws))
         Py_RETURN_NONE;
     at::AutoDispatchBelowADInplaceOrView guard;
-    at::Tensor y = fresh({tokens, hidden}, {hidden, 1}, at::kBFloat16, *x);
-    at::Tensor ids = fresh({tokens, top_k}, {top_k, 1}, at::kInt, *x);
-    at::Tensor weights = fresh({tokens, top_k}, {top_k, 1}, at::kFloat, *x);
-    const fp8_status st = fp8_mx4_moe(x->data_ptr(), tokens, hidden, ldx, router->data_ptr(), ldr,
-                                      reinterpret_cast<const fp8_mx4_experts*>(v[0]),
-                                      reinterpret_cast<const fp8_mx4_experts*>(v[1]), v[2], v[3], top_k, (int32_t)v[5],
-                                      y.data_ptr(), hidden, data<int32_t>(ids), data<float>(weights), ws->data_ptr(),
-                                      (size_t)ws->numel(), nullptr, stream());
+    at::Tensor y, ids, weights;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        y = fresh({tokens, hidden}, {hidden, 1}, at::kBFloat16, *x);
+        ids = fresh({tokens, top_k}, {top_k, 1}, at::kInt, *x);
+        weights = fresh({tokens, top_k}, {top_k, 1}, at::kFloat, *x);
+        st = fp8_mx4_moe(x->data_ptr(), tokens, hidden, ldx, router->data_ptr(), ldr,
+                         reinterpret_cast<const fp8_mx4_experts*>(v[0]),
+                         reinterpret_cast<const fp8_mx4_experts*>(v[1]), v[2], v[3], top_k, (int32_t)v[5],
+                         y.data_ptr(), hidden, data<int32_t>(ids), data<float>(weights), ws->data_ptr(),
+                         (size_t)ws->numel(), nullptr, stream());
+    }
     if (st != FP8_OK) return PyLong_FromLong(st);
     PyObject* out = PyTuple_New(3);
     if (!out) return nullptr;

@@ -409,3 +409,39 @@ def test_mm_counts_only_the_outputs_there_are(m, n, k):
         ctr = fm.Counters()
         y = fm.mx4_mm(a, b, counters=ctr)
         assert torch.equal(torch.isnan(y).cpu(), nan) and ctr.read()["nonfinite_out"] == int(nan.sum())
+
+
+def test_calls_let_other_threads_run():
+    """A call releases the interpreter while it enqueues: another thread gets
+    on although the switch interval never ends."""
+    import sys
+    import threading
+    import time
+    x = _x(64, 512).cuda()
+    q, _ = fm.mx4_quantize(x)
+    turns, stop, started = [0], threading.Event(), threading.Event()
+
+    def count():
+        started.set()
+        while not stop.is_set():
+            turns[0] += 1
+            time.sleep(1e-5)
+
+    old = sys.getswitchinterval()
+    thread = threading.Thread(target=count)
+    thread.start()
+    started.wait()
+    sys.setswitchinterval(1000.0)
+    try:
+        got = []
+        for call in (lambda: fm.mx4_quantize(x), lambda: fm.mx4_dequantize(q), lambda: fm.mx4_mm(q, q)):
+            before = turns[0]
+            for _ in range(3000):
+                call()
+            got.append(turns[0] - before)
+    finally:
+        sys.setswitchinterval(old)
+        stop.set()
+        thread.join()
+    torch.cuda.synchronize()
+    assert min(got) >= 30, got      # once in a hundred calls
