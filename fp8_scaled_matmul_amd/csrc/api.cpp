@@ -535,9 +535,8 @@ fp8_status fp8_mx4_quantize(const void* x, fp8_dtype dtype, int64_t rows, int64_
     if (q_t && (st = check_mx4(q_t, ldq_t, s_t, ps_t, cols, rows, "q_t")) != FP8_OK) return st;
     if (misaligned(x, dtype == FP8_IN_BF16 ? 2 : 4)) return fail(FP8_ERR_INVALID_ARG, "x: misaligned");
     if (misaligned(seed, 8)) return fail(FP8_ERR_INVALID_ARG, "seed: must be 8-byte aligned");
-    // one workgroup per 128 x 128 tile or 16 rows x 512 columns
-    if (cdiv(rows, 512) * cdiv(cols, 512) >= ((int64_t)1 << 26))
-        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "tensor too large");
+    if (mx4_quantize_items(rows, cols, q_t != nullptr) >= kMaxLaunch)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "tensor too large for one launch");
     if ((st = check_device()) != FP8_OK) return st;
     Mx4QuantArgs a;
     a.x = x;
@@ -567,8 +566,8 @@ fp8_status fp8_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, i
     if ((st = check_mx4(q, ldq, s, ps, rows, cols, "q")) != FP8_OK) return st;
     if ((st = check_2d(y, rows, cols, ldy, "y")) != FP8_OK) return st;
     if (misaligned(y, dtype == FP8_IN_BF16 ? 2 : 4)) return fail(FP8_ERR_INVALID_ARG, "y: misaligned");
-    if (cdiv(rows, 512) * cdiv(cols, 512) >= ((int64_t)1 << 27))
-        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "tensor too large");
+    if (mx4_dequantize_items(rows, cols) >= kMaxLaunch)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "tensor too large for one launch");
     if ((st = check_device()) != FP8_OK) return st;
     hipError_t e = launch_mx4_dequantize(q, ldq, s, ps, rows, cols, y, dtype, ldy, stream);
     return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_dequantize launch");
@@ -586,8 +585,7 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
     // byte offsets inside one 256-row operand or output tile are 32-bit
     if (m > 0 && n > 0 && (lda >= ((int64_t)1 << 22) || ldb >= ((int64_t)1 << 22) || ldc >= ((int64_t)1 << 21)))
         return fail(FP8_ERR_UNSUPPORTED_SHAPE, "lda, ldb must be below 2^22 and ldc below 2^21");
-    // tiles are 32 x 64 at least, one workgroup each
-    if (cdiv(m, 32) * cdiv(n, 64) >= ((int64_t)1 << 31)) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "output too large");
+    if (!mx4_gemm_fits(m, n)) return fail(FP8_ERR_UNSUPPORTED_SHAPE, "output too large");
     if ((st = check_device()) != FP8_OK) return st;
     Mx4GemmArgs g;
     g.a = a;
@@ -611,7 +609,8 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
 size_t fp8_mx4_moe_workspace_size(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner)
 {
     if (tokens <= 0 || tokens > kMoeMaxTokens || experts <= 0 || experts > kMoeMaxExperts || top_k <= 0 ||
-        top_k > kMoeMaxTopK || hidden <= 0 || hidden >= kMoeMaxWidth || inner <= 0 || inner >= kMoeMaxWidth)
+        top_k > kMoeMaxTopK || hidden <= 0 || hidden >= kMoeMaxWidth || inner <= 0 || inner >= kMoeMaxWidth ||
+        mx4_moe_items(tokens, experts, top_k, inner) >= kMaxLaunch)
         return 0;
     return mx4_moe_workspace(tokens, experts, top_k, hidden, inner);
 }
@@ -627,6 +626,8 @@ fp8_status fp8_mx4_moe(const void* x, int64_t tokens, int64_t hidden, int64_t ld
         inner >= kMoeMaxWidth)
         return fail(FP8_ERR_UNSUPPORTED_SHAPE,
                     "moe: at most 64 tokens, 512 experts, top_k 16; hidden and inner below 2^24");
+    if (mx4_moe_items(tokens, experts, top_k, inner) >= kMaxLaunch)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "moe: inner too large for one launch");
     fp8_status st;
     if ((st = check_2d(x, tokens, hidden, ldx, "x")) != FP8_OK) return st;
     if ((st = check_2d(router, experts, hidden, ldr, "router")) != FP8_OK) return st;

@@ -140,6 +140,9 @@ int gemm_num_cus();
 hipError_t launch_gemm_persistent(const GemmArgs& g, int num_cus, hipStream_t stream);
 hipError_t launch_gemm(const GemmArgs& g, hipStream_t stream);
 
+// A launch holds fewer than 2^32 work-items.
+constexpr int64_t kMaxLaunch = (int64_t)1 << 32;
+
 // 4-bit quantizer (mx4_quantize.hip).  Scale panels of 16 bytes a row lie
 // `sps` (`stps`) bytes apart.
 struct Mx4QuantArgs {
@@ -158,6 +161,9 @@ struct Mx4QuantArgs {
     fp8_counters* ctr;      // nullable
 };
 hipError_t launch_mx4_quantize(const Mx4QuantArgs& g, hipStream_t stream);
+// Work-items of their launches.
+int64_t mx4_quantize_items(int64_t rows, int64_t cols, bool transposed);
+int64_t mx4_dequantize_items(int64_t rows, int64_t cols);
 hipError_t launch_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t sps, int64_t rows,
                                  int64_t cols, void* y, int dtype, int64_t ldy, hipStream_t stream);
 
@@ -177,6 +183,9 @@ struct Mx4GemmArgs {
     fp8_counters* ctr;
 };
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream);
+// Whether the largest tiles, which need no workgroup each, can be numbered.
+bool mx4_gemm_fits(int64_t m, int64_t n);
+
 // Mixture-of-experts layer with 4-bit weights (mx4_moe.hip).
 struct Mx4MoeArgs {
     const void* x;
@@ -194,6 +203,8 @@ struct Mx4MoeArgs {
     fp8_counters* ctr;
 };
 size_t mx4_moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner);
+// Work-items of the largest of its launches.
+int64_t mx4_moe_items(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner);
 hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream);
 // Zeros (k = 0), in gemm.hip.
 hipError_t launch_zero_bf16(uint16_t* c, int m, int n, int64_t ldc, hipStream_t stream);

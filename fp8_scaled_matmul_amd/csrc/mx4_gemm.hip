@@ -253,13 +253,15 @@ __global__ void __launch_bounds__(64 * WR * WC) k_mx4_tile_gemm(MxArgs p)
     flush_counters(p.ctr, 0, 0, 0, nonfinite);
 }
 
+int tiles_of(int64_t size, int64_t tile) { return (int)((size + tile - 1) / tile); }
+
 template <int WR, int WC, int MF, int STAGES>
 hipError_t launch_tile(MxArgs p, hipStream_t stream)
 {
     constexpr int TM = 32 * MF * WR, TN = 64 * WC;
     constexpr int kLds = STAGES * ((TM + TN) * (kRowBytes + kScaleBytes));
-    p.tiles_m = (p.m + TM - 1) / TM;
-    p.tiles_n = (p.n + TN - 1) / TN;
+    p.tiles_m = tiles_of(p.m, TM);
+    p.tiles_n = tiles_of(p.n, TN);
     p.group_m = 4;
     const auto kernel = k_mx4_tile_gemm<WR, WC, MF, STAGES>;
     static mx4::LdsLimit limit;
@@ -517,8 +519,8 @@ __global__ void __launch_bounds__(kBigThreads, 2) k_mx4_big_gemm(MxArgs p)
 
 hipError_t launch_big(MxArgs p, hipStream_t stream)
 {
-    p.tiles_m = (p.m + kBig - 1) / kBig;
-    p.tiles_n = (p.n + kBig - 1) / kBig;
+    p.tiles_m = tiles_of(p.m, kBig);
+    p.tiles_n = tiles_of(p.n, kBig);
     p.group_m = 4;
     p.pair_store = p.pair_store && p.n % 2 == 0;
     static mx4::LdsLimit limit;
@@ -663,8 +665,8 @@ __global__ void __launch_bounds__(64 * KW) k_mx4_direct_gemm(MxArgs p)
 template <int RT, int CT, int KW, int U>
 hipError_t launch_direct(MxArgs p, hipStream_t stream)
 {
-    p.tiles_m = (p.m + 16 * CT - 1) / (16 * CT);
-    p.tiles_n = (p.n + 16 * RT - 1) / (16 * RT);
+    p.tiles_m = tiles_of(p.m, 16 * CT);
+    p.tiles_n = tiles_of(p.n, 16 * RT);
     p.group_m = 4;
     const int lds = KW * RT * CT * 1024;
     hipLaunchKernelGGL((k_mx4_direct_gemm<RT, CT, KW, U>), dim3(p.tiles_m * p.tiles_n), dim3(64 * KW), lds, stream, p);
@@ -672,6 +674,11 @@ hipError_t launch_direct(MxArgs p, hipStream_t stream)
 }
 
 }  // namespace
+
+bool mx4_gemm_fits(int64_t m, int64_t n)
+{
+    return ((m + kBig - 1) / kBig) * ((n + kBig - 1) / kBig) < (int64_t)1 << 31;
+}
 
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
 {
@@ -712,14 +719,16 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream)
     static constexpr struct {
         int tm, tn;
         double row;
-    } kTiles[] = {{16, 16, 1.0}, {16, 32, 1.0},     {16, 64, 1.0},     {32, 32, 1.0},
-                  {64, 32, 1.0}, {64, 64, 1.0}, {128, 128, 0.55}, {256, 256, 0.65}};
-    int best = 0;
+        int threads;        // of a tile; 0: workgroups walk the tiles
+    } kTiles[] = {{16, 16, 1.0, 256}, {16, 32, 1.0, 256}, {16, 64, 1.0, 256},    {32, 32, 1.0, 256},
+                  {64, 32, 1.0, 256}, {64, 64, 1.0, 128}, {128, 128, 0.55, 512}, {256, 256, 0.65, 0}};
+    int best = -1;
     double least = 0.0;
     for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
         const int64_t tiles = ((g.m + kTiles[i].tm - 1) / kTiles[i].tm) * ((g.n + kTiles[i].tn - 1) / kTiles[i].tn);
+        if (tiles * kTiles[i].threads >= kMaxLaunch) continue;
         const double cost = (double)((tiles + cus - 1) / cus) * (kTiles[i].tm + kTiles[i].tn) * kTiles[i].row;
-        if (i == 0 || cost < least) {
+        if (best < 0 || cost < least) {
             best = i;
             least = cost;
         }

@@ -843,6 +843,11 @@ struct MoeLayout {
     size_t arrived_rows, logits, xq, count, up_groups, groups, prob, aq, part, total;
     int64_t max_up_groups, max_groups;
 };
+// Most groups of `size` tokens: an expert's last may be short.
+int64_t most_groups(int64_t pairs, int64_t experts, int64_t size)
+{
+    return std::min(pairs, std::min(pairs, experts) + pairs / size);
+}
 MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner)
 {
     const auto up = [](int64_t v, int64_t a) { return (v + a - 1) / a * a; };
@@ -859,10 +864,8 @@ MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hid
     m.logits = take(std::max<int64_t>(kSplitBytes, route_splits(tokens, experts, hidden) * tokens * experts * 8));
     m.xq = take(tokens * hp * 2);
     m.count = take(8);
-    // an expert's last group may be short
-    const auto most = [&](int64_t size) { return std::min(pairs, std::min(pairs, experts) + pairs / size); };
-    m.max_up_groups = most(kUpTokens);
-    m.max_groups = most(kDownTokens);
+    m.max_up_groups = most_groups(pairs, experts, kUpTokens);
+    m.max_groups = most_groups(pairs, experts, kDownTokens);
     m.up_groups = take(m.max_up_groups * (int64_t)sizeof(MoeGroup));
     m.groups = take(m.max_groups * (int64_t)sizeof(MoeGroup));
     m.prob = take(pairs * 4);
@@ -877,6 +880,11 @@ MoeLayout moe_layout(int64_t tokens, int64_t experts, int64_t top_k, int64_t hid
 size_t mx4_moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t hidden, int64_t inner)
 {
     return moe_layout(tokens, experts, top_k, hidden, inner).total;
+}
+
+int64_t mx4_moe_items(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner)
+{
+    return most_groups(tokens * top_k, experts, kUpTokens) * ((inner + 31) / 32) * kUpThreads;
 }
 
 hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)

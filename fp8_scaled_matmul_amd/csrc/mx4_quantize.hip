@@ -511,27 +511,42 @@ __global__ void __launch_bounds__(kRowThreads) k_mx4_dequantize(Mx4DeqArgs p)
     }
 }
 
+int64_t panels_of(int64_t cols) { return (cols + mx4::kPanel - 1) / mx4::kPanel; }
+// Workgroups: of four waves that take kRowsPerWave rows of a panel each; of a
+// tile each, in column tiles to the end of the last scale panel and row tiles
+// to the end of the transposed copy's.
+int64_t row_groups(int64_t rows, int64_t cols)
+{
+    return ((rows + kRowsPerWave - 1) / kRowsPerWave * panels_of(cols) + kRowThreads / 64 - 1) / (kRowThreads / 64);
+}
+int64_t tile_groups(int64_t rows, int64_t cols)
+{
+    return panels_of(cols) * (mx4::kPanel / kTileCols) * panels_of(rows) * (mx4::kPanel / kTileRows);
+}
+
 template <int DT, bool SR, bool COUNT>
 hipError_t launch_dir(const Mx4Args& p, hipStream_t stream)
 {
     Mx4Args a = p;
     if (p.qt) {
-        // column tiles to the end of the last scale panel, row tiles to the
-        // end of the transposed copy's
-        a.tiles_c = (int)((p.cols + mx4::kPanel - 1) / mx4::kPanel) * (mx4::kPanel / kTileCols);
-        const int64_t tiles_r = (p.rows + mx4::kPanel - 1) / mx4::kPanel * (mx4::kPanel / kTileRows);
-        const dim3 grid((unsigned)(a.tiles_c * tiles_r));
+        a.tiles_c = (int)panels_of(p.cols) * (mx4::kPanel / kTileCols);
+        const dim3 grid((unsigned)tile_groups(p.rows, p.cols));
         hipLaunchKernelGGL((k_mx4_tile<DT, SR, COUNT>), grid, dim3(kTileThreads), 0, stream, a);
         return hipGetLastError();
     }
-    a.tiles_c = (int)((p.cols + mx4::kPanel - 1) / mx4::kPanel);
-    const int64_t items = (p.rows + kRowsPerWave - 1) / kRowsPerWave * a.tiles_c;
-    const dim3 grid((unsigned)((items + kRowThreads / 64 - 1) / (kRowThreads / 64)));
+    a.tiles_c = (int)panels_of(p.cols);
+    const dim3 grid((unsigned)row_groups(p.rows, p.cols));
     hipLaunchKernelGGL((k_mx4_rows<DT, SR, COUNT>), grid, dim3(kRowThreads), 0, stream, a);
     return hipGetLastError();
 }
 
 }  // namespace
+
+int64_t mx4_quantize_items(int64_t rows, int64_t cols, bool transposed)
+{
+    return transposed ? tile_groups(rows, cols) * kTileThreads : row_groups(rows, cols) * kRowThreads;
+}
+int64_t mx4_dequantize_items(int64_t rows, int64_t cols) { return row_groups(rows, cols) * kRowThreads; }
 
 hipError_t launch_mx4_quantize(const Mx4QuantArgs& g, hipStream_t stream)
 {
@@ -564,9 +579,8 @@ hipError_t launch_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s
                                  int64_t cols, void* y, int dtype, int64_t ldy, hipStream_t stream)
 {
     if (rows == 0 || cols == 0) return hipSuccess;
-    Mx4DeqArgs p{q, ldq, s, sps, rows, cols, y, ldy, (int)((cols + mx4::kPanel - 1) / mx4::kPanel)};
-    const int64_t items = (rows + kRowsPerWave - 1) / kRowsPerWave * p.panels;
-    const dim3 grid((unsigned)((items + kRowThreads / 64 - 1) / (kRowThreads / 64)));
+    Mx4DeqArgs p{q, ldq, s, sps, rows, cols, y, ldy, (int)panels_of(cols)};
+    const dim3 grid((unsigned)row_groups(rows, cols));
     if (dtype == FP8_IN_BF16)
         hipLaunchKernelGGL((k_mx4_dequantize<0>), grid, dim3(kRowThreads), 0, stream, p);
     else

@@ -346,7 +346,10 @@ fp8_status fp8_requant_weights(const fp8_weight_cache* caches, const void* const
  *   elements of other blocks whose code is +-0.  Counters follow q alone.
  *   q_t, s_t    optional: the quantization of the transpose x^T [cols, rows]
  *       (blocks of 32 rows of a column, with scales of their own).
- * x as in fp8_quantize, bf16 or fp32; rows and cols below 2^31. */
+ * x as in fp8_quantize, bf16 or fp32; rows and cols below 2^31.  One
+ * launch takes a tensor (else FP8_ERR_UNSUPPORTED_SHAPE): with a transposed
+ * copy ceil(rows/512) ceil(cols/512) below 2^20, without one (and to
+ * dequantize) ceil(rows/4) ceil(cols/512) at most 2^26 - 4. */
 fp8_status fp8_mx4_quantize(const void* x, fp8_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
                             uint8_t* q, int64_t ldq, uint8_t* s, int64_t ps,
                             uint8_t* q_t, int64_t ldq_t, uint8_t* s_t, int64_t ps_t,
@@ -362,7 +365,7 @@ fp8_status fp8_mx4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* s, i
  * products, fp32 sums in an order that the sizes alone set, one rounding to
  * nearest even.  Codes past k are read: they have to be 0 in A or B, and no scale
  * byte there 255 (as fp8_mx4_quantize leaves them).  lda, ldb below 2^22
- * bytes, ldc below 2^21, m, n and k below 2^31; k = 0 writes zeros.
+ * bytes (so k at most 2^23 - 256), ldc below 2^21, m below 2^31; k = 0 writes zeros.
  * ctr (may be NULL) counts nonfinite_out. */
 fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t psa,
                       const uint8_t* b, int64_t ldb, const uint8_t* sb, int64_t psb,
@@ -381,7 +384,9 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
  * and the chosen experts alone set.
  * A token whose x holds an Inf or NaN gets NaN in y.
  * ids int32 and weights fp32 [tokens, top_k], contiguous.  top_k <= 16,
- * experts <= 512; hidden, inner below 2^24, ldq below 2^26; ldx, ldr, ldy in elements.
+ * experts <= 512; hidden, inner below 2^24, ldq below 2^26, and
+ * ceil(inner/32) min(pairs, experts + pairs/16) below 2^24 for pairs = tokens
+ * top_k; ldx, ldr, ldy in elements.
  * workspace: fp8_mx4_moe_workspace_size() bytes (grows with tokens), 16-byte
  * aligned, ZERO before its first call and before one with other sizes than
  * tokens (it begins with counts that each call leaves zero), and no two calls

@@ -207,3 +207,32 @@ def test_moe_workspace_grows_with_tokens():
     for experts, top_k, hidden, inner in sizes:
         size = [fm.lib().fp8_mx4_moe_workspace_size(t, experts, top_k, hidden, inner) for t in range(1, 65)]
         assert size[0] > 0 and all(a <= b for a, b in zip(size, size[1:])), (experts, top_k, hidden, inner)
+
+
+@pytest.mark.parametrize("rows,cols,want_t", [
+    ((1 << 28) + 1, 1, False), ((1 << 19) + 1, 1 << 19, False), ((1 << 31) - 1, 1, False), ((1 << 29) + 1, 1, True),
+    (1, (1 << 29) + 1, True), (1 << 19, (1 << 19) + 1, True)])
+def test_tensors_too_large_for_one_launch(rows, cols, want_t):
+    """A launch holds fewer than 2^32 work-items: larger tensors are refused
+    as such."""
+    ldq, ldt = 128 * -(-cols // 256), 128 * -(-rows // 256)
+    st = fm.fp8_mx4_quantize(BAD, fm.BF16, rows, cols, cols, BAD, ldq, BAD, 16 * rows, BAD if want_t else None, ldt,
+                             BAD if want_t else None, 16 * cols, None, None, None)
+    assert st == fm.FP8_ERR_UNSUPPORTED_SHAPE
+    if not want_t:
+        st = fm.fp8_mx4_dequantize(BAD, ldq, BAD, 16 * rows, rows, cols, BAD, fm.BF16, cols, None)
+        assert st == fm.FP8_ERR_UNSUPPORTED_SHAPE
+
+
+def test_outputs_and_layers_too_large_for_one_launch():
+    m, n = (1 << 31) - 1, (1 << 21) - 1
+    st = fm.fp8_mx4_mm(BAD, 128, BAD, 0, BAD, 128, BAD, 0, m, n, 32, BAD, n, None, None)
+    assert st == fm.FP8_ERR_UNSUPPORTED_SHAPE
+    # 512 experts and 64 tokens' groups of 32-row tiles: 576 * 2^15 workgroups
+    assert fm.lib().fp8_mx4_moe_workspace_size(64, 512, 16, 64, 1 << 20) == 0
+    assert fm.lib().fp8_mx4_moe_workspace_size(64, 8, 2, 64, 1 << 20) > 0
+    inner = 1 << 20
+    w1 = fm.Mx4Experts(BAD, BAD, 128, 1 << 30, 32 * inner, 1 << 30)
+    w2 = fm.Mx4Experts(BAD, BAD, inner // 2, 1 << 30, 1024, 1 << 30)
+    st = fm.fp8_mx4_moe(BAD, 64, 64, 64, BAD, 64, w1, w2, 512, inner, 16, 1, BAD, 64, BAD, BAD, BAD, 1 << 60, None, None)
+    assert st == fm.FP8_ERR_UNSUPPORTED_SHAPE
