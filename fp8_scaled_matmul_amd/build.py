@@ -1,12 +1,15 @@
 """Build the HIP library libfp8mi.so in-tree for gfx950 with hipcc, and the
 extension module _fp8mi_torch.so that calls it with torch tensors.
 
-Usage: python -m fp8_scaled_matmul_amd.build   (or call build()).
+Usage: python -m fp8_scaled_matmul_amd.build   (or call build()).  The library
+needs hipcc alone; the extension module torch and g++, too.  Where those are
+not there, the library is built all the same and the error says so.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -52,15 +55,20 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _hip_include() -> str:
+    """HIP's headers, from the compiler's place; HIPCC may be a name on PATH."""
+    hipcc = os.path.realpath(shutil.which(HIPCC) or HIPCC)
+    return os.path.join(os.path.dirname(os.path.dirname(hipcc)), "include")
+
+
 def _compile_binding() -> str:
     import torch
     os.makedirs(BUILD, exist_ok=True)
     obj = os.path.join(BUILD, "binding.cpp.o")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
-    rocm = os.path.dirname(os.path.dirname(HIPCC))
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-Wall", "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.join(ROOT, "include"),
-           "-isystem", inc, "-isystem", os.path.join(rocm, "include"),
+           "-isystem", inc, "-isystem", _hip_include(),
            "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -76,18 +84,24 @@ def _link(cmd: list, out: str) -> None:
     os.replace(tmp, out)
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every HIP/C++ source and link libfp8mi.so and the extension
-    module (always rebuilds)."""
+def _link_binding(obj: str) -> None:
     import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _link(["g++", "-shared", "-fPIC", obj, "-L", PKG, "-l:libfp8mi.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"], BINDING)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every HIP/C++ source and link libfp8mi.so, then the extension
+    module (always rebuilds)."""
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
-        binding = binding.result()
-    _link([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs], LIB)
-    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-    _link(["g++", "-shared", "-fPIC", binding, "-L", PKG, "-l:libfp8mi.so", "-Wl,-rpath,$ORIGIN", "-L", libs,
-           "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"], BINDING)
+        _link([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs], LIB)
+        try:
+            _link_binding(binding.result())
+        except Exception as e:
+            raise RuntimeError(f"{LIB} is built, but not its extension module: {e}") from e
     if verbose:
         print("built", LIB, BINDING)
     return LIB
