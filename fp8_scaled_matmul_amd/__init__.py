@@ -15,7 +15,9 @@ If the library has not been built, importing works but every call raises
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libfp8mi.so")
@@ -219,18 +221,29 @@ def _torch():
 _ext_module = None
 
 
+class _NoExt:
+    """Leaves every call to the code here."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _ext():
     """The extension module for calls that are all in order: it returns None
-    for any other, and the code here takes those."""
+    for any other, and the code here takes those.  Where it has not been built,
+    the code here takes all of them, through ctypes."""
     global _ext_module
     if _ext_module is None:
         _torch()        # its libraries come first
         try:
-            from . import _fp8mi_torch
+            _ext_module = importlib.import_module("._fp8mi_torch", __name__)
+        except ModuleNotFoundError:
+            warnings.warn("_fp8mi_torch.so is not there: short 4-bit calls take the host about 4 us more each "
+                          "(`python -m fp8_scaled_matmul_amd.build` builds it)", RuntimeWarning, stacklevel=3)
+            _ext_module = _NoExt()
         except ImportError as e:
             raise RuntimeError("_fp8mi_torch.so does not load: build it with "
                                "`python -m fp8_scaled_matmul_amd.build`") from e
-        _ext_module = _fp8mi_torch
     return _ext_module
 
 

@@ -445,3 +445,20 @@ def test_calls_let_other_threads_run():
         thread.join()
     torch.cuda.synchronize()
     assert min(got) >= 30, got      # once in a hundred calls
+
+
+def test_same_results_without_the_extension(monkeypatch):
+    x = _x(70, 300).cuda()
+    seed = torch.tensor([9], dtype=torch.int64, device="cuda")
+
+    def calls():
+        q, qt = fm.mx4_quantize(x, want_t=True, seed=seed)
+        a = fm.Mx4(q.q, q.s, 300)
+        e = fm.Mx4(torch.stack([qt.q[:140], qt.q[140:280]]), torch.stack([qt.s[:, :140], qt.s[:, 140:280]]), 70)
+        w2 = fm.Mx4(q.q[:, :128][None].repeat(2, 1, 1).contiguous(), q.s[None].repeat(2, 1, 1, 1), 70)
+        layer = fm.MoeMx4(torch.ones(2, 70, dtype=torch.bfloat16, device="cuda"), e, w2, 1, max_tokens=3)
+        return [q.q, q.s, qt.q, qt.s, fm.mx4_dequantize(a, torch.float32), fm.mx4_mm(a, q), *layer(x[:3, :70])]
+
+    want = calls()
+    monkeypatch.setattr(fm, "_ext_module", fm._NoExt())
+    assert all(torch.equal(g, w) for g, w in zip(calls(), want))

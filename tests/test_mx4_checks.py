@@ -236,3 +236,16 @@ def test_outputs_and_layers_too_large_for_one_launch():
     w2 = fm.Mx4Experts(BAD, BAD, inner // 2, 1 << 30, 1024, 1 << 30)
     st = fm.fp8_mx4_moe(BAD, 64, 64, 64, BAD, 64, w1, w2, 512, inner, 16, 1, BAD, 64, BAD, BAD, BAD, 1 << 60, None, None)
     assert st == fm.FP8_ERR_UNSUPPORTED_SHAPE
+
+
+def test_without_the_extension_python_takes_every_call(monkeypatch):
+    import sys
+    monkeypatch.setitem(sys.modules, fm.__name__ + "._fp8mi_torch", None)      # as if it had not been built
+    monkeypatch.setattr(fm, "_ext_module", None)
+    q, s = torch.zeros(5, 256, dtype=torch.uint8), torch.zeros(1, 5, 16, dtype=torch.uint8)
+    with pytest.warns(RuntimeWarning, match="not there"):
+        a = fm.Mx4(q, s, 500)
+    assert a.shape == (5, 500) and a._held == (256, 80)
+    test_mx4_layout_is_checked()
+    test_binding_rejects()
+    test_moe_binding_rejects()
