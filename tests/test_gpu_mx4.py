@@ -461,4 +461,5 @@ def test_same_results_without_the_extension(monkeypatch):
 
     want = calls()
     monkeypatch.setattr(fm, "_ext_module", fm._NoExt())
-    assert all(torch.equal(g, w) for g, w in zip(calls(), want))
+    # outputs past the range are NaN on both sides
+    assert all(torch.equal(g.view(torch.uint8), w.view(torch.uint8)) for g, w in zip(calls(), want))
