@@ -276,8 +276,11 @@ def _ptr(t):
 
 
 def _ld(t):
-    """Leading dimension of a 2-D tensor (an empty tensor's stride may be 0)."""
-    return t.stride(0) if t.shape[0] > 0 else max(t.shape[1], 1)
+    """Leading dimension of a 2-D tensor (an empty tensor's stride may be 0, a
+    single row's anything)."""
+    if t.shape[0] > 1:
+        return t.stride(0)
+    return max(t.stride(0) if t.shape[0] else 1, t.shape[1], 1)
 
 
 # Host-side checks of every tensor handed to the C ABI.  The library sees raw

@@ -13,6 +13,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+
 #include "fp8mi.h"
 
 namespace {
@@ -26,11 +28,11 @@ const at::Tensor* plain(PyObject* o)
 // On the GPU that kernels are launched on.
 bool here(const at::Tensor& t) { return t.is_cuda() && t.get_device() == c10::hip::current_device(); }
 
-// A matrix whose rows lie `ld` apart.
+// A matrix whose rows lie `ld` apart (a single row's stride may be anything).
 bool matrix(const at::Tensor& t, int64_t& ld)
 {
     if (t.dim() != 2 || t.numel() == 0 || (t.size(1) > 1 && t.stride(1) != 1)) return false;
-    ld = t.stride(0);
+    ld = t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1));
     return true;
 }
 

@@ -463,3 +463,18 @@ def test_same_results_without_the_extension(monkeypatch):
     monkeypatch.setattr(fm, "_ext_module", fm._NoExt())
     # outputs past the range are NaN on both sides
     assert all(torch.equal(g.view(torch.uint8), w.view(torch.uint8)) for g, w in zip(calls(), want))
+
+
+def test_a_single_row_may_have_any_row_stride():
+    """A column turned into a row: stride 1 between rows that there are not."""
+    x = _x(300, 1).cuda().t()
+    assert x.shape == (1, 300) and x.stride() == (1, 1)
+    same = x.contiguous().as_strided((1, 300), (300, 1))
+    want, want_t = fm.mx4_quantize(same, want_t=True)
+    for kw in ({}, {"counters": fm.Counters()}):
+        q, qt = fm.mx4_quantize(x, want_t=True, **kw)
+        assert all(torch.equal(a, b) for a, b in ((q.q, want.q), (q.s, want.s), (qt.q, want_t.q), (qt.s, want_t.s)))
+    row = torch.zeros(300, 1, dtype=torch.bfloat16, device="cuda").t()
+    assert torch.equal(fm.mx4_dequantize(q, out=row), fm.mx4_dequantize(q))
+    y = torch.zeros(1, 1, dtype=torch.bfloat16, device="cuda").expand(1, 1)
+    assert torch.equal(fm.mx4_mm(q, q, out=y), fm.mx4_mm(q, q))

@@ -320,3 +320,16 @@ def test_moe_fewer_tokens_through_a_layer_for_more(most, t, e, k, h, i):
     for n in (t, most):
         x = m.x(n, h)
         m.check(x, m.moe(x.cuda()))
+
+
+def test_moe_a_single_row_may_have_any_row_stride():
+    m = Layer(1, 1, 1, 200, 96, True)
+    x = m.x(1, 200).cuda()
+    want = [v.clone() for v in m.moe(x)]
+    column = x.reshape(200, 1).clone().t()
+    assert column.stride() == (1, 1)
+    m.moe.router = m.router.cuda().reshape(200, 1).t()
+    m.moe = fm.MoeMx4(m.moe.router, m.w1, m.w2, 1, max_tokens=1)
+    out = torch.zeros(200, 1, dtype=torch.bfloat16, device="cuda").t()
+    for got in (m.moe(column), m.moe(column, out=out)):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
