@@ -796,6 +796,9 @@ class MoeMx4:
         if wsb == 0:
             raise ValueError("at most 512 experts, top_k 16, hidden and inner below 2^24")
         self._ws = torch.zeros(wsb, dtype=torch.uint8, device=router.device)
+        if not torch.cuda.is_current_stream_capturing():
+            # calls on any stream find the zeros there
+            torch.cuda.current_stream(router.device).synchronize()
 
         def held(w):
             return Mx4Experts(w.q.data_ptr(), w.s.data_ptr(), w.q.stride(1) if w.rows > 1 else w.q.shape[2],

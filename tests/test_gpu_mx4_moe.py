@@ -333,3 +333,22 @@ def test_moe_a_single_row_may_have_any_row_stride():
     out = torch.zeros(200, 1, dtype=torch.bfloat16, device="cuda").t()
     for got in (m.moe(column), m.moe(column, out=out)):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_moe_built_on_a_busy_stream_and_called_on_another():
+    """The layer's workspace is ready when it has been built, whatever its
+    stream still had to do."""
+    m = Layer(5, 12, 3, 256, 96, True)
+    x = m.x(5, 256).cuda()
+    router = m.router.cuda()
+    want = [v.clone() for v in m.moe(x)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # memory that is not zero, for the allocator to hand out again
+    torch.full((m.moe._ws.numel(),), 0x5A, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(20_000_000)
+    layer = fm.MoeMx4(router, m.w1, m.w2, 3, max_tokens=5)
+    with torch.cuda.stream(side):
+        got = layer(x)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
