@@ -770,8 +770,9 @@ class MoeMx4:
     max_tokens, hidden] bf16 and returns (y bf16 [tokens, hidden], ids int32
     and weights fp32 [tokens, top_k]).  renormalize: the chosen experts'
     weights sum to 1 (else the softmax runs over all experts).  The tensors
-    are held by reference; their storage must stay where it is.  The layer
-    owns a workspace: one call at a time."""
+    are held by reference; their storage must stay where it is.  The last bits
+    of a token's y may depend on the tokens beside it.  The layer owns a
+    workspace: one call at a time."""
     MAX_TOKENS = 64
 
     def __init__(self, router, w1: Mx4, w2: Mx4, top_k: int, max_tokens: int = MAX_TOKENS, renormalize: bool = True,

@@ -378,10 +378,12 @@ fp8_status fp8_mx4_mm(const uint8_t* a, int64_t lda, const uint8_t* sa, int64_t 
  *   ids[t]  = the top_k largest l of a token in falling order, equal ones by the lower expert, NaN last
  *   weights = exp(l - max) / sum exp(l - max), the sum over ids[t] (renormalize) or over all experts
  *   y[t]    = sum over ids[t] of weight * W2[e] (silu(W1[e][:inner] x[t]) * (W1[e][inner:] x[t])), bf16
- * w1 [experts, 2 inner, hidden], w2 [experts, hidden, inner].  Weights
- * and x enter the products as they are (a weight past bf16's range as Inf), the
- * inner activations as fp32 numbers; sums are fp32, in an order that the sizes
- * and the chosen experts alone set.
+ * w1 [experts, 2 inner, hidden], w2 [experts, hidden, inner].  Weights and x
+ * enter the products as they are (a weight past bf16's range as Inf), the inner
+ * activations as fp32 numbers.  Sums of y are fp32, in an order that the sizes
+ * and the experts chosen by all tokens of the call set: the last bits of a
+ * token's y may depend on the tokens beside it.  ids and weights depend on their
+ * number alone, by the order of the 64-bit sums.
  * A token whose x holds an Inf or NaN gets NaN in y.
  * ids int32 and weights fp32 [tokens, top_k], contiguous.  top_k <= 16,
  * experts <= 512; hidden, inner below 2^24, ldq below 2^26, and

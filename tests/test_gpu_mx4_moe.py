@@ -352,3 +352,45 @@ def test_moe_built_on_a_busy_stream_and_called_on_another():
         got = layer(x)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("t,e,k,h,i", [(16, 512, 4, 2100, 16), (64, 128, 8, 4096, 16), (1, 300, 5, 4100, 16),
+                                       (5, 512, 3, 1600, 16), (3, 200, 2, 9000, 8)])
+def test_moe_router_takes_several_rounds(t, e, k, h, i):
+    """Long rows and many experts: one split and three rounds of reads with a
+    ragged end, two reads a round, eight splits, sums of several splits for
+    every number of experts a lane."""
+    m = Layer(t, e, k, h, i, False)
+    x = m.x(t, h)
+    m.check(x, m.moe(x.cuda()))
+
+
+def test_moe_other_tokens_change_a_token_within_its_bound_alone():
+    """Without the tokens that hold an Inf or NaN the others choose the same
+    experts with the same weights; their sums may take another order."""
+    m = Layer(20, 30, 4, 200, 96, True, seed=3)
+    x = m.x(20, 200)
+    bad = x.clone()
+    bad[3, 17] = float("nan")
+    bad[11, 199] = float("inf")
+    got = m.moe(bad.cuda())
+    ok = [t for t in range(20) if t not in (3, 11)]
+    m.check(x[ok], [v[ok] for v in got])
+    want = m.moe(x.cuda())
+    assert torch.equal(got[1][ok], want[1][ok]) and torch.equal(got[2][ok], want[2][ok])
+
+
+def test_moe_counts_only_the_outputs_there_are():
+    """Rows and tokens that fill no tile, with counts asked for, in either of
+    the second layer's forms."""
+    for t, e, k, h, i in ((3, 5, 2, 70, 33), (64, 8, 4, 2050, 1100)):
+        ctr = fm.Counters()
+        m = Layer(t, e, k, h, i, True, counters=ctr)
+        x = m.x(t, h)
+        y, ids, _ = m.moe(x.cuda())
+        assert torch.isfinite(y).all() and ctr.read()["nonfinite_out"] == 0
+        m.w2.s[int(ids[0, 0]), 0, h - 1, 0] = 255
+        y, ids2, _ = m.moe(x.cuda())
+        hit = (ids2 == ids[0, 0]).any(1)
+        assert torch.equal(torch.isnan(y)[:, h - 1], hit) and torch.isnan(y).sum() == hit.sum()
+        assert ctr.read()["nonfinite_out"] == int(hit.sum())
