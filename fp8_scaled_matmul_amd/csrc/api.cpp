@@ -116,10 +116,6 @@ fp8_status check_quantize_args(const void* x, fp8_dtype dtype, int64_t rows, int
     return FP8_OK;
 }
 
-// Limits of the mixture-of-experts layer: a 64-bit mask of an expert's tokens,
-// 32-bit offsets inside an expert's row tile.
-constexpr int64_t kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxWidth = (int64_t)1 << 24;
-
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 // A quantized 4-bit operand [rows, cols].

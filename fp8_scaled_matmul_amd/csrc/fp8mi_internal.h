@@ -186,7 +186,11 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& g, hipStream_t stream);
 // Whether the largest tiles, which need no workgroup each, can be numbered.
 bool mx4_gemm_fits(int64_t m, int64_t n);
 
-// Mixture-of-experts layer with 4-bit weights (mx4_moe.hip).
+// Mixture-of-experts layer with 4-bit weights (mx4_moe.hip).  Its limits: a
+// 64-bit mask of an expert's tokens, a thread each expert and pair in one
+// workgroup, 32-bit offsets inside an expert's row tile.
+constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 16;
+constexpr int64_t kMoeMaxWidth = (int64_t)1 << 24;
 struct Mx4MoeArgs {
     const void* x;
     int64_t tokens, hidden, ldx;

@@ -52,13 +52,6 @@ __device__ inline uint32_t mix(uint32_t v)
 __device__ inline uint32_t row_key(uint32_t row, uint32_t seed_lo) { return mix(row * 0x9E3779B1u + seed_lo); }
 __device__ inline uint32_t pair_key(uint32_t pair, uint32_t seed_hi) { return pair * 0x3C6EF373u + seed_hi; }
 
-// Two elements to a byte of codes (byte 0 of the result; the others are
-// unspecified), rounded to nearest even.
-__device__ inline uint32_t cvt_rne(float lo, float hi, float s)
-{
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, lo, hi, s, 0);
-}
-
 // Eight elements to a word of codes.
 __device__ inline uint32_t cast8_rne(const float x[8], float s)
 {

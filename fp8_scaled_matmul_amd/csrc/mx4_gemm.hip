@@ -29,7 +29,6 @@ using gemm::v4f;
 using gemm::v4u;
 using gemm::v8i;
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr int kRowBytes = 128;      // one K step: 256 elements of a row
 constexpr int kScaleBytes = 16;     // a row's scale bytes of one panel (two K steps)

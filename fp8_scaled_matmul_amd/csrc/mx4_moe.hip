@@ -43,7 +43,6 @@ typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 constexpr int kUnit = 256;          // K elements of a row of codes: rows are padded to whole units
 constexpr int kPieces = 3;          // bf16 numbers that add up to an fp32 one
-constexpr int kMaxTokens = 64, kMaxExperts = 512, kMaxTopK = 16;
 
 // Some tokens of an expert: the first ones of the mask, which lie among all
 // chosen (token, expert) pairs, in order of the experts, then of the tokens,
@@ -358,7 +357,7 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
 {
     __shared__ uint32_t s_sum[kRouteWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    static_assert(kRouteThreads >= kMaxExperts && kRouteThreads >= kMaxTokens * kMaxTopK, "a thread each");
+    static_assert(kRouteThreads >= kMoeMaxExperts && kRouteThreads >= kMoeMaxTokens * kMoeMaxTopK, "a thread each");
     mask[threadIdx.x] = 0;
     __syncthreads();
     const int t = threadIdx.x / p.top_k;
@@ -425,8 +424,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
         return;
     }
     __shared__ __attribute__((aligned(16))) double red[kRouteWaves][256];
-    __shared__ int s_ids[kMaxTokens * kMaxTopK];
-    __shared__ float s_weights[kMaxTokens * kMaxTopK];
+    __shared__ int s_ids[kMoeMaxTokens * kMoeMaxTopK];
+    __shared__ float s_weights[kMoeMaxTokens * kMoeMaxTopK];
     static_assert(sizeof(red) >= kRouteThreads * (sizeof(uint64_t) + sizeof(uint32_t)), "the lists' masks and places");
     const int tt = blockIdx.x / (p.tiles_e * p.splits), rest = blockIdx.x - tt * p.tiles_e * p.splits;
     const int split = rest / p.tiles_e, te = rest - split * p.tiles_e;
@@ -488,7 +487,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
             select<8>(p, at, s_ids, s_weights);
     }
     if (p.tiles_t > 1) {
-        if (!last_of(p.arrived + kMaxTokens / 16, (uint32_t)p.tiles_t)) return;
+        if (!last_of(p.arrived + kMoeMaxTokens / 16, (uint32_t)p.tiles_t)) return;
         if ((int)threadIdx.x < p.tokens * p.top_k) {
             s_ids[threadIdx.x] = agent_load(p.ids + threadIdx.x);
             s_weights[threadIdx.x] = agent_load(p.weights + threadIdx.x);
@@ -776,7 +775,7 @@ __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)
     if (p.shares > 1) {
         if (!last_of(p.arrived_rows + block, (uint32_t)p.shares)) return;
         // all reads of 8 outputs a thread (of 64 tokens) in flight at once
-        constexpr int kAt = kMaxTokens * kDownRows / kDownThreads;
+        constexpr int kAt = kMoeMaxTokens * kDownRows / kDownThreads;
         const int r = threadIdx.x % kDownRows, t0 = threadIdx.x / kDownRows;
         constexpr int kApart = kDownThreads / kDownRows;
         const float* from = p.part + row0 + min(r, rows - 1);
@@ -815,10 +814,10 @@ constexpr int kDownRowsFew = 32, kDownRowsMany = 64;
 int down_rows(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner)
 {
     const int64_t steps = tokens * top_k * ((inner + kUnit - 1) / kUnit) * ((hidden + 63) / 64);
-    return steps < 64 * 256 ? kDownRowsFew : kDownRowsMany;
+    return steps < 64 * (int64_t)gemm_num_cus() ? kDownRowsFew : kDownRowsMany;
 }
 
-// Workgroups that share a row block of y: enough for one on each of 256 CUs,
+// Workgroups that share a row block of y: enough for one on each CU,
 // of two steps a wave at least.  (64 tokens, 128 experts of 4096 x 1024: 213
 // us with 3, 197 with 4, 203 with 8; one token of 2048 x 1408: 26.6 with 4, 28.2
 // with 8.)
@@ -826,7 +825,7 @@ int down_shares(int64_t tokens, int64_t top_k, int64_t hidden, int64_t inner, in
 {
     const int64_t blocks = (hidden + rows - 1) / rows;
     const int64_t steps = tokens * top_k * ((inner + kUnit - 1) / kUnit);
-    return (int)std::clamp<int64_t>(std::min((256 + blocks - 1) / blocks, steps / (2 * kDownWaves)), 1, kMaxShares);
+    return (int)std::clamp<int64_t>(std::min((gemm_num_cus() + blocks - 1) / blocks, steps / (2 * kDownWaves)), 1, kMaxShares);
 }
 
 // K splits of the router: one round of reads a wave, as far as the partial sums
@@ -952,7 +951,7 @@ hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream)
     const auto kernel = rows == kDownRowsFew ? k_moe_down<kDownRowsFew / 16> : k_moe_down<kDownRowsMany / 16>;
     if (rows == kDownRowsMany) {
         static mx4::LdsLimit limit;
-        e = limit.raise(reinterpret_cast<const void*>(kernel), kDownWaves * kMaxTokens * kDownRowsMany * 4);
+        e = limit.raise(reinterpret_cast<const void*>(kernel), kDownWaves * kMoeMaxTokens * kDownRowsMany * 4);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(kernel, dim3(blocks * p.shares), dim3(kDownThreads), lds, stream, p);

@@ -25,7 +25,6 @@ namespace {
 
 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 // The same 16 bytes wherever an element may lie: one access of any alignment.
 typedef uint32_t u4x2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u4x4 __attribute__((ext_vector_type(4), aligned(4)));
