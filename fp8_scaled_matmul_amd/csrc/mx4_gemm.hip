@@ -6,9 +6,10 @@
 // v_mfma_scale_f32_32x32x64_f8f6f4 computes exactly that sum for a 32 x 32
 // tile and 64 K: lane l holds 32 consecutive elements (16 bytes) of row l % 32
 // of each operand and the byte of its own block's scale, so the scales cost no
-// arithmetic and the products are exact before the fp32 sum.  At the nominal
-// clock the instruction does about 10 PFLOP/s on the chip; on random codes,
-// fed from registers alone, 6.0 to 6.7 (power holds the clock near 1.6 GHz).
+// arithmetic and the products are exact before the fp32 sum (off by 2^-22.9 of
+// the summed sizes at most, measured).  At the nominal clock the instruction
+// does about 10 PFLOP/s on the chip; on random codes power holds the clock near
+// 1.6 GHz: 6.6 with operands in registers, 6.0 with a tile's reads from LDS.
 //
 // Three kernels: 256 x 256 tiles where the output has enough of them, 128 x
 // 128 tiles, and small tiles straight from memory where outputs are few.  The
@@ -279,10 +280,10 @@ hipError_t launch_tile(MxArgs p, hipStream_t stream)
 // ahead, so that a tile's first stages arrive while the one before is stored.
 // Fragments are read half a stage ahead of their products, which leaves one
 // barrier a stage: in its middle, once the whole of it has been read.
-// 16384 x 8192 x 7168: 465 us, 4.1 PFLOP/s, matrix units busy 55 % of the time
-// at 1.76 GHz; zeros for operands, which take little power, 350 us: the 34 KB of
-// a stage at 44 GB/s a CU.  (One tile a workgroup: 522 us; reads and products of
-// a stage not overlapped: 587 us on random operands.)
+// 16384 x 8192 x 7168: 460 to 480 us, 4.0 to 4.2 PFLOP/s, matrix units busy 53 %
+// of the time at 1.8 GHz; zeros for operands, which take little power, 358 us: the
+// 34 KB of a stage at 43.5 GB/s a CU.  (One tile a workgroup: 522 us; reads and
+// products of a stage not overlapped: 587 us on random operands.)
 constexpr int kBig = 256, kBigThreads = 512;
 constexpr int kStageBytes = 2 * kBig * 64;      // A's 256 rows, then B's
 constexpr int kPanelBytes = 2 * kBig * kScaleBytes;
@@ -292,7 +293,9 @@ constexpr int kBigStores = 64;                  // of a tile, by a wave
 
 // Position of 16-byte chunk c (0..3) in the 64-byte LDS row r: as for swz32,
 // 16 rows at one chunk fill the 16 slots of a 256-byte line and 32 rows with
-// two chunks the 32 of 512 bytes.  An involution in c.
+// two chunks the 32 of 512 bytes (timed alone, as fast as adjacent addresses;
+// the scale words, 16 bytes apart, take 1.3 times as long as adjacent ones).  An
+// involution in c.
 __device__ inline int swz64(int r, int c) { return c ^ (((r >> 2) & 1) | (((r >> 1) ^ (r >> 2) ^ (r >> 3)) & 1) << 1); }
 
 struct BigTile {

@@ -411,9 +411,10 @@ __device__ inline void list_reached(const MoeArgs& p, unsigned long long* mask, 
 // logits and a share of K, which their waves split.  The last of 16 tokens to
 // arrive selects, the last of those lists the reached experts.  The others
 // bring x to its places.  fp64 sums: products of bf16 are exact in fp64, so that
-// the chosen experts do not hang on the order of a sum.  One token, 64 experts
-// of 2048: 7.6 us, of which the logits 3.7, their way to one workgroup 0.6, the
-// selection 2.0 and the lists 1.3; 64 tokens, 128 experts of 4096: 14 us.
+// another order of a sum could choose other experts only between logits equal
+// to about 2^-50.  One token, 64 experts of 2048: 7.6 us (9.5 under a profiler),
+// of which the logits 3.7, their way to one workgroup 0.6, the selection 2.0 and
+// the lists 1.3; 64 tokens, 128 experts of 4096: 14 us.
 __global__ void __launch_bounds__(kRouteThreads) k_moe_route(MoeArgs p)
 {
     const int lane = threadIdx.x & 63;
@@ -546,8 +547,8 @@ __device__ inline void split(float v, uint32_t& a, uint32_t& b, uint32_t& c)
 
 // A workgroup takes an expert's 32 gate rows and the 32 up rows of the same
 // outputs, K over its waves, for a group of up to 16 tokens, a column each.
-// 64 tokens, 128 experts of 4096 x 1024: 106 us, 5.4 TB/s; one token, 8 experts
-// of 2048 x 1408: 9.7 us for 24.5 MB.  (64 tokens, the whole layer, 203 us: 201
+// 64 tokens, 128 experts of 4096 x 1024: 105 us, 5.3 TB/s; one token, 8 experts
+// of 2048 x 1408: 9.5 us for 24.5 MB.  (64 tokens, the whole layer, 203 us: 201
 // with 8 waves a workgroup, 205 with 2, 214 with the next unit's weights read
 // ahead; without the barrier below the compiler puts half of the reads off
 // until others have arrived: 212.)
@@ -637,7 +638,7 @@ constexpr int kMaxShares = 8;
 // are read two steps ahead and its columns one: reads come back in order, so
 // the columns of the next step are asked for before the weights of the one
 // after it, and no read in the loop hangs on a branch.
-// 64 tokens, 128 experts of 4096 x 1024: 80 us, 3.6 TB/s, of which 19 us are the
+// 64 tokens, 128 experts of 4096 x 1024: 80 us, 3.5 TB/s, of which 19 us are the
 // columns (from L2); one token, 8 experts of 2048 x 1408: 9 us for 12.2 MB.
 template <int R>
 __global__ void __launch_bounds__(kDownThreads, 2) k_moe_down(MoeArgs p)

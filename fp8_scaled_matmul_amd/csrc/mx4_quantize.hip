@@ -267,12 +267,16 @@ constexpr int kTileRows = 128, kTileCols = 128;
 // column) meet in LDS, so that a column's 128 codes leave as 64 adjacent
 // bytes.  In LDS column 8 c8 + c is the 64 bytes from 64 (16 c + c8) on, and
 // wave w's 16 bytes of it lie at chunk w ^ (c8 / 4): the lanes of a wave then
-// write to all 64 banks.  16384 x 7168 bf16: 71 us, 5.0 TB/s; 16384 x 2048:
-// 25 us, 4.1.  (256 rows and 8 waves left one workgroup a CU: 96 and 30 us;
-// forcing more waves onto a CU spills: 89 and 31 us.)  Rounding
-// stochastically, 8191 x 5000 takes 44 us, 2.8 TB/s: two random words and four
-// conversions a pair of elements, about 1300 VALU instructions for a lane's
-// 64 elements, are then half of the time.
+// write to all 64 banks.  Of the 16 columns that a wave reads at once eight start
+// at the same bank: such reads, two a lane against eight writes, take 1.35 times
+// as long as adjacent ones, and LDS is busy 7 % of the time at most.  16384 x 7168
+// bf16: 71 us, 5.1 TB/s; 16384 x 2048: 25 us, 4.1.  (256 rows and 8 waves left
+// one workgroup a CU: 96 and 30 us; forcing more waves onto a CU spills: 89 and
+// 31 us.)  Rounding stochastically, 8191 x 5000 takes 47 us, 2.7 TB/s: two
+// random words and four conversions a pair of elements, about 1300 VALU
+// instructions for a lane's 64 elements, are then half of the time, and a lane
+// that loads, computes and ends overlaps them with its reads only as far as
+// other waves do.
 template <int DT, bool SR, bool COUNT>
 __global__ void __launch_bounds__(kTileThreads) k_mx4_tile(Mx4Args p)
 {
