@@ -57,8 +57,9 @@ def train(tokens=4096, hidden=1024, out=2048, steps=40, lr=0.5):
 
 
 def _experts(count, rows, cols):
-    held = [fm.mx4_quantize(torch.randn(rows, cols, device="cuda") * cols ** -0.5)[0] for _ in range(count)]
-    return fm.Mx4(torch.stack([h.q for h in held]), torch.stack([h.s for h in held]), cols)
+    # one call for all of them, and views of what it gives
+    held, _ = fm.mx4_quantize(torch.randn(count * rows, cols, device="cuda") * cols ** -0.5)
+    return fm.Mx4(held.q.view(count, rows, -1), held.s.view(-1, count, rows, 16).transpose(0, 1), cols)
 
 
 def serve(experts=16, top_k=2, hidden=1024, inner=704, tokens=200):
