@@ -14,6 +14,7 @@ If the library has not been built, importing works but every call raises
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib
 import os
@@ -40,6 +41,8 @@ EXPORTED = [
     "fp8_requant_workspace_size", "fp8_requant_weights",
     "fp8_mx4_quantize", "fp8_mx4_dequantize", "fp8_mx4_mm",
     "fp8_mx4_moe_workspace_size", "fp8_mx4_moe",
+    "fp8_linear_ce_workspace_size", "fp8_linear_ce", "fp8_linear_ce_backward",
+    "fp8_moe_route_workspace_size", "fp8_moe_route", "fp8_moe_route_backward", "fp8_dropout",
     "fp8_counters_reset", "fp8_debug_set_wait_limit",
 ]
 
@@ -123,6 +126,21 @@ def lib():
         L.fp8_mx4_moe.restype = i32
         L.fp8_mx4_moe.argtypes = [vp, i64, i64, i64, vp, i64, ctypes.POINTER(Mx4Experts), ctypes.POINTER(Mx4Experts),
                                   i64, i64, i64, ctypes.c_int32, vp, i64, vp, vp, vp, sz, vp, vp]
+        L.fp8_linear_ce_workspace_size.restype = sz
+        L.fp8_linear_ce_workspace_size.argtypes = [i64, i64, i64, ctypes.c_int32]
+        L.fp8_linear_ce.restype = i32
+        L.fp8_linear_ce.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.fp8_linear_ce_backward.restype = i32
+        L.fp8_linear_ce_backward.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, ctypes.c_float, vp, vp, i64, vp, i64,
+                                             vp, i64, vp, sz, vp]
+        L.fp8_moe_route_workspace_size.restype = sz
+        L.fp8_moe_route_workspace_size.argtypes = [i64, i64]
+        L.fp8_moe_route.restype = i32
+        L.fp8_moe_route.argtypes = [vp, i32, i64, i64, i64, i64, ctypes.c_int32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.fp8_moe_route_backward.restype = i32
+        L.fp8_moe_route_backward.argtypes = [vp, i32, i64, i64, i64, i64, ctypes.c_int32, vp, vp, vp, vp, vp, vp, i64, vp]
+        L.fp8_dropout.restype = i32
+        L.fp8_dropout.argtypes = [vp, i32, i64, i64, i64, vp, i64, ctypes.c_double, vp, vp, i64, vp]
         L.fp8_counters_reset.restype = i32
         L.fp8_counters_reset.argtypes = [vp, vp]
         L.fp8_debug_set_wait_limit.restype = ctypes.c_int32
@@ -206,6 +224,34 @@ def fp8_mx4_moe(x, tokens, hidden, ldx, router, ldr, w1, w2, experts, inner, top
                 workspace, workspace_bytes, ctr, stream) -> int:
     return lib().fp8_mx4_moe(x, tokens, hidden, ldx, router, ldr, w1, w2, experts, inner, top_k, renormalize, y, ldy,
                              ids, weights, workspace, workspace_bytes, ctr, stream)
+
+
+def fp8_linear_ce(x, ldx, w, ldw, tokens, vocab, hidden, targets, softcap, loss, lse, workspace, workspace_bytes,
+                  stream) -> int:
+    return lib().fp8_linear_ce(x, ldx, w, ldw, tokens, vocab, hidden, targets, softcap, loss, lse, workspace,
+                               workspace_bytes, stream)
+
+
+def fp8_linear_ce_backward(x, ldx, w, ldw, tokens, vocab, hidden, targets, softcap, lse, grad_loss, grad_step, dx, lddx,
+                           dw, lddw, workspace, workspace_bytes, stream) -> int:
+    return lib().fp8_linear_ce_backward(x, ldx, w, ldw, tokens, vocab, hidden, targets, softcap, lse, grad_loss, grad_step,
+                                        dx, lddx, dw, lddw, workspace, workspace_bytes, stream)
+
+
+def fp8_moe_route(logits, dtype, tokens, experts, ld, top_k, renormalize, mask, ids, weights, counts, balance, workspace,
+                  workspace_bytes, stream) -> int:
+    return lib().fp8_moe_route(logits, dtype, tokens, experts, ld, top_k, renormalize, mask, ids, weights, counts, balance,
+                               workspace, workspace_bytes, stream)
+
+
+def fp8_moe_route_backward(logits, dtype, tokens, experts, ld, top_k, renormalize, ids, weights, counts, grad_weights,
+                           grad_balance, dlogits, ldd, stream) -> int:
+    return lib().fp8_moe_route_backward(logits, dtype, tokens, experts, ld, top_k, renormalize, ids, weights, counts,
+                                        grad_weights, grad_balance, dlogits, ldd, stream)
+
+
+def fp8_dropout(x, dtype, rows, cols, ld, residual, ldr, rate, seed, y, ldy, stream) -> int:
+    return lib().fp8_dropout(x, dtype, rows, cols, ld, residual, ldr, rate, seed, y, ldy, stream)
 
 
 def fp8_counters_reset(ctr, stream) -> int:
@@ -333,6 +379,14 @@ def _check_devices(*tensors):
             dev = t.device
         elif t.device != dev:
             raise ValueError(f"tensors of one call must share a device ({dev} vs {t.device})")
+
+
+def _on(device):
+    """Calls go to the current device and its current stream: the tensors'."""
+    torch = _torch()
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def scale_shape(gran: int, rows: int, cols: int) -> tuple[int, ...]:
@@ -835,3 +889,174 @@ class MoeMx4:
                                 y.data_ptr(), _ld(y), ids.data_ptr(), weights.data_ptr(), self._ws.data_ptr(),
                                 self._ws.numel(), self.counters.ptr() if self.counters else None, _stream()))
         return y, ids, weights
+
+
+# ---------------------------------------------------------------- around the linear layers
+def _workspace(workspace, need: int, device):
+    """The caller's workspace if it is large enough, or a new one."""
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace needs {need} bytes, got {workspace.numel()}")
+    return workspace
+
+
+def _check_head(x, w, targets, softcap, workspace):
+    torch = _torch()
+    _check_tensor(x, "x", (torch.bfloat16,), unit_col_stride=True)
+    _check_tensor(w, "w", (torch.bfloat16,), unit_col_stride=True)
+    if x.shape[1] != w.shape[1]:
+        raise ValueError(f"x and w disagree on their columns: {x.shape[1]} and {w.shape[1]}")
+    _check_tensor(targets, "targets", (torch.int64,), (x.shape[0],), contiguous=True)
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", (torch.uint8,), contiguous=True)
+    softcap = float(softcap)
+    if not 0.0 <= softcap < float("inf"):
+        raise ValueError(f"softcap must be 0 (none) or positive, got {softcap}")
+    return x.shape[0], w.shape[0], x.shape[1], softcap
+
+
+def linear_cross_entropy(x, w, targets, softcap: float = 0.0, workspace=None):
+    """Softmax cross entropy of the logits x w^T (capped to softcap tanh(l /
+    softcap) where softcap is not 0), which are never written: x [tokens,
+    hidden] and w [vocab, hidden] bf16, targets int64 [tokens].  Returns (loss,
+    lse) fp32 [tokens], lse the logarithm of the sum of the exponentials, which
+    the backward pass needs.  A negative target leaves its token out (loss 0);
+    one past the vocabulary gives NaN.  workspace: optional uint8 device tensor of
+    fp8_linear_ce_workspace_size(tokens, vocab, hidden, 0) bytes."""
+    torch = _torch()
+    tokens, vocab, hidden, softcap = _check_head(x, w, targets, softcap, workspace)
+    _check_devices(x, w, targets, workspace)
+    with _on(x.device):
+        loss = torch.empty(tokens, dtype=torch.float32, device=x.device)
+        lse = torch.empty(tokens, dtype=torch.float32, device=x.device)
+        ws = _workspace(workspace, lib().fp8_linear_ce_workspace_size(tokens, vocab, hidden, 0), x.device)
+        check(fp8_linear_ce(x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), tokens, vocab, hidden, targets.data_ptr(), softcap,
+                            loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream()))
+    return loss, lse
+
+
+def linear_cross_entropy_backward(x, w, targets, lse, grad_loss, softcap: float = 0.0, want_x: bool = True,
+                                  want_w: bool = True, out_x=None, out_w=None, workspace=None):
+    """(dx, dw) bf16 of linear_cross_entropy's losses, None for what is not
+    wanted.  lse is the forward's; grad_loss fp32 [tokens], the losses'
+    gradients (an expanded scalar, too).  Tokens whose target lies outside the
+    vocabulary add nothing, whatever x and grad_loss hold there.  workspace:
+    optional uint8 device tensor of fp8_linear_ce_workspace_size(tokens, vocab,
+    hidden, 1) bytes."""
+    torch = _torch()
+    tokens, vocab, hidden, softcap = _check_head(x, w, targets, softcap, workspace)
+    _check_tensor(lse, "lse", (torch.float32,), (tokens,), contiguous=True)
+    _check_tensor(grad_loss, "grad_loss", (torch.float32,), (tokens,))
+    for out, name, wanted, shape in ((out_x, "out_x", want_x, x.shape), (out_w, "out_w", want_w, w.shape)):
+        if out is not None:
+            if not wanted:
+                raise ValueError(f"{name} given for a gradient that is not wanted")
+            _check_tensor(out, name, (torch.bfloat16,), shape, unit_col_stride=True)
+    _check_devices(x, w, targets, lse, grad_loss, out_x, out_w, workspace)
+    with _on(x.device):
+        dx = out_x if out_x is not None or not want_x else torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        dw = out_w if out_w is not None or not want_w else torch.empty(w.shape, dtype=torch.bfloat16, device=x.device)
+        ws = _workspace(workspace, lib().fp8_linear_ce_workspace_size(tokens, vocab, hidden, 1), x.device)
+        check(fp8_linear_ce_backward(x.data_ptr(), _ld(x), w.data_ptr(), _ld(w), tokens, vocab, hidden, targets.data_ptr(),
+                                     softcap, lse.data_ptr(), grad_loss.data_ptr(), grad_loss.stride(0) if tokens > 1 else 0,
+                                     _ptr(dx), _ld(dx) if want_x else 0, _ptr(dw), _ld(dw) if want_w else 0,
+                                     ws.data_ptr(), ws.numel(), _stream()))
+    return dx, dw
+
+
+class Route:
+    """What moe_route chose: ids int32 and weights fp32 [tokens, top_k] (-1 and
+    0 for tokens left out), counts int32 [experts], balance fp32, a scalar."""
+    __slots__ = ("ids", "weights", "counts", "balance", "renormalize")
+
+    def __init__(self, ids, weights, counts, balance, renormalize: bool):
+        self.ids, self.weights, self.counts, self.balance, self.renormalize = ids, weights, counts, balance, renormalize
+
+
+def moe_route(logits, top_k: int, renormalize: bool = True, mask=None, workspace=None) -> Route:
+    """A mixture of experts' router in training: of logits [tokens, experts]
+    bf16 or fp32 the top_k experts of each token and their weights (chosen as
+    MoeMx4 chooses), the tokens of each expert and the balance loss experts
+    sum_e f_e P_e.  renormalize: a token's weights sum to 1 (else the softmax
+    runs over all experts).  mask: optional bool [tokens], False leaves a token
+    out; so does a row of -inf alone.  workspace: optional uint8 device tensor of
+    fp8_moe_route_workspace_size(tokens, experts) bytes."""
+    torch = _torch()
+    _check_tensor(logits, "logits", (torch.bfloat16, torch.float32), unit_col_stride=True)
+    tokens, experts = logits.shape
+    top_k = int(top_k)
+    if not 1 <= top_k <= experts:
+        raise ValueError(f"top_k must be 1 to {experts}, got {top_k}")
+    if mask is not None:
+        _check_tensor(mask, "mask", (torch.bool,), (tokens,), contiguous=True)
+    if workspace is not None:
+        _check_tensor(workspace, "workspace", (torch.uint8,), contiguous=True)
+    _check_devices(logits, mask, workspace)
+    with _on(logits.device):
+        new, device = torch.empty, logits.device
+        ids = new((tokens, top_k), dtype=torch.int32, device=device)
+        weights = new((tokens, top_k), dtype=torch.float32, device=device)
+        counts = new(experts, dtype=torch.int32, device=device)
+        balance = new((), dtype=torch.float32, device=device)
+        ws = _workspace(workspace, lib().fp8_moe_route_workspace_size(tokens, experts), device)
+        check(fp8_moe_route(logits.data_ptr(), _dtype_code(logits), tokens, experts, _ld(logits), top_k, bool(renormalize),
+                            _ptr(mask), ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), balance.data_ptr(),
+                            ws.data_ptr(), ws.numel(), _stream()))
+    return Route(ids, weights, counts, balance, bool(renormalize))
+
+
+def moe_route_backward(logits, route: Route, grad_weights=None, grad_balance=None, out=None):
+    """The logits' gradient, in their type, from those of route.weights (fp32
+    [tokens, top_k]) and route.balance (fp32, one element); None counts as 0."""
+    torch = _torch()
+    _check_tensor(logits, "logits", (torch.bfloat16, torch.float32), unit_col_stride=True)
+    tokens, experts = logits.shape
+    if not isinstance(route, Route):
+        raise ValueError(f"route must be a Route, got {type(route).__name__}")
+    top_k = route.ids.shape[-1]
+    _check_tensor(route.ids, "route.ids", (torch.int32,), (tokens, top_k), contiguous=True)
+    _check_tensor(route.weights, "route.weights", (torch.float32,), (tokens, top_k), contiguous=True)
+    _check_tensor(route.counts, "route.counts", (torch.int32,), (experts,), contiguous=True)
+    if grad_weights is not None:
+        _check_tensor(grad_weights, "grad_weights", (torch.float32,), (tokens, top_k), contiguous=True)
+    if grad_balance is not None:
+        _check_tensor(grad_balance, "grad_balance", (torch.float32,))
+        if grad_balance.numel() != 1:
+            raise ValueError(f"grad_balance must have one element, got shape {tuple(grad_balance.shape)}")
+    if out is not None:
+        _check_tensor(out, "out", (logits.dtype,), (tokens, experts), unit_col_stride=True)
+    _check_devices(logits, route.ids, route.weights, route.counts, grad_weights, grad_balance, out)
+    with _on(logits.device):
+        dl = out if out is not None else torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+        check(fp8_moe_route_backward(logits.data_ptr(), _dtype_code(logits), tokens, experts, _ld(logits), top_k,
+                                     route.renormalize, route.ids.data_ptr(), route.weights.data_ptr(),
+                                     route.counts.data_ptr(), _ptr(grad_weights), _ptr(grad_balance), dl.data_ptr(), _ld(dl),
+                                     _stream()))
+    return dl
+
+
+def dropout(x, rate: float, seed, residual=None, out=None):
+    """x [rows, cols] bf16 or fp32 with each element dropped with probability
+    rate (to the nearest 65536th) and the others scaled by its inverse, added
+    to residual where given.  seed: an int64 device tensor of one element (a
+    captured graph reads it anew at each replay); the backward pass is
+    dropout(dy, rate, seed).  out may be x or residual."""
+    torch = _torch()
+    _check_tensor(x, "x", (torch.bfloat16, torch.float32), unit_col_stride=True)
+    rows, cols = x.shape
+    rate = float(rate)
+    if not 0.0 <= rate <= 1.0:
+        raise ValueError(f"rate must be from 0 to 1, got {rate}")
+    _check_tensor(seed, "seed", (torch.int64,), (1,))
+    for t, name in ((residual, "residual"), (out, "out")):
+        if t is not None:
+            _check_tensor(t, name, (x.dtype,), (rows, cols), unit_col_stride=True)
+    _check_devices(x, seed, residual, out)
+    with _on(x.device):
+        y = out if out is not None else torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        check(fp8_dropout(x.data_ptr(), _dtype_code(x), rows, cols, _ld(x), _ptr(residual),
+                          _ld(residual) if residual is not None else 0, rate, seed.data_ptr(), y.data_ptr(), _ld(y),
+                          _stream()))
+    return y

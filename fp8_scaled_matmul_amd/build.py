@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libfp8mi.so")
 BINDING = os.path.join(PKG, "_fp8mi_torch.so")
 
 SOURCES = ["quantize.hip", "gemm.hip", "gemm_persistent.hip", "gemm_astat.hip", "mx4_quantize.hip", "mx4_gemm.hip",
-           "mx4_moe.hip", "api.cpp"]
+           "mx4_moe.hip", "cross_entropy.hip", "moe_route.hip", "dropout.hip", "api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -6,6 +6,7 @@
 // here; workspaces come from the caller.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -136,6 +137,44 @@ fp8_status check_mx4(const uint8_t* q, int64_t ldq, const uint8_t* s, int64_t ps
     if (cols > 512 && ps < 16 * rows) return bad(FP8_ERR_INVALID_ARG, "scale panels are 16 rows bytes");
     if (misaligned(q, 16) || misaligned(s, 16) || ldq % 16 != 0 || ps % 16 != 0)
         return bad(FP8_ERR_INVALID_ARG, "q, s, their row and panel distances must be multiples of 16 bytes");
+    return FP8_OK;
+}
+
+fp8_status check_workspace(const void* p, size_t bytes, size_t need, const char* name)
+{
+    static thread_local char buf[160];
+    if (p && !misaligned(p, 16) && bytes >= need) return FP8_OK;
+    std::snprintf(buf, sizeof buf, "%s: workspace smaller than %zu bytes or misaligned", name, need);
+    return fail(FP8_ERR_INVALID_ARG, buf);
+}
+
+fp8_status check_linear_ce(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t vocab,
+                           int64_t hidden, const int64_t* targets, float softcap)
+{
+    if (vocab < 1 || hidden < 1) return fail(FP8_ERR_INVALID_ARG, "linear_ce: vocab and hidden are positive");
+    fp8_status st;
+    if ((st = check_2d(x, tokens, hidden, ldx, "x")) != FP8_OK) return st;
+    if ((st = check_2d(w, vocab, hidden, ldw, "w")) != FP8_OK) return st;
+    if (!(softcap >= 0.0f) || softcap > 1e30f) return fail(FP8_ERR_INVALID_ARG, "linear_ce: softcap is 0 or positive");
+    if (softcap != 0.0f && softcap < 1e-30f) return fail(FP8_ERR_INVALID_ARG, "linear_ce: softcap is 0 or at least 1e-30");
+    if (misaligned(x, 2) || misaligned(w, 2) || misaligned(targets, 8))
+        return fail(FP8_ERR_INVALID_ARG, "linear_ce: misaligned pointer");
+    if (tokens >= kCeMaxTokens || vocab >= kCeMaxVocab || ldx >= kCeMaxLd || ldw >= kCeMaxLd)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "linear_ce: tokens and vocab below 2^24, leading dimensions below 2^21");
+    if (tokens > 0 && !targets) return fail(FP8_ERR_INVALID_ARG, "linear_ce: null targets");
+    return FP8_OK;
+}
+
+fp8_status check_route(const void* logits, fp8_dtype dtype, int64_t tokens, int64_t experts, int64_t ld, int64_t top_k)
+{
+    if (!valid_dtype(dtype)) return fail(FP8_ERR_INVALID_ARG, "unknown input dtype");
+    if (experts < 1 || top_k < 1 || top_k > experts)
+        return fail(FP8_ERR_INVALID_ARG, "moe_route: experts are positive, top_k from 1 to experts");
+    fp8_status st;
+    if ((st = check_2d(logits, tokens, experts, ld, "logits")) != FP8_OK) return st;
+    if (misaligned(logits, dtype == FP8_IN_BF16 ? 2 : 4)) return fail(FP8_ERR_INVALID_ARG, "logits: misaligned");
+    if (experts > kMoeMaxExperts || top_k > kMoeMaxTopK || tokens >= kRouteMaxTokens)
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "moe_route: at most 512 experts, top_k 16, tokens below 2^27");
     return FP8_OK;
 }
 
@@ -664,6 +703,190 @@ fp8_status fp8_mx4_moe(const void* x, int64_t tokens, int64_t hidden, int64_t ld
     g.ctr = ctr;
     hipError_t e = launch_mx4_moe(g, stream);
     return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_mx4_moe launch");
+}
+
+size_t fp8_linear_ce_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, int32_t backward)
+{
+    if (tokens <= 0 || tokens >= kCeMaxTokens || vocab <= 0 || vocab >= kCeMaxVocab || hidden <= 0 || hidden >= kCeMaxLd)
+        return 0;
+    return backward ? ce_backward_workspace(tokens, vocab, hidden) : ce_forward_workspace(tokens, vocab, hidden);
+}
+
+fp8_status fp8_linear_ce(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t vocab,
+                         int64_t hidden, const int64_t* targets, float softcap, float* loss, float* lse, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream)
+{
+    fp8_status st;
+    if ((st = check_linear_ce(x, ldx, w, ldw, tokens, vocab, hidden, targets, softcap)) != FP8_OK) return st;
+    if (tokens == 0) return FP8_OK;
+    if (!loss || !lse || misaligned(loss, 4) || misaligned(lse, 4))
+        return fail(FP8_ERR_INVALID_ARG, "linear_ce: loss and lse are 4-byte aligned device pointers");
+    if ((st = check_workspace(workspace, workspace_bytes, ce_forward_workspace(tokens, vocab, hidden), "linear_ce")) != FP8_OK)
+        return st;
+    if ((st = check_device()) != FP8_OK) return st;
+    CeArgs g = {};
+    g.x = x;
+    g.ldx = ldx;
+    g.w = w;
+    g.ldw = ldw;
+    g.tokens = tokens;
+    g.vocab = vocab;
+    g.hidden = hidden;
+    g.targets = targets;
+    g.softcap = softcap;
+    g.loss = loss;
+    g.lse = lse;
+    g.ws = workspace;
+    hipError_t e = launch_ce_forward(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_linear_ce launch");
+}
+
+fp8_status fp8_linear_ce_backward(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t tokens, int64_t vocab,
+                                  int64_t hidden, const int64_t* targets, float softcap, const float* lse,
+                                  const float* grad_loss, int64_t grad_step, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    fp8_status st;
+    if ((st = check_linear_ce(x, ldx, w, ldw, tokens, vocab, hidden, targets, softcap)) != FP8_OK) return st;
+    if (dx && (st = check_2d(dx, tokens, hidden, lddx, "dx")) != FP8_OK) return st;
+    if (dw && (st = check_2d(dw, vocab, hidden, lddw, "dw")) != FP8_OK) return st;
+    if ((dx && lddx >= kCeMaxLd) || (dw && lddw >= kCeMaxLd))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "linear_ce: leading dimensions below 2^21");
+    if (misaligned(dx, 2) || misaligned(dw, 2)) return fail(FP8_ERR_INVALID_ARG, "linear_ce: misaligned gradient");
+    if (grad_step < 0) return fail(FP8_ERR_INVALID_ARG, "linear_ce: negative distance between the losses' gradients");
+    if (!dx && !dw) return FP8_OK;
+    if (tokens > 0) {
+        if (!lse || !grad_loss || misaligned(lse, 4) || misaligned(grad_loss, 4))
+            return fail(FP8_ERR_INVALID_ARG, "linear_ce: lse and grad_loss are 4-byte aligned device pointers");
+        if ((st = check_workspace(workspace, workspace_bytes, ce_backward_workspace(tokens, vocab, hidden), "linear_ce")) !=
+            FP8_OK)
+            return st;
+    }
+    if ((st = check_device()) != FP8_OK) return st;
+    CeArgs g = {};
+    g.x = x;
+    g.ldx = ldx;
+    g.w = w;
+    g.ldw = ldw;
+    g.tokens = tokens;
+    g.vocab = vocab;
+    g.hidden = hidden;
+    g.targets = targets;
+    g.softcap = softcap;
+    g.lse = const_cast<float*>(lse);
+    g.grad = grad_loss;
+    g.grad_step = grad_step;
+    g.dx = dx;
+    g.lddx = lddx;
+    g.dw = dw;
+    g.lddw = lddw;
+    g.ws = workspace;
+    hipError_t e = launch_ce_backward(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_linear_ce_backward launch");
+}
+
+size_t fp8_moe_route_workspace_size(int64_t tokens, int64_t experts)
+{
+    if (tokens <= 0 || tokens >= kRouteMaxTokens || experts <= 0 || experts > kMoeMaxExperts) return 0;
+    return route_workspace(tokens, experts);
+}
+
+fp8_status fp8_moe_route(const void* logits, fp8_dtype dtype, int64_t tokens, int64_t experts, int64_t ld, int64_t top_k,
+                         int32_t renormalize, const uint8_t* mask, int32_t* ids, float* weights, int32_t* counts,
+                         float* balance, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    fp8_status st;
+    if ((st = check_route(logits, dtype, tokens, experts, ld, top_k)) != FP8_OK) return st;
+    if (!counts || !balance || misaligned(counts, 4) || misaligned(balance, 4) || misaligned(ids, 4) || misaligned(weights, 4))
+        return fail(FP8_ERR_INVALID_ARG, "moe_route: outputs are 4-byte aligned device pointers");
+    if (tokens > 0) {
+        if (!ids || !weights) return fail(FP8_ERR_INVALID_ARG, "moe_route: null ids or weights");
+        if ((st = check_workspace(workspace, workspace_bytes, route_workspace(tokens, experts), "moe_route")) != FP8_OK)
+            return st;
+    }
+    if ((st = check_device()) != FP8_OK) return st;
+    RouteArgs g = {};
+    g.logits = logits;
+    g.dtype = dtype;
+    g.tokens = tokens;
+    g.experts = experts;
+    g.ld = ld;
+    g.top_k = top_k;
+    g.renormalize = renormalize != 0;
+    g.mask = mask;
+    g.ids = ids;
+    g.weights = weights;
+    g.counts = counts;
+    g.balance = balance;
+    g.ws = workspace;
+    hipError_t e = launch_route(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_moe_route launch");
+}
+
+fp8_status fp8_moe_route_backward(const void* logits, fp8_dtype dtype, int64_t tokens, int64_t experts, int64_t ld,
+                                  int64_t top_k, int32_t renormalize, const int32_t* ids, const float* weights,
+                                  const int32_t* counts, const float* grad_weights, const float* grad_balance,
+                                  void* dlogits, int64_t ldd, hipStream_t stream)
+{
+    fp8_status st;
+    if ((st = check_route(logits, dtype, tokens, experts, ld, top_k)) != FP8_OK) return st;
+    if ((st = check_2d(dlogits, tokens, experts, ldd, "dlogits")) != FP8_OK) return st;
+    if (misaligned(dlogits, dtype == FP8_IN_BF16 ? 2 : 4)) return fail(FP8_ERR_INVALID_ARG, "moe_route: misaligned dlogits");
+    if (tokens == 0) return FP8_OK;
+    if (!ids || !weights || !counts) return fail(FP8_ERR_INVALID_ARG, "moe_route: null ids, weights or counts");
+    if (misaligned(ids, 4) || misaligned(weights, 4) || misaligned(counts, 4) || misaligned(grad_weights, 4) ||
+        misaligned(grad_balance, 4))
+        return fail(FP8_ERR_INVALID_ARG, "moe_route: misaligned pointer");
+    if ((st = check_device()) != FP8_OK) return st;
+    RouteArgs g = {};
+    g.logits = logits;
+    g.dtype = dtype;
+    g.tokens = tokens;
+    g.experts = experts;
+    g.ld = ld;
+    g.top_k = top_k;
+    g.renormalize = renormalize != 0;
+    g.ids = const_cast<int32_t*>(ids);
+    g.weights = const_cast<float*>(weights);
+    g.counts = const_cast<int32_t*>(counts);
+    g.grad_weights = grad_weights;
+    g.grad_balance = grad_balance;
+    g.dlogits = dlogits;
+    g.ldd = ldd;
+    hipError_t e = launch_route_backward(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_moe_route_backward launch");
+}
+
+fp8_status fp8_dropout(const void* x, fp8_dtype dtype, int64_t rows, int64_t cols, int64_t ld, const void* residual,
+                       int64_t ldr, double rate, const uint64_t* seed, void* y, int64_t ldy, hipStream_t stream)
+{
+    if (!valid_dtype(dtype)) return fail(FP8_ERR_INVALID_ARG, "unknown input dtype");
+    if (!(rate >= 0.0 && rate <= 1.0)) return fail(FP8_ERR_INVALID_ARG, "dropout: rate is from 0 to 1");
+    fp8_status st;
+    if ((st = check_2d(x, rows, cols, ld, "x")) != FP8_OK) return st;
+    if (residual && (st = check_2d(residual, rows, cols, ldr, "residual")) != FP8_OK) return st;
+    if ((st = check_2d(y, rows, cols, ldy, "y")) != FP8_OK) return st;
+    const uintptr_t size = dtype == FP8_IN_BF16 ? 2 : 4;
+    if (misaligned(x, size) || misaligned(residual, size) || misaligned(y, size))
+        return fail(FP8_ERR_INVALID_ARG, "dropout: misaligned pointer");
+    if (!seed || misaligned(seed, 8)) return fail(FP8_ERR_INVALID_ARG, "seed: an 8-byte aligned device pointer");
+    if (rows >= ((int64_t)1 << 31) || cols >= ((int64_t)1 << 31))
+        return fail(FP8_ERR_UNSUPPORTED_SHAPE, "dropout: rows and cols below 2^31");
+    if ((st = check_device()) != FP8_OK) return st;
+    DropoutArgs g = {};
+    g.x = x;
+    g.dtype = dtype;
+    g.rows = rows;
+    g.cols = cols;
+    g.ld = ld;
+    g.residual = residual;
+    g.ldr = ldr;
+    g.cut = (uint32_t)std::nearbyint(rate * 65536.0);
+    g.seed = seed;
+    g.y = y;
+    g.ldy = ldy;
+    hipError_t e = launch_dropout(g, stream);
+    return e == hipSuccess ? FP8_OK : hip_fail(e, "fp8_dropout launch");
 }
 
 fp8_status fp8_counters_reset(fp8_counters* ctr, hipStream_t stream)

@@ -1,0 +1,310 @@
+// bf16 matrix products of the vocabulary loss, for gfx950: C = A B^T over
+// tiles, fp32 sums, with an epilogue of the caller's.
+//
+// An operand is K-contiguous (its rows are C's rows or columns, 16-byte reads
+// of 8 K each) or K-strided (its rows are K; ds_read_b64_tr_b16 hands a lane
+// 4 K of one column).  So the loss' three products need no transposed copy:
+//   logits  [v, t] = w [v, h] x [t, h]        both K-contiguous
+//   dx      [h, t] = w [v, h] dl [t, v]       A K-strided, B K-contiguous
+//   dw      [h, v] = x [t, h] dl [t, v]       both K-strided
+// C's rows are the contiguous dimension of what is stored: a fragment's 32
+// rows are dealt out so that a lane ends up with 16 MF adjacent ones.
+#pragma once
+
+#include <stdint.h>
+
+#include "gemm_common.h"
+
+namespace fp8mi {
+namespace ce {
+
+using gemm::v4f;
+using gemm::v4u;
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+
+constexpr int kStageK = 32;             // K of a stage: 64 bytes of a K-contiguous row
+constexpr int kRing = 4;                // stages in LDS
+
+struct Operand {
+    const uint8_t* p;
+    int64_t ld;                         // bytes between rows
+};
+
+struct GemmShape {
+    Operand a, b;
+    int m, n, k;                        // a row of a K-contiguous operand holds zeros from k to the next multiple of 8
+    int tiles_m, tiles_n, group_m;
+    int splits;                         // of K
+};
+
+// One unit of work: a tile and its range of stages.
+struct Item {
+    int id;                             // past the last: none
+    int tm, tn, split;
+    int first, end;                     // stages
+};
+
+// Linear item number to tile and split: numbers go to the XCDs in turn, so XCD
+// x takes a contiguous range of the order, which walks group_m tile rows at a
+// time through all tiles of one split, then of the next.
+__device__ inline Item item_of(const GemmShape& s, int id)
+{
+    Item it{id, 0, 0, 0, 0, 0};
+    const int tiles = s.tiles_m * s.tiles_n, total = tiles * s.splits;
+    if (id >= total) return it;
+    const int xcd = id & 7, local = id >> 3;
+    int t = xcd * (total >> 3) + min(xcd, total & 7) + local;
+    it.split = t / tiles;
+    t -= it.split * tiles;
+    const int in_group = s.group_m * s.tiles_n;
+    const int g = t / in_group;
+    const int first_m = g * s.group_m;
+    const int gsize = min(s.tiles_m - first_m, s.group_m);
+    const int r = t - g * in_group;
+    it.tm = first_m + r % gsize;
+    it.tn = r / gsize;
+    const int64_t stages = (s.k + kStageK - 1) / kStageK;
+    it.first = (int)(stages * it.split / s.splits);
+    it.end = (int)(stages * (it.split + 1) / s.splits);
+    return it;
+}
+
+// Position of 16-byte chunk c (0..3) in the 64-byte LDS row r of a
+// K-contiguous operand (an involution in c).  Fragment reads of 32 rows, in
+// order or dealt out, run at the rate of adjacent addresses (measured: 195 to
+// 203 bytes a clock and CU, adjacent ones 192).
+__device__ inline int swz64(int r, int c) { return c ^ (((r >> 2) & 1) | (((r >> 1) ^ (r >> 2) ^ (r >> 3)) & 1) << 1); }
+
+// A K-strided operand's stage holds 32 rows of 2 T bytes; its 32-byte granules
+// are permuted by the row, so that the 4 rows and 64 bytes of each which half
+// a wave reads lie in different banks (172 bytes a clock and CU; unpermuted 64).
+//   A: granules i and i + MF (the fragment's rows are dealt out)
+//   B: granules 2 j and 2 j + 1
+template <int MF>
+__device__ inline int swz_a(int row)
+{
+    if constexpr (MF == 4) return row & 3;
+    if constexpr (MF == 2) return (row & 1) | (row & 2) << 1;
+    return (row & 3) << 1;
+}
+template <int T>
+__device__ inline int swz_b(int row)
+{
+    if constexpr (T >= 128) return (row & 3) << 1;
+    if constexpr (T == 64) return row & 2;
+    return 0;
+}
+
+// The tile C[TM, TN] of one item: WR x WC waves of MF x NF fragments of 32 x
+// 32.  The stages of all of a workgroup's items are one stream in a ring of
+// four, filled by DMA four ahead, so an item's first stages arrive during the
+// epilogue of the one before.  Fragments are read half a stage ahead of their
+// products; one barrier a stage, in its middle, past which every wave has read
+// all of it.
+template <bool ATR, bool BTR, int WR, int WC, int MF, int NF>
+struct Tile {
+    static constexpr int W = WR * WC, TM = 32 * MF * WR, TN = 32 * NF * WC;
+    static constexpr int kStage = (TM + TN) * 64;
+    static constexpr int kLds = kRing * kStage;
+    // DMA instructions of a wave and stage; where an operand has fewer than
+    // waves, some repeat another's (the same bytes to the same place)
+    static constexpr int kA = TM / 16 >= W ? TM / 16 / W : 1;
+    static constexpr int kB = TN / 16 >= W ? TN / 16 / W : 1;
+    static constexpr int kPer = kA + kB;
+    static_assert((TM / 16 % W == 0 || TM / 16 < W) && (TN / 16 % W == 0 || TN / 16 < W), "whole DMA instructions");
+    static_assert(!ATR || TM == 256, "swz_a stays inside a row of 8 granules or more");
+
+    typedef v16f Acc[MF][NF];
+
+    // Epi: static constexpr int kStores, the vector memory operations that
+    // every call of it issues last, at least; operator()(item, acc).
+    template <typename Epi>
+    __device__ static void run(const GemmShape& s, uint8_t* lds, Epi& epi)
+    {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int lane = threadIdx.x & 63;
+        const uint32_t base = gemm::lds_addr(lds);
+
+        // ---- the stream of fills
+        Item f = item_of(s, blockIdx.x);
+        int ft = f.first, fslot = 0;
+        // K-contiguous: lane l brings chunk l % 4 of row l / 4 of 16; K-strided:
+        // 16 bytes of a row of 2 T.
+        const int kc_chunk = 16 * swz64(lane >> 2, lane & 3);
+        const auto first_dma = [&](int per, int t) { return t / 16 >= W ? wave * per : wave % (t / 16); };
+        const int ua = first_dma(kA, TM), ub = first_dma(kB, TN);
+        uint32_t va[kA], vb[kB];
+#pragma unroll
+        for (int j = 0; j < kA; ++j) {
+            const int byte = 1024 * (ua + j) + 16 * lane, row = byte / (2 * TM), in = byte % (2 * TM);
+            va[j] = ATR ? (uint32_t)(row * s.a.ld + (((in >> 5) ^ swz_a<MF>(row)) << 5) + (in & 31))
+                        : (uint32_t)((16 * (ua + j) + (lane >> 2)) * s.a.ld + kc_chunk);
+        }
+#pragma unroll
+        for (int j = 0; j < kB; ++j) {
+            const int byte = 1024 * (ub + j) + 16 * lane, row = byte / (2 * TN), in = byte % (2 * TN);
+            vb[j] = BTR ? (uint32_t)(row * s.b.ld + (((in >> 5) ^ swz_b<TN>(row)) << 5) + (in & 31))
+                        : (uint32_t)((16 * (ub + j) + (lane >> 2)) * s.b.ld + kc_chunk);
+        }
+        // Where an item's data begin, and how much there is from there on
+        // (less than 2^31: one stage's offsets never reach that).
+        const uint8_t *pa, *pb;
+        int64_t la, lb;
+        const uint32_t row_bytes = 2u * (uint32_t)((s.k + 7) & ~7);
+        const auto describe = [&]() {
+            const bool live = f.id < s.tiles_m * s.tiles_n * s.splits;
+            const int m0 = f.tm * TM, n0 = f.tn * TN;
+            const int64_t k0 = (int64_t)ft * kStageK;
+            if constexpr (ATR) {
+                pa = s.a.p + k0 * s.a.ld + 2 * (int64_t)m0;
+                la = (s.k - 1 - k0) * s.a.ld + 2 * (int64_t)(s.m - m0);
+            } else {
+                pa = s.a.p + m0 * s.a.ld;
+                la = (int64_t)(min(s.m - m0, TM) - 1) * s.a.ld + row_bytes;
+            }
+            if constexpr (BTR) {
+                pb = s.b.p + k0 * s.b.ld + 2 * (int64_t)n0;
+                lb = (s.k - 1 - k0) * s.b.ld + 2 * (int64_t)(s.n - n0);
+            } else {
+                pb = s.b.p + n0 * s.b.ld;
+                lb = (int64_t)(min(s.n - n0, TN) - 1) * s.b.ld + row_bytes;
+            }
+            if (!live) la = lb = 0;
+        };
+        describe();
+        const auto records = [](int64_t bytes) {
+            return (uint32_t)min(max(bytes, (int64_t)0), (int64_t)0x7FFFFFFF);
+        };
+        const auto fill = [&]() {
+            const uint32_t to = base + fslot * kStage;
+            const uint32_t kb = (uint32_t)ft * (2 * kStageK);
+            const bool past = kb + kc_chunk >= row_bytes;       // K-contiguous: behind the row's end
+            const v4u ra = gemm::make_rsrc(pa, records(la)), rb = gemm::make_rsrc(pb, records(lb));
+#pragma unroll
+            for (int j = 0; j < kA; ++j)
+                gemm::dma16(to + 1024 * (ua + j), ATR ? va[j] : past ? gemm::kOutOfRange : va[j] + kb, ra);
+#pragma unroll
+            for (int j = 0; j < kB; ++j)
+                gemm::dma16(to + TM * 64 + 1024 * (ub + j), BTR ? vb[j] : past ? gemm::kOutOfRange : vb[j] + kb, rb);
+            fslot = (fslot + 1) & (kRing - 1);
+            if constexpr (ATR) {
+                pa += kStageK * s.a.ld;
+                la -= kStageK * s.a.ld;
+            }
+            if constexpr (BTR) {
+                pb += kStageK * s.b.ld;
+                lb -= kStageK * s.b.ld;
+            }
+            if (++ft >= f.end && f.id < s.tiles_m * s.tiles_n * s.splits) {
+                f = item_of(s, f.id + gridDim.x);
+                ft = f.first;
+                describe();
+            }
+        };
+
+        // ---- the fragments
+        const int wm = (wave % WR) * 32 * MF, wn = (wave / WR) * 32 * NF;
+        const int c = lane & 31, half = lane >> 5;
+        // K 16 kk + 8 half .. + 7 of both operands.  K-contiguous: chunk half + 2 kk.
+        // A's row of instruction row c: 16 MF (c / 4 % 2) + 4 (c / 8) + c % 4
+        const int ar = 16 * MF * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
+        const int tk = 8 * half + ((lane & 15) >> 2);           // K-strided: this lane's row of a read
+        const int tc = (lane >> 4 & 1) * 4 + (lane & 3);        // and its 4 columns' place among the fragment's 32
+        uint32_t at[MF], bt[NF];
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            at[i] = ATR ? tk * 2 * TM + ((((wm + 16 * MF * (tc & 1) + 16 * i) >> 4) ^ swz_a<MF>(tk)) << 5) + (tc >> 1) * 8
+                        : (wm + ar + 16 * i) * 64 + 16 * swz64(ar, half);
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            bt[j] = TM * 64 + (BTR ? tk * 2 * TN + ((((wn + 32 * j) >> 4) + (tc >> 2) ^ swz_b<TN>(tk)) << 5) + (tc & 3) * 8
+                                   : (wn + 32 * j + c) * 64 + 16 * swz64(c, half));
+        v8bf fa[2][MF], fb[2][NF];
+        int slot = 0;
+        const auto get = [&](auto TR, uint32_t from, int kk, int row_bytes) -> v8bf {
+            if constexpr (decltype(TR)::value) {
+                struct {
+                    v4s lo, hi;
+                } v;
+                v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + from + 16 * kk * row_bytes));
+                v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + from + (16 * kk + 4) * row_bytes));
+                return __builtin_bit_cast(v8bf, v);
+            } else {
+                return *reinterpret_cast<const v8bf*>(lds + (from ^ (32u * kk)));
+            }
+        };
+        const auto read = [&](auto KK) {
+            constexpr int kk = decltype(KK)::value;
+            const uint32_t ring = slot * kStage;
+#pragma unroll
+            for (int j = 0; j < NF; ++j) fb[kk][j] = get(std::integral_constant<bool, BTR>{}, bt[j] + ring, kk, 2 * TN);
+#pragma unroll
+            for (int i = 0; i < MF; ++i) fa[kk][i] = get(std::integral_constant<bool, ATR>{}, at[i] + ring, kk, 2 * TM);
+        };
+        Acc acc;
+        // Matrix instructions lo .. hi - 1 of a half stage's MF NF.  What is
+        // written around a call stays on its side.
+        const auto products = [&](auto KK, int lo, int hi) {
+            constexpr int kk = decltype(KK)::value;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int m = 0; m < MF * NF; ++m)
+                if (m >= lo && m < hi)
+                    acc[m / NF][m % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][m / NF], fb[kk][m % NF],
+                                                                                  acc[m / NF][m % NF], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        const auto clear = [&]() {
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < NF; ++j)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        };
+        constexpr int kAll = MF * NF;
+        constexpr std::integral_constant<int, 0> k0{};
+        constexpr std::integral_constant<int, 1> k1{};
+        clear();
+#pragma unroll 1
+        for (int i = 0; i < kRing; ++i) fill();
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * kPer) : "memory");     // the first stage
+        gemm::barrier_lds();
+        read(k0);
+        int stored = 3;         // stages since the last epilogue's stores, up to 3
+        const int total = s.tiles_m * s.tiles_n * s.splits;
+        for (Item it = item_of(s, blockIdx.x); it.id < total; it = item_of(s, it.id + gridDim.x)) {
+            for (int t = it.first; t < it.end; ++t) {
+                products(k0, 0, kAll / 4);
+                read(k1);
+                products(k0, kAll / 4, kAll);
+                // The next stage has landed: the two after it are younger, and an
+                // epilogue's stores are to the three stages filled before them.
+                constexpr int kLoose = 2 * kPer + Epi::kStores < 63 ? 2 * kPer + Epi::kStores : 63;
+                if (stored < 3) {
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoose) : "memory");
+                    ++stored;
+                } else {
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kPer) : "memory");
+                }
+                // past this every wave has read the whole stage: its slot is free
+                gemm::barrier_lds();
+                products(k1, 0, kAll / 2);
+                fill();
+                slot = (slot + 1) & (kRing - 1);
+                read(k0);
+                products(k1, kAll / 2, kAll);
+            }
+            epi(it, acc, it.tm * TM + wm + 16 * MF * half, it.tn * TN + wn + c);
+            stored = 0;
+            clear();
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // the fills past the end
+    }
+};
+
+}  // namespace ce
+}  // namespace fp8mi

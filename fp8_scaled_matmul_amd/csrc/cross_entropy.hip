@@ -1,0 +1,621 @@
+// Softmax cross entropy of a projection onto a vocabulary, for gfx950:
+//   l = x w^T,  z = cap tanh(l / cap) or l,  lse = log sum_v exp z_v,
+//   loss = lse - z_target,
+// and its gradients
+//   dl = g (exp(z - lse) - [v = target]) (1 - (z / cap)^2),  dx = dl w,  dw = dl^T x.
+// The logits exist only as fp32 accumulators of a tile: the forward keeps of a
+// tile each token's maximum and sum of exponentials, the backward recomputes
+// them for a piece of the vocabulary at a time and writes dl, rounded to bf16,
+// for the two products that follow.
+#include <algorithm>
+
+#include "ce_gemm.h"
+#include "device_common.h"
+#include "fp8mi_internal.h"
+#include "mx4_common.h"
+
+namespace fp8mi {
+
+namespace {
+
+using ce::GemmShape;
+using ce::Item;
+using ce::v16f;
+using gemm::v4f;
+using gemm::v4u;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ inline float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// cap tanh(l / cap).  tanh u = u N / D, the convergent of Lambert's continued
+// fraction whose error is below 1e-9 of it for |u| <= 1; past that 1 - 2 /
+// (exp(2 |u|) + 1), which loses nothing there.
+__device__ inline float softcap(float l, float cap, float inv_cap)
+{
+    const float u = l * inv_cap, t = u * u;
+    const float n = __builtin_fmaf(__builtin_fmaf(21.0f, t, 1260.0f), t, 10395.0f);
+    const float d = __builtin_fmaf(__builtin_fmaf(t + 210.0f, t, 4725.0f), t, 10395.0f);
+    float z = l * n * __builtin_amdgcn_rcpf(d);
+    if (__any(!(t <= 1.0f))) {
+        const float far = __builtin_copysignf(
+            cap - 2.0f * cap * __builtin_amdgcn_rcpf(exp2_fast(2.0f * kLog2e * __builtin_fabsf(u)) + 1.0f), l);
+        z = t <= 1.0f ? z : l != l ? l : far;
+    }
+    return z;
+}
+
+// ------------------------------------------------------------------ epilogues
+// A lane holds, for tokens (columns) col + 32 j, 16 MF adjacent rows from
+// `row` on: acc[i][j][r] is row + 16 i + r.
+
+// The forward's: of each token and block of 32 MF vocabulary rows the maximum
+// and the sum of exp(z - maximum); the target's z, by the one lane that has it.
+template <int WR, int MF, int NF>
+struct StatsEpilogue {
+    static constexpr int kStores = NF;
+    int m, n;                   // vocabulary rows of this launch, tokens
+    int64_t v0;                 // its first row
+    int block0;                 // its first block
+    float cap, inv_cap;
+    const int64_t* targets;
+    float2* part;               // [blocks, n]
+    float* zt;
+
+    __device__ void operator()(const Item& it, v16f (&acc)[MF][NF], int row, int col) const
+    {
+        const int lane = threadIdx.x & 63;
+        const int wave_row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WR;
+        float2* to = part + (int64_t)(block0 + it.tm * WR + wave_row) * n;
+        const __amdgpu_buffer_rsrc_t rp = gemm::make_store_rsrc(to, (uint32_t)n * 8u);
+        const bool edge = (it.tm + 1) * (32 * MF * WR) > m;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int t = col + 32 * j;
+            if (cap != 0.0f) {
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) acc[i][j][r] = softcap(acc[i][j][r], cap, inv_cap);
+            }
+            if (edge) {
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (row + 16 * i + r >= m) acc[i][j][r] = -__builtin_inff();
+            }
+            const int64_t at = (t < n ? targets[t] : -1) - v0 - row;
+            if (__any(at >= 0 && at < 16 * MF)) {
+                float z = 0.0f;
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) z = at == 16 * i + r ? acc[i][j][r] : z;
+                if (at >= 0 && at < 16 * MF && t < n && row + at < m) zt[t] = z;
+            }
+            float mx = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            const float off = mx == -__builtin_inff() ? 0.0f : -mx * kLog2e;
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s += exp2_fast(__builtin_fmaf(acc[i][j][r], kLog2e, off));
+            s += __shfl_xor(s, 32, 64);
+            const uint32_t where = lane < 32 && t < n ? (uint32_t)t * 8u : gemm::kOutOfRange;
+            __builtin_amdgcn_raw_buffer_store_b64(
+                __builtin_bit_cast(__attribute__((__vector_size__(8))) unsigned int, float2{mx, s}), rp, (int)where, 0, 0);
+        }
+    }
+};
+
+// The backward's: dl, rounded to bf16 (by 2^-8 of each value at most, what the
+// operands' own type has; the matrix instruction takes one type), rows past
+// the vocabulary's end and tokens that do not count as zeros.
+template <int WR, int MF, int NF>
+struct GradEpilogue {
+    static constexpr int kStores = 2 * MF * NF;
+    int m, n;
+    int64_t v0, vocab;
+    float cap, inv_cap;
+    const int64_t* targets;
+    const float* lse;
+    const float* grad;          // of the losses
+    int64_t grad_step;
+    uint16_t* dl;               // [n, ld]
+    int64_t ld;
+
+    __device__ void operator()(const Item& it, v16f (&acc)[MF][NF], int row, int col) const
+    {
+        const int n0 = col & ~31;       // uniform: this wave's first token
+        const __amdgpu_buffer_rsrc_t rd = gemm::make_store_rsrc(
+            dl + (int64_t)__builtin_amdgcn_readfirstlane(n0) * ld,
+            (uint32_t)(max(min(n - __builtin_amdgcn_readfirstlane(n0), 32 * NF), 0) * ld * 2));
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int t = col + 32 * j;
+            int64_t at = -1;
+            float off = 0.0f, g = 0.0f;
+            if (t < n) {
+                at = targets[t];
+                off = -lse[t] * kLog2e;
+                g = grad[t * grad_step];
+            }
+            const bool counts = at >= 0 && at < vocab;
+            const int rel = counts ? (int)min(max(at - v0 - row, (int64_t)-1), (int64_t)(16 * MF)) : -1;
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                float d[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float z = acc[i][j][r], slope = 1.0f;
+                    if (cap != 0.0f) {
+                        z = softcap(z, cap, inv_cap);
+                        const float u = z * inv_cap;
+                        slope = __builtin_fmaf(-u, u, 1.0f);
+                    }
+                    float p = exp2_fast(__builtin_fmaf(z, kLog2e, off));
+                    p = rel == 16 * i + r ? p - 1.0f : p;
+                    d[r] = p * (cap != 0.0f ? g * slope : g);
+                    d[r] = counts && row + 16 * i + r < m ? d[r] : 0.0f;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v4u w;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[q] = gemm::pack_bf16(d[8 * h + 2 * q], d[8 * h + 2 * q + 1]);
+                    gemm::store16(w, (uint32_t)(((t - n0) * ld + row + 16 * i + 8 * h) * 2), rd);
+                }
+            }
+        }
+    }
+};
+
+// A gradient: fp32 planes (one for each split of K, added to what an earlier
+// piece of the vocabulary left), or bf16 at the end.
+template <int WR, int MF, int NF>
+struct OutEpilogue {
+    static constexpr int kStores = 0;
+    int m, n;                   // the gradient's columns and rows
+    float* plane;               // [splits, n, ld_plane], or null
+    int64_t ld_plane;           // a multiple of 16
+    int add;                    // onto the planes' contents
+    uint16_t* out;              // bf16 [n, ld], or null: to the planes
+    int64_t ld;
+    int wide;                   // 16-byte stores are in place
+
+    __device__ void operator()(const Item& it, v16f (&acc)[MF][NF], int row, int col) const
+    {
+        const int n0 = __builtin_amdgcn_readfirstlane(col & ~31);
+        const int rows = max(min(n - n0, 32 * NF), 0);
+        const __amdgpu_buffer_rsrc_t rp = gemm::make_store_rsrc(
+            plane + ((int64_t)it.split * n + n0) * ld_plane, plane ? (uint32_t)(rows * ld_plane * 4) : 0u);
+        const __amdgpu_buffer_rsrc_t ro = gemm::make_store_rsrc(
+            out + n0 * ld, out && rows ? (uint32_t)(((rows - 1) * ld + m) * 2) : 0u);
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            const int t = col + 32 * j;
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                const int first = row + 16 * i;
+                v4f v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    v[q] = v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                const uint32_t at = first < m ? (uint32_t)(((t - n0) * ld_plane + first) * 4) : gemm::kOutOfRange;
+                if (add) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        v[q] += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 16 * q), 0, 0));
+                }
+                if (!out) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) gemm::store16(__builtin_bit_cast(v4u, v[q]), at + 16 * q, rp);
+                } else if (wide) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        v4u w;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            w[q] = gemm::pack_bf16(v[2 * h + (q >> 1)][2 * (q & 1)], v[2 * h + (q >> 1)][2 * (q & 1) + 1]);
+                        gemm::store16(w, first + 8 * h < m ? (uint32_t)(((t - n0) * ld + first + 8 * h) * 2) : gemm::kOutOfRange,
+                                      ro);
+                    }
+                } else if (t < n) {
+                    uint16_t* to = out + t * ld + first;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (first + r < m) to[r] = gemm::to_bf16(v[r >> 2][r & 3]);
+                }
+            }
+        }
+    }
+};
+
+template <bool ATR, bool BTR, int WR, int WC, int MF, int NF, template <int, int, int> class Epi>
+__global__ void __launch_bounds__(64 * WR * WC, 2) k_ce_gemm(GemmShape s, Epi<WR, MF, NF> epi)
+{
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    ce::Tile<ATR, BTR, WR, WC, MF, NF>::run(s, lds, epi);
+}
+
+int tiles_of(int64_t size, int64_t tile) { return (int)((size + tile - 1) / tile); }
+
+template <bool ATR, bool BTR, int WR, int WC, int MF, int NF, template <int, int, int> class Epi, typename Init>
+hipError_t launch_tile(GemmShape s, Init init, hipStream_t stream)
+{
+    using T = ce::Tile<ATR, BTR, WR, WC, MF, NF>;
+    s.tiles_m = tiles_of(s.m, T::TM);
+    s.tiles_n = tiles_of(s.n, T::TN);
+    s.group_m = 4;
+    Epi<WR, MF, NF> epi;
+    init(epi);
+    const auto kernel = k_ce_gemm<ATR, BTR, WR, WC, MF, NF, Epi>;
+    static mx4::LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), T::kLds);
+    if (e != hipSuccess) return e;
+    const int64_t items = (int64_t)s.tiles_m * s.tiles_n * s.splits;
+    const int per_cu = 2 * T::kLds <= 160 * 1024 ? 2 : 1;
+    const int grid = (int)std::min<int64_t>(items, (int64_t)gemm_num_cus() * per_cu);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WR * WC), T::kLds, stream, s, epi);
+    return hipGetLastError();
+}
+
+// Tokens of a tile: the least of 32, 64, 128, 256 that holds them all.
+int token_tile(int64_t tokens) { return tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
+
+template <bool ATR, template <int, int, int> class Epi, typename Init>
+hipError_t launch_tokens(const GemmShape& s, Init init, hipStream_t stream)
+{
+    switch (token_tile(s.n)) {
+    case 32: return launch_tile<ATR, false, 4, 1, 2, 1, Epi>(s, init, stream);
+    case 64: return launch_tile<ATR, false, 4, 1, 2, 2, Epi>(s, init, stream);
+    case 128: return launch_tile<ATR, false, 4, 2, 2, 2, Epi>(s, init, stream);
+    default: return launch_tile<ATR, false, 2, 4, 4, 2, Epi>(s, init, stream);
+    }
+}
+int stat_rows(int64_t tokens) { return token_tile(tokens) <= 128 ? 64 : 128; }    // vocabulary rows of a block of statistics
+
+// ------------------------------------------------------------------ around the products
+// Rows of bf16 at 16-byte places with zeros behind them; with targets, rows of
+// tokens that do not count as zeros (their x may hold anything).
+__global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, int64_t rows, int cols, uint4* out,
+                                                 int chunks, const int64_t* targets, int64_t vocab, int aligned)
+{
+    const int64_t total = rows * chunks;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+        const int64_t r = u / chunks;
+        const int c = (int)(u - r * chunks) * 8;
+        uint4 v = {0, 0, 0, 0};
+        const int64_t t = targets ? targets[r] : 0;
+        if (t >= 0 && t < vocab) {
+            const uint16_t* from = x + r * ld + c;
+            if (aligned && c + 8 <= cols) {
+                v = *reinterpret_cast<const uint4*>(from);
+            } else {
+                uint16_t e[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? from[i] : 0;
+                v = uint4{e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                          e[6] | (uint32_t)e[7] << 16};
+            }
+        }
+        out[u] = v;
+    }
+}
+
+// Of each token the blocks' maxima and sums to lse, and the loss.  TX tokens a
+// workgroup, 256 / TX threads each over the blocks.
+template <int TX>
+__global__ void __launch_bounds__(256) k_ce_loss(const float2* part, int blocks, int n, const float* zt,
+                                                 const int64_t* targets, int64_t vocab, float* loss, float* lse)
+{
+    __shared__ float2 sh[256];
+    const int x = threadIdx.x % TX, y = threadIdx.x / TX;
+    const int t = blockIdx.x * TX + x;
+    constexpr int TY = 256 / TX;
+    const auto join = [](float2 a, float2 b) {
+        const float m = fmaxf(a.x, b.x);
+        if (m == -__builtin_inff()) return float2{m, a.y + b.y};
+        return float2{m, a.y * exp2_fast((a.x - m) * kLog2e) + b.y * exp2_fast((b.x - m) * kLog2e)};
+    };
+    float2 a = {-__builtin_inff(), 0.0f};
+    if (t < n) {
+        int b = y;
+        for (; b + 3 * TY < blocks; b += 4 * TY) {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = part[(int64_t)(b + i * TY) * n + t];
+            a = join(a, join(join(v[0], v[1]), join(v[2], v[3])));
+        }
+        for (; b < blocks; b += TY) a = join(a, part[(int64_t)b * n + t]);
+    }
+    sh[threadIdx.x] = a;
+    __syncthreads();
+    for (int h = TY / 2; h >= 1; h >>= 1) {
+        if (y < h) sh[threadIdx.x] = join(sh[threadIdx.x], sh[threadIdx.x + h * TX]);
+        __syncthreads();
+    }
+    if (y == 0 && t < n) {
+        const float2 s = sh[x];
+        const float l = s.x + __builtin_amdgcn_logf(s.y) * kLn2;
+        const int64_t at = targets[t];
+        lse[t] = l;
+        loss[t] = at < 0 ? 0.0f : at < vocab ? l - zt[t] : __builtin_nanf("");
+    }
+}
+
+// The planes' sum, in their order, to bf16.
+__global__ void __launch_bounds__(256) k_ce_reduce(const float* plane, int splits, int64_t rows, int cols, int64_t ld_plane,
+                                                   uint16_t* out, int64_t ld, int wide)
+{
+    const int chunks = (int)(ld_plane / 8);
+    const int64_t total = rows * chunks;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+        const int64_t r = u / chunks;
+        const int c = (int)(u - r * chunks) * 8;
+        const float* from = plane + r * ld_plane + c;
+        v4f a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
+        for (int s = 0; s < splits; ++s, from += rows * ld_plane) {
+            a += *reinterpret_cast<const v4f*>(from);
+            b += *reinterpret_cast<const v4f*>(from + 4);
+        }
+        uint16_t* to = out + r * ld + c;
+        if (wide && c + 8 <= cols) {
+            *reinterpret_cast<v4u*>(to) = v4u{gemm::pack_bf16(a[0], a[1]), gemm::pack_bf16(a[2], a[3]),
+                                              gemm::pack_bf16(b[0], b[1]), gemm::pack_bf16(b[2], b[3])};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < cols) to[i] = gemm::to_bf16(i < 4 ? a[i] : b[i - 4]);
+        }
+    }
+}
+
+int grid_of(int64_t units) { return (int)std::min<int64_t>((units + 255) / 256, 8 * gemm_num_cus()); }
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+bool aligned16(const void* p, int64_t ld) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 15u) == 0; }
+
+hipError_t pack(const void* x, int64_t ld, int64_t rows, int64_t cols, void* out, const int64_t* targets, int64_t vocab,
+                hipStream_t stream)
+{
+    const int chunks = (int)(up(cols, 8) / 8);
+    hipLaunchKernelGGL(k_ce_pack, dim3(grid_of(rows * chunks)), dim3(256), 0, stream, static_cast<const uint16_t*>(x), ld,
+                       rows, (int)cols, static_cast<uint4*>(out), chunks, targets, vocab, (int)aligned16(x, ld));
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ plans
+// Tokens of a forward pass: its statistics stay below 8 bytes a token and
+// block.  Vocabulary rows of a piece: dl and, where w has to be packed, its
+// rows.
+constexpr int64_t kTokenChunk = 32768;
+constexpr int64_t kPieceBytes = (int64_t)1 << 29;
+
+struct Layout {
+    int64_t piece, pieces;      // vocabulary rows (a multiple of 256) and number
+    int64_t splits;             // of dx
+    size_t x, w, stats, zt, dl, planes, total;      // offsets in the workspace
+};
+size_t take(size_t& at, int64_t bytes)
+{
+    const size_t here = at;
+    at += (size_t)up(bytes, 256);
+    return here;
+}
+void pieces_of(Layout& l, int64_t vocab, int64_t most)
+{
+    most = std::max<int64_t>(most / 256 * 256, 256);
+    l.pieces = (vocab + most - 1) / most;
+    l.piece = up((vocab + l.pieces - 1) / l.pieces, 256);
+    l.pieces = (vocab + l.piece - 1) / l.piece;
+}
+Layout forward_layout(int64_t tokens, int64_t vocab, int64_t hidden)
+{
+    Layout l = {};
+    const int64_t row = up(hidden, 8) * 2, chunk = std::min(tokens, kTokenChunk);
+    pieces_of(l, vocab, std::max<int64_t>(kPieceBytes / row, 4096));
+    size_t at = 0;
+    l.x = take(at, chunk * row);
+    l.w = take(at, std::min(l.piece, vocab) * row);
+    l.stats = take(at, (up(vocab, 256) / stat_rows(chunk)) * chunk * 8);
+    l.zt = take(at, chunk * 4);
+    l.total = at;
+    return l;
+}
+Layout backward_layout(int64_t tokens, int64_t vocab, int64_t hidden)
+{
+    Layout l = {};
+    const int64_t row = up(hidden, 8) * 2;
+    pieces_of(l, vocab, std::max<int64_t>(kPieceBytes / (2 * tokens), 4096));
+    // too few tiles of dx for the chip: its K, the vocabulary, is split
+    const int tile = token_tile(tokens);
+    const int64_t tiles = (int64_t)tiles_of(hidden, 256) * tiles_of(tokens, tile);
+    const int64_t want = (int64_t)gemm_num_cus() * (tile <= 64 ? 2 : 1);
+    l.splits = std::max<int64_t>(std::min<int64_t>(want / tiles, std::min(l.piece, vocab) / 512), 1);
+    size_t at = 0;
+    l.x = take(at, tokens * row);
+    l.w = take(at, std::min(l.piece, vocab) * row);
+    l.dl = take(at, tokens * l.piece * 2);
+    l.planes = take(at, l.splits > 1 || l.pieces > 1 ? l.splits * tokens * up(hidden, 16) * 4 : 0);
+    l.total = at;
+    return l;
+}
+
+}  // namespace
+
+size_t ce_forward_workspace(int64_t tokens, int64_t vocab, int64_t hidden)
+{
+    return forward_layout(tokens, vocab, hidden).total;
+}
+size_t ce_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden)
+{
+    return backward_layout(tokens, vocab, hidden).total;
+}
+
+hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
+{
+    const Layout l = forward_layout(g.tokens, g.vocab, g.hidden);
+    uint8_t* ws = static_cast<uint8_t*>(g.ws);
+    const bool pack_w = !aligned16(g.w, g.ldw) || g.hidden % 8 != 0, pack_x = !aligned16(g.x, g.ldx) || g.hidden % 8 != 0;
+    hipError_t e;
+    for (int64_t t0 = 0; t0 < g.tokens; t0 += kTokenChunk) {
+        const int64_t n = std::min(g.tokens - t0, kTokenChunk);
+        const uint16_t* x = static_cast<const uint16_t*>(g.x) + t0 * g.ldx;
+        GemmShape s = {};
+        s.b = {reinterpret_cast<const uint8_t*>(x), g.ldx * 2};
+        if (pack_x) {
+            if ((e = pack(x, g.ldx, n, g.hidden, ws + l.x, nullptr, 1, stream)) != hipSuccess) return e;
+            s.b = {ws + l.x, up(g.hidden, 8) * 2};
+        }
+        s.n = (int)n;
+        s.k = (int)g.hidden;
+        s.splits = 1;
+        // the statistics' blocks of a piece: those of whole tiles of 256 rows
+        const int per_tile = 256 / stat_rows(n);
+        int blocks = 0;
+        for (int64_t p = 0; p < (pack_w ? l.pieces : 1); ++p) {
+            const int64_t v0 = p * l.piece, m = pack_w ? std::min(l.piece, g.vocab - v0) : g.vocab;
+            const uint16_t* w = static_cast<const uint16_t*>(g.w) + v0 * g.ldw;
+            s.a = {reinterpret_cast<const uint8_t*>(w), g.ldw * 2};
+            if (pack_w) {
+                if ((e = pack(w, g.ldw, m, g.hidden, ws + l.w, nullptr, 1, stream)) != hipSuccess) return e;
+                s.a = {ws + l.w, up(g.hidden, 8) * 2};
+            }
+            s.m = (int)m;
+            e = launch_tokens<false, StatsEpilogue>(s, [&](auto& epi) {
+                epi.m = (int)m;
+                epi.n = (int)n;
+                epi.v0 = v0;
+                epi.block0 = blocks;
+                epi.cap = g.softcap;
+                epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
+                epi.targets = g.targets + t0;
+                epi.part = reinterpret_cast<float2*>(ws + l.stats);
+                epi.zt = reinterpret_cast<float*>(ws + l.zt);
+            }, stream);
+            if (e != hipSuccess) return e;
+            blocks += tiles_of(m, 256) * per_tile;
+        }
+        const auto finish = [&](auto kernel, int tx) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)((n + tx - 1) / tx)), dim3(256), 0, stream,
+                               reinterpret_cast<const float2*>(ws + l.stats), blocks, (int)n,
+                               reinterpret_cast<const float*>(ws + l.zt), g.targets + t0, g.vocab, g.loss + t0, g.lse + t0);
+            return hipGetLastError();
+        };
+        e = n <= 512 ? finish(k_ce_loss<1>, 1) : n <= 4096 ? finish(k_ce_loss<8>, 8) : finish(k_ce_loss<32>, 32);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
+{
+    hipError_t e;
+    if (g.tokens == 0) {
+        if (!g.dw) return hipSuccess;
+        return launch_zero_bf16(static_cast<uint16_t*>(g.dw), (int)g.vocab, (int)g.hidden, g.lddw, stream);
+    }
+    const Layout l = backward_layout(g.tokens, g.vocab, g.hidden);
+    uint8_t* ws = static_cast<uint8_t*>(g.ws);
+    const bool pack_w = !aligned16(g.w, g.ldw) || g.hidden % 8 != 0;
+    const int64_t packed = up(g.hidden, 8) * 2;
+    const int T = (int)g.tokens, H = (int)g.hidden, H8 = (int)up(g.hidden, 8);
+    // x always as a copy, in which the tokens that do not count are zeros:
+    // their products with dl's zeros have to be zeros in dw
+    if ((e = pack(g.x, g.ldx, g.tokens, g.hidden, ws + l.x, g.targets, g.vocab, stream)) != hipSuccess) return e;
+    const ce::Operand x = {ws + l.x, packed};
+    float* planes = reinterpret_cast<float*>(ws + l.planes);
+    uint16_t* dl = reinterpret_cast<uint16_t*>(ws + l.dl);
+    const ce::Operand d = {ws + l.dl, l.piece * 2};
+    for (int64_t p = 0; p < l.pieces; ++p) {
+        const int64_t v0 = p * l.piece, m = std::min(l.piece, g.vocab - v0);
+        const uint16_t* wp = static_cast<const uint16_t*>(g.w) + v0 * g.ldw;
+        ce::Operand w = {reinterpret_cast<const uint8_t*>(wp), g.ldw * 2};
+        if (pack_w) {
+            if ((e = pack(wp, g.ldw, m, g.hidden, ws + l.w, nullptr, 1, stream)) != hipSuccess) return e;
+            w = {ws + l.w, packed};
+        }
+        GemmShape s = {};
+        s.a = w;
+        s.b = x;
+        s.m = (int)m;
+        s.n = T;
+        s.k = H;
+        s.splits = 1;
+        e = launch_tokens<false, GradEpilogue>(s, [&](auto& epi) {
+            epi.m = (int)m;
+            epi.n = T;
+            epi.v0 = v0;
+            epi.vocab = g.vocab;
+            epi.cap = g.softcap;
+            epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
+            epi.targets = g.targets;
+            epi.lse = g.lse;
+            epi.grad = g.grad;
+            epi.grad_step = g.grad_step;
+            epi.dl = dl;
+            epi.ld = l.piece;
+        }, stream);
+        if (e != hipSuccess) return e;
+        if (g.dx) {
+            const bool last = p == l.pieces - 1;
+            s.a = w;
+            s.b = d;
+            s.m = H8;
+            s.n = T;
+            s.k = (int)m;
+            s.splits = (int)std::min<int64_t>(l.splits, (m + ce::kStageK - 1) / ce::kStageK);
+            const bool direct = last && l.splits == 1;
+            e = launch_tokens<true, OutEpilogue>(s, [&](auto& epi) {
+                epi.m = H;
+                epi.n = T;
+                epi.plane = l.splits > 1 || l.pieces > 1 ? planes : nullptr;
+                epi.ld_plane = up(g.hidden, 16);
+                epi.add = p > 0;
+                epi.out = direct ? static_cast<uint16_t*>(g.dx) : nullptr;
+                epi.ld = g.lddx;
+                epi.wide = aligned16(g.dx, g.lddx) && H % 8 == 0;
+            }, stream);
+            if (e != hipSuccess) return e;
+            if (last && !direct) {
+                const int64_t ld = up(g.hidden, 16);
+                // a short last piece may have had fewer splits; the first has written all planes
+                hipLaunchKernelGGL(k_ce_reduce, dim3(grid_of(g.tokens * ld / 8)), dim3(256), 0, stream, planes, (int)l.splits,
+                                   g.tokens, H, ld, static_cast<uint16_t*>(g.dx), g.lddx, (int)aligned16(g.dx, g.lddx));
+                if ((e = hipGetLastError()) != hipSuccess) return e;
+            }
+        }
+        if (g.dw) {
+            s.a = x;
+            s.b = d;
+            s.m = H8;
+            s.n = (int)up(m, 8);    // dl's rows go on with zeros
+            s.k = T;
+            s.splits = 1;
+            uint16_t* dw = static_cast<uint16_t*>(g.dw) + v0 * g.lddw;
+            e = launch_tile<true, true, 2, 4, 4, 2, OutEpilogue>(s, [&](auto& epi) {
+                epi.m = H;
+                epi.n = (int)m;
+                epi.plane = nullptr;
+                epi.ld_plane = 16;
+                epi.add = 0;
+                epi.out = dw;
+                epi.ld = g.lddw;
+                epi.wide = aligned16(dw, g.lddw) && H % 8 == 0;
+            }, stream);
+            if (e != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
+}  // namespace fp8mi

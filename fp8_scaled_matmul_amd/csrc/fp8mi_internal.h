@@ -210,6 +210,69 @@ size_t mx4_moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t
 // Work-items of the largest of its launches.
 int64_t mx4_moe_items(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner);
 hipError_t launch_mx4_moe(const Mx4MoeArgs& g, hipStream_t stream);
+// Cross entropy of a projection onto a vocabulary (cross_entropy.hip).  Its
+// limits: 32-bit offsets inside a tile of 256 rows.
+constexpr int64_t kCeMaxTokens = (int64_t)1 << 24, kCeMaxVocab = (int64_t)1 << 24, kCeMaxLd = (int64_t)1 << 21;
+struct CeArgs {
+    const void* x;
+    int64_t ldx;
+    const void* w;
+    int64_t ldw;
+    int64_t tokens, vocab, hidden;
+    const int64_t* targets;
+    float softcap;              // 0: none
+    float* loss;                // forward
+    float* lse;                 // written by the forward, read by the backward
+    const float* grad;          // backward: of the losses
+    int64_t grad_step;
+    void* dx;                   // nullable
+    int64_t lddx;
+    void* dw;                   // nullable
+    int64_t lddw;
+    void* ws;
+};
+size_t ce_forward_workspace(int64_t tokens, int64_t vocab, int64_t hidden);
+size_t ce_backward_workspace(int64_t tokens, int64_t vocab, int64_t hidden);
+hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream);
+hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream);
+
+// A router in training (moe_route.hip); experts and top_k as for the 4-bit layer.
+constexpr int64_t kRouteMaxTokens = (int64_t)1 << 27;      // pairs are counted in 32 bits
+struct RouteArgs {
+    const void* logits;
+    int dtype;
+    int64_t tokens, experts, ld;
+    int64_t top_k;
+    int renormalize;
+    const uint8_t* mask;        // nullable
+    int32_t* ids;
+    float* weights;
+    int32_t* counts;
+    float* balance;
+    const float* grad_weights;  // backward, nullable
+    const float* grad_balance;  // backward, nullable
+    void* dlogits;
+    int64_t ldd;
+    void* ws;
+};
+size_t route_workspace(int64_t tokens, int64_t experts);
+hipError_t launch_route(const RouteArgs& g, hipStream_t stream);
+hipError_t launch_route_backward(const RouteArgs& g, hipStream_t stream);
+
+// Dropout (dropout.hip).
+struct DropoutArgs {
+    const void* x;
+    int dtype;
+    int64_t rows, cols, ld;
+    const void* residual;       // nullable
+    int64_t ldr;
+    uint32_t cut;               // of 65536
+    const uint64_t* seed;
+    void* y;
+    int64_t ldy;
+};
+hipError_t launch_dropout(const DropoutArgs& g, hipStream_t stream);
+
 // Zeros (k = 0), in gemm.hip.
 hipError_t launch_zero_bf16(uint16_t* c, int m, int n, int64_t ldc, hipStream_t stream);
 

@@ -408,6 +408,80 @@ fp8_status fp8_mx4_moe(const void* x_bf16, int64_t tokens, int64_t hidden, int64
                        void* y_bf16, int64_t ldy, int32_t* ids, float* weights,
                        void* workspace, size_t workspace_bytes, fp8_counters* ctr, hipStream_t stream);
 
+/* ------------------------------------------------------------------ around the linear layers
+ * Softmax cross entropy of a projection onto a vocabulary:
+ *   l = x w^T,  z = softcap tanh(l / softcap) (l where softcap is 0),
+ *   lse[t] = log sum_v exp z[t, v],  loss[t] = lse[t] - z[t, targets[t]]
+ * x [tokens, hidden], w [vocab, hidden] bf16; loss and lse fp32.  The logits are
+ * fp32 sums of exact products and stay in the kernels.  A token with a negative
+ * target does not count: its loss is 0.  One with a target of vocab or more has
+ * a NaN loss (lse is computed for both).
+ * Backward, of losses with the gradients grad_loss[t * grad_step] (fp32; step 0:
+ * the same for all):
+ *   dl = grad_loss (exp(z - lse) - [v = target]) (1 - (z / softcap)^2), rounded to bf16
+ *   dx = dl w,  dw = dl^T x                  bf16, fp32 sums in an order that the sizes set
+ * for a piece of the vocabulary at a time.  Tokens with targets outside 0 ..
+ * vocab - 1 add nothing, whatever their x and grad_loss hold; their dx is 0.
+ * lse is the forward's.  dx or dw may be NULL.  tokens 0 writes zeros to dw.
+ * Any sizes and alignment of elements; operands whose rows do not all lie at
+ * multiples of 16 bytes (or have a hidden that is no multiple of 8) are copied
+ * first.  tokens, vocab below 2^24, leading dimensions below 2^21.
+ * workspace: fp8_linear_ce_workspace_size() bytes (backward: nonzero for
+ * fp8_linear_ce_backward; 0 for sizes that are refused), 16-byte aligned; what
+ * it holds does not matter, and no two calls at once on one workspace.  The
+ * backward's grows with tokens: a piece of dl takes 512 MiB or 8192 bytes a token. */
+size_t     fp8_linear_ce_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, int32_t backward);
+fp8_status fp8_linear_ce(const void* x_bf16, int64_t ldx, const void* w_bf16, int64_t ldw,
+                         int64_t tokens, int64_t vocab, int64_t hidden, const int64_t* targets, float softcap,
+                         float* loss, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+fp8_status fp8_linear_ce_backward(const void* x_bf16, int64_t ldx, const void* w_bf16, int64_t ldw,
+                                  int64_t tokens, int64_t vocab, int64_t hidden, const int64_t* targets, float softcap,
+                                  const float* lse, const float* grad_loss, int64_t grad_step,
+                                  void* dx_bf16, int64_t lddx, void* dw_bf16, int64_t lddw,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* A mixture of experts' router in training, from its logits l [tokens, experts]
+ * (bf16 or fp32):
+ *   ids[t]   the top_k largest l of a token in falling order, equal ones by the lower expert, NaN last
+ *   weights  exp(l - max) / sum exp(l - max), the sum over ids[t] (renormalize) or over all experts
+ *   counts   [experts] how often each expert was chosen
+ *   balance  experts sum_e f_e P_e with f_e = counts[e] / (n top_k), P_e the mean
+ *            over the tokens of the softmax of l over all experts
+ * as fp8_mx4_moe chooses them, in 32 bits.  mask (may be NULL): a byte a token, 0 leaves the
+ * token out; so does a row of -Inf alone.  Tokens left out have ids -1 and
+ * weights 0, and n counts the others (balance is 0 where there are none).  The
+ * sum of a token with a NaN or +Inf is NaN.
+ * Backward, from the gradients of weights (fp32 [tokens, top_k], may be NULL) and of
+ * balance (one fp32 on the device, may be NULL): dlogits in the logits' type.
+ * The choice, and so f, has no gradient.  ids, weights and counts are the forward's.
+ * ids int32 and weights fp32 [tokens, top_k], contiguous.  experts <= 512, top_k
+ * <= 16, tokens below 2^27.  tokens 0 writes zeros to counts and balance.
+ * workspace: fp8_moe_route_workspace_size() bytes, 16-byte aligned; what it holds
+ * does not matter, and no two calls at once on one workspace. */
+size_t     fp8_moe_route_workspace_size(int64_t tokens, int64_t experts);
+fp8_status fp8_moe_route(const void* logits, fp8_dtype dtype, int64_t tokens, int64_t experts, int64_t ld,
+                         int64_t top_k, int32_t renormalize, const uint8_t* mask,
+                         int32_t* ids, float* weights, int32_t* counts, float* balance,
+                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+fp8_status fp8_moe_route_backward(const void* logits, fp8_dtype dtype, int64_t tokens, int64_t experts, int64_t ld,
+                                  int64_t top_k, int32_t renormalize, const int32_t* ids, const float* weights,
+                                  const int32_t* counts, const float* grad_weights, const float* grad_balance,
+                                  void* dlogits, int64_t ldd, hipStream_t stream);
+
+/* Dropout: y = (r >= cut ? x 65536 / (65536 - cut) : 0) + residual, cut = rate
+ * 65536 to the nearest, r the element's 16 random bits:
+ *   mix(mix(row * 0x9E3779B1 + seed_lo) ^ ((col>>1) * 0x3C6EF373 + (seed_hi ^ 0xA54FF53A)))
+ * mod 2^32, the low half for an even column, the high half for an odd one; mix
+ * as for fp8_mx4_quantize, whose bits under the same seed are others.  seed: a DEVICE pointer
+ * to 64 bits.  The mask is not stored: dropout of dy under the same rate and
+ * seed is the backward pass (the residual's gradient is dy).  An element that is
+ * dropped counts as 0 whatever it holds.  residual may be NULL; y may be x or
+ * residual (the same rows at the same places), not overlap them otherwise.
+ * x, residual, y [rows, cols], bf16 or fp32 alike; rows and cols below 2^31. */
+fp8_status fp8_dropout(const void* x, fp8_dtype dtype, int64_t rows, int64_t cols, int64_t ld,
+                       const void* residual, int64_t ldr, double rate, const uint64_t* seed,
+                       void* y, int64_t ldy, hipStream_t stream);
+
 /* Zero a counter block on `stream` (a small fill kernel, safe to capture). */
 fp8_status fp8_counters_reset(fp8_counters* ctr, hipStream_t stream);
 
