@@ -8,7 +8,8 @@
 //   dx      [h, t] = w [v, h] dl [t, v]       A K-strided, B K-contiguous
 //   dw      [h, v] = x [t, h] dl [t, v]       both K-strided
 // C's rows are the contiguous dimension of what is stored: a fragment's 32
-// rows are dealt out so that a lane ends up with 16 MF adjacent ones.
+// rows are dealt out so that a lane ends up with 16 adjacent ones, half a wave
+// each with one half of the fragment.
 #pragma once
 
 #include <stdint.h>
@@ -79,23 +80,13 @@ __device__ inline Item item_of(const GemmShape& s, int id)
 __device__ inline int swz64(int r, int c) { return c ^ (((r >> 2) & 1) | (((r >> 1) ^ (r >> 2) ^ (r >> 3)) & 1) << 1); }
 
 // A K-strided operand's stage holds 32 rows of 2 T bytes; its 32-byte granules
-// are permuted by the row, so that the 4 rows and 64 bytes of each which half
-// a wave reads lie in different banks (172 bytes a clock and CU; unpermuted 64).
-//   A: granules i and i + MF (the fragment's rows are dealt out)
-//   B: granules 2 j and 2 j + 1
-template <int MF>
-__device__ inline int swz_a(int row)
-{
-    if constexpr (MF == 4) return row & 3;
-    if constexpr (MF == 2) return (row & 1) | (row & 2) << 1;
-    return (row & 3) << 1;
-}
+// are permuted by the row, so that the 4 rows and 64 bytes of each (granules 2 j
+// and 2 j + 1) which half a wave reads lie in different banks (172 bytes a clock
+// and CU; unpermuted 64).
 template <int T>
-__device__ inline int swz_b(int row)
+__device__ inline int swz_strided(int row)
 {
-    if constexpr (T >= 128) return (row & 3) << 1;
-    if constexpr (T == 64) return row & 2;
-    return 0;
+    return (row & 3) << 1;
 }
 
 // The tile C[TM, TN] of one item: WR x WC waves of MF x NF fragments of 32 x
@@ -108,19 +99,28 @@ template <bool ATR, bool BTR, int WR, int WC, int MF, int NF>
 struct Tile {
     static constexpr int W = WR * WC, TM = 32 * MF * WR, TN = 32 * NF * WC;
     static constexpr int kStage = (TM + TN) * 64;
-    static constexpr int kLds = kRing * kStage;
+    // what an epilogue wants of its tile's columns: 64 lanes x 16 bytes for each
+    // wave column, of the items whose stages are on their way and the one at work
+    static constexpr int kNotes = 1024 * WC;
+    template <typename Epi>
+    static constexpr int lds_bytes()
+    {
+        return kRing * kStage + (Epi::kNotes ? (kRing + 1) * kNotes : 0);
+    }
     // DMA instructions of a wave and stage; where an operand has fewer than
     // waves, some repeat another's (the same bytes to the same place)
     static constexpr int kA = TM / 16 >= W ? TM / 16 / W : 1;
     static constexpr int kB = TN / 16 >= W ? TN / 16 / W : 1;
     static constexpr int kPer = kA + kB;
+    static_assert((!ATR || TM >= 128) && (!BTR || TN >= 128), "K-strided rows of 8 granules or more");
     static_assert((TM / 16 % W == 0 || TM / 16 < W) && (TN / 16 % W == 0 || TN / 16 < W), "whole DMA instructions");
-    static_assert(!ATR || TM == 256, "swz_a stays inside a row of 8 granules or more");
 
-    typedef v16f Acc[MF][NF];
+    typedef v16f Acc[NF][MF];
 
-    // Epi: static constexpr int kStores, the vector memory operations that
-    // every call of it issues last, at least; operator()(item, acc).
+    // Epi: operator()(item, acc, row, column, notes): a lane holds rows row + 32 i
+    // + r in acc[j][i][r], column + 32 j.  It returns whether it has issued
+    // at least kStores vector memory operations.  With kNotes
+    // set, note(lds, item, column) brings 1 KB, which a call finds at notes.
     template <typename Epi>
     __device__ static void run(const GemmShape& s, uint8_t* lds, Epi& epi)
     {
@@ -130,7 +130,7 @@ struct Tile {
 
         // ---- the stream of fills
         Item f = item_of(s, blockIdx.x);
-        int ft = f.first, fslot = 0;
+        int ft = f.first, fslot = 0, fnote = 0;
         // K-contiguous: lane l brings chunk l % 4 of row l / 4 of 16; K-strided:
         // 16 bytes of a row of 2 T.
         const int kc_chunk = 16 * swz64(lane >> 2, lane & 3);
@@ -140,13 +140,13 @@ struct Tile {
 #pragma unroll
         for (int j = 0; j < kA; ++j) {
             const int byte = 1024 * (ua + j) + 16 * lane, row = byte / (2 * TM), in = byte % (2 * TM);
-            va[j] = ATR ? (uint32_t)(row * s.a.ld + (((in >> 5) ^ swz_a<MF>(row)) << 5) + (in & 31))
+            va[j] = ATR ? (uint32_t)(row * s.a.ld + (((in >> 5) ^ swz_strided<TM>(row)) << 5) + (in & 31))
                         : (uint32_t)((16 * (ua + j) + (lane >> 2)) * s.a.ld + kc_chunk);
         }
 #pragma unroll
         for (int j = 0; j < kB; ++j) {
             const int byte = 1024 * (ub + j) + 16 * lane, row = byte / (2 * TN), in = byte % (2 * TN);
-            vb[j] = BTR ? (uint32_t)(row * s.b.ld + (((in >> 5) ^ swz_b<TN>(row)) << 5) + (in & 31))
+            vb[j] = BTR ? (uint32_t)(row * s.b.ld + (((in >> 5) ^ swz_strided<TN>(row)) << 5) + (in & 31))
                         : (uint32_t)((16 * (ub + j) + (lane >> 2)) * s.b.ld + kc_chunk);
         }
         // Where an item's data begin, and how much there is from there on
@@ -173,6 +173,10 @@ struct Tile {
                 lb = (int64_t)(min(s.n - n0, TN) - 1) * s.b.ld + row_bytes;
             }
             if (!live) la = lb = 0;
+            if constexpr (Epi::kNotes) {
+                if (wave < WC && live) epi.note(base + kRing * kStage + fnote * kNotes + 1024 * wave, f, n0 + 32 * NF * wave);
+                fnote = fnote == kRing ? 0 : fnote + 1;
+            }
         };
         describe();
         const auto records = [](int64_t bytes) {
@@ -209,18 +213,18 @@ struct Tile {
         const int wm = (wave % WR) * 32 * MF, wn = (wave / WR) * 32 * NF;
         const int c = lane & 31, half = lane >> 5;
         // K 16 kk + 8 half .. + 7 of both operands.  K-contiguous: chunk half + 2 kk.
-        // A's row of instruction row c: 16 MF (c / 4 % 2) + 4 (c / 8) + c % 4
-        const int ar = 16 * MF * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
+        // A's row of instruction row c: 16 (c / 4 % 2) + 4 (c / 8) + c % 4
+        const int ar = 16 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
         const int tk = 8 * half + ((lane & 15) >> 2);           // K-strided: this lane's row of a read
         const int tc = (lane >> 4 & 1) * 4 + (lane & 3);        // and its 4 columns' place among the fragment's 32
         uint32_t at[MF], bt[NF];
 #pragma unroll
         for (int i = 0; i < MF; ++i)
-            at[i] = ATR ? tk * 2 * TM + ((((wm + 16 * MF * (tc & 1) + 16 * i) >> 4) ^ swz_a<MF>(tk)) << 5) + (tc >> 1) * 8
-                        : (wm + ar + 16 * i) * 64 + 16 * swz64(ar, half);
+            at[i] = ATR ? tk * 2 * TM + (((((wm + 32 * i) >> 4) + (tc & 1)) ^ swz_strided<TM>(tk)) << 5) + (tc >> 1) * 8
+                        : (wm + 32 * i + ar) * 64 + 16 * swz64(ar, half);
 #pragma unroll
         for (int j = 0; j < NF; ++j)
-            bt[j] = TM * 64 + (BTR ? tk * 2 * TN + ((((wn + 32 * j) >> 4) + (tc >> 2) ^ swz_b<TN>(tk)) << 5) + (tc & 3) * 8
+            bt[j] = TM * 64 + (BTR ? tk * 2 * TN + (((((wn + 32 * j) >> 4) + (tc >> 2)) ^ swz_strided<TN>(tk)) << 5) + (tc & 3) * 8
                                    : (wn + 32 * j + c) * 64 + 16 * swz64(c, half));
         v8bf fa[2][MF], fb[2][NF];
         int slot = 0;
@@ -253,8 +257,8 @@ struct Tile {
 #pragma unroll
             for (int m = 0; m < MF * NF; ++m)
                 if (m >= lo && m < hi)
-                    acc[m / NF][m % NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][m / NF], fb[kk][m % NF],
-                                                                                  acc[m / NF][m % NF], 0, 0, 0);
+                    acc[m % NF][m / NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][m / NF], fb[kk][m % NF],
+                                                                                  acc[m % NF][m / NF], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         };
         const auto clear = [&]() {
@@ -263,7 +267,7 @@ struct Tile {
 #pragma unroll
                 for (int j = 0; j < NF; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+                    for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
         };
         constexpr int kAll = MF * NF;
         constexpr std::integral_constant<int, 0> k0{};
@@ -275,6 +279,7 @@ struct Tile {
         gemm::barrier_lds();
         read(k0);
         int stored = 3;         // stages since the last epilogue's stores, up to 3
+        int note = 0;
         const int total = s.tiles_m * s.tiles_n * s.splits;
         for (Item it = item_of(s, blockIdx.x); it.id < total; it = item_of(s, it.id + gridDim.x)) {
             for (int t = it.first; t < it.end; ++t) {
@@ -298,8 +303,9 @@ struct Tile {
                 read(k0);
                 products(k1, kAll / 2, kAll);
             }
-            epi(it, acc, it.tm * TM + wm + 16 * MF * half, it.tn * TN + wn + c);
-            stored = 0;
+            const uint8_t* notes = lds + kRing * kStage + note * kNotes + 1024 * (wave / WR);
+            stored = epi(it, acc, it.tm * TM + wm + 16 * half, it.tn * TN + wn + c, notes) ? 0 : 3;
+            note = note == kRing ? 0 : note + 1;
             clear();
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // the fills past the end

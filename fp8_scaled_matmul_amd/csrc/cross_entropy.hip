@@ -23,6 +23,7 @@ using ce::Item;
 using ce::v16f;
 using gemm::v4f;
 using gemm::v4u;
+typedef uint32_t v16u __attribute__((ext_vector_type(16)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -32,38 +33,97 @@ __device__ inline float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 // cap tanh(l / cap).  tanh u = u N / D, the convergent of Lambert's continued
 // fraction whose error is below 1e-9 of it for |u| <= 1; past that 1 - 2 /
 // (exp(2 |u|) + 1), which loses nothing there.
-__device__ inline float softcap(float l, float cap, float inv_cap)
+__device__ inline float softcap_near(float l, float inv_cap)
 {
     const float u = l * inv_cap, t = u * u;
     const float n = __builtin_fmaf(__builtin_fmaf(21.0f, t, 1260.0f), t, 10395.0f);
     const float d = __builtin_fmaf(__builtin_fmaf(t + 210.0f, t, 4725.0f), t, 10395.0f);
-    float z = l * n * __builtin_amdgcn_rcpf(d);
-    if (__any(!(t <= 1.0f))) {
-        const float far = __builtin_copysignf(
-            cap - 2.0f * cap * __builtin_amdgcn_rcpf(exp2_fast(2.0f * kLog2e * __builtin_fabsf(u)) + 1.0f), l);
-        z = t <= 1.0f ? z : l != l ? l : far;
+    return l * n * __builtin_amdgcn_rcpf(d);
+}
+__device__ inline float softcap_any(float l, float cap, float inv_cap)
+{
+    const float u = __builtin_fabsf(l * inv_cap);
+    const float far = cap - 2.0f * cap * __builtin_amdgcn_rcpf(exp2_fast(2.0f * kLog2e * u) + 1.0f);
+    return u <= 1.0f ? softcap_near(l, inv_cap) : l != l ? l : __builtin_copysignf(far, l);
+}
+// Of a fragment's column, the far form only where one of the wave's needs it.
+template <int MF>
+__device__ inline void softcap_column(v16f (&acc)[MF], float cap, float inv_cap)
+{
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) most = fmaxf(most, __builtin_fabsf(acc[i][r]));      // NaN: either form gives NaN
+    const bool far = __any(most * inv_cap > 1.0f);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) {
+        __builtin_amdgcn_sched_barrier(0);      // one fragment after another: registers
+        if (far) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][r] = softcap_any(acc[i][r], cap, inv_cap);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][r] = softcap_near(acc[i][r], inv_cap);
+        }
     }
-    return z;
 }
 
 // ------------------------------------------------------------------ epilogues
-// A lane holds, for tokens (columns) col + 32 j, 16 MF adjacent rows from
-// `row` on: acc[i][j][r] is row + 16 i + r.
+// A lane holds, for tokens (columns) col + 32 j, the rows row + 32 i + r:
+// acc[j][i][r].  A store of 16 bytes a lane as they lie would touch 64 places;
+// swapped between the 16-lane groups first, four lanes share 64 bytes.
+
+// Odd groups of 16 lanes of a and even ones of b change places; upper half of a
+// and lower half of b.
+__device__ inline void swap16(uint32_t& a, uint32_t& b)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ inline void swap32(uint32_t& a, uint32_t& b)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// 16 values of a lane to bf16, for two stores: after the swap lane l holds 8
+// values from row 8 (l / 16 % 2) on of its half's 16, of column l % 16 (a) and
+// 16 + l % 16 (b).
+__device__ inline void to_bf16_chunks(const v16f& v, v4u& a, v4u& b)
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t lo = gemm::pack_bf16(v[2 * q], v[2 * q + 1]), hi = gemm::pack_bf16(v[8 + 2 * q], v[8 + 2 * q + 1]);
+        swap16(lo, hi);
+        a[q] = lo;
+        b[q] = hi;
+    }
+}
 
 // The forward's: of each token and block of 32 MF vocabulary rows the maximum
 // and the sum of exp(z - maximum); the target's z, by the one lane that has it.
 template <int WR, int MF, int NF>
 struct StatsEpilogue {
     static constexpr int kStores = NF;
+    static constexpr bool kNotes = true;
     int m, n;                   // vocabulary rows of this launch, tokens
-    int64_t v0;                 // its first row
+    int v0;                     // its first row
     int block0;                 // its first block
     float cap, inv_cap;
     const int64_t* targets;
     float2* part;               // [blocks, n]
     float* zt;
 
-    __device__ void operator()(const Item& it, v16f (&acc)[MF][NF], int row, int col) const
+    // the targets' low halves: a match by mistake is of a target that is not used
+    __device__ void note(uint32_t lds, const Item&, int col) const
+    {
+        gemm::dma4(lds, (uint32_t)(col + (threadIdx.x & 63)) * 8u, gemm::make_rsrc(targets, (uint32_t)n * 8u));
+    }
+
+    __device__ bool operator()(const Item& it, v16f (&acc)[NF][MF], int row, int col, const uint8_t* notes) const
     {
         const int lane = threadIdx.x & 63;
         const int wave_row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WR;
@@ -73,107 +133,126 @@ struct StatsEpilogue {
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
             const int t = col + 32 * j;
-            if (cap != 0.0f) {
-#pragma unroll
-                for (int i = 0; i < MF; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[i][j][r] = softcap(acc[i][j][r], cap, inv_cap);
-            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (cap != 0.0f) softcap_column<MF>(acc[j], cap, inv_cap);
             if (edge) {
+                int left = m - row;
+                asm("" : "+v"(left));       // one column's comparisons are not kept for the next: registers
 #pragma unroll
                 for (int i = 0; i < MF; ++i)
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
-                        if (row + 16 * i + r >= m) acc[i][j][r] = -__builtin_inff();
+                        if (32 * i + r >= left) acc[j][i][r] = -__builtin_inff();
             }
-            const int64_t at = (t < n ? targets[t] : -1) - v0 - row;
-            if (__any(at >= 0 && at < 16 * MF)) {
+            const int at = reinterpret_cast<const int*>(notes)[32 * j + (lane & 31)] - v0 - row;
+            if (__any((uint32_t)at < 32u * MF)) {
                 float z = 0.0f;
 #pragma unroll
                 for (int i = 0; i < MF; ++i)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) z = at == 16 * i + r ? acc[i][j][r] : z;
-                if (at >= 0 && at < 16 * MF && t < n && row + at < m) zt[t] = z;
+                    for (int r = 0; r < 16; ++r) z = at == 32 * i + r ? acc[j][i][r] : z;
+                const bool here = (uint32_t)at < 32u * MF && (at & 16) == 0;
+                if (here && t < n && row + at < m) zt[t] = z;
             }
             float mx = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[i][j][r]);
+                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[j][i][r]);
             mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
             const float off = mx == -__builtin_inff() ? 0.0f : -mx * kLog2e;
-            float s = 0.0f;
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s += exp2_fast(__builtin_fmaf(acc[i][j][r], kLog2e, off));
-            s += __shfl_xor(s, 32, 64);
+                for (int r = 0; r < 16; ++r) s[r & 3] += exp2_fast(__builtin_fmaf(acc[j][i][r], kLog2e, off));
+            float sum = (s[0] + s[1]) + (s[2] + s[3]);
+            sum += __shfl_xor(sum, 32, 64);
             const uint32_t where = lane < 32 && t < n ? (uint32_t)t * 8u : gemm::kOutOfRange;
-            __builtin_amdgcn_raw_buffer_store_b64(
-                __builtin_bit_cast(__attribute__((__vector_size__(8))) unsigned int, float2{mx, s}), rp, (int)where, 0, 0);
+            typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, float2{mx, sum}), rp, (int)where, 0, 0);
         }
+        return true;
     }
+};
+
+// What the backward's logits need of a token: a token that does not count has
+// the exponential of -Inf, 0, and the gradient 0 (and x all zeros).
+struct TokenNote {
+    float off;                  // -lse log2 e
+    float grad;
+    int target;                 // -1: none
+    int unused;
 };
 
 // The backward's: dl, rounded to bf16 (by 2^-8 of each value at most, what the
 // operands' own type has; the matrix instruction takes one type), rows past
-// the vocabulary's end and tokens that do not count as zeros.
+// the vocabulary's end as zeros.
 template <int WR, int MF, int NF>
 struct GradEpilogue {
     static constexpr int kStores = 2 * MF * NF;
+    static constexpr bool kNotes = true;
     int m, n;
-    int64_t v0, vocab;
+    int v0;
     float cap, inv_cap;
-    const int64_t* targets;
-    const float* lse;
-    const float* grad;          // of the losses
-    int64_t grad_step;
+    const TokenNote* tokens;
     uint16_t* dl;               // [n, ld]
     int64_t ld;
 
-    __device__ void operator()(const Item& it, v16f (&acc)[MF][NF], int row, int col) const
+    __device__ void note(uint32_t lds, const Item&, int col) const
     {
-        const int n0 = col & ~31;       // uniform: this wave's first token
-        const __amdgpu_buffer_rsrc_t rd = gemm::make_store_rsrc(
-            dl + (int64_t)__builtin_amdgcn_readfirstlane(n0) * ld,
-            (uint32_t)(max(min(n - __builtin_amdgcn_readfirstlane(n0), 32 * NF), 0) * ld * 2));
+        const int64_t left = (int64_t)(n - col) * 16;
+        gemm::dma16(lds, (uint32_t)(threadIdx.x & 63) * 16u,
+                    gemm::make_rsrc(tokens + col, (uint32_t)min(max(left, (int64_t)0), (int64_t)1024)));
+    }
+
+    __device__ bool operator()(const Item& it, v16f (&acc)[NF][MF], int row, int col, const uint8_t* notes) const
+    {
+        const int lane = threadIdx.x & 63;
+        const int n0 = __builtin_amdgcn_readfirstlane(col & ~31);       // this wave's first token
+        const __amdgpu_buffer_rsrc_t rd =
+            gemm::make_store_rsrc(dl + n0 * ld, (uint32_t)(max(min(n - n0, 32 * NF), 0) * ld * 2));
+        const uint32_t to = (uint32_t)((lane & 15) * ld + row + 8 * (lane >> 4 & 1)) * 2u;
+        const bool edge = (it.tm + 1) * (32 * MF * WR) > m;
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const int t = col + 32 * j;
-            int64_t at = -1;
-            float off = 0.0f, g = 0.0f;
-            if (t < n) {
-                at = targets[t];
-                off = -lse[t] * kLog2e;
-                g = grad[t * grad_step];
-            }
-            const bool counts = at >= 0 && at < vocab;
-            const int rel = counts ? (int)min(max(at - v0 - row, (int64_t)-1), (int64_t)(16 * MF)) : -1;
+            const TokenNote k = reinterpret_cast<const TokenNote*>(notes)[32 * j + (lane & 31)];
+            const int at = k.target < 0 ? -1 : k.target - v0 - row;
+            if (cap != 0.0f) softcap_column<MF>(acc[j], cap, inv_cap);
+            const bool target_here = __any((uint32_t)at < 32u * MF);
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
-                float d[16];
+                __builtin_amdgcn_sched_barrier(0);      // one fragment after another: registers
+                v16f d;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float z = acc[i][j][r], slope = 1.0f;
-                    if (cap != 0.0f) {
-                        z = softcap(z, cap, inv_cap);
-                        const float u = z * inv_cap;
-                        slope = __builtin_fmaf(-u, u, 1.0f);
+                for (int r = 0; r < 16; ++r) d[r] = exp2_fast(__builtin_fmaf(acc[j][i][r], kLog2e, k.off));
+                if (target_here) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) d[r] = at == 32 * i + r ? d[r] - 1.0f : d[r];
+                }
+                if (cap != 0.0f) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float u = acc[j][i][r] * inv_cap;
+                        d[r] *= __builtin_fmaf(-u, u, 1.0f);
                     }
-                    float p = exp2_fast(__builtin_fmaf(z, kLog2e, off));
-                    p = rel == 16 * i + r ? p - 1.0f : p;
-                    d[r] = p * (cap != 0.0f ? g * slope : g);
-                    d[r] = counts && row + 16 * i + r < m ? d[r] : 0.0f;
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v4u w;
+                for (int r = 0; r < 16; ++r) d[r] *= k.grad;
+                if (edge) {
+                    int left = m - row;
+                    asm("" : "+v"(left));   // as above
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) w[q] = gemm::pack_bf16(d[8 * h + 2 * q], d[8 * h + 2 * q + 1]);
-                    gemm::store16(w, (uint32_t)(((t - n0) * ld + row + 16 * i + 8 * h) * 2), rd);
+                    for (int r = 0; r < 16; ++r) d[r] = 32 * i + r < left ? d[r] : 0.0f;
                 }
+                v4u a, b;
+                to_bf16_chunks(d, a, b);
+                const uint32_t first = to + (uint32_t)(32 * j * ld + 32 * i) * 2u;
+                gemm::store16(a, first, rd);
+                gemm::store16(b, first + (uint32_t)(16 * ld) * 2u, rd);
             }
         }
+        return true;
     }
 };
 
@@ -181,7 +260,8 @@ struct GradEpilogue {
 // piece of the vocabulary left), or bf16 at the end.
 template <int WR, int MF, int NF>
 struct OutEpilogue {
-    static constexpr int kStores = 0;
+    static constexpr int kStores = 2 * MF * NF;
+    static constexpr bool kNotes = false;
     int m, n;                   // the gradient's columns and rows
     float* plane;               // [splits, n, ld_plane], or null
     int64_t ld_plane;           // a multiple of 16
@@ -190,51 +270,105 @@ struct OutEpilogue {
     int64_t ld;
     int wide;                   // 16-byte stores are in place
 
-    __device__ void operator()(const Item& it, v16f (&acc)[MF][NF], int row, int col) const
+    __device__ void note(uint32_t, const Item&, int) const {}
+
+    __device__ bool operator()(const Item& it, v16f (&acc)[NF][MF], int row, int col, const uint8_t*) const
     {
+        const int lane = threadIdx.x & 63, half = lane >> 5, group = lane >> 4 & 1;
         const int n0 = __builtin_amdgcn_readfirstlane(col & ~31);
         const int rows = max(min(n - n0, 32 * NF), 0);
+        // the planes: four lanes share 64 bytes, 16 rows of a fragment's half
         const __amdgpu_buffer_rsrc_t rp = gemm::make_store_rsrc(
             plane + ((int64_t)it.split * n + n0) * ld_plane, plane ? (uint32_t)(rows * ld_plane * 4) : 0u);
-        const __amdgpu_buffer_rsrc_t ro = gemm::make_store_rsrc(
-            out + n0 * ld, out && rows ? (uint32_t)(((rows - 1) * ld + m) * 2) : 0u);
+        const int base = row - 16 * half;
+        const auto place = [&](int i, int j, int h, int upper) {
+            const int first = base + 32 * i + 16 * h;
+            return first < m ? (uint32_t)((32 * j + 16 * upper + (lane & 15)) * ld_plane + first + 8 * half + 4 * group) * 4u
+                             : gemm::kOutOfRange;
+        };
+        if (plane && (add || !out)) {
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    // v[2 h + upper]: of half h's 16 rows, columns 16 upper + l % 16.
+                    // (Cast as a whole: the compiler takes element 0 four times
+                    // for four casts of elements.)
+                    v4u v[4];
+                    v16u bits = __builtin_bit_cast(v16u, acc[j][i]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t a = bits[q], b = bits[4 + q], c = bits[8 + q], d = bits[12 + q];
+                        swap16(a, b);
+                        swap16(c, d);
+                        swap32(a, c);
+                        swap32(b, d);
+                        v[0][q] = a;
+                        v[1][q] = b;
+                        v[2][q] = c;
+                        v[3][q] = d;
+                    }
+                    if (add) {
+                        v4u o[4];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            o[p] = __builtin_bit_cast(
+                                v4u, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)place(i, j, p >> 1, p & 1), 0, 0));
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            v[p] = __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, v[p]) + __builtin_bit_cast(v4f, o[p]));
+                    }
+                    if (!out) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) gemm::store16(v[p], place(i, j, p >> 1, p & 1), rp);
+                    } else {
+                        // back to where they were
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t a = v[0][q], b = v[1][q], c = v[2][q], d = v[3][q];
+                            swap32(a, c);
+                            swap32(b, d);
+                            swap16(a, b);
+                            swap16(c, d);
+                            bits[q] = a;
+                            bits[4 + q] = b;
+                            bits[8 + q] = c;
+                            bits[12 + q] = d;
+                        }
+                        acc[j][i] = __builtin_bit_cast(v16f, bits);
+                    }
+                }
+            if (!out) return true;
+        }
+        if (wide) {
+            const __amdgpu_buffer_rsrc_t ro =
+                gemm::make_store_rsrc(out + n0 * ld, rows ? (uint32_t)(((rows - 1) * ld + m) * 2) : 0u);
+            const uint32_t to = (uint32_t)((lane & 15) * ld + row + 8 * group) * 2u;
+#pragma unroll
+            for (int j = 0; j < NF; ++j)
+#pragma unroll
+                for (int i = 0; i < MF; ++i) {
+                    v4u a, b;
+                    to_bf16_chunks(acc[j][i], a, b);
+                    const uint32_t first = row + 8 * group + 32 * i < m ? to + (uint32_t)(32 * j * ld + 32 * i) * 2u : gemm::kOutOfRange;
+                    gemm::store16(a, first, ro);
+                    gemm::store16(b, first + (uint32_t)(16 * ld) * 2u, ro);
+                }
+            return true;
+        }
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
             const int t = col + 32 * j;
+            if (t >= n) continue;
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
-                const int first = row + 16 * i;
-                v4f v[4];
+                uint16_t* to = out + t * ld + row + 32 * i;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    v[q] = v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                const uint32_t at = first < m ? (uint32_t)(((t - n0) * ld_plane + first) * 4) : gemm::kOutOfRange;
-                if (add) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        v[q] += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(at + 16 * q), 0, 0));
-                }
-                if (!out) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) gemm::store16(__builtin_bit_cast(v4u, v[q]), at + 16 * q, rp);
-                } else if (wide) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        v4u w;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            w[q] = gemm::pack_bf16(v[2 * h + (q >> 1)][2 * (q & 1)], v[2 * h + (q >> 1)][2 * (q & 1) + 1]);
-                        gemm::store16(w, first + 8 * h < m ? (uint32_t)(((t - n0) * ld + first + 8 * h) * 2) : gemm::kOutOfRange,
-                                      ro);
-                    }
-                } else if (t < n) {
-                    uint16_t* to = out + t * ld + first;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (first + r < m) to[r] = gemm::to_bf16(v[r >> 2][r & 3]);
-                }
+                for (int r = 0; r < 16; ++r)
+                    if (row + 32 * i + r < m) to[r] = gemm::to_bf16(acc[j][i][r]);
             }
         }
+        return false;
     }
 };
 
@@ -251,19 +385,21 @@ template <bool ATR, bool BTR, int WR, int WC, int MF, int NF, template <int, int
 hipError_t launch_tile(GemmShape s, Init init, hipStream_t stream)
 {
     using T = ce::Tile<ATR, BTR, WR, WC, MF, NF>;
+    using E = Epi<WR, MF, NF>;
+    constexpr int kLds = T::template lds_bytes<E>();
     s.tiles_m = tiles_of(s.m, T::TM);
     s.tiles_n = tiles_of(s.n, T::TN);
     s.group_m = 4;
-    Epi<WR, MF, NF> epi;
+    E epi;
     init(epi);
     const auto kernel = k_ce_gemm<ATR, BTR, WR, WC, MF, NF, Epi>;
     static mx4::LdsLimit limit;
-    const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), T::kLds);
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), kLds);
     if (e != hipSuccess) return e;
     const int64_t items = (int64_t)s.tiles_m * s.tiles_n * s.splits;
-    const int per_cu = 2 * T::kLds <= 160 * 1024 ? 2 : 1;
+    const int per_cu = 2 * kLds <= 160 * 1024 ? 2 : 1;
     const int grid = (int)std::min<int64_t>(items, (int64_t)gemm_num_cus() * per_cu);
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WR * WC), T::kLds, stream, s, epi);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WR * WC), kLds, stream, s, epi);
     return hipGetLastError();
 }
 
@@ -283,18 +419,37 @@ hipError_t launch_tokens(const GemmShape& s, Init init, hipStream_t stream)
 int stat_rows(int64_t tokens) { return token_tile(tokens) <= 128 ? 64 : 128; }    // vocabulary rows of a block of statistics
 
 // ------------------------------------------------------------------ around the products
-// Rows of bf16 at 16-byte places with zeros behind them; with targets, rows of
-// tokens that do not count as zeros (their x may hold anything).
+// Rows of bf16 at 16-byte places with zeros behind them.  For tokens of a
+// backward pass, rows of those that do not count as zeros (their x may hold
+// anything), and the notes.
+struct PackTokens {
+    const int64_t* targets;
+    int64_t vocab;
+    const float* lse;
+    const float* grad;
+    int64_t grad_step;
+    TokenNote* notes;
+};
+template <bool TOKENS>
 __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, int64_t rows, int cols, uint4* out,
-                                                 int chunks, const int64_t* targets, int64_t vocab, int aligned)
+                                                 int chunks, int aligned, PackTokens k)
 {
     const int64_t total = rows * chunks;
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
         const int64_t r = u / chunks;
         const int c = (int)(u - r * chunks) * 8;
         uint4 v = {0, 0, 0, 0};
-        const int64_t t = targets ? targets[r] : 0;
-        if (t >= 0 && t < vocab) {
+        bool on = true;
+        if constexpr (TOKENS) {
+            const int64_t t = k.targets[r];
+            on = t >= 0 && t < k.vocab;
+            if (c == 0) {
+                TokenNote note = {-__builtin_inff(), 0.0f, -1, 0};
+                if (on) note = TokenNote{-k.lse[r] * kLog2e, k.grad[r * k.grad_step], (int)t, 0};
+                k.notes[r] = note;
+            }
+        }
+        if (on) {
             const uint16_t* from = x + r * ld + c;
             if (aligned && c + 8 <= cols) {
                 v = *reinterpret_cast<const uint4*>(from);
@@ -384,13 +539,15 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 bool aligned16(const void* p, int64_t ld) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 15u) == 0; }
 
-hipError_t pack(const void* x, int64_t ld, int64_t rows, int64_t cols, void* out, const int64_t* targets, int64_t vocab,
-                hipStream_t stream)
+hipError_t pack(const void* x, int64_t ld, int64_t rows, int64_t cols, void* out, const PackTokens* tokens, hipStream_t stream)
 {
     const int chunks = (int)(up(cols, 8) / 8);
-    hipLaunchKernelGGL(k_ce_pack, dim3(grid_of(rows * chunks)), dim3(256), 0, stream, static_cast<const uint16_t*>(x), ld,
-                       rows, (int)cols, static_cast<uint4*>(out), chunks, targets, vocab, (int)aligned16(x, ld));
-    return hipGetLastError();
+    const auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(grid_of(rows * chunks)), dim3(256), 0, stream, static_cast<const uint16_t*>(x), ld, rows,
+                           (int)cols, static_cast<uint4*>(out), chunks, (int)aligned16(x, ld), tokens ? *tokens : PackTokens{});
+        return hipGetLastError();
+    };
+    return tokens ? launch(k_ce_pack<true>) : launch(k_ce_pack<false>);
 }
 
 // ------------------------------------------------------------------ plans
@@ -403,7 +560,7 @@ constexpr int64_t kPieceBytes = (int64_t)1 << 29;
 struct Layout {
     int64_t piece, pieces;      // vocabulary rows (a multiple of 256) and number
     int64_t splits;             // of dx
-    size_t x, w, stats, zt, dl, planes, total;      // offsets in the workspace
+    size_t x, w, stats, zt, notes, dl, planes, total;      // offsets in the workspace
 };
 size_t take(size_t& at, int64_t bytes)
 {
@@ -444,6 +601,7 @@ Layout backward_layout(int64_t tokens, int64_t vocab, int64_t hidden)
     size_t at = 0;
     l.x = take(at, tokens * row);
     l.w = take(at, std::min(l.piece, vocab) * row);
+    l.notes = take(at, tokens * (int64_t)sizeof(TokenNote));
     l.dl = take(at, tokens * l.piece * 2);
     l.planes = take(at, l.splits > 1 || l.pieces > 1 ? l.splits * tokens * up(hidden, 16) * 4 : 0);
     l.total = at;
@@ -473,7 +631,7 @@ hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
         GemmShape s = {};
         s.b = {reinterpret_cast<const uint8_t*>(x), g.ldx * 2};
         if (pack_x) {
-            if ((e = pack(x, g.ldx, n, g.hidden, ws + l.x, nullptr, 1, stream)) != hipSuccess) return e;
+            if ((e = pack(x, g.ldx, n, g.hidden, ws + l.x, nullptr, stream)) != hipSuccess) return e;
             s.b = {ws + l.x, up(g.hidden, 8) * 2};
         }
         s.n = (int)n;
@@ -487,14 +645,14 @@ hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
             const uint16_t* w = static_cast<const uint16_t*>(g.w) + v0 * g.ldw;
             s.a = {reinterpret_cast<const uint8_t*>(w), g.ldw * 2};
             if (pack_w) {
-                if ((e = pack(w, g.ldw, m, g.hidden, ws + l.w, nullptr, 1, stream)) != hipSuccess) return e;
+                if ((e = pack(w, g.ldw, m, g.hidden, ws + l.w, nullptr, stream)) != hipSuccess) return e;
                 s.a = {ws + l.w, up(g.hidden, 8) * 2};
             }
             s.m = (int)m;
             e = launch_tokens<false, StatsEpilogue>(s, [&](auto& epi) {
                 epi.m = (int)m;
                 epi.n = (int)n;
-                epi.v0 = v0;
+                epi.v0 = (int)v0;
                 epi.block0 = blocks;
                 epi.cap = g.softcap;
                 epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
@@ -531,7 +689,9 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
     const int T = (int)g.tokens, H = (int)g.hidden, H8 = (int)up(g.hidden, 8);
     // x always as a copy, in which the tokens that do not count are zeros:
     // their products with dl's zeros have to be zeros in dw
-    if ((e = pack(g.x, g.ldx, g.tokens, g.hidden, ws + l.x, g.targets, g.vocab, stream)) != hipSuccess) return e;
+    TokenNote* notes = reinterpret_cast<TokenNote*>(ws + l.notes);
+    const PackTokens tokens = {g.targets, g.vocab, g.lse, g.grad, g.grad_step, notes};
+    if ((e = pack(g.x, g.ldx, g.tokens, g.hidden, ws + l.x, &tokens, stream)) != hipSuccess) return e;
     const ce::Operand x = {ws + l.x, packed};
     float* planes = reinterpret_cast<float*>(ws + l.planes);
     uint16_t* dl = reinterpret_cast<uint16_t*>(ws + l.dl);
@@ -541,7 +701,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
         const uint16_t* wp = static_cast<const uint16_t*>(g.w) + v0 * g.ldw;
         ce::Operand w = {reinterpret_cast<const uint8_t*>(wp), g.ldw * 2};
         if (pack_w) {
-            if ((e = pack(wp, g.ldw, m, g.hidden, ws + l.w, nullptr, 1, stream)) != hipSuccess) return e;
+            if ((e = pack(wp, g.ldw, m, g.hidden, ws + l.w, nullptr, stream)) != hipSuccess) return e;
             w = {ws + l.w, packed};
         }
         GemmShape s = {};
@@ -554,14 +714,10 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
         e = launch_tokens<false, GradEpilogue>(s, [&](auto& epi) {
             epi.m = (int)m;
             epi.n = T;
-            epi.v0 = v0;
-            epi.vocab = g.vocab;
+            epi.v0 = (int)v0;
             epi.cap = g.softcap;
             epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
-            epi.targets = g.targets;
-            epi.lse = g.lse;
-            epi.grad = g.grad;
-            epi.grad_step = g.grad_step;
+            epi.tokens = notes;
             epi.dl = dl;
             epi.ld = l.piece;
         }, stream);
