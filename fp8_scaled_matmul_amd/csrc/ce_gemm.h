@@ -67,9 +67,11 @@ __device__ inline Item item_of(const GemmShape& s, int id)
     const int r = t - g * in_group;
     it.tm = first_m + r % gsize;
     it.tn = r / gsize;
-    const int64_t stages = (s.k + kStageK - 1) / kStageK;
-    it.first = (int)(stages * it.split / s.splits);
-    it.end = (int)(stages * (it.split + 1) / s.splits);
+    // the first (stages % splits) splits are one stage longer
+    const int stages = (s.k + kStageK - 1) / kStageK;
+    const int each = stages / s.splits, more = stages - each * s.splits;
+    it.first = __builtin_amdgcn_readfirstlane(each * it.split + min(it.split, more));
+    it.end = it.first + __builtin_amdgcn_readfirstlane(each + (it.split < more));
     return it;
 }
 
@@ -99,9 +101,9 @@ template <bool ATR, bool BTR, int WR, int WC, int MF, int NF>
 struct Tile {
     static constexpr int W = WR * WC, TM = 32 * MF * WR, TN = 32 * NF * WC;
     static constexpr int kStage = (TM + TN) * 64;
-    // what an epilogue wants of its tile's columns: 64 lanes x 16 bytes for each
-    // wave column, of the items whose stages are on their way and the one at work
-    static constexpr int kNotes = 1024 * WC;
+    // what an epilogue wants of its tile's columns: 16 bytes each, in runs of 64
+    // columns of a wave, of the items whose stages are on their way and the one at work
+    static constexpr int kRuns = (NF + 1) / 2, kNotes = 1024 * kRuns * WC;
     template <typename Epi>
     static constexpr int lds_bytes()
     {
@@ -120,7 +122,7 @@ struct Tile {
     // Epi: operator()(item, acc, row, column, notes): a lane holds rows row + 32 i
     // + r in acc[j][i][r], column + 32 j.  It returns whether it has issued
     // at least kStores vector memory operations.  With kNotes
-    // set, note(lds, item, column) brings 1 KB, which a call finds at notes.
+    // set, note(lds, column) brings 1 KB for each run of 64 columns, which a call finds at notes.
     template <typename Epi>
     __device__ static void run(const GemmShape& s, uint8_t* lds, Epi& epi)
     {
@@ -149,60 +151,71 @@ struct Tile {
             vb[j] = BTR ? (uint32_t)(row * s.b.ld + (((in >> 5) ^ swz_strided<TN>(row)) << 5) + (in & 31))
                         : (uint32_t)((16 * (ub + j) + (lane >> 2)) * s.b.ld + kc_chunk);
         }
-        // Where an item's data begin, and how much there is from there on
-        // (less than 2^31: one stage's offsets never reach that).
+        // Where an operand's stage lies and what of it may be read.  K-contiguous:
+        // the tile's rows, the same for all stages of an item.  K-strided: the
+        // rows from K k0 on, 32 or what is left.  Past the last item: nothing.
         const uint8_t *pa, *pb;
-        int64_t la, lb;
+        uint32_t bytes_a, bytes_b;
+        int k_left;
         const uint32_t row_bytes = 2u * (uint32_t)((s.k + 7) & ~7);
+        const int total = s.tiles_m * s.tiles_n * s.splits;
         const auto describe = [&]() {
-            const bool live = f.id < s.tiles_m * s.tiles_n * s.splits;
+            const bool live = f.id < total;
             const int m0 = f.tm * TM, n0 = f.tn * TN;
-            const int64_t k0 = (int64_t)ft * kStageK;
+            const int k0 = ft * kStageK;
             if constexpr (ATR) {
                 pa = s.a.p + k0 * s.a.ld + 2 * (int64_t)m0;
-                la = (s.k - 1 - k0) * s.a.ld + 2 * (int64_t)(s.m - m0);
+                bytes_a = 2u * (uint32_t)(s.m - m0);
             } else {
                 pa = s.a.p + m0 * s.a.ld;
-                la = (int64_t)(min(s.m - m0, TM) - 1) * s.a.ld + row_bytes;
+                bytes_a = live ? (uint32_t)((min(s.m - m0, TM) - 1) * s.a.ld) + row_bytes : 0u;
             }
             if constexpr (BTR) {
                 pb = s.b.p + k0 * s.b.ld + 2 * (int64_t)n0;
-                lb = (s.k - 1 - k0) * s.b.ld + 2 * (int64_t)(s.n - n0);
+                bytes_b = 2u * (uint32_t)(s.n - n0);
             } else {
                 pb = s.b.p + n0 * s.b.ld;
-                lb = (int64_t)(min(s.n - n0, TN) - 1) * s.b.ld + row_bytes;
+                bytes_b = live ? (uint32_t)((min(s.n - n0, TN) - 1) * s.b.ld) + row_bytes : 0u;
             }
-            if (!live) la = lb = 0;
+            k_left = live ? s.k - k0 : 0;
+            if (!live) f.end = 0x7FFFFFFF;      // no item after it
             if constexpr (Epi::kNotes) {
-                if (wave < WC && live) epi.note(base + kRing * kStage + fnote * kNotes + 1024 * wave, f, n0 + 32 * NF * wave);
+                if (wave < WC && live) {
+#pragma unroll
+                    for (int h = 0; h < kRuns; ++h)
+                        epi.note(base + kRing * kStage + fnote * kNotes + 1024 * (kRuns * wave + h), n0 + 32 * NF * wave + 64 * h);
+                }
                 fnote = fnote == kRing ? 0 : fnote + 1;
             }
         };
         describe();
-        const auto records = [](int64_t bytes) {
-            return (uint32_t)min(max(bytes, (int64_t)0), (int64_t)0x7FFFFFFF);
+        // The next stage: what its instructions share, the j-th of them, the step on.
+        uint32_t to;
+        v4u ra, rb;
+        bool past;
+        const auto fill_begin = [&]() {
+            to = base + fslot * kStage;
+            past = (uint32_t)ft * (2 * kStageK) + kc_chunk >= row_bytes;     // K-contiguous: behind the row's end
+            const int rows = min(k_left, kStageK);
+            ra = gemm::make_rsrc(ATR ? pa : pa + ft * (2 * kStageK),
+                                 !ATR ? bytes_a - min(bytes_a, (uint32_t)ft * (2 * kStageK))
+                                      : rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)s.a.ld + bytes_a : 0u);
+            rb = gemm::make_rsrc(BTR ? pb : pb + ft * (2 * kStageK),
+                                 !BTR ? bytes_b - min(bytes_b, (uint32_t)ft * (2 * kStageK))
+                                      : rows > 0 ? (uint32_t)(rows - 1) * (uint32_t)s.b.ld + bytes_b : 0u);
         };
-        const auto fill = [&]() {
-            const uint32_t to = base + fslot * kStage;
-            const uint32_t kb = (uint32_t)ft * (2 * kStageK);
-            const bool past = kb + kc_chunk >= row_bytes;       // K-contiguous: behind the row's end
-            const v4u ra = gemm::make_rsrc(pa, records(la)), rb = gemm::make_rsrc(pb, records(lb));
-#pragma unroll
-            for (int j = 0; j < kA; ++j)
-                gemm::dma16(to + 1024 * (ua + j), ATR ? va[j] : past ? gemm::kOutOfRange : va[j] + kb, ra);
-#pragma unroll
-            for (int j = 0; j < kB; ++j)
-                gemm::dma16(to + TM * 64 + 1024 * (ub + j), BTR ? vb[j] : past ? gemm::kOutOfRange : vb[j] + kb, rb);
+        const auto fill_one = [&](int j) {
+            if (j < kA)
+                gemm::dma16(to + 1024 * (ua + j), !ATR && past ? gemm::kOutOfRange : va[j], ra);
+            else
+                gemm::dma16(to + TM * 64 + 1024 * (ub + j - kA), !BTR && past ? gemm::kOutOfRange : vb[j - kA], rb);
+        };
+        const auto fill_end = [&]() {
             fslot = (fslot + 1) & (kRing - 1);
-            if constexpr (ATR) {
-                pa += kStageK * s.a.ld;
-                la -= kStageK * s.a.ld;
-            }
-            if constexpr (BTR) {
-                pb += kStageK * s.b.ld;
-                lb -= kStageK * s.b.ld;
-            }
-            if (++ft >= f.end && f.id < s.tiles_m * s.tiles_n * s.splits) {
+            if constexpr (ATR) pa += kStageK * s.a.ld;
+            if constexpr (BTR) pb += kStageK * s.b.ld;
+            k_left -= kStageK;
+            if (++ft >= f.end) {
                 f = item_of(s, f.id + gridDim.x);
                 ft = f.first;
                 describe();
@@ -217,49 +230,54 @@ struct Tile {
         const int ar = 16 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);
         const int tk = 8 * half + ((lane & 15) >> 2);           // K-strided: this lane's row of a read
         const int tc = (lane >> 4 & 1) * 4 + (lane & 3);        // and its 4 columns' place among the fragment's 32
-        uint32_t at[MF], bt[NF];
+        // K-strided: a row's address for each fragment, the second half stage 16 rows
+        // on.  K-contiguous: fragments lie 32 rows apart, the second half stage
+        // across bit 5 (chunk half + 2).
+        constexpr int kAt = ATR ? MF : 2, kBt = BTR ? NF : 2;
+        uint32_t at[kAt], bt[kBt];
 #pragma unroll
-        for (int i = 0; i < MF; ++i)
+        for (int i = 0; i < kAt; ++i)
             at[i] = ATR ? tk * 2 * TM + (((((wm + 32 * i) >> 4) + (tc & 1)) ^ swz_strided<TM>(tk)) << 5) + (tc >> 1) * 8
-                        : (wm + 32 * i + ar) * 64 + 16 * swz64(ar, half);
+                        : ((wm + ar) * 64 + 16 * swz64(ar, half)) ^ (32 * i);
 #pragma unroll
-        for (int j = 0; j < NF; ++j)
+        for (int j = 0; j < kBt; ++j)
             bt[j] = TM * 64 + (BTR ? tk * 2 * TN + (((((wn + 32 * j) >> 4) + (tc >> 2)) ^ swz_strided<TN>(tk)) << 5) + (tc & 3) * 8
-                                   : (wn + 32 * j + c) * 64 + 16 * swz64(c, half));
+                                   : ((wn + c) * 64 + 16 * swz64(c, half)) ^ (32 * j));
         v8bf fa[2][MF], fb[2][NF];
         int slot = 0;
-        const auto get = [&](auto TR, uint32_t from, int kk, int row_bytes) -> v8bf {
-            if constexpr (decltype(TR)::value) {
-                struct {
-                    v4s lo, hi;
-                } v;
-                v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + from + 16 * kk * row_bytes));
-                v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + from + (16 * kk + 4) * row_bytes));
-                return __builtin_bit_cast(v8bf, v);
-            } else {
-                return *reinterpret_cast<const v8bf*>(lds + (from ^ (32u * kk)));
-            }
+        const auto strided = [&](uint32_t from, int kk, int row_bytes) -> v8bf {
+            struct {
+                v4s lo, hi;
+            } v;
+            v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + from + 16 * kk * row_bytes));
+            v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(lds + from + (16 * kk + 4) * row_bytes));
+            return __builtin_bit_cast(v8bf, v);
         };
-        const auto read = [&](auto KK) {
+        // The j-th of a half stage's fragments, B's first.
+        const auto read_one = [&](auto KK, int j) {
             constexpr int kk = decltype(KK)::value;
             const uint32_t ring = slot * kStage;
-#pragma unroll
-            for (int j = 0; j < NF; ++j) fb[kk][j] = get(std::integral_constant<bool, BTR>{}, bt[j] + ring, kk, 2 * TN);
-#pragma unroll
-            for (int i = 0; i < MF; ++i) fa[kk][i] = get(std::integral_constant<bool, ATR>{}, at[i] + ring, kk, 2 * TM);
+            if (j < NF)
+                fb[kk][j] = BTR ? strided(bt[j % kBt] + ring, kk, 2 * TN)
+                                : *reinterpret_cast<const v8bf*>(lds + (bt[kk] + ring) + 2048 * j);
+            else
+                fa[kk][j - NF] = ATR ? strided(at[(j - NF) % kAt] + ring, kk, 2 * TM)
+                                     : *reinterpret_cast<const v8bf*>(lds + (at[kk] + ring) + 2048 * (j - NF));
         };
         Acc acc;
-        // Matrix instructions lo .. hi - 1 of a half stage's MF NF.  What is
-        // written around a call stays on its side.
-        const auto products = [&](auto KK, int lo, int hi) {
+        // A half stage's matrix instructions, and after the m-th what `between` does.
+        // Nothing moves from its place: the reads and DMA of other stages are
+        // issued under the matrix instructions' time.
+        const auto products = [&](auto KK, auto between) {
             constexpr int kk = decltype(KK)::value;
-            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int m = 0; m < MF * NF; ++m)
-                if (m >= lo && m < hi)
-                    acc[m % NF][m / NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][m / NF], fb[kk][m % NF],
-                                                                                  acc[m % NF][m / NF], 0, 0, 0);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int m = 0; m < MF * NF; ++m) {
+                acc[m % NF][m / NF] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[kk][m / NF], fb[kk][m % NF],
+                                                                              acc[m % NF][m / NF], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                between(m);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         };
         const auto clear = [&]() {
 #pragma unroll
@@ -269,23 +287,30 @@ struct Tile {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) acc[j][i][r] = 0.0f;
         };
-        constexpr int kAll = MF * NF;
+        constexpr int kAll = MF * NF, kReads = MF + NF;
         constexpr std::integral_constant<int, 0> k0{};
         constexpr std::integral_constant<int, 1> k1{};
         clear();
 #pragma unroll 1
-        for (int i = 0; i < kRing; ++i) fill();
+        for (int i = 0; i < kRing; ++i) {
+            fill_begin();
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) fill_one(j);
+            fill_end();
+        }
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(3 * kPer) : "memory");     // the first stage
         gemm::barrier_lds();
-        read(k0);
+#pragma unroll
+        for (int j = 0; j < kReads; ++j) read_one(k0, j);
         int stored = 3;         // stages since the last epilogue's stores, up to 3
         int note = 0;
-        const int total = s.tiles_m * s.tiles_n * s.splits;
         for (Item it = item_of(s, blockIdx.x); it.id < total; it = item_of(s, it.id + gridDim.x)) {
             for (int t = it.first; t < it.end; ++t) {
-                products(k0, 0, kAll / 4);
-                read(k1);
-                products(k0, kAll / 4, kAll);
+                products(k0, [&](int m) {
+#pragma unroll
+                    for (int j = 0; j < kReads; ++j)
+                        if (j * kAll / kReads == m) read_one(k1, j);
+                });
                 // The next stage has landed: the two after it are younger, and an
                 // epilogue's stores are to the three stages filled before them.
                 constexpr int kLoose = 2 * kPer + Epi::kStores < 63 ? 2 * kPer + Epi::kStores : 63;
@@ -297,13 +322,19 @@ struct Tile {
                 }
                 // past this every wave has read the whole stage: its slot is free
                 gemm::barrier_lds();
-                products(k1, 0, kAll / 2);
-                fill();
+                fill_begin();
                 slot = (slot + 1) & (kRing - 1);
-                read(k0);
-                products(k1, kAll / 2, kAll);
+                products(k1, [&](int m) {
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+                        if (j * kAll / kPer == m) fill_one(j);
+#pragma unroll
+                    for (int j = 0; j < kReads; ++j)
+                        if (j * kAll / kReads == m) read_one(k0, j);
+                });
+                fill_end();
             }
-            const uint8_t* notes = lds + kRing * kStage + note * kNotes + 1024 * (wave / WR);
+            const uint8_t* notes = lds + kRing * kStage + note * kNotes + 1024 * kRuns * (wave / WR);
             stored = epi(it, acc, it.tm * TM + wm + 16 * half, it.tn * TN + wn + c, notes) ? 0 : 3;
             note = note == kRing ? 0 : note + 1;
             clear();

@@ -118,7 +118,7 @@ struct StatsEpilogue {
     float* zt;
 
     // the targets' low halves: a match by mistake is of a target that is not used
-    __device__ void note(uint32_t lds, const Item&, int col) const
+    __device__ void note(uint32_t lds, int col) const
     {
         gemm::dma4(lds, (uint32_t)(col + (threadIdx.x & 63)) * 8u, gemm::make_rsrc(targets, (uint32_t)n * 8u));
     }
@@ -144,7 +144,7 @@ struct StatsEpilogue {
                     for (int r = 0; r < 16; ++r)
                         if (32 * i + r >= left) acc[j][i][r] = -__builtin_inff();
             }
-            const int at = reinterpret_cast<const int*>(notes)[32 * j + (lane & 31)] - v0 - row;
+            const int at = reinterpret_cast<const int*>(notes + 1024 * (j / 2))[32 * (j % 2) + (lane & 31)] - v0 - row;
             if (__any((uint32_t)at < 32u * MF)) {
                 float z = 0.0f;
 #pragma unroll
@@ -199,7 +199,7 @@ struct GradEpilogue {
     uint16_t* dl;               // [n, ld]
     int64_t ld;
 
-    __device__ void note(uint32_t lds, const Item&, int col) const
+    __device__ void note(uint32_t lds, int col) const
     {
         const int64_t left = (int64_t)(n - col) * 16;
         gemm::dma16(lds, (uint32_t)(threadIdx.x & 63) * 16u,
@@ -270,7 +270,7 @@ struct OutEpilogue {
     int64_t ld;
     int wide;                   // 16-byte stores are in place
 
-    __device__ void note(uint32_t, const Item&, int) const {}
+    __device__ void note(uint32_t, int) const {}
 
     __device__ bool operator()(const Item& it, v16f (&acc)[NF][MF], int row, int col, const uint8_t*) const
     {
