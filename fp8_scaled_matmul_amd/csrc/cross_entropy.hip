@@ -20,10 +20,9 @@ namespace {
 
 using ce::GemmShape;
 using ce::Item;
-using ce::v16f;
 using gemm::v4f;
 using gemm::v4u;
-typedef uint32_t v16u __attribute__((ext_vector_type(16)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -48,62 +47,50 @@ __device__ inline float softcap_any(float l, float cap, float inv_cap)
 }
 // Of a fragment's column, the far form only where one of the wave's needs it.
 template <int MF>
-__device__ inline void softcap_column(v16f (&acc)[MF], float cap, float inv_cap)
+__device__ inline void softcap_column(v4f (&acc)[MF], float cap, float inv_cap)
 {
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) most = fmaxf(most, __builtin_fabsf(acc[i][r]));      // NaN: either form gives NaN
+        for (int r = 0; r < 4; ++r) most = fmaxf(most, __builtin_fabsf(acc[i][r]));      // NaN: either form gives NaN
     const bool far = __any(most * inv_cap > 1.0f);
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
         __builtin_amdgcn_sched_barrier(0);      // one fragment after another: registers
         if (far) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][r] = softcap_any(acc[i][r], cap, inv_cap);
+            for (int r = 0; r < 4; ++r) acc[i][r] = softcap_any(acc[i][r], cap, inv_cap);
         } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][r] = softcap_near(acc[i][r], inv_cap);
+            for (int r = 0; r < 4; ++r) acc[i][r] = softcap_near(acc[i][r], inv_cap);
         }
     }
 }
 
 // ------------------------------------------------------------------ epilogues
-// A lane holds, for tokens (columns) col + 32 j, the rows row + 32 i + r:
-// acc[j][i][r].  A store of 16 bytes a lane as they lie would touch 64 places;
-// swapped between the 16-lane groups first, four lanes share 64 bytes.
+// A lane holds, for tokens (columns) col + 16 j, the rows row + 16 i + r:
+// acc[j][i][r].
 
-// Odd groups of 16 lanes of a and even ones of b change places; upper half of a
-// and lower half of b.
-__device__ inline void swap16(uint32_t& a, uint32_t& b)
+// Two fragments below each other (16 i and 16 (i + 1)) to bf16, for a store of
+// 16 bytes a lane.  As they lie a lane has 4 rows of either; odd groups of 16
+// lanes of the first and even ones of the second change places, and a lane has 8
+// rows from chunk_row() on, the four lanes of a column 32: 64 bytes.
+__device__ inline v4u to_bf16_chunk(const v4f& first, const v4f& second)
 {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-__device__ inline void swap32(uint32_t& a, uint32_t& b)
-{
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-
-// 16 values of a lane to bf16, for two stores: after the swap lane l holds 8
-// values from row 8 (l / 16 % 2) on of its half's 16, of column l % 16 (a) and
-// 16 + l % 16 (b).
-__device__ inline void to_bf16_chunks(const v16f& v, v4u& a, v4u& b)
-{
+    v4u out;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        uint32_t lo = gemm::pack_bf16(v[2 * q], v[2 * q + 1]), hi = gemm::pack_bf16(v[8 + 2 * q], v[8 + 2 * q + 1]);
-        swap16(lo, hi);
-        a[q] = lo;
-        b[q] = hi;
+    for (int q = 0; q < 2; ++q) {
+        const auto r = __builtin_amdgcn_permlane16_swap(gemm::pack_bf16(first[2 * q], first[2 * q + 1]),
+                                                        gemm::pack_bf16(second[2 * q], second[2 * q + 1]), false, false);
+        out[q] = r[0];
+        out[2 + q] = r[1];
     }
+    return out;
 }
+__device__ inline int chunk_row() { return 16 * (threadIdx.x >> 4 & 1) + 8 * (threadIdx.x >> 5 & 1); }
 
-// The forward's: of each token and block of 32 MF vocabulary rows the maximum
+// The forward's: of each token and block of 16 MF vocabulary rows the maximum
 // and the sum of exp(z - maximum); the target's z, by the one lane that has it.
 template <int WR, int MF, int NF>
 struct StatsEpilogue {
@@ -123,16 +110,16 @@ struct StatsEpilogue {
         gemm::dma4(lds, (uint32_t)(col + (threadIdx.x & 63)) * 8u, gemm::make_rsrc(targets, (uint32_t)n * 8u));
     }
 
-    __device__ bool operator()(const Item& it, v16f (&acc)[NF][MF], int row, int col, const uint8_t* notes) const
+    __device__ bool operator()(const Item& it, v4f (&acc)[NF][MF], int row, int col, const uint8_t* notes) const
     {
         const int lane = threadIdx.x & 63;
         const int wave_row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % WR;
         float2* to = part + (int64_t)(block0 + it.tm * WR + wave_row) * n;
         const __amdgpu_buffer_rsrc_t rp = gemm::make_store_rsrc(to, (uint32_t)n * 8u);
-        const bool edge = (it.tm + 1) * (32 * MF * WR) > m;
+        const bool edge = (it.tm + 1) * (16 * MF * WR) > m;
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const int t = col + 32 * j;
+            const int t = col + 16 * j;
             __builtin_amdgcn_sched_barrier(0);
             if (cap != 0.0f) softcap_column<MF>(acc[j], cap, inv_cap);
             if (edge) {
@@ -141,35 +128,36 @@ struct StatsEpilogue {
 #pragma unroll
                 for (int i = 0; i < MF; ++i)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (32 * i + r >= left) acc[j][i][r] = -__builtin_inff();
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * i + r >= left) acc[j][i][r] = -__builtin_inff();
             }
-            const int at = reinterpret_cast<const int*>(notes + 1024 * (j / 2))[32 * (j % 2) + (lane & 31)] - v0 - row;
-            if (__any((uint32_t)at < 32u * MF)) {
+            const int at = reinterpret_cast<const int*>(notes + 1024 * (j / 4))[16 * (j % 4) + (lane & 15)] - v0 - row;
+            if (__any((uint32_t)at < 16u * MF)) {
                 float z = 0.0f;
 #pragma unroll
                 for (int i = 0; i < MF; ++i)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) z = at == 32 * i + r ? acc[j][i][r] : z;
-                const bool here = (uint32_t)at < 32u * MF && (at & 16) == 0;
+                    for (int r = 0; r < 4; ++r) z = at == 16 * i + r ? acc[j][i][r] : z;
+                const bool here = (uint32_t)at < 16u * MF && (at & 12) == 0;
                 if (here && t < n && row + at < m) zt[t] = z;
             }
             float mx = -__builtin_inff();
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, acc[j][i][r]);
+                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, acc[j][i][r]);
+            mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
             mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
             const float off = mx == -__builtin_inff() ? 0.0f : -mx * kLog2e;
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[r & 3] += exp2_fast(__builtin_fmaf(acc[j][i][r], kLog2e, off));
+                for (int r = 0; r < 4; ++r) s[r] += exp2_fast(__builtin_fmaf(acc[j][i][r], kLog2e, off));
             float sum = (s[0] + s[1]) + (s[2] + s[3]);
+            sum += __shfl_xor(sum, 16, 64);
             sum += __shfl_xor(sum, 32, 64);
-            const uint32_t where = lane < 32 && t < n ? (uint32_t)t * 8u : gemm::kOutOfRange;
-            typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+            const uint32_t where = lane < 16 && t < n ? (uint32_t)t * 8u : gemm::kOutOfRange;
             __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, float2{mx, sum}), rp, (int)where, 0, 0);
         }
         return true;
@@ -190,7 +178,7 @@ struct TokenNote {
 // the vocabulary's end as zeros.
 template <int WR, int MF, int NF>
 struct GradEpilogue {
-    static constexpr int kStores = 2 * MF * NF;
+    static constexpr int kStores = MF / 2 * NF;
     static constexpr bool kNotes = true;
     int m, n;
     int v0;
@@ -206,50 +194,54 @@ struct GradEpilogue {
                     gemm::make_rsrc(tokens + col, (uint32_t)min(max(left, (int64_t)0), (int64_t)1024)));
     }
 
-    __device__ bool operator()(const Item& it, v16f (&acc)[NF][MF], int row, int col, const uint8_t* notes) const
+    __device__ bool operator()(const Item& it, v4f (&acc)[NF][MF], int row, int col, const uint8_t* notes) const
     {
         const int lane = threadIdx.x & 63;
-        const int n0 = __builtin_amdgcn_readfirstlane(col & ~31);       // this wave's first token
+        const int n0 = __builtin_amdgcn_readfirstlane(col & ~15);       // this wave's first token
         const __amdgpu_buffer_rsrc_t rd =
-            gemm::make_store_rsrc(dl + n0 * ld, (uint32_t)(max(min(n - n0, 32 * NF), 0) * ld * 2));
-        const uint32_t to = (uint32_t)((lane & 15) * ld + row + 8 * (lane >> 4 & 1)) * 2u;
-        const bool edge = (it.tm + 1) * (32 * MF * WR) > m;
+            gemm::make_store_rsrc(dl + n0 * ld, (uint32_t)(max(min(n - n0, 16 * NF), 0) * ld * 2));
+        const uint32_t to = (uint32_t)((lane & 15) * ld + (row & ~15) + chunk_row()) * 2u;
+        const bool edge = (it.tm + 1) * (16 * MF * WR) > m;
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const TokenNote k = reinterpret_cast<const TokenNote*>(notes)[32 * j + (lane & 31)];
+            const TokenNote k = reinterpret_cast<const TokenNote*>(notes)[16 * j + (lane & 15)];
             const int at = k.target < 0 ? -1 : k.target - v0 - row;
             if (cap != 0.0f) softcap_column<MF>(acc[j], cap, inv_cap);
-            const bool target_here = __any((uint32_t)at < 32u * MF);
+            const bool target_here = __any((uint32_t)at < 16u * MF);
 #pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                __builtin_amdgcn_sched_barrier(0);      // one fragment after another: registers
-                v16f d;
+            for (int i = 0; i < MF; i += 2) {
+                __builtin_amdgcn_sched_barrier(0);      // one pair after another: registers
+                v4f d[2];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) d[r] = exp2_fast(__builtin_fmaf(acc[j][i][r], kLog2e, k.off));
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) d[h][r] = exp2_fast(__builtin_fmaf(acc[j][i + h][r], kLog2e, k.off));
                 if (target_here) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) d[r] = at == 32 * i + r ? d[r] - 1.0f : d[r];
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) d[h][r] = at == 16 * (i + h) + r ? d[h][r] - 1.0f : d[h][r];
                 }
                 if (cap != 0.0f) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const float u = acc[j][i][r] * inv_cap;
-                        d[r] *= __builtin_fmaf(-u, u, 1.0f);
-                    }
-                }
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) d[r] *= k.grad;
+                        for (int r = 0; r < 4; ++r) {
+                            const float u = acc[j][i + h][r] * inv_cap;
+                            d[h][r] *= __builtin_fmaf(-u, u, 1.0f);
+                        }
+                }
+                d[0] *= k.grad;
+                d[1] *= k.grad;
                 if (edge) {
                     int left = m - row;
                     asm("" : "+v"(left));   // as above
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) d[r] = 32 * i + r < left ? d[r] : 0.0f;
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) d[h][r] = 16 * (i + h) + r < left ? d[h][r] : 0.0f;
                 }
-                v4u a, b;
-                to_bf16_chunks(d, a, b);
-                const uint32_t first = to + (uint32_t)(32 * j * ld + 32 * i) * 2u;
-                gemm::store16(a, first, rd);
-                gemm::store16(b, first + (uint32_t)(16 * ld) * 2u, rd);
+                gemm::store16(to_bf16_chunk(d[0], d[1]), to + (uint32_t)(16 * j * ld + 16 * i) * 2u, rd);
             }
         }
         return true;
@@ -260,7 +252,7 @@ struct GradEpilogue {
 // piece of the vocabulary left), or bf16 at the end.
 template <int WR, int MF, int NF>
 struct OutEpilogue {
-    static constexpr int kStores = 2 * MF * NF;
+    static constexpr int kStores = MF / 2 * NF;
     static constexpr bool kNotes = false;
     int m, n;                   // the gradient's columns and rows
     float* plane;               // [splits, n, ld_plane], or null
@@ -272,100 +264,56 @@ struct OutEpilogue {
 
     __device__ void note(uint32_t, int) const {}
 
-    __device__ bool operator()(const Item& it, v16f (&acc)[NF][MF], int row, int col, const uint8_t*) const
+    __device__ bool operator()(const Item& it, v4f (&acc)[NF][MF], int row, int col, const uint8_t*) const
     {
-        const int lane = threadIdx.x & 63, half = lane >> 5, group = lane >> 4 & 1;
-        const int n0 = __builtin_amdgcn_readfirstlane(col & ~31);
-        const int rows = max(min(n - n0, 32 * NF), 0);
-        // the planes: four lanes share 64 bytes, 16 rows of a fragment's half
-        const __amdgpu_buffer_rsrc_t rp = gemm::make_store_rsrc(
-            plane + ((int64_t)it.split * n + n0) * ld_plane, plane ? (uint32_t)(rows * ld_plane * 4) : 0u);
-        const int base = row - 16 * half;
-        const auto place = [&](int i, int j, int h, int upper) {
-            const int first = base + 32 * i + 16 * h;
-            return first < m ? (uint32_t)((32 * j + 16 * upper + (lane & 15)) * ld_plane + first + 8 * half + 4 * group) * 4u
-                             : gemm::kOutOfRange;
-        };
+        const int lane = threadIdx.x & 63;
+        const int n0 = __builtin_amdgcn_readfirstlane(col & ~15);
+        const int rows = max(min(n - n0, 16 * NF), 0);
         if (plane && (add || !out)) {
+            const __amdgpu_buffer_rsrc_t rp = gemm::make_store_rsrc(plane + ((int64_t)it.split * n + n0) * ld_plane,
+                                                                    (uint32_t)(rows * ld_plane * 4));
+            const uint32_t at = (uint32_t)((lane & 15) * ld_plane + row) * 4u;
+            const auto place = [&](int i, int j) {
+                return row + 16 * i < m ? at + (uint32_t)(16 * j * ld_plane + 16 * i) * 4u : gemm::kOutOfRange;
+            };
+            if (add) {
 #pragma unroll
-            for (int j = 0; j < NF; ++j)
+                for (int j = 0; j < NF; ++j)
 #pragma unroll
-                for (int i = 0; i < MF; ++i) {
-                    // v[2 h + upper]: of half h's 16 rows, columns 16 upper + l % 16.
-                    // (Cast as a whole: the compiler takes element 0 four times
-                    // for four casts of elements.)
-                    v4u v[4];
-                    v16u bits = __builtin_bit_cast(v16u, acc[j][i]);
+                    for (int i = 0; i < MF; ++i)
+                        acc[j][i] += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)place(i, j), 0, 0));
+            }
+            if (!out) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t a = bits[q], b = bits[4 + q], c = bits[8 + q], d = bits[12 + q];
-                        swap16(a, b);
-                        swap16(c, d);
-                        swap32(a, c);
-                        swap32(b, d);
-                        v[0][q] = a;
-                        v[1][q] = b;
-                        v[2][q] = c;
-                        v[3][q] = d;
-                    }
-                    if (add) {
-                        v4u o[4];
+                for (int j = 0; j < NF; ++j)
 #pragma unroll
-                        for (int p = 0; p < 4; ++p)
-                            o[p] = __builtin_bit_cast(
-                                v4u, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)place(i, j, p >> 1, p & 1), 0, 0));
-#pragma unroll
-                        for (int p = 0; p < 4; ++p)
-                            v[p] = __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, v[p]) + __builtin_bit_cast(v4f, o[p]));
-                    }
-                    if (!out) {
-#pragma unroll
-                        for (int p = 0; p < 4; ++p) gemm::store16(v[p], place(i, j, p >> 1, p & 1), rp);
-                    } else {
-                        // back to where they were
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t a = v[0][q], b = v[1][q], c = v[2][q], d = v[3][q];
-                            swap32(a, c);
-                            swap32(b, d);
-                            swap16(a, b);
-                            swap16(c, d);
-                            bits[q] = a;
-                            bits[4 + q] = b;
-                            bits[8 + q] = c;
-                            bits[12 + q] = d;
-                        }
-                        acc[j][i] = __builtin_bit_cast(v16f, bits);
-                    }
-                }
-            if (!out) return true;
+                    for (int i = 0; i < MF; ++i) gemm::store16(__builtin_bit_cast(v4u, acc[j][i]), place(i, j), rp);
+                return true;
+            }
         }
         if (wide) {
             const __amdgpu_buffer_rsrc_t ro =
                 gemm::make_store_rsrc(out + n0 * ld, rows ? (uint32_t)(((rows - 1) * ld + m) * 2) : 0u);
-            const uint32_t to = (uint32_t)((lane & 15) * ld + row + 8 * group) * 2u;
+            const int first = (row & ~15) + chunk_row();
+            const uint32_t to = (uint32_t)((lane & 15) * ld + first) * 2u;
 #pragma unroll
             for (int j = 0; j < NF; ++j)
 #pragma unroll
-                for (int i = 0; i < MF; ++i) {
-                    v4u a, b;
-                    to_bf16_chunks(acc[j][i], a, b);
-                    const uint32_t first = row + 8 * group + 32 * i < m ? to + (uint32_t)(32 * j * ld + 32 * i) * 2u : gemm::kOutOfRange;
-                    gemm::store16(a, first, ro);
-                    gemm::store16(b, first + (uint32_t)(16 * ld) * 2u, ro);
-                }
+                for (int i = 0; i < MF; i += 2)
+                    gemm::store16(to_bf16_chunk(acc[j][i], acc[j][i + 1]),
+                                  first + 16 * i < m ? to + (uint32_t)(16 * j * ld + 16 * i) * 2u : gemm::kOutOfRange, ro);
             return true;
         }
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-            const int t = col + 32 * j;
+            const int t = col + 16 * j;
             if (t >= n) continue;
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
-                uint16_t* to = out + t * ld + row + 32 * i;
+                uint16_t* to = out + t * ld + row + 16 * i;
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (row + 32 * i + r < m) to[r] = gemm::to_bf16(acc[j][i][r]);
+                for (int r = 0; r < 4; ++r)
+                    if (row + 16 * i + r < m) to[r] = gemm::to_bf16(acc[j][i][r]);
             }
         }
         return false;
@@ -410,10 +358,10 @@ template <bool ATR, template <int, int, int> class Epi, typename Init>
 hipError_t launch_tokens(const GemmShape& s, Init init, hipStream_t stream)
 {
     switch (token_tile(s.n)) {
-    case 32: return launch_tile<ATR, false, 4, 1, 2, 1, Epi>(s, init, stream);
-    case 64: return launch_tile<ATR, false, 4, 1, 2, 2, Epi>(s, init, stream);
-    case 128: return launch_tile<ATR, false, 4, 2, 2, 2, Epi>(s, init, stream);
-    default: return launch_tile<ATR, false, 2, 4, 4, 2, Epi>(s, init, stream);
+    case 32: return launch_tile<ATR, false, 4, 1, 4, 2, Epi>(s, init, stream);
+    case 64: return launch_tile<ATR, false, 4, 1, 4, 4, Epi>(s, init, stream);
+    case 128: return launch_tile<ATR, false, 4, 2, 4, 4, Epi>(s, init, stream);
+    default: return launch_tile<ATR, false, 2, 4, 8, 4, Epi>(s, init, stream);
     }
 }
 int stat_rows(int64_t tokens) { return token_tile(tokens) <= 128 ? 64 : 128; }    // vocabulary rows of a block of statistics
@@ -758,7 +706,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
             s.k = T;
             s.splits = 1;
             uint16_t* dw = static_cast<uint16_t*>(g.dw) + v0 * g.lddw;
-            e = launch_tile<true, true, 2, 4, 4, 2, OutEpilogue>(s, [&](auto& epi) {
+            e = launch_tile<true, true, 2, 4, 8, 4, OutEpilogue>(s, [&](auto& epi) {
                 epi.m = H;
                 epi.n = (int)m;
                 epi.plane = nullptr;
