@@ -4,6 +4,7 @@
 //   E sum_e f_e P_e,  f_e = counts_e / (N top_k),  P_e = mean softmax(l)_e,
 // N the tokens that count; and the logits' gradient.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "fp8mi_internal.h"
@@ -14,7 +15,7 @@ namespace fp8mi {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kWaves = 4, kParts = 256;     // waves of a workgroup, workgroups at most
+constexpr int kWaves = 16, kParts = 256;    // waves of a workgroup; workgroups at most
 
 struct RouteKArgs {
     const void* logits;
@@ -24,143 +25,295 @@ struct RouteKArgs {
     const uint8_t* mask;
     int32_t* ids;
     float* weights;
-    float* part_p;          // [workgroups, experts]
-    int32_t* part_c;        // [workgroups, experts]
-    int32_t* part_n;        // [workgroups]
-    const int32_t* counts;  // backward
+    int32_t* counts;
+    float* balance;
+    float* part_p;          // [parts, experts]
+    int32_t* part_c;        // [parts, experts]
+    int32_t* part_n;        // [parts]
+    int parts;
+    double* part_loss;      // [blocks of 32 experts]
+    int32_t* ticket;
     const float* grad_weights;
     const float* grad_balance;
     void* dlogits;
     int64_t ldd;
 };
 
-__device__ inline float get(const uint16_t* p) { return __builtin_bit_cast(float, (uint32_t)*p << 16); }
-__device__ inline float get(const float* p) { return *p; }
-__device__ inline void put(uint16_t* p, float v) { *p = gemm::to_bf16(v); }
-__device__ inline void put(float* p, float v) { *p = v; }
-
-__device__ inline float wave_fmax(float v)
+// A token is handled by L = 16, 32 or 64 lanes with V experts each, V sub .. V
+// sub + V - 1: up to 128 experts by 16 lanes, so that a wave has 4 tokens at
+// work.  Reductions over a token's lanes are rotations inside 16 (DPP) and, for
+// more, exchanges of groups.
+template <int N>
+__device__ inline uint32_t rotated(uint32_t v)
 {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int N>
+__device__ inline float rotated(float v) { return __builtin_bit_cast(float, rotated<N>(__builtin_bit_cast(uint32_t, v))); }
+template <int N>
+__device__ inline double rotated(double v)
+{
+    const uint2 b = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(double, uint2{rotated<N>(b.x), rotated<N>(b.y)});
+}
+// v of the lane's own and of the other group of 16 (32)
+__device__ inline uint2 both16(uint32_t v)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return uint2{r[0], r[1]};
+}
+__device__ inline uint2 both32(uint32_t v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return uint2{r[0], r[1]};
+}
+template <int L, typename T, typename F>
+__device__ inline T reduce(T v, F f)
+{
+    v = f(v, rotated<8>(v));
+    v = f(v, rotated<4>(v));
+    v = f(v, rotated<2>(v));
+    v = f(v, rotated<1>(v));
+    const auto across = [&](auto both) {
+        if constexpr (sizeof(T) == 4) {
+            const uint2 r = both(__builtin_bit_cast(uint32_t, v));
+            v = f(__builtin_bit_cast(T, r.x), __builtin_bit_cast(T, r.y));
+        } else {
+            const uint2 b = __builtin_bit_cast(uint2, v);
+            const uint2 x = both(b.x), y = both(b.y);
+            v = f(__builtin_bit_cast(T, uint2{x.x, y.x}), __builtin_bit_cast(T, uint2{x.y, y.y}));
+        }
+    };
+    if constexpr (L >= 32) across(both16);
+    if constexpr (L >= 64) across(both32);
     return v;
 }
-__device__ inline float wave_fsum(float v)
-{
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
-}
 
-// A token's logits, V to a lane (expert lane + 64 i), -Inf past the last;
-// returns false where all are -Inf.
-template <typename T, int V>
-__device__ inline bool load_row(const RouteKArgs& a, int64_t t, float (&l)[V], float& mx)
-{
-    const int lane = threadIdx.x & 63;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    mx = -__builtin_inff();
-    bool some = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        l[i] = e < a.experts ? get(row + e) : -__builtin_inff();
-        mx = fmaxf(mx, l[i]);
-        some |= !(l[i] == -__builtin_inff());
+// Keys that order as the selection does: larger logits first, then lower
+// experts, NaN last; distinct, and what no expert has is below them all.
+//   bf16: the ordered bits above the expert's complement, one 32-bit word
+//   fp32: the value as a double, whose 29 free bits hold the expert so that a
+//         lower one is larger (infinities and NaN beyond the type's range)
+struct Key16 {
+    typedef uint32_t T;
+    static __device__ T none() { return 0; }
+    static __device__ T make(float l, int e)
+    {
+        const uint32_t u = __builtin_bit_cast(uint32_t, l + 0.0f) >> 16;       // -0 as 0
+        const uint32_t k = l != l ? 0u : (u & 0x8000u) ? 0xFFFFu - u : u + 0x8000u;
+        return k << 16 | (uint32_t)(0xFFFF - e);
     }
-    mx = wave_fmax(mx);
-    return __any(some);
+    static __device__ int expert(T k) { return 0xFFFF - (int)(k & 0xFFFFu); }
+    static __device__ float value(T k)
+    {
+        const uint32_t o = k >> 16, u = o & 0x8000u ? o - 0x8000u : 0xFFFFu - o;
+        return __builtin_bit_cast(float, o == 0 ? 0x7FC00000u : u << 16);
+    }
+    static __device__ T largest(T a, T b) { return max(a, b); }
+    static __device__ T smallest(T a, T b) { return min(a, b); }
+};
+struct Key32 {
+    typedef double T;
+    static constexpr double kFar = 0x1p200;
+    static __device__ T none() { return -4 * kFar; }
+    static __device__ T make(float l, int e)
+    {
+        // (beyond fp32's range by far; NaN below -Inf)
+        const double v = l != l ? -2 * kFar : __builtin_fabsf(l) == __builtin_inff() ? (double)__builtin_copysignf(1.0f, l) * kFar : (double)(l + 0.0f);
+        uint64_t b = __builtin_bit_cast(uint64_t, v);
+        b |= (b >> 63) ? (uint32_t)e : (uint32_t)(511 - e);
+        return __builtin_bit_cast(double, b);
+    }
+    static __device__ int expert(T k)
+    {
+        const uint64_t b = __builtin_bit_cast(uint64_t, k);
+        const int low = (int)(b & 511u);
+        return (b >> 63) ? low : 511 - low;
+    }
+    static __device__ float value(T k)
+    {
+        const double v = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, k) & ~511ull);
+        return v <= -2 * kFar ? __builtin_nanf("") : __builtin_fabs(v) >= kFar ? __builtin_copysignf(__builtin_inff(), (float)v) : (float)v;
+    }
+    static __device__ T largest(T a, T b) { return __builtin_fmax(a, b); }
+    static __device__ T smallest(T a, T b) { return __builtin_fmin(a, b); }
+};
+
+// A lane's V keys in falling order.
+template <typename K, int V>
+__device__ inline void sort_keys(typename K::T (&k)[V])
+{
+    const auto order = [&](int i, int j) {
+        const auto a = k[i], b = k[j];
+        k[i] = K::largest(a, b);
+        k[j] = K::smallest(a, b);
+    };
+    // merge sort of pairs, fours, eights (odd-even merges)
+#pragma unroll
+    for (int i = 0; i + 1 < V; i += 2) order(i, i + 1);
+#pragma unroll
+    for (int i = 0; i + 3 < V; i += 4) {
+        order(i, i + 2);
+        order(i + 1, i + 3);
+        order(i + 1, i + 2);
+    }
+    if constexpr (V == 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) order(i, i + 4);
+        order(2, 4);
+        order(3, 5);
+#pragma unroll
+        for (int i = 1; i < 7; i += 2) order(i, i + 1);
+    }
 }
 
-// exp(l - max) in place of l, and their sum.
+struct __attribute__((packed, aligned(2))) Bf16s {
+    uint32_t w[4];
+};
+struct __attribute__((packed, aligned(4))) Floats {
+    float v[8];
+};
 template <int V>
-__device__ inline float exponentials(float (&l)[V], float mx)
+__device__ inline void load_row(const uint16_t* row, int e0, int experts, float (&l)[V])
 {
-    float s = 0.0f;
+    if (V == 8 && e0 + V <= experts) {
+        const Bf16s b = *reinterpret_cast<const Bf16s*>(row + e0);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        l[i] = __builtin_amdgcn_exp2f((l[i] - mx) * kLog2e);
-        s += l[i];
+        for (int i = 0; i < V; ++i) l[i] = __builtin_bit_cast(float, i & 1 ? b.w[i / 2] & 0xFFFF0000u : b.w[i / 2] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            l[i] = e0 + i < experts ? __builtin_bit_cast(float, (uint32_t)row[e0 + i] << 16) : -__builtin_inff();
     }
-    return wave_fsum(s);
+}
+template <int V>
+__device__ inline void load_row(const float* row, int e0, int experts, float (&l)[V])
+{
+    if (V == 8 && e0 + V <= experts) {
+        const Floats b = *reinterpret_cast<const Floats*>(row + e0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = b.v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = e0 + i < experts ? row[e0 + i] : -__builtin_inff();
+    }
+}
+template <int V>
+__device__ inline void store_row(uint16_t* row, int e0, int experts, const float (&v)[V])
+{
+    if (V == 8 && e0 + V <= experts) {
+        Bf16s b;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) b.w[i] = gemm::pack_bf16(v[2 * i], v[(2 * i + 1) % V]);
+        *reinterpret_cast<Bf16s*>(row + e0) = b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e0 + i < experts) row[e0 + i] = gemm::to_bf16(v[i]);
+    }
+}
+template <int V>
+__device__ inline void store_row(float* row, int e0, int experts, const float (&v)[V])
+{
+    if (V == 8 && e0 + V <= experts) {
+        Floats b;
+#pragma unroll
+        for (int i = 0; i < V; ++i) b.v[i] = v[i];
+        *reinterpret_cast<Floats*>(row + e0) = b;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e0 + i < experts) row[e0 + i] = v[i];
+    }
 }
 
-template <typename T, int V>
+__device__ inline float add(float a, float b) { return a + b; }
+
+// Each lane sorts its keys; then top_k times the largest of the lanes' first
+// ones is taken out.  Lane j of a token keeps the j-th.
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
 {
+    using K = std::conditional_t<sizeof(T) == 2, Key16, Key32>;
+    constexpr int G = 64 / L;       // tokens of a wave
     __shared__ int32_t count[512];
-    __shared__ float prob[kWaves][512];
+    __shared__ float prob[kWaves][L * V];
     __shared__ int32_t number[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (int e = threadIdx.x; e < 512; e += 64 * kWaves) count[e] = 0;
+    const int sub = lane % L, e0 = V * sub;
+    if (threadIdx.x < 512) count[threadIdx.x] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
     __syncthreads();
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.0f;
     int n = 0;
-    for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.tokens; t += (int64_t)gridDim.x * kWaves) {
-        float l[V], mx;
-        bool on = !a.mask || a.mask[t] != 0;
-        if (on) on = load_row<T, V>(a, t, l, mx);
-        if (!on) {
-            if (lane < a.top_k) {
-                a.ids[t * a.top_k + lane] = -1;
-                a.weights[t * a.top_k + lane] = 0.0f;
-            }
-            continue;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * G; t0 < a.tokens; t0 += (int64_t)gridDim.x * kWaves * G) {
+        const int64_t t = t0 + lane / L;
+        const bool there = t < a.tokens;
+        bool on = there && (!a.mask || a.mask[t] != 0);
+        float l[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = -__builtin_inff();
+        if (on) load_row<V>(static_cast<const T*>(a.logits) + t * a.ld, e0, a.experts, l);
+        typename K::T key[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = e0 + i < a.experts ? K::make(l[i], e0 + i) : K::none();
+        sort_keys<K, V>(key);
+        typename K::T mine = K::none();
+        float mx = 0.0f;
+        for (int j = 0; j < a.top_k; ++j) {
+            const typename K::T best = reduce<L>(key[0], K::largest);
+            if (j == 0) mx = K::value(best);
+            if (sub == j) mine = best;
+            const bool won = key[0] == best;
+#pragma unroll
+            for (int i = 0; i + 1 < V; ++i) key[i] = won ? key[i + 1] : key[i];
+            key[V - 1] = won ? K::none() : key[V - 1];
         }
-        ++n;
-        // order: larger logits, then lower experts, NaN last; 0: not there
-        uint64_t key[V];
+        on = on && !(mx == -__builtin_inff());
+        // exp(l - max): of all for the sum, of the chosen for the weights
+        float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane + 64 * i;
-            const uint32_t u = __builtin_bit_cast(uint32_t, l[i] + 0.0f);
-            const uint32_t k = l[i] != l[i] ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-            key[i] = e < a.experts ? (uint64_t)k << 32 | (uint32_t)~e : 0;
+            l[i] = __builtin_amdgcn_exp2f((l[i] - mx) * kLog2e);
+            total += l[i];
         }
-        const float total = exponentials<V>(l, mx);
+        total = reduce<L>(total, add);
+        const float chosen = sub < a.top_k ? __builtin_amdgcn_exp2f((K::value(mine) - mx) * kLog2e) : 0.0f;
+        const float below = a.renormalize ? reduce<L>(chosen, add) : total;
+        if (on) {
+            n += sub == 0;
+            const float inv = 1.0f / total;
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum[i] += l[i] / total;
-        int mine = 0;
-        float w = 0.0f, chosen = 0.0f;
-        for (int j = 0; j < a.top_k; ++j) {
-            uint64_t best = key[0];
-#pragma unroll
-            for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
-#pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) {
-                const uint64_t other = __shfl_xor((unsigned long long)best, off, 64);
-                best = other > best ? other : best;
-            }
-            const int e = (int)~(uint32_t)best;
-            float p = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (e == lane + 64 * i) {
-                    key[i] = 0;
-                    p = l[i];
-                }
-            }
-            p = __shfl(p, e & 63, 64);
-            chosen += p;
-            if (lane == j) {
-                mine = e;
-                w = p;
-            }
+            for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(l[i], inv, sum[i]);
         }
-        if (lane < a.top_k) {
-            a.ids[t * a.top_k + lane] = mine;
-            a.weights[t * a.top_k + lane] = w / (a.renormalize ? chosen : total);
-            atomicAdd(&count[mine], 1);
+        if (there && sub < a.top_k) {
+            const int e = on ? K::expert(mine) : -1;
+            a.ids[t * a.top_k + sub] = e;
+            a.weights[t * a.top_k + sub] = on ? chosen / below : 0.0f;
+            if (on) atomicAdd(&count[e], 1);
         }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) prob[wave][lane + 64 * i] = sum[i];
+    for (int i = 0; i < V; ++i) {
+        // the wave's tokens together, in a fixed order
+        if constexpr (L <= 16) {
+            const uint2 r = both16(__builtin_bit_cast(uint32_t, sum[i]));
+            sum[i] = __builtin_bit_cast(float, r.x) + __builtin_bit_cast(float, r.y);
+        }
+        if constexpr (L <= 32) {
+            const uint2 r = both32(__builtin_bit_cast(uint32_t, sum[i]));
+            sum[i] = __builtin_bit_cast(float, r.x) + __builtin_bit_cast(float, r.y);
+        }
+        if (lane < L) prob[wave][e0 + i] = sum[i];
+    }
+    n = (int)wave_sum((uint32_t)n);
     if (lane == 0) number[wave] = n;
     __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += 64 * kWaves) {
         float s = 0.0f;
+#pragma unroll
         for (int w = 0; w < kWaves; ++w) s += prob[w][e];
         a.part_p[(int64_t)blockIdx.x * a.experts + e] = s;
         a.part_c[(int64_t)blockIdx.x * a.experts + e] = count[e];
@@ -172,119 +325,167 @@ __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
     }
 }
 
-// The parts' sums, the balance loss.
-__global__ void __launch_bounds__(1024) k_route_finish(const float* part_p, const int32_t* part_c, const int32_t* part_n,
-                                                       int parts, int experts, int top_k, int32_t* counts, float* balance)
+// The parts' sums; the last of the workgroups (32 experts each) adds up the
+// balance loss, in their order.
+__global__ void __launch_bounds__(1024) k_route_finish(RouteKArgs a)
 {
     __shared__ double sh[1024];
-    __shared__ int32_t shc[1024];
-    __shared__ double loss;
+    __shared__ int32_t shc[1024], shn[1024];
+    __shared__ int last;
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    if (threadIdx.x == 0) loss = 0.0;
-    int64_t n = 0;
-    for (int i = 0; i < parts; ++i) n += part_n[i];
-    for (int e0 = 0; e0 < experts; e0 += 32) {
-        const int e = e0 + x;
-        double s = 0.0;
-        int32_t c = 0;
-        if (e < experts)
-            for (int i = y; i < parts; i += 32) {
-                s += part_p[(int64_t)i * experts + e];
-                c += part_c[(int64_t)i * experts + e];
-            }
-        sh[threadIdx.x] = s;
-        shc[threadIdx.x] = c;
-        __syncthreads();
-        for (int h = 16; h >= 1; h >>= 1) {
-            if (y < h) {
-                sh[threadIdx.x] += sh[threadIdx.x + 32 * h];
-                shc[threadIdx.x] += shc[threadIdx.x + 32 * h];
-            }
-            __syncthreads();
+    const int e = blockIdx.x * 32 + x;
+    double s = 0.0;
+    int32_t c = 0;
+    if (e < a.experts) {
+#pragma unroll 4
+        for (int i = y; i < a.parts; i += 32) {
+            s += a.part_p[(int64_t)i * a.experts + e];
+            c += a.part_c[(int64_t)i * a.experts + e];
         }
-        if (threadIdx.x == 0)
-            for (int i = 0; i < 32 && e0 + i < experts; ++i) loss += sh[i] * shc[i];
-        if (y == 0 && e < experts) counts[e] = shc[x];
+    }
+    sh[threadIdx.x] = s;
+    shc[threadIdx.x] = c;
+    shn[threadIdx.x] = (int)threadIdx.x < a.parts ? a.part_n[threadIdx.x] : 0;
+    static_assert(kParts <= 1024, "a part a thread");
+    __syncthreads();
+    for (int h = 512; h >= 32; h >>= 1) {
+        if ((int)threadIdx.x < h) {
+            sh[threadIdx.x] += sh[threadIdx.x + h];
+            shc[threadIdx.x] += shc[threadIdx.x + h];
+            shn[threadIdx.x] += shn[threadIdx.x + h];
+        }
         __syncthreads();
     }
-    if (threadIdx.x == 0) *balance = n ? (float)(loss * experts / ((double)n * n * top_k)) : 0.0f;
+    if (threadIdx.x == 0) {
+        double loss = 0.0;
+        int64_t n = 0;
+        for (int i = 0; i < 32; ++i) {
+            loss += sh[i] * shc[i];
+            n += shn[i];
+        }
+        const double nn = (double)n;
+        loss = n ? loss * a.experts / (nn * nn * a.top_k) : 0.0;
+        a.part_loss[blockIdx.x] = loss;
+        __threadfence();
+        last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+    }
+    if (y == 0 && e < a.experts) a.counts[e] = shc[x];
+    __syncthreads();
+    if (last && threadIdx.x == 0) {
+        __threadfence();
+        double loss = 0.0;
+        for (int i = 0; i < (int)gridDim.x; ++i) loss += __hip_atomic_load(a.part_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *a.balance = (float)loss;
+    }
 }
 
-template <typename T, int V>
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(64 * kWaves) k_route_backward(RouteKArgs a)
 {
+    constexpr int G = 64 / L;
+    // what the chosen experts get beside the rest, by expert
+    __shared__ __attribute__((aligned(16))) float extra[kWaves][G][L * V];
+    __shared__ int32_t pairs;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const float gb = a.grad_balance ? *a.grad_balance : 0.0f;
-    // the balance loss' gradient for each probability, times the tokens' 1 / N
+    const int sub = lane % L, e0 = V * sub;
+    float* own = extra[wave][lane / L];
+    if (threadIdx.x == 0) pairs = 0;
+    __syncthreads();
+    // the balance loss' gradient for each probability
     float share[V];
-    int64_t pairs = 0;
+    int c = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        const int32_t c = e < a.experts ? a.counts[e] : 0;
-        share[i] = (float)c;
-        pairs += c;
+        const int32_t k = e0 + i < a.experts ? a.counts[e0 + i] : 0;
+        share[i] = (float)k;
+        c += k;
     }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) pairs += __shfl_xor((long long)pairs, off, 64);
+    c = (int)wave_sum(lane < L ? (uint32_t)c : 0u);
+    if (threadIdx.x == 0) pairs = c;
+    __syncthreads();
     const double n = (double)pairs / a.top_k;
+    const float gb = a.grad_balance ? *a.grad_balance : 0.0f;
     const float to_share = n > 0.0 ? (float)(gb * (double)a.experts / (n * n * a.top_k)) : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) share[i] *= to_share;
-    for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.tokens; t += (int64_t)gridDim.x * kWaves) {
-        T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
-        const int32_t* ids = a.ids + t * a.top_k;
-        if (ids[0] < 0) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (lane + 64 * i < a.experts) put(out + lane + 64 * i, 0.0f);
-            continue;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * G; t0 < a.tokens; t0 += (int64_t)gridDim.x * kWaves * G) {
+        const int64_t t = t0 + lane / L;
+        const bool there = t < a.tokens;
+        int id = -1;
+        float w = 0.0f, g = 0.0f;
+        if (there && sub < a.top_k) {
+            id = a.ids[t * a.top_k + sub];
+            if (a.grad_weights && id >= 0) {
+                w = a.weights[t * a.top_k + sub];
+                g = a.grad_weights[t * a.top_k + sub];
+            }
         }
-        float p[V], mx;
-        load_row<T, V>(a, t, p, mx);
-        const float total = exponentials<V>(p, mx);
+        float p[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = -__builtin_inff();
+        if (there) load_row<V>(static_cast<const T*>(a.logits) + t * a.ld, e0, a.experts, p);
+        float mx = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            own[e0 + i] = 0.0f;
+            mx = fmaxf(mx, p[i]);
+        }
+        mx = reduce<L>(mx, [](float x, float y) { return fmaxf(x, y); });
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = __builtin_amdgcn_exp2f((p[i] - mx) * kLog2e);
+            total += p[i];
+        }
+        total = reduce<L>(total, add);
+        const float inv = 1.0f / total;
         float down = 0.0f;      // sum of p times its gradient
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] /= total;
+            p[i] *= inv;
             down = __builtin_fmaf(p[i], share[i], down);
         }
-        down = wave_fsum(down);
-        float inner = 0.0f, extra[V];
+        down = reduce<L>(down, add);
+        const float inner = reduce<L>(w * g, add);
+        if (!a.renormalize) down += inner;
+        // a wave's LDS operations are done in their order, if the compiler keeps it
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (id >= 0 && id < L * V) own[id] = a.renormalize ? w * (g - inner) : w * g;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const bool on = __shfl(id, lane / L * L, 64) >= 0;
+        float d[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) extra[i] = 0.0f;
-        if (a.grad_weights) {
-            for (int j = 0; j < a.top_k; ++j) {
-                const float w = a.weights[t * a.top_k + j], g = a.grad_weights[t * a.top_k + j];
-                inner = __builtin_fmaf(w, g, inner);
-            }
-            for (int j = 0; j < a.top_k; ++j) {
-                const float w = a.weights[t * a.top_k + j], g = a.grad_weights[t * a.top_k + j];
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (ids[j] == lane + 64 * i) extra[i] = a.renormalize ? w * (g - inner) : w * g;
-            }
-            if (!a.renormalize) down += inner;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane + 64 * i < a.experts) put(out + lane + 64 * i, __builtin_fmaf(p[i], share[i] - down, extra[i]));
+        for (int i = 0; i < V; ++i) d[i] = on ? __builtin_fmaf(p[i], share[i] - down, own[e0 + i]) : 0.0f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (there) store_row<V>(static_cast<T*>(a.dlogits) + t * a.ldd, e0, a.experts, d);
     }
 }
 
-int parts_of(int64_t tokens) { return (int)std::min<int64_t>((tokens + kWaves - 1) / kWaves, kParts); }
-
+// Lanes of a token and experts of a lane.
 template <typename F>
 void by_experts(int experts, int dtype, F f)
 {
     const auto with = [&](auto t) {
-        if (experts <= 64) f(t, std::integral_constant<int, 1>{});
-        else if (experts <= 128) f(t, std::integral_constant<int, 2>{});
-        else if (experts <= 256) f(t, std::integral_constant<int, 4>{});
-        else f(t, std::integral_constant<int, 8>{});
+        const auto go = [&](auto l, auto v) { f(t, l, v); };
+        using std::integral_constant;
+        if (experts <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+        else if (experts <= 32) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+        else if (experts <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+        else if (experts <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+        else if (experts <= 256) go(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+        else go(integral_constant<int, 64>{}, integral_constant<int, 8>{});
     };
     dtype == FP8_IN_BF16 ? with(uint16_t{}) : with(float{});
 }
+int tokens_of_wave(int64_t experts) { return experts <= 128 ? 4 : experts <= 256 ? 2 : 1; }
+
+// Workgroups of the forward, whose sums the second kernel adds up.
+int parts_of(int64_t tokens, int64_t experts)
+{
+    const int64_t per = kWaves * tokens_of_wave(experts);
+    return (int)std::min<int64_t>((tokens + per - 1) / per, kParts);
+}
+int blocks_of(int64_t experts) { return (int)((experts + 31) / 32); }
 
 RouteKArgs kernel_args(const RouteArgs& g)
 {
@@ -298,31 +499,44 @@ RouteKArgs kernel_args(const RouteArgs& g)
     a.mask = g.mask;
     a.ids = g.ids;
     a.weights = g.weights;
+    a.counts = g.counts;
     return a;
+}
+
+__global__ void __launch_bounds__(512) k_route_nothing(int32_t* counts, int experts, float* balance)
+{
+    if ((int)threadIdx.x < experts) counts[threadIdx.x] = 0;
+    if (threadIdx.x == 0) *balance = 0.0f;
 }
 
 }  // namespace
 
 size_t route_workspace(int64_t tokens, int64_t experts)
 {
-    return (size_t)parts_of(tokens) * (size_t)(2 * experts + 1) * 4;
+    return (size_t)blocks_of(experts) * 8 + 16 + (size_t)parts_of(tokens, experts) * (size_t)(2 * experts + 1) * 4;
 }
 
 hipError_t launch_route(const RouteArgs& g, hipStream_t stream)
 {
     RouteKArgs a = kernel_args(g);
-    const int parts = parts_of(g.tokens);
-    a.part_p = static_cast<float*>(g.ws);
-    a.part_c = reinterpret_cast<int32_t*>(a.part_p + (int64_t)parts * g.experts);
-    a.part_n = a.part_c + (int64_t)parts * g.experts;
-    if (parts)
-        by_experts(a.experts, g.dtype, [&](auto t, auto v) {
-            hipLaunchKernelGGL((k_route<decltype(t), decltype(v)::value>), dim3(parts), dim3(64 * kWaves), 0, stream, a);
-        });
+    a.balance = g.balance;
+    if (g.tokens == 0) {
+        hipLaunchKernelGGL(k_route_nothing, dim3(1), dim3(512), 0, stream, g.counts, a.experts, g.balance);
+        return hipGetLastError();
+    }
+    a.parts = parts_of(g.tokens, g.experts);
+    a.part_loss = static_cast<double*>(g.ws);
+    a.ticket = reinterpret_cast<int32_t*>(a.part_loss + blocks_of(g.experts));
+    a.part_p = reinterpret_cast<float*>(a.ticket + 4);
+    a.part_c = reinterpret_cast<int32_t*>(a.part_p + (int64_t)a.parts * g.experts);
+    a.part_n = a.part_c + (int64_t)a.parts * g.experts;
+    by_experts(a.experts, g.dtype, [&](auto t, auto l, auto v) {
+        hipLaunchKernelGGL((k_route<decltype(t), decltype(l)::value, decltype(v)::value>), dim3(a.parts), dim3(64 * kWaves), 0,
+                           stream, a);
+    });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_route_finish, dim3(1), dim3(1024), 0, stream, a.part_p, a.part_c, a.part_n, parts, a.experts, a.top_k,
-                       g.counts, g.balance);
+    hipLaunchKernelGGL(k_route_finish, dim3(blocks_of(g.experts)), dim3(1024), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -330,14 +544,15 @@ hipError_t launch_route_backward(const RouteArgs& g, hipStream_t stream)
 {
     if (g.tokens == 0) return hipSuccess;
     RouteKArgs a = kernel_args(g);
-    a.counts = g.counts;
     a.grad_weights = g.grad_weights;
     a.grad_balance = g.grad_balance;
     a.dlogits = g.dlogits;
     a.ldd = g.ldd;
-    const int grid = (int)std::min<int64_t>((g.tokens + kWaves - 1) / kWaves, 8 * gemm_num_cus());
-    by_experts(a.experts, g.dtype, [&](auto t, auto v) {
-        hipLaunchKernelGGL((k_route_backward<decltype(t), decltype(v)::value>), dim3(grid), dim3(64 * kWaves), 0, stream, a);
+    const int64_t per = kWaves * tokens_of_wave(g.experts);
+    const int grid = (int)std::min<int64_t>((g.tokens + per - 1) / per, 2 * gemm_num_cus());
+    by_experts(a.experts, g.dtype, [&](auto t, auto l, auto v) {
+        hipLaunchKernelGGL((k_route_backward<decltype(t), decltype(l)::value, decltype(v)::value>), dim3(grid),
+                           dim3(64 * kWaves), 0, stream, a);
     });
     return hipGetLastError();
 }
