@@ -284,7 +284,7 @@ def _ext():
         try:
             _ext_module = importlib.import_module("._fp8mi_torch", __name__)
         except ModuleNotFoundError:
-            warnings.warn("_fp8mi_torch.so is not there: short 4-bit calls take the host about 4 us more each "
+            warnings.warn("_fp8mi_torch.so is not there: short calls take the host about 4 us more each "
                           "(`python -m fp8_scaled_matmul_amd.build` builds it)", RuntimeWarning, stacklevel=3)
             _ext_module = _NoExt()
         except ImportError as e:
@@ -892,6 +892,9 @@ class MoeMx4:
 
 
 # ---------------------------------------------------------------- around the linear layers
+_FAR = 1e30         # caps of logits lie below
+
+
 def _workspace(workspace, need: int, device):
     """The caller's workspace if it is large enough, or a new one."""
     torch = _torch()
@@ -912,8 +915,8 @@ def _check_head(x, w, targets, softcap, workspace):
     if workspace is not None:
         _check_tensor(workspace, "workspace", (torch.uint8,), contiguous=True)
     softcap = float(softcap)
-    if not 0.0 <= softcap < float("inf"):
-        raise ValueError(f"softcap must be 0 (none) or positive, got {softcap}")
+    if not 0.0 <= softcap < _FAR:
+        raise ValueError(f"softcap must be 0 (none) or positive and below {_FAR:g}, got {softcap}")
     return x.shape[0], w.shape[0], x.shape[1], softcap
 
 
@@ -925,6 +928,12 @@ def linear_cross_entropy(x, w, targets, softcap: float = 0.0, workspace=None):
     the backward pass needs.  A negative target leaves its token out (loss 0);
     one past the vocabulary gives NaN.  workspace: optional uint8 device tensor of
     fp8_linear_ce_workspace_size(tokens, vocab, hidden, 0) bytes."""
+    if workspace is None and 0.0 <= softcap < _FAR:
+        r = _ext().linear_ce(x, w, targets, float(softcap))
+        if r is not None:
+            if type(r) is int:
+                check(r)
+            return r
     torch = _torch()
     tokens, vocab, hidden, softcap = _check_head(x, w, targets, softcap, workspace)
     _check_devices(x, w, targets, workspace)
@@ -945,6 +954,12 @@ def linear_cross_entropy_backward(x, w, targets, lse, grad_loss, softcap: float 
     vocabulary add nothing, whatever x and grad_loss hold there.  workspace:
     optional uint8 device tensor of fp8_linear_ce_workspace_size(tokens, vocab,
     hidden, 1) bytes."""
+    if out_x is None and out_w is None and workspace is None and 0.0 <= softcap < _FAR:
+        r = _ext().linear_ce_backward(x, w, targets, float(softcap), lse, grad_loss, bool(want_x), bool(want_w))
+        if r is not None:
+            if type(r) is int:
+                check(r)
+            return r
     torch = _torch()
     tokens, vocab, hidden, softcap = _check_head(x, w, targets, softcap, workspace)
     _check_tensor(lse, "lse", (torch.float32,), (tokens,), contiguous=True)
@@ -983,6 +998,12 @@ def moe_route(logits, top_k: int, renormalize: bool = True, mask=None, workspace
     runs over all experts).  mask: optional bool [tokens], False leaves a token
     out; so does a row of -inf alone.  workspace: optional uint8 device tensor of
     fp8_moe_route_workspace_size(tokens, experts) bytes."""
+    if workspace is None:
+        r = _ext().moe_route(logits, int(top_k), bool(renormalize), mask)
+        if r is not None:
+            if type(r) is int:
+                check(r)
+            return Route(*r, bool(renormalize))
     torch = _torch()
     _check_tensor(logits, "logits", (torch.bfloat16, torch.float32), unit_col_stride=True)
     tokens, experts = logits.shape
@@ -1010,6 +1031,13 @@ def moe_route(logits, top_k: int, renormalize: bool = True, mask=None, workspace
 def moe_route_backward(logits, route: Route, grad_weights=None, grad_balance=None, out=None):
     """The logits' gradient, in their type, from those of route.weights (fp32
     [tokens, top_k]) and route.balance (fp32, one element); None counts as 0."""
+    if out is None and isinstance(route, Route):
+        dl = _ext().moe_route_backward(logits, route.ids, route.weights, route.counts, route.renormalize, grad_weights,
+                                       grad_balance)
+        if dl is not None:
+            if type(dl) is int:
+                check(dl)
+            return dl
     torch = _torch()
     _check_tensor(logits, "logits", (torch.bfloat16, torch.float32), unit_col_stride=True)
     tokens, experts = logits.shape
@@ -1043,10 +1071,16 @@ def dropout(x, rate: float, seed, residual=None, out=None):
     to residual where given.  seed: an int64 device tensor of one element (a
     captured graph reads it anew at each replay); the backward pass is
     dropout(dy, rate, seed).  out may be x or residual."""
+    rate = float(rate)
+    if out is None:
+        y = _ext().dropout(x, rate, seed, residual)
+        if y is not None:
+            if type(y) is int:
+                check(y)
+            return y
     torch = _torch()
     _check_tensor(x, "x", (torch.bfloat16, torch.float32), unit_col_stride=True)
     rows, cols = x.shape
-    rate = float(rate)
     if not 0.0 <= rate <= 1.0:
         raise ValueError(f"rate must be from 0 to 1, got {rate}")
     _check_tensor(seed, "seed", (torch.int64,), (1,))

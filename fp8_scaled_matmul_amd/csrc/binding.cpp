@@ -1,4 +1,4 @@
-// Python entry to the 4-bit operators for the calls that are all in order:
+// Python entry to the 4-bit and the training operators for the calls that are all in order:
 // plain torch tensors on the current device, outputs to be allocated.  It
 // checks, allocates, fetches the current stream and calls the C ABI in one
 // step, which takes the host 6 us where the same through ctypes takes 10
@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "fp8mi.h"
 
@@ -256,12 +257,225 @@ PyObject* mx4_moe(PyObject*, PyObject* const* args, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// A vector of `n` adjacent elements here, or nothing.
+bool vector(PyObject* o, at::ScalarType dtype, int64_t n, const at::Tensor*& t)
+{
+    t = plain(o);
+    return t && t->scalar_type() == dtype && t->dim() == 1 && t->size(0) == n && (n <= 1 || t->stride(0) == 1) && here(*t);
+}
+bool contiguous(PyObject* o, at::ScalarType dtype, int64_t rows, int64_t cols, const at::Tensor*& t)
+{
+    t = plain(o);
+    return t && t->scalar_type() == dtype && t->dim() == 2 && t->size(0) == rows && t->size(1) == cols && t->is_contiguous() &&
+           here(*t);
+}
+bool number(PyObject* o, double& v)
+{
+    if (!PyFloat_CheckExact(o)) return false;
+    v = PyFloat_AS_DOUBLE(o);
+    return true;
+}
+bool values(const at::Tensor& t) { return t.scalar_type() == at::kBFloat16 || t.scalar_type() == at::kFloat; }
+fp8_dtype code(const at::Tensor& t) { return t.scalar_type() == at::kBFloat16 ? FP8_IN_BF16 : FP8_IN_FP32; }
+
+PyObject* tuple(std::initializer_list<at::Tensor*> of)
+{
+    PyObject* out = PyTuple_New((Py_ssize_t)of.size());
+    if (!out) return nullptr;
+    Py_ssize_t i = 0;
+    for (at::Tensor* t : of) {
+        if (t->defined()) {
+            PyTuple_SET_ITEM(out, i++, THPVariable_Wrap(std::move(*t)));
+        } else {
+            Py_INCREF(Py_None);
+            PyTuple_SET_ITEM(out, i++, Py_None);
+        }
+    }
+    return out;
+}
+
+// (x, rate, seed, residual): y
+PyObject* dropout(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    const at::Tensor* x = n == 4 ? plain(args[0]) : nullptr;
+    const at::Tensor *seed = nullptr, *residual = nullptr;
+    int64_t ld, ldr = 0;
+    double rate;
+    if (!x || !matrix(*x, ld) || !here(*x) || !values(*x) || !number(args[1], rate) || !vector(args[2], at::kLong, 1, seed))
+        Py_RETURN_NONE;
+    if (args[3] != Py_None) {
+        residual = plain(args[3]);
+        if (!residual || !matrix(*residual, ldr) || !here(*residual) || residual->scalar_type() != x->scalar_type() ||
+            residual->sizes() != x->sizes())
+            Py_RETURN_NONE;
+    }
+    const int64_t rows = x->size(0), cols = x->size(1);
+    at::AutoDispatchBelowADInplaceOrView guard;
+    at::Tensor y;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        y = fresh({rows, cols}, {cols, 1}, x->scalar_type(), *x);
+        st = fp8_dropout(x->data_ptr(), code(*x), rows, cols, ld, residual ? residual->data_ptr() : nullptr, ldr, rate,
+                         data<const uint64_t>(*seed), y.data_ptr(), cols, stream());
+    }
+    if (st != FP8_OK) return PyLong_FromLong(st);
+    return THPVariable_Wrap(std::move(y));
+    END_HANDLE_TH_ERRORS
+}
+
+// (logits, top_k, renormalize, mask): (ids, weights, counts, balance)
+PyObject* moe_route(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    const at::Tensor* l = n == 4 ? plain(args[0]) : nullptr;
+    const at::Tensor* mask = nullptr;
+    int64_t ld, k;
+    if (!l || !matrix(*l, ld) || !here(*l) || !values(*l)) Py_RETURN_NONE;
+    if (!ints(args + 1, 1, &k)) return nullptr;
+    const int64_t tokens = l->size(0), experts = l->size(1);
+    if (k < 1 || k > experts || (args[3] != Py_None && !vector(args[3], at::kBool, tokens, mask))) Py_RETURN_NONE;
+    at::AutoDispatchBelowADInplaceOrView guard;
+    at::Tensor ids, weights, counts, balance, ws;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        ids = fresh({tokens, k}, {k, 1}, at::kInt, *l);
+        weights = fresh({tokens, k}, {k, 1}, at::kFloat, *l);
+        counts = fresh({experts}, {1}, at::kInt, *l);
+        balance = fresh({}, {}, at::kFloat, *l);
+        const int64_t need = std::max<int64_t>((int64_t)fp8_moe_route_workspace_size(tokens, experts), 1);
+        ws = fresh({need}, {1}, at::kByte, *l);
+        st = fp8_moe_route(l->data_ptr(), code(*l), tokens, experts, ld, k, args[2] == Py_True,
+                           mask ? data<const uint8_t>(*mask) : nullptr, data<int32_t>(ids), data<float>(weights),
+                           data<int32_t>(counts), data<float>(balance), ws.data_ptr(), (size_t)need, stream());
+    }
+    if (st != FP8_OK) return PyLong_FromLong(st);
+    return tuple({&ids, &weights, &counts, &balance});
+    END_HANDLE_TH_ERRORS
+}
+
+// (logits, ids, weights, counts, renormalize, gradient of the weights, of the balance): dlogits
+PyObject* moe_route_backward(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    const at::Tensor* l = n == 7 ? plain(args[0]) : nullptr;
+    const at::Tensor* i = l ? plain(args[1]) : nullptr;
+    const at::Tensor *ids, *weights, *counts, *gw = nullptr, *gb = nullptr;
+    int64_t ld;
+    if (!i || !matrix(*l, ld) || !here(*l) || !values(*l) || i->dim() != 2) Py_RETURN_NONE;
+    const int64_t tokens = l->size(0), experts = l->size(1), k = i->size(1);
+    if (!contiguous(args[1], at::kInt, tokens, k, ids) || !contiguous(args[2], at::kFloat, tokens, k, weights) ||
+        !vector(args[3], at::kInt, experts, counts) ||
+        (args[5] != Py_None && !contiguous(args[5], at::kFloat, tokens, k, gw)))
+        Py_RETURN_NONE;
+    if (args[6] != Py_None) {
+        gb = plain(args[6]);
+        if (!gb || gb->scalar_type() != at::kFloat || gb->numel() != 1 || !here(*gb)) Py_RETURN_NONE;
+    }
+    at::AutoDispatchBelowADInplaceOrView guard;
+    at::Tensor dl;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        dl = fresh({tokens, experts}, {experts, 1}, l->scalar_type(), *l);
+        st = fp8_moe_route_backward(l->data_ptr(), code(*l), tokens, experts, ld, k, args[4] == Py_True,
+                                    data<const int32_t>(*ids), data<const float>(*weights), data<const int32_t>(*counts),
+                                    gw ? data<const float>(*gw) : nullptr, gb ? data<const float>(*gb) : nullptr,
+                                    dl.data_ptr(), experts, stream());
+    }
+    if (st != FP8_OK) return PyLong_FromLong(st);
+    return THPVariable_Wrap(std::move(dl));
+    END_HANDLE_TH_ERRORS
+}
+
+// x [tokens, hidden], w [vocab, hidden], targets [tokens], softcap.
+struct Head {
+    const at::Tensor *x, *w, *targets;
+    int64_t ldx, ldw, tokens, vocab, hidden;
+    double softcap;
+};
+bool head(PyObject* const* args, Head& h)
+{
+    h.x = plain(args[0]);
+    h.w = h.x ? plain(args[1]) : nullptr;
+    if (!h.w || !matrix(*h.x, h.ldx) || !matrix(*h.w, h.ldw) || !here(*h.x) || !here(*h.w) ||
+        h.x->scalar_type() != at::kBFloat16 || h.w->scalar_type() != at::kBFloat16 || h.x->size(1) != h.w->size(1))
+        return false;
+    h.tokens = h.x->size(0);
+    h.vocab = h.w->size(0);
+    h.hidden = h.x->size(1);
+    return vector(args[2], at::kLong, h.tokens, h.targets) && number(args[3], h.softcap);
+}
+
+// (x, w, targets, softcap): (loss, lse)
+PyObject* linear_ce(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Head h;
+    if (n != 4 || !head(args, h)) Py_RETURN_NONE;
+    at::AutoDispatchBelowADInplaceOrView guard;
+    at::Tensor loss, lse, ws;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        loss = fresh({h.tokens}, {1}, at::kFloat, *h.x);
+        lse = fresh({h.tokens}, {1}, at::kFloat, *h.x);
+        const int64_t need = std::max<int64_t>((int64_t)fp8_linear_ce_workspace_size(h.tokens, h.vocab, h.hidden, 0), 1);
+        ws = fresh({need}, {1}, at::kByte, *h.x);
+        st = fp8_linear_ce(h.x->data_ptr(), h.ldx, h.w->data_ptr(), h.ldw, h.tokens, h.vocab, h.hidden,
+                           data<const int64_t>(*h.targets), (float)h.softcap, data<float>(loss), data<float>(lse),
+                           ws.data_ptr(), (size_t)need, stream());
+    }
+    if (st != FP8_OK) return PyLong_FromLong(st);
+    return tuple({&loss, &lse});
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, w, targets, softcap, lse, gradient of the losses, want dx, want dw): (dx, dw)
+PyObject* linear_ce_backward(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    Head h;
+    const at::Tensor *lse, *grad;
+    if (n != 8 || !head(args, h) || !vector(args[4], at::kFloat, h.tokens, lse)) Py_RETURN_NONE;
+    grad = plain(args[5]);
+    if (!grad || grad->scalar_type() != at::kFloat || grad->dim() != 1 || grad->size(0) != h.tokens || !here(*grad))
+        Py_RETURN_NONE;
+    at::AutoDispatchBelowADInplaceOrView guard;
+    at::Tensor dx, dw, ws;
+    fp8_status st;
+    {
+        Unlocked unlocked;
+        if (args[6] == Py_True) dx = fresh({h.tokens, h.hidden}, {h.hidden, 1}, at::kBFloat16, *h.x);
+        if (args[7] == Py_True) dw = fresh({h.vocab, h.hidden}, {h.hidden, 1}, at::kBFloat16, *h.x);
+        const int64_t need = std::max<int64_t>((int64_t)fp8_linear_ce_workspace_size(h.tokens, h.vocab, h.hidden, 1), 1);
+        ws = fresh({need}, {1}, at::kByte, *h.x);
+        st = fp8_linear_ce_backward(h.x->data_ptr(), h.ldx, h.w->data_ptr(), h.ldw, h.tokens, h.vocab, h.hidden,
+                                    data<const int64_t>(*h.targets), (float)h.softcap, data<const float>(*lse),
+                                    data<const float>(*grad), h.tokens > 1 ? grad->stride(0) : 0,
+                                    dx.defined() ? dx.data_ptr() : nullptr, h.hidden, dw.defined() ? dw.data_ptr() : nullptr,
+                                    h.hidden, ws.data_ptr(), (size_t)need, stream());
+    }
+    if (st != FP8_OK) return PyLong_FromLong(st);
+    return tuple({&dx, &dw});
+    END_HANDLE_TH_ERRORS
+}
+
+#define FP8MI_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
+
 PyMethodDef methods[] = {
     {"mx4_held", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(mx4_held)), METH_FASTCALL, nullptr},
     {"mx4_quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(mx4_quantize)), METH_FASTCALL, nullptr},
     {"mx4_dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(mx4_dequantize)), METH_FASTCALL, nullptr},
     {"mx4_mm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(mx4_mm)), METH_FASTCALL, nullptr},
     {"mx4_moe", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(mx4_moe)), METH_FASTCALL, nullptr},
+    FP8MI_METHOD(dropout),
+    FP8MI_METHOD(moe_route),
+    FP8MI_METHOD(moe_route_backward),
+    FP8MI_METHOD(linear_ce),
+    FP8MI_METHOD(linear_ce_backward),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fp8mi_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

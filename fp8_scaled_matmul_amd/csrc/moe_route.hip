@@ -139,6 +139,14 @@ struct Key32 {
     static __device__ T smallest(T a, T b) { return __builtin_fmin(a, b); }
 };
 
+// a where the mask's bits are set, b elsewhere.
+__device__ inline uint32_t choose(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
+__device__ inline double choose(uint32_t mask, double a, double b)
+{
+    const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
+    return __builtin_bit_cast(double, uint2{choose(mask, x.x, y.x), choose(mask, x.y, y.y)});
+}
+
 // A lane's V keys in falling order.
 template <typename K, int V>
 __device__ inline void sort_keys(typename K::T (&k)[V])
@@ -266,10 +274,12 @@ __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
             const typename K::T best = reduce<L>(key[0], K::largest);
             if (j == 0) mx = K::value(best);
             if (sub == j) mine = best;
-            const bool won = key[0] == best;
+            // the winner's list moves up; by a mask that the compiler does not see
+            // through, else it makes the moves an indexed access
+            uint32_t won = key[0] == best ? ~0u : 0u;
+            asm("" : "+v"(won));
 #pragma unroll
-            for (int i = 0; i + 1 < V; ++i) key[i] = won ? key[i + 1] : key[i];
-            key[V - 1] = won ? K::none() : key[V - 1];
+            for (int i = 0; i < V; ++i) key[i] = choose(won, i + 1 < V ? key[(i + 1) % V] : K::none(), key[i]);
         }
         on = on && !(mx == -__builtin_inff());
         // exp(l - max): of all for the sum, of the chosen for the weights
@@ -284,7 +294,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
         const float below = a.renormalize ? reduce<L>(chosen, add) : total;
         if (on) {
             n += sub == 0;
-            const float inv = 1.0f / total;
+            const float inv = __builtin_amdgcn_rcpf(total);     // off by one step at most
 #pragma unroll
             for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(l[i], inv, sum[i]);
         }
@@ -356,13 +366,16 @@ __global__ void __launch_bounds__(1024) k_route_finish(RouteKArgs a)
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
-        double loss = 0.0;
-        int64_t n = 0;
-        for (int i = 0; i < 32; ++i) {
-            loss += sh[i] * shc[i];
-            n += shn[i];
+    // the first wave's lower half: in the order of the exchanges
+    double loss = threadIdx.x < 32 ? sh[threadIdx.x] * shc[threadIdx.x] : 0.0;
+    int n = threadIdx.x < 32 ? shn[threadIdx.x] : 0;
+    if (threadIdx.x < 64) {
+        for (int off = 16; off >= 1; off >>= 1) {
+            loss += __shfl_xor(loss, off, 64);
+            n += __shfl_xor(n, off, 64);
         }
+    }
+    if (threadIdx.x == 0) {
         const double nn = (double)n;
         loss = n ? loss * a.experts / (nn * nn * a.top_k) : 0.0;
         a.part_loss[blockIdx.x] = loss;
@@ -383,7 +396,10 @@ template <typename T, int L, int V>
 __global__ void __launch_bounds__(64 * kWaves) k_route_backward(RouteKArgs a)
 {
     constexpr int G = 64 / L;
-    // what the chosen experts get beside the rest, by expert
+    // what the chosen experts get beside the rest; a lane's V floats in runs of 4,
+    // so that its 16 bytes lie beside its neighbours'
+    constexpr int R = V < 4 ? V : 4;
+    const auto place = [](int e) { return (e % V) / R * (L * R) + e / V * R + e % R; };
     __shared__ __attribute__((aligned(16))) float extra[kWaves][G][L * V];
     __shared__ int32_t pairs;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -411,23 +427,26 @@ __global__ void __launch_bounds__(64 * kWaves) k_route_backward(RouteKArgs a)
     for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * G; t0 < a.tokens; t0 += (int64_t)gridDim.x * kWaves * G) {
         const int64_t t = t0 + lane / L;
         const bool there = t < a.tokens;
-        int id = -1;
-        float w = 0.0f, g = 0.0f;
-        if (there && sub < a.top_k) {
-            id = a.ids[t * a.top_k + sub];
-            if (a.grad_weights && id >= 0) {
-                w = a.weights[t * a.top_k + sub];
-                g = a.grad_weights[t * a.top_k + sub];
-            }
-        }
         float p[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] = -__builtin_inff();
         if (there) load_row<V>(static_cast<const T*>(a.logits) + t * a.ld, e0, a.experts, p);
+        int id = -1;
+        float w = 0.0f, g = 0.0f;
+        if (there && sub < a.top_k) {
+            id = a.ids[t * a.top_k + sub];
+            if (a.grad_weights) {
+                w = a.weights[t * a.top_k + sub];
+                g = a.grad_weights[t * a.top_k + sub];
+            }
+        }
+        // of a token that is left out the gradient may hold anything
+        w = id >= 0 ? w : 0.0f;
+        g = id >= 0 ? g : 0.0f;
         float mx = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            own[e0 + i] = 0.0f;
+            own[place(e0 + i)] = 0.0f;
             mx = fmaxf(mx, p[i]);
         }
         mx = reduce<L>(mx, [](float x, float y) { return fmaxf(x, y); });
@@ -438,7 +457,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_route_backward(RouteKArgs a)
             total += p[i];
         }
         total = reduce<L>(total, add);
-        const float inv = 1.0f / total;
+        const float inv = __builtin_amdgcn_rcpf(total);
         float down = 0.0f;      // sum of p times its gradient
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -450,12 +469,12 @@ __global__ void __launch_bounds__(64 * kWaves) k_route_backward(RouteKArgs a)
         if (!a.renormalize) down += inner;
         // a wave's LDS operations are done in their order, if the compiler keeps it
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (id >= 0 && id < L * V) own[id] = a.renormalize ? w * (g - inner) : w * g;
+        if (id >= 0 && id < L * V) own[place(id)] = a.renormalize ? w * (g - inner) : w * g;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         const bool on = __shfl(id, lane / L * L, 64) >= 0;
         float d[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = on ? __builtin_fmaf(p[i], share[i] - down, own[e0 + i]) : 0.0f;
+        for (int i = 0; i < V; ++i) d[i] = on ? __builtin_fmaf(p[i], share[i] - down, own[place(e0 + i)]) : 0.0f;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (there) store_row<V>(static_cast<T*>(a.dlogits) + t * a.ldd, e0, a.experts, d);
     }

@@ -109,7 +109,9 @@ def test_rows_that_leave_nothing(renormalize):
     gw[5] = 0
     ref = fm.moe_route(l[on].cuda(), 3, renormalize)
     assert torch.equal(r.ids[on], ref.ids) and torch.equal(r.weights[on], ref.weights) and torch.equal(r.counts, ref.counts)
-    assert torch.equal(r.balance, ref.balance)
+    # the mean of 4 tokens' probabilities, added up in another order: 4 fp32
+    # additions of numbers that are positive, a rounding of the result
+    assert abs(r.balance.item() - ref.balance.item()) <= 2 * 5 * 2.0 ** -24 * ref.balance.item()
     assert torch.equal(dl[on], fm.moe_route_backward(l[on].cuda(), ref, gw[on].cuda(), torch.ones((), device="cuda")))
     assert (dl[[0, 5]] == 0).all()
     none = fm.moe_route(l2.cuda(), 3, renormalize, mask=torch.zeros(6, dtype=torch.bool, device="cuda"))
