@@ -345,7 +345,7 @@ hipError_t launch_tile(GemmShape s, Init init, hipStream_t stream)
     const hipError_t e = limit.raise(reinterpret_cast<const void*>(kernel), kLds);
     if (e != hipSuccess) return e;
     const int64_t items = (int64_t)s.tiles_m * s.tiles_n * s.splits;
-    const int per_cu = 2 * kLds <= 160 * 1024 ? 2 : 1;
+    const int per_cu = std::min(160 * 1024 / kLds, 3);
     const int grid = (int)std::min<int64_t>(items, (int64_t)gemm_num_cus() * per_cu);
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * WR * WC), kLds, stream, s, epi);
     return hipGetLastError();
@@ -358,13 +358,15 @@ template <bool ATR, template <int, int, int> class Epi, typename Init>
 hipError_t launch_tokens(const GemmShape& s, Init init, hipStream_t stream)
 {
     switch (token_tile(s.n)) {
-    case 32: return launch_tile<ATR, false, 4, 1, 4, 2, Epi>(s, init, stream);
-    case 64: return launch_tile<ATR, false, 4, 1, 4, 4, Epi>(s, init, stream);
+    case 32: return launch_tile<ATR, false, 4, 1, 2, 2, Epi>(s, init, stream);
+    case 64: return launch_tile<ATR, false, 4, 1, 2, 4, Epi>(s, init, stream);
     case 128: return launch_tile<ATR, false, 4, 2, 4, 4, Epi>(s, init, stream);
     default: return launch_tile<ATR, false, 2, 4, 8, 4, Epi>(s, init, stream);
     }
 }
-int stat_rows(int64_t tokens) { return token_tile(tokens) <= 128 ? 64 : 128; }    // vocabulary rows of a block of statistics
+// Rows of its tile, and the vocabulary rows of a block of statistics (a wave's).
+int row_tile(int64_t tokens) { return token_tile(tokens) <= 64 ? 128 : 256; }
+int stat_rows(int64_t tokens) { return token_tile(tokens) <= 64 ? 32 : token_tile(tokens) <= 128 ? 64 : 128; }
 
 // ------------------------------------------------------------------ around the products
 // Rows of bf16 at 16-byte places with zeros behind them.  For tokens of a
@@ -454,21 +456,44 @@ __global__ void __launch_bounds__(256) k_ce_loss(const float2* part, int blocks,
     }
 }
 
-// The planes' sum, in their order, to bf16.
+// The planes' sum to bf16: S threads share a chunk of 8 columns, each adds up
+// every S-th plane, and their sums are added in order.
+template <int S>
 __global__ void __launch_bounds__(256) k_ce_reduce(const float* plane, int splits, int64_t rows, int cols, int64_t ld_plane,
                                                    uint16_t* out, int64_t ld, int wide)
 {
+    __shared__ v4f sh[S > 1 ? 512 : 1];
+    constexpr int C = 256 / S;          // chunks of a workgroup
+    const int x = threadIdx.x % C, y = threadIdx.x / C;
     const int chunks = (int)(ld_plane / 8);
     const int64_t total = rows * chunks;
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+    for (int64_t u0 = (int64_t)blockIdx.x * C; u0 < total; u0 += (int64_t)gridDim.x * C) {
+        const int64_t u = u0 + x;
         const int64_t r = u / chunks;
         const int c = (int)(u - r * chunks) * 8;
-        const float* from = plane + r * ld_plane + c;
         v4f a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-        for (int s = 0; s < splits; ++s, from += rows * ld_plane) {
-            a += *reinterpret_cast<const v4f*>(from);
-            b += *reinterpret_cast<const v4f*>(from + 4);
+        if (u < total) {
+            const float* from = plane + r * ld_plane + c;
+#pragma unroll 4
+            for (int s = y; s < splits; s += S) {
+                a += *reinterpret_cast<const v4f*>(from + s * rows * ld_plane);
+                b += *reinterpret_cast<const v4f*>(from + s * rows * ld_plane + 4);
+            }
         }
+        if constexpr (S > 1) {
+            sh[threadIdx.x] = a;
+            sh[256 + threadIdx.x] = b;
+            __syncthreads();
+            if (y == 0) {
+#pragma unroll
+                for (int s = 1; s < S; ++s) {
+                    a += sh[s * C + x];
+                    b += sh[256 + s * C + x];
+                }
+            }
+            __syncthreads();
+        }
+        if (y != 0 || u >= total) continue;
         uint16_t* to = out + r * ld + c;
         if (wide && c + 8 <= cols) {
             *reinterpret_cast<v4u*>(to) = v4u{gemm::pack_bf16(a[0], a[1]), gemm::pack_bf16(a[2], a[3]),
@@ -543,7 +568,7 @@ Layout backward_layout(int64_t tokens, int64_t vocab, int64_t hidden)
     pieces_of(l, vocab, std::max<int64_t>(kPieceBytes / (2 * tokens), 4096));
     // too few tiles of dx for the chip: its K, the vocabulary, is split
     const int tile = token_tile(tokens);
-    const int64_t tiles = (int64_t)tiles_of(hidden, 256) * tiles_of(tokens, tile);
+    const int64_t tiles = (int64_t)tiles_of(hidden, row_tile(tokens)) * tiles_of(tokens, tile);
     const int64_t want = (int64_t)gemm_num_cus() * (tile <= 64 ? 2 : 1);
     l.splits = std::max<int64_t>(std::min<int64_t>(want / tiles, std::min(l.piece, vocab) / 512), 1);
     size_t at = 0;
@@ -585,8 +610,6 @@ hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
         s.n = (int)n;
         s.k = (int)g.hidden;
         s.splits = 1;
-        // the statistics' blocks of a piece: those of whole tiles of 256 rows
-        const int per_tile = 256 / stat_rows(n);
         int blocks = 0;
         for (int64_t p = 0; p < (pack_w ? l.pieces : 1); ++p) {
             const int64_t v0 = p * l.piece, m = pack_w ? std::min(l.piece, g.vocab - v0) : g.vocab;
@@ -609,7 +632,7 @@ hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
                 epi.zt = reinterpret_cast<float*>(ws + l.zt);
             }, stream);
             if (e != hipSuccess) return e;
-            blocks += tiles_of(m, 256) * per_tile;
+            blocks += tiles_of(m, row_tile(n)) * (row_tile(n) / stat_rows(n));      // of whole tiles
         }
         const auto finish = [&](auto kernel, int tx) {
             hipLaunchKernelGGL(kernel, dim3((unsigned)((n + tx - 1) / tx)), dim3(256), 0, stream,
@@ -693,8 +716,13 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
             if (last && !direct) {
                 const int64_t ld = up(g.hidden, 16);
                 // a short last piece may have had fewer splits; the first has written all planes
-                hipLaunchKernelGGL(k_ce_reduce, dim3(grid_of(g.tokens * ld / 8)), dim3(256), 0, stream, planes, (int)l.splits,
-                                   g.tokens, H, ld, static_cast<uint16_t*>(g.dx), g.lddx, (int)aligned16(g.dx, g.lddx));
+                const auto reduce = [&](auto kernel, int share) {
+                    const int64_t groups = (g.tokens * ld / 8 + 256 / share - 1) / (256 / share);
+                    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(groups, 8 * gemm_num_cus())), dim3(256), 0, stream,
+                                       planes, (int)l.splits, g.tokens, H, ld, static_cast<uint16_t*>(g.dx), g.lddx,
+                                       (int)aligned16(g.dx, g.lddx));
+                };
+                l.splits >= 8 ? reduce(k_ce_reduce<16>, 16) : reduce(k_ce_reduce<1>, 1);
                 if ((e = hipGetLastError()) != hipSuccess) return e;
             }
         }
