@@ -3,8 +3,10 @@
 // row, column pair) alone, so the backward pass draws the forward's mask anew
 // and nothing is stored.
 //   y = (r >= cut ? x 65536 / (65536 - cut) : 0) + residual
-// Bound by memory: 2 reads and a write of 16 bytes a lane (bf16), about 12
-// VALU operations an element.
+// Bound by memory; about 13 VALU operations an element, two 32-bit products among
+// them.  16384 x 2048 bf16: 26 us (5.1 TB/s), onto a residual 37.5 us (5.3);
+// 8191 x 5000 fp32: 54 us (6.0).  Two or four pieces of a wave read before the
+// first is written: 30 to 65 us for the first of these.
 #include <algorithm>
 
 #include "device_common.h"
@@ -29,85 +31,91 @@ struct DropArgs {
     const uint64_t* seed;
     void* y;
     int64_t ldy;
-    int lanes_log2;             // lanes of a row: 8 columns each
-    int64_t chunks;             // of 8 << lanes_log2 columns
+    int lanes_log2;             // lanes of a row: 16 bytes each
+    int64_t chunks;             // of 16 << lanes_log2 bytes
     int64_t units;              // of 64 lanes
 };
 
-// 8 elements at any alignment of theirs.
-struct __attribute__((packed, aligned(2))) Bf16x8 {
-    uint32_t w[4];
-};
-struct __attribute__((packed, aligned(4))) F32x8 {
-    float v[8];
-};
-
-__device__ inline void load8(const uint16_t* from, float v[8])
+// A lane's 16 bytes as words, at any alignment of its elements.
+template <typename T>
+using Lane = uint32_t __attribute__((ext_vector_type(4), aligned(sizeof(T))));
+template <typename T, bool FAR>
+__device__ inline Lane<T> load16(const T* from)
 {
-    const Bf16x8 b = *reinterpret_cast<const Bf16x8*>(from);
+    const Lane<T>* p = reinterpret_cast<const Lane<T>*>(from);
+    return FAR ? __builtin_nontemporal_load(p) : *p;
+}
+template <typename T, bool FAR>
+__device__ inline void store16(T* to, Lane<T> v)
+{
+    Lane<T>* p = reinterpret_cast<Lane<T>*>(to);
+    if (FAR)
+        __builtin_nontemporal_store(v, p);
+    else
+        *p = v;
+}
+__device__ inline void unpack(const gemm::v4u& w, float (&v)[8])
+{
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(b.w[i]);
-        v[2 * i + 1] = bf16_hi(b.w[i]);
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
     }
 }
-__device__ inline void load8(const float* from, float v[8])
+__device__ inline void unpack(const gemm::v4u& w, float (&v)[4])
 {
-    const F32x8 b = *reinterpret_cast<const F32x8*>(from);
+    // (Cast as a whole: the compiler takes element 0 four times for four casts.)
+    const gemm::v4f f = __builtin_bit_cast(gemm::v4f, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = b.v[i];
+    for (int i = 0; i < 4; ++i) v[i] = f[i];
 }
-__device__ inline void store8(uint16_t* to, const float v[8])
+__device__ inline gemm::v4u pack(const float (&v)[8])
 {
-    Bf16x8 b;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b.w[i] = gemm::pack_bf16(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<Bf16x8*>(to) = b;
+    return {gemm::pack_bf16(v[0], v[1]), gemm::pack_bf16(v[2], v[3]), gemm::pack_bf16(v[4], v[5]), gemm::pack_bf16(v[6], v[7])};
 }
-__device__ inline void store8(float* to, const float v[8])
+__device__ inline gemm::v4u pack(const float (&v)[4])
 {
-    F32x8 b;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b.v[i] = v[i];
-    *reinterpret_cast<F32x8*>(to) = b;
+    return __builtin_bit_cast(gemm::v4u, gemm::v4f{v[0], v[1], v[2], v[3]});
 }
 __device__ inline float load1(const uint16_t* from) { return __builtin_bit_cast(float, (uint32_t)*from << 16); }
 __device__ inline float load1(const float* from) { return *from; }
 __device__ inline void store1(uint16_t* to, float v) { *to = gemm::to_bf16(v); }
 __device__ inline void store1(float* to, float v) { *to = v; }
 
-template <typename T, bool RES>
+template <typename T, bool RES, bool FAR>
 __global__ void __launch_bounds__(256) k_dropout(DropArgs p)
 {
+    constexpr int E = 16 / sizeof(T);
     const int lane = threadIdx.x & 63;
     const uint64_t seed = *p.seed;
     const uint32_t hi = (uint32_t)(seed >> 32) ^ kStream;
-    const int per_row = 1 << p.lanes_log2, sub = lane & (per_row - 1);
-    const int64_t step = (int64_t)gridDim.x * 4;
-    for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < p.units; u += step) {
+    const int sub = lane & ((1 << p.lanes_log2) - 1);
+    const int64_t waves = (int64_t)gridDim.x * 4;
+    for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < p.units; u += waves) {
         const int64_t block = u / p.chunks;
         const int64_t row = (block << (6 - p.lanes_log2)) + (lane >> p.lanes_log2);
-        const int64_t col = ((u - block * p.chunks) << (3 + p.lanes_log2)) + 8 * sub;
+        const int64_t col = ((u - block * p.chunks) << p.lanes_log2) * E + E * sub;
         if (row >= p.rows || col >= p.cols) continue;
         const T* x = static_cast<const T*>(p.x) + row * p.ld + col;
         const T* res = static_cast<const T*>(p.residual) + row * p.ldr + col;
         T* y = static_cast<T*>(p.y) + row * p.ldy + col;
-        const int n = (int)min(p.cols - col, (int64_t)8);
-        float v[8], r[8];
-        if (n == 8) {
-            load8(x, v);
-            if (RES) load8(res, r);
+        const int n = (int)min(p.cols - col, (int64_t)E);
+        float v[E], r[E];
+        if (n == E) {
+            unpack(load16<T, FAR>(x), v);
+            if (RES) unpack(load16<T, FAR>(res), r);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < E; ++i) {
                 v[i] = i < n ? load1(x + i) : 0.0f;
                 if (RES) r[i] = i < n ? load1(res + i) : 0.0f;
             }
         }
         const uint32_t rk = mx4::row_key((uint32_t)row, (uint32_t)seed);
+        const uint32_t pk = mx4::pair_key((uint32_t)(col >> 1), hi);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t h = mx4::mix(rk ^ ((uint32_t)((col >> 1) + c) * 0x3C6EF373u + hi));
+        for (int c = 0; c < E / 2; ++c) {
+            const uint32_t h = mx4::mix(rk ^ (pk + (uint32_t)c * 0x3C6EF373u));
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool keep = (e ? h >> 16 : h & 0xFFFFu) >= p.cut;
@@ -118,11 +126,11 @@ __global__ void __launch_bounds__(256) k_dropout(DropArgs p)
                     v[i] = keep ? v[i] * p.scale : 0.0f;
             }
         }
-        if (n == 8) {
-            store8(y, v);
+        if (n == E) {
+            store16<T, FAR>(y, pack(v));
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < E; ++i)
                 if (i < n) store1(y + i, v[i]);
         }
     }
@@ -145,18 +153,28 @@ hipError_t launch_dropout(const DropoutArgs& g, hipStream_t stream)
     p.seed = g.seed;
     p.y = g.y;
     p.ldy = g.ldy;
-    const int64_t groups = (g.cols + 7) / 8;
+    const int64_t each = g.dtype == FP8_IN_BF16 ? 8 : 4, groups = (g.cols + each - 1) / each;
     p.lanes_log2 = 0;
     while (p.lanes_log2 < 6 && ((int64_t)1 << p.lanes_log2) < groups) ++p.lanes_log2;
     p.chunks = (groups + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
     const int64_t per = 64 >> p.lanes_log2;
     p.units = (g.rows + per - 1) / per * p.chunks;
     const unsigned grid = (unsigned)std::min<int64_t>((p.units + 3) / 4, (int64_t)gemm_num_cus() * 64);
+    // More than the last-level cache holds (256 MB): reads and writes that leave
+    // it alone, 8191 x 5000 fp32 54 us against 63 (16384 x 2048 bf16 onto a
+    // residual 34 against 37.5).  Below that the plain forms: what reads y next
+    // may find it there.
+    const int64_t moved = g.rows * g.cols * (16 / each) * (g.residual ? 3 : 2);
+    const bool far = moved > (int64_t)256 << 20;
     const auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, p); };
-    if (g.dtype == FP8_IN_BF16)
-        g.residual ? launch(k_dropout<uint16_t, true>) : launch(k_dropout<uint16_t, false>);
-    else
-        g.residual ? launch(k_dropout<float, true>) : launch(k_dropout<float, false>);
+    const auto with = [&](auto t) {
+        using T = decltype(t);
+        if (g.residual)
+            far ? launch(k_dropout<T, true, true>) : launch(k_dropout<T, true, false>);
+        else
+            far ? launch(k_dropout<T, false, true>) : launch(k_dropout<T, false, false>);
+    };
+    g.dtype == FP8_IN_BF16 ? with(uint16_t{}) : with(float{});
     return hipGetLastError();
 }
 
