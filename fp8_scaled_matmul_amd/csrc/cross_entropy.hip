@@ -148,12 +148,14 @@ struct StatsEpilogue {
                 for (int r = 0; r < 4; ++r) mx = fmaxf(mx, acc[j][i][r]);
             mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
             mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-            const float off = mx == -__builtin_inff() ? 0.0f : -mx * kLog2e;
+            // (the difference first: the product alone may overflow, and its
+            // rounding grows with the logits)
+            const float base = mx == -__builtin_inff() ? 0.0f : mx;
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < MF; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] += exp2_fast(__builtin_fmaf(acc[j][i][r], kLog2e, off));
+                for (int r = 0; r < 4; ++r) s[r] += exp2_fast((acc[j][i][r] - base) * kLog2e);
             float sum = (s[0] + s[1]) + (s[2] + s[3]);
             sum += __shfl_xor(sum, 16, 64);
             sum += __shfl_xor(sum, 32, 64);
@@ -165,9 +167,9 @@ struct StatsEpilogue {
 };
 
 // What the backward's logits need of a token: a token that does not count has
-// the exponential of -Inf, 0, and the gradient 0 (and x all zeros).
+// an lse of +Inf, so exponentials of 0, and the gradient 0 (and x all zeros).
 struct TokenNote {
-    float off;                  // -lse log2 e
+    float lse;                  // +Inf: the token does not count
     float grad;
     int target;                 // -1: none
     int unused;
@@ -215,7 +217,7 @@ struct GradEpilogue {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) d[h][r] = exp2_fast(__builtin_fmaf(acc[j][i + h][r], kLog2e, k.off));
+                    for (int r = 0; r < 4; ++r) d[h][r] = exp2_fast((acc[j][i + h][r] - k.lse) * kLog2e);
                 if (target_here) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -394,8 +396,8 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, 
             const int64_t t = k.targets[r];
             on = t >= 0 && t < k.vocab;
             if (c == 0) {
-                TokenNote note = {-__builtin_inff(), 0.0f, -1, 0};
-                if (on) note = TokenNote{-k.lse[r] * kLog2e, k.grad[r * k.grad_step], (int)t, 0};
+                TokenNote note = {__builtin_inff(), 0.0f, -1, 0};
+                if (on) note = TokenNote{k.lse[r], k.grad[r * k.grad_step], (int)t, 0};
                 k.notes[r] = note;
             }
         }

@@ -16,6 +16,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kWaves = 16, kParts = 256;    // waves of a workgroup; workgroups at most
+constexpr int kBackwardBlocks = 1;          // the backward's workgroups a CU at most
 
 struct RouteKArgs {
     const void* logits;
@@ -99,15 +100,15 @@ struct Key16 {
     static __device__ T none() { return 0; }
     static __device__ T make(float l, int e)
     {
-        const uint32_t u = __builtin_bit_cast(uint32_t, l + 0.0f) >> 16;       // -0 as 0
-        const uint32_t k = l != l ? 0u : (u & 0x8000u) ? 0xFFFFu - u : u + 0x8000u;
-        return k << 16 | (uint32_t)(0xFFFF - e);
+        const uint32_t b = __builtin_bit_cast(uint32_t, l + 0.0f);     // -0 as 0
+        const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+        return l != l ? (uint32_t)(0xFFFF - e) : (k & 0xFFFF0000u) | (uint32_t)(0xFFFF - e);
     }
     static __device__ int expert(T k) { return 0xFFFF - (int)(k & 0xFFFFu); }
     static __device__ float value(T k)
     {
-        const uint32_t o = k >> 16, u = o & 0x8000u ? o - 0x8000u : 0xFFFFu - o;
-        return __builtin_bit_cast(float, o == 0 ? 0x7FC00000u : u << 16);
+        const uint32_t o = k & 0xFFFF0000u, b = o & 0x80000000u ? o ^ 0x80000000u : ~o & 0xFFFF0000u;
+        return __builtin_bit_cast(float, o == 0 ? 0x7FC00000u : b);
     }
     static __device__ T largest(T a, T b) { return max(a, b); }
     static __device__ T smallest(T a, T b) { return min(a, b); }
@@ -256,14 +257,26 @@ __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.0f;
     int n = 0;
-    for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * G; t0 < a.tokens; t0 += (int64_t)gridDim.x * kWaves * G) {
+    const int64_t step = (int64_t)gridDim.x * kWaves * G;
+    // a token's row, read while the one before is worked on
+    float l[V], next[V];
+    bool on, next_on;
+    const auto fetch = [&](int64_t t0, float (&row)[V], bool& live) {
+        const int64_t t = t0 + lane / L;
+        live = t < a.tokens && (!a.mask || a.mask[t] != 0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) row[i] = -__builtin_inff();
+        if (live) load_row<V>(static_cast<const T*>(a.logits) + t * a.ld, e0, a.experts, row);
+    };
+    const int64_t first = ((int64_t)blockIdx.x * kWaves + wave) * G;
+    fetch(first, next, next_on);
+    for (int64_t t0 = first; t0 < a.tokens; t0 += step) {
         const int64_t t = t0 + lane / L;
         const bool there = t < a.tokens;
-        bool on = there && (!a.mask || a.mask[t] != 0);
-        float l[V];
+        on = next_on;
 #pragma unroll
-        for (int i = 0; i < V; ++i) l[i] = -__builtin_inff();
-        if (on) load_row<V>(static_cast<const T*>(a.logits) + t * a.ld, e0, a.experts, l);
+        for (int i = 0; i < V; ++i) l[i] = next[i];
+        fetch(t0 + step, next, next_on);
         typename K::T key[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = e0 + i < a.experts ? K::make(l[i], e0 + i) : K::none();
@@ -301,7 +314,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
         if (there && sub < a.top_k) {
             const int e = on ? K::expert(mine) : -1;
             a.ids[t * a.top_k + sub] = e;
-            a.weights[t * a.top_k + sub] = on ? chosen / below : 0.0f;
+            a.weights[t * a.top_k + sub] = on ? chosen * __builtin_amdgcn_rcpf(below) : 0.0f;
             if (on) atomicAdd(&count[e], 1);
         }
     }
@@ -401,12 +414,33 @@ __global__ void __launch_bounds__(64 * kWaves) k_route_backward(RouteKArgs a)
     constexpr int R = V < 4 ? V : 4;
     const auto place = [](int e) { return (e % V) / R * (L * R) + e / V * R + e % R; };
     __shared__ __attribute__((aligned(16))) float extra[kWaves][G][L * V];
-    __shared__ int32_t pairs;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = lane % L, e0 = V * sub;
     float* own = extra[wave][lane / L];
-    if (threadIdx.x == 0) pairs = 0;
-    __syncthreads();
+    const int64_t step = (int64_t)gridDim.x * kWaves * G, first = ((int64_t)blockIdx.x * kWaves + wave) * G;
+    // what belongs to a token, read while the one before is worked on
+    struct Row {
+        float p[V];
+        int id;
+        float w, g;
+    } next;
+    const auto fetch = [&](int64_t t0, Row& r) {
+        const int64_t t = t0 + lane / L;
+        const bool there = t < a.tokens;
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.p[i] = -__builtin_inff();
+        if (there) load_row<V>(static_cast<const T*>(a.logits) + t * a.ld, e0, a.experts, r.p);
+        r.id = -1;
+        r.w = r.g = 0.0f;
+        if (there && sub < a.top_k) {
+            r.id = a.ids[t * a.top_k + sub];
+            if (a.grad_weights) {
+                r.w = a.weights[t * a.top_k + sub];
+                r.g = a.grad_weights[t * a.top_k + sub];
+            }
+        }
+    };
+    fetch(first, next);
     // the balance loss' gradient for each probability
     float share[V];
     int c = 0;
@@ -417,29 +451,19 @@ __global__ void __launch_bounds__(64 * kWaves) k_route_backward(RouteKArgs a)
         c += k;
     }
     c = (int)wave_sum(lane < L ? (uint32_t)c : 0u);
-    if (threadIdx.x == 0) pairs = c;
-    __syncthreads();
-    const double n = (double)pairs / a.top_k;
+    const double n = (double)c / a.top_k;
     const float gb = a.grad_balance ? *a.grad_balance : 0.0f;
     const float to_share = n > 0.0 ? (float)(gb * (double)a.experts / (n * n * a.top_k)) : 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) share[i] *= to_share;
-    for (int64_t t0 = ((int64_t)blockIdx.x * kWaves + wave) * G; t0 < a.tokens; t0 += (int64_t)gridDim.x * kWaves * G) {
+    for (int64_t t0 = first; t0 < a.tokens; t0 += step) {
         const int64_t t = t0 + lane / L;
         const bool there = t < a.tokens;
-        float p[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = -__builtin_inff();
-        if (there) load_row<V>(static_cast<const T*>(a.logits) + t * a.ld, e0, a.experts, p);
-        int id = -1;
-        float w = 0.0f, g = 0.0f;
-        if (there && sub < a.top_k) {
-            id = a.ids[t * a.top_k + sub];
-            if (a.grad_weights) {
-                w = a.weights[t * a.top_k + sub];
-                g = a.grad_weights[t * a.top_k + sub];
-            }
-        }
+        Row now = next;
+        fetch(t0 + step, next);
+        float (&p)[V] = now.p;
+        const int id = now.id;
+        float w = now.w, g = now.g;
         // of a token that is left out the gradient may hold anything
         w = id >= 0 ? w : 0.0f;
         g = id >= 0 ? g : 0.0f;
@@ -568,7 +592,7 @@ hipError_t launch_route_backward(const RouteArgs& g, hipStream_t stream)
     a.dlogits = g.dlogits;
     a.ldd = g.ldd;
     const int64_t per = kWaves * tokens_of_wave(g.experts);
-    const int grid = (int)std::min<int64_t>((g.tokens + per - 1) / per, 2 * gemm_num_cus());
+    const int grid = (int)std::min<int64_t>((g.tokens + per - 1) / per, kBackwardBlocks * gemm_num_cus());
     by_experts(a.experts, g.dtype, [&](auto t, auto l, auto v) {
         hipLaunchKernelGGL((k_route_backward<decltype(t), decltype(l)::value, decltype(v)::value>), dim3(grid),
                            dim3(64 * kWaves), 0, stream, a);
