@@ -25,7 +25,6 @@ using gemm::v4u;
 typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ inline float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
@@ -37,7 +36,9 @@ __device__ inline float softcap_near(float l, float inv_cap)
     const float u = l * inv_cap, t = u * u;
     const float n = __builtin_fmaf(__builtin_fmaf(21.0f, t, 1260.0f), t, 10395.0f);
     const float d = __builtin_fmaf(__builtin_fmaf(t + 210.0f, t, 4725.0f), t, 10395.0f);
-    return l * n * __builtin_amdgcn_rcpf(d);
+    // the quotient with its residual put back: off by a step, not by three
+    const float ln = l * n, r = __builtin_amdgcn_rcpf(d), q = ln * r;
+    return __builtin_fmaf(__builtin_fmaf(-q, d, ln), r, q);
 }
 __device__ inline float softcap_any(float l, float cap, float inv_cap)
 {
@@ -170,14 +171,18 @@ struct StatsEpilogue {
 // an lse of +Inf, so exponentials of 0, and the gradient 0 (and x all zeros).
 struct TokenNote {
     float lse;                  // +Inf: the token does not count
-    float grad;
+    float grad;                 // of its loss, over the largest of all tokens'
     int target;                 // -1: none
     int unused;
 };
 
-// The backward's: dl, rounded to bf16 (by 2^-8 of each value at most, what the
-// operands' own type has; the matrix instruction takes one type), rows past
-// the vocabulary's end as zeros.
+// The backward's: dl over the largest gradient of the losses, rounded to bf16 (by
+// 2^-8 of each value at most, what the operands' own type has; the matrix
+// instruction takes one type), rows past the vocabulary's end as zeros.  Losses
+// have one gradient as a rule, the mean's, and most targets one near -1: divided by
+// it they round to -1 with almost no error, where the gradient's own mantissa
+// would put the same error into all of them (0.0031 of the gradients' size against
+// 0.0017 for their rounding alone).
 template <int WR, int MF, int NF>
 struct GradEpilogue {
     static constexpr int kStores = MF / 2 * NF;
@@ -263,6 +268,7 @@ struct OutEpilogue {
     uint16_t* out;              // bf16 [n, ld], or null: to the planes
     int64_t ld;
     int wide;                   // 16-byte stores are in place
+    const float* scale;         // of bf16 outputs
 
     __device__ void note(uint32_t, int) const {}
 
@@ -293,6 +299,11 @@ struct OutEpilogue {
                 return true;
             }
         }
+        const float by = *scale;
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+#pragma unroll
+            for (int i = 0; i < MF; ++i) acc[j][i] *= by;
         if (wide) {
             const __amdgpu_buffer_rsrc_t ro =
                 gemm::make_store_rsrc(out + n0 * ld, rows ? (uint32_t)(((rows - 1) * ld + m) * 2) : 0u);
@@ -380,6 +391,7 @@ struct PackTokens {
     const float* lse;
     const float* grad;
     int64_t grad_step;
+    const float* scale;
     TokenNote* notes;
 };
 template <bool TOKENS>
@@ -397,7 +409,7 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, 
             on = t >= 0 && t < k.vocab;
             if (c == 0) {
                 TokenNote note = {__builtin_inff(), 0.0f, -1, 0};
-                if (on) note = TokenNote{k.lse[r], k.grad[r * k.grad_step], (int)t, 0};
+                if (on) note = TokenNote{k.lse[r], k.grad[r * k.grad_step] / *k.scale, (int)t, 0};
                 k.notes[r] = note;
             }
         }
@@ -414,6 +426,32 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, 
             }
         }
         out[u] = v;
+    }
+}
+
+// The largest |gradient| of the losses that count (1 where all are 0 or one is no
+// number: the quotients then say so).  One workgroup.
+__global__ void __launch_bounds__(1024) k_ce_scale(PackTokens k, int64_t n, float* scale)
+{
+    __shared__ float sh[16];
+    float most = 0.0f;
+    bool bad = false;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < n; t += 1024) {
+        const int64_t at = k.targets[t];
+        const float g = at >= 0 && at < k.vocab ? __builtin_fabsf(k.grad[t * k.grad_step]) : 0.0f;
+        most = fmaxf(most, g);
+        bad |= !(g <= 3.0e38f);
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+    const bool any_bad = __syncthreads_or(bad);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 16; ++w) most = fmaxf(most, sh[w]);
+        // (below the smallest normal number a quotient could overflow)
+        *scale = any_bad || most < 0x1p-126f ? 1.0f : most;
     }
 }
 
@@ -451,10 +489,12 @@ __global__ void __launch_bounds__(256) k_ce_loss(const float2* part, int blocks,
     }
     if (y == 0 && t < n) {
         const float2 s = sh[x];
-        const float l = s.x + __builtin_amdgcn_logf(s.y) * kLn2;
+        // the loss without lse's rounding: where the target is the largest, it is the
+        // logarithm alone
+        const float log_sum = logf(s.y);
         const int64_t at = targets[t];
-        lse[t] = l;
-        loss[t] = at < 0 ? 0.0f : at < vocab ? l - zt[t] : __builtin_nanf("");
+        lse[t] = s.x + log_sum;
+        loss[t] = at < 0 ? 0.0f : at < vocab ? (s.x - zt[t]) + log_sum : __builtin_nanf("");
     }
 }
 
@@ -462,9 +502,10 @@ __global__ void __launch_bounds__(256) k_ce_loss(const float2* part, int blocks,
 // every S-th plane, and their sums are added in order.
 template <int S>
 __global__ void __launch_bounds__(256) k_ce_reduce(const float* plane, int splits, int64_t rows, int cols, int64_t ld_plane,
-                                                   uint16_t* out, int64_t ld, int wide)
+                                                   uint16_t* out, int64_t ld, int wide, const float* scale)
 {
     __shared__ v4f sh[S > 1 ? 512 : 1];
+    const float by = *scale;
     constexpr int C = 256 / S;          // chunks of a workgroup
     const int x = threadIdx.x % C, y = threadIdx.x / C;
     const int chunks = (int)(ld_plane / 8);
@@ -496,6 +537,8 @@ __global__ void __launch_bounds__(256) k_ce_reduce(const float* plane, int split
             __syncthreads();
         }
         if (y != 0 || u >= total) continue;
+        a *= by;
+        b *= by;
         uint16_t* to = out + r * ld + c;
         if (wide && c + 8 <= cols) {
             *reinterpret_cast<v4u*>(to) = v4u{gemm::pack_bf16(a[0], a[1]), gemm::pack_bf16(a[2], a[3]),
@@ -535,7 +578,7 @@ constexpr int64_t kPieceBytes = (int64_t)1 << 29;
 struct Layout {
     int64_t piece, pieces;      // vocabulary rows (a multiple of 256) and number
     int64_t splits;             // of dx
-    size_t x, w, stats, zt, notes, dl, planes, total;      // offsets in the workspace
+    size_t x, w, stats, zt, scale, notes, dl, planes, total;      // offsets in the workspace
 };
 size_t take(size_t& at, int64_t bytes)
 {
@@ -576,6 +619,7 @@ Layout backward_layout(int64_t tokens, int64_t vocab, int64_t hidden)
     size_t at = 0;
     l.x = take(at, tokens * row);
     l.w = take(at, std::min(l.piece, vocab) * row);
+    l.scale = take(at, 4);
     l.notes = take(at, tokens * (int64_t)sizeof(TokenNote));
     l.dl = take(at, tokens * l.piece * 2);
     l.planes = take(at, l.splits > 1 || l.pieces > 1 ? l.splits * tokens * up(hidden, 16) * 4 : 0);
@@ -663,7 +707,10 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
     // x always as a copy, in which the tokens that do not count are zeros:
     // their products with dl's zeros have to be zeros in dw
     TokenNote* notes = reinterpret_cast<TokenNote*>(ws + l.notes);
-    const PackTokens tokens = {g.targets, g.vocab, g.lse, g.grad, g.grad_step, notes};
+    float* scale = reinterpret_cast<float*>(ws + l.scale);
+    const PackTokens tokens = {g.targets, g.vocab, g.lse, g.grad, g.grad_step, scale, notes};
+    hipLaunchKernelGGL(k_ce_scale, dim3(1), dim3(1024), 0, stream, tokens, g.tokens, scale);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = pack(g.x, g.ldx, g.tokens, g.hidden, ws + l.x, &tokens, stream)) != hipSuccess) return e;
     const ce::Operand x = {ws + l.x, packed};
     float* planes = reinterpret_cast<float*>(ws + l.planes);
@@ -713,6 +760,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
                 epi.out = direct ? static_cast<uint16_t*>(g.dx) : nullptr;
                 epi.ld = g.lddx;
                 epi.wide = aligned16(g.dx, g.lddx) && H % 8 == 0;
+                epi.scale = scale;
             }, stream);
             if (e != hipSuccess) return e;
             if (last && !direct) {
@@ -722,7 +770,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
                     const int64_t groups = (g.tokens * ld / 8 + 256 / share - 1) / (256 / share);
                     hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(groups, 8 * gemm_num_cus())), dim3(256), 0, stream,
                                        planes, (int)l.splits, g.tokens, H, ld, static_cast<uint16_t*>(g.dx), g.lddx,
-                                       (int)aligned16(g.dx, g.lddx));
+                                       (int)aligned16(g.dx, g.lddx), scale);
                 };
                 l.splits >= 8 ? reduce(k_ce_reduce<16>, 16) : reduce(k_ce_reduce<1>, 1);
                 if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -745,6 +793,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
                 epi.out = dw;
                 epi.ld = g.lddw;
                 epi.wide = aligned16(dw, g.lddw) && H % 8 == 0;
+                epi.scale = scale;
             }, stream);
             if (e != hipSuccess) return e;
         }
