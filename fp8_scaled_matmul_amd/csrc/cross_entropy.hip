@@ -255,50 +255,24 @@ struct GradEpilogue {
     }
 };
 
-// A gradient: fp32 planes (one for each split of K, added to what an earlier
-// piece of the vocabulary left), or bf16 at the end.
-template <int WR, int MF, int NF>
-struct OutEpilogue {
+// A gradient in bf16.
+template <int MF, int NF, bool FAR>
+struct Bf16Out {
     static constexpr int kStores = MF / 2 * NF;
     static constexpr bool kNotes = false;
     int m, n;                   // the gradient's columns and rows
-    float* plane;               // [splits, n, ld_plane], or null
-    int64_t ld_plane;           // a multiple of 16
-    int add;                    // onto the planes' contents
-    uint16_t* out;              // bf16 [n, ld], or null: to the planes
+    uint16_t* out;              // bf16 [n, ld]
     int64_t ld;
     int wide;                   // 16-byte stores are in place
-    const float* scale;         // of bf16 outputs
+    const float* scale;
 
     __device__ void note(uint32_t, int) const {}
 
-    __device__ bool operator()(const Item& it, v4f (&acc)[NF][MF], int row, int col, const uint8_t*) const
+    __device__ bool operator()(const Item&, v4f (&acc)[NF][MF], int row, int col, const uint8_t*) const
     {
         const int lane = threadIdx.x & 63;
         const int n0 = __builtin_amdgcn_readfirstlane(col & ~15);
         const int rows = max(min(n - n0, 16 * NF), 0);
-        if (plane && (add || !out)) {
-            const __amdgpu_buffer_rsrc_t rp = gemm::make_store_rsrc(plane + ((int64_t)it.split * n + n0) * ld_plane,
-                                                                    (uint32_t)(rows * ld_plane * 4));
-            const uint32_t at = (uint32_t)((lane & 15) * ld_plane + row) * 4u;
-            const auto place = [&](int i, int j) {
-                return row + 16 * i < m ? at + (uint32_t)(16 * j * ld_plane + 16 * i) * 4u : gemm::kOutOfRange;
-            };
-            if (add) {
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-#pragma unroll
-                    for (int i = 0; i < MF; ++i)
-                        acc[j][i] += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)place(i, j), 0, 0));
-            }
-            if (!out) {
-#pragma unroll
-                for (int j = 0; j < NF; ++j)
-#pragma unroll
-                    for (int i = 0; i < MF; ++i) gemm::store16(__builtin_bit_cast(v4u, acc[j][i]), place(i, j), rp);
-                return true;
-            }
-        }
         const float by = *scale;
 #pragma unroll
         for (int j = 0; j < NF; ++j)
@@ -313,8 +287,10 @@ struct OutEpilogue {
             for (int j = 0; j < NF; ++j)
 #pragma unroll
                 for (int i = 0; i < MF; i += 2)
-                    gemm::store16(to_bf16_chunk(acc[j][i], acc[j][i + 1]),
-                                  first + 16 * i < m ? to + (uint32_t)(16 * j * ld + 16 * i) * 2u : gemm::kOutOfRange, ro);
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        to_bf16_chunk(acc[j][i], acc[j][i + 1]), ro,
+                        (int)(first + 16 * i < m ? to + (uint32_t)(16 * j * ld + 16 * i) * 2u : gemm::kOutOfRange), 0,
+                        FAR ? 18 : 0);              // sc1 nt
             return true;
         }
 #pragma unroll
@@ -330,6 +306,51 @@ struct OutEpilogue {
             }
         }
         return false;
+    }
+};
+
+template <int WR, int MF, int NF>
+struct NearEpilogue : Bf16Out<MF, NF, false> {};
+template <int WR, int MF, int NF>
+struct FarEpilogue : Bf16Out<MF, NF, true> {};
+
+// A gradient in parts: fp32 planes, one for each split of K, added to what an
+// earlier piece of the vocabulary left.
+template <int WR, int MF, int NF>
+struct PlanesEpilogue {
+    static constexpr int kStores = MF * NF;
+    static constexpr bool kNotes = false;
+    int m, n;                   // the gradient's columns and rows
+    float* plane;               // [splits, n, ld]
+    int64_t ld;                 // a multiple of 16
+    int add;
+
+    __device__ void note(uint32_t, int) const {}
+
+    __device__ bool operator()(const Item& it, v4f (&acc)[NF][MF], int row, int col, const uint8_t*) const
+    {
+        const int lane = threadIdx.x & 63;
+        const int n0 = __builtin_amdgcn_readfirstlane(col & ~15);
+        const int rows = max(min(n - n0, 16 * NF), 0);
+        const __amdgpu_buffer_rsrc_t rp =
+            gemm::make_store_rsrc(plane + ((int64_t)it.split * n + n0) * ld, (uint32_t)(rows * ld * 4));
+        const uint32_t at = (uint32_t)((lane & 15) * ld + row) * 4u;
+        const auto place = [&](int i, int j) {
+            return row + 16 * i < m ? at + (uint32_t)(16 * j * ld + 16 * i) * 4u : gemm::kOutOfRange;
+        };
+        // a column after another: more loads in flight would spill
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            if (add) {
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+                    acc[j][i] += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)place(i, j), 0, 0));
+            }
+#pragma unroll
+            for (int i = 0; i < MF; ++i) gemm::store16(__builtin_bit_cast(v4u, acc[j][i]), place(i, j), rp);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        return true;
     }
 };
 
@@ -381,6 +402,28 @@ hipError_t launch_tokens(const GemmShape& s, Init init, hipStream_t stream)
 int row_tile(int64_t tokens) { return token_tile(tokens) <= 64 ? 128 : 256; }
 int stat_rows(int64_t tokens) { return token_tile(tokens) <= 64 ? 32 : token_tile(tokens) <= 128 ? 64 : 128; }
 
+// Tiles of 256 x 256 come in rounds of one a CU.  Where the last round would be a
+// small part of one, the rows behind the whole rounds go in tiles of 128 x 128
+// instead, one a CU at most, in a launch of their own: returns the rows before
+// them.  2001 x 50001 x 1000, 6.1 rounds: backward 698 us against 733; 1023 tokens,
+// 3.1 rounds: forward 134 against 144.  (Up to two small tiles a CU: the same.)
+int64_t whole_rounds(int64_t rows, int64_t others)
+{
+    const int64_t cus = gemm_num_cus(), across = tiles_of(others, 256), tiles = tiles_of(rows, 256);
+    const int64_t main = tiles * across / cus * cus / across;
+    if (main == 0 || main >= tiles) return rows;
+    return (int64_t)tiles_of(rows - 256 * main, 128) * tiles_of(others, 128) <= cus ? 256 * main : rows;
+}
+constexpr int kTailRows = 128, kTailStatRows = 64;
+
+// Blocks of statistics of `rows` of the vocabulary.
+int64_t stat_blocks(int64_t rows, int64_t tokens)
+{
+    if (token_tile(tokens) < 256) return (int64_t)tiles_of(rows, row_tile(tokens)) * (row_tile(tokens) / stat_rows(tokens));
+    const int64_t big = whole_rounds(rows, tokens);
+    return (int64_t)tiles_of(big, 256) * 2 + (int64_t)tiles_of(rows - big, kTailRows) * (kTailRows / kTailStatRows);
+}
+
 // ------------------------------------------------------------------ around the products
 // Rows of bf16 at 16-byte places with zeros behind them.  For tokens of a
 // backward pass, rows of those that do not count as zeros (their x may hold
@@ -391,14 +434,55 @@ struct PackTokens {
     const float* lse;
     const float* grad;
     int64_t grad_step;
-    const float* scale;
+    float* scale;
     TokenNote* notes;
 };
+// The largest |gradient| of the losses that count (1 where all are 0 or one is no
+// number: the quotients then say so), by a whole workgroup.
+template <int THREADS>
+__device__ inline float largest_grad(const PackTokens& k, int64_t n)
+{
+    __shared__ float sh[THREADS / 64];
+    float most = 0.0f;
+    bool bad = false;
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < n; t += THREADS) {
+        const int64_t at = k.targets[t];
+        const float g = __builtin_fabsf(k.grad[t * k.grad_step]);
+        const bool on = at >= 0 && at < k.vocab;
+        most = on ? fmaxf(most, g) : most;
+        bad |= on && !(g <= 3.0e38f);
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = most;
+    const bool any_bad = __syncthreads_or(bad);
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) most = fmaxf(most, sh[w]);
+    // (below the smallest normal number a quotient could overflow)
+    return any_bad || most < 0x1p-126f ? 1.0f : most;
+}
+__global__ void __launch_bounds__(1024) k_ce_scale(PackTokens k, int64_t n)
+{
+    const float by = largest_grad<1024>(k, n);
+    if (threadIdx.x == 0) *k.scale = by;
+}
+constexpr int64_t kFewTokens = 1024;        // each workgroup of the copy looks through them itself
+
 template <bool TOKENS>
 __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, int64_t rows, int cols, uint4* out,
                                                  int chunks, int aligned, PackTokens k)
 {
     const int64_t total = rows * chunks;
+    float by = 1.0f;
+    if constexpr (TOKENS) {
+        if (rows <= kFewTokens) {
+            by = largest_grad<256>(k, rows);
+            if (blockIdx.x == 0 && threadIdx.x == 0) *k.scale = by;
+        } else {
+            by = *k.scale;
+        }
+    }
     for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
         const int64_t r = u / chunks;
         const int c = (int)(u - r * chunks) * 8;
@@ -409,7 +493,7 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, 
             on = t >= 0 && t < k.vocab;
             if (c == 0) {
                 TokenNote note = {__builtin_inff(), 0.0f, -1, 0};
-                if (on) note = TokenNote{k.lse[r], k.grad[r * k.grad_step] / *k.scale, (int)t, 0};
+                if (on) note = TokenNote{k.lse[r], k.grad[r * k.grad_step] / by, (int)t, 0};
                 k.notes[r] = note;
             }
         }
@@ -426,32 +510,6 @@ __global__ void __launch_bounds__(256) k_ce_pack(const uint16_t* x, int64_t ld, 
             }
         }
         out[u] = v;
-    }
-}
-
-// The largest |gradient| of the losses that count (1 where all are 0 or one is no
-// number: the quotients then say so).  One workgroup.
-__global__ void __launch_bounds__(1024) k_ce_scale(PackTokens k, int64_t n, float* scale)
-{
-    __shared__ float sh[16];
-    float most = 0.0f;
-    bool bad = false;
-#pragma unroll 4
-    for (int64_t t = threadIdx.x; t < n; t += 1024) {
-        const int64_t at = k.targets[t];
-        const float g = at >= 0 && at < k.vocab ? __builtin_fabsf(k.grad[t * k.grad_step]) : 0.0f;
-        most = fmaxf(most, g);
-        bad |= !(g <= 3.0e38f);
-    }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
-    const bool any_bad = __syncthreads_or(bad);
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = most;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < 16; ++w) most = fmaxf(most, sh[w]);
-        // (below the smallest normal number a quotient could overflow)
-        *scale = any_bad || most < 0x1p-126f ? 1.0f : most;
     }
 }
 
@@ -574,6 +632,9 @@ hipError_t pack(const void* x, int64_t ld, int64_t rows, int64_t cols, void* out
 // rows.
 constexpr int64_t kTokenChunk = 32768;
 constexpr int64_t kPieceBytes = (int64_t)1 << 29;
+// A dw of more than this is written past the caches: 64 x 65536 x 2048 61 us against
+// 116, x 1536 52 against 75, x 1024 (128 MiB) 35 against 38, x 768 30 against 28.
+constexpr int64_t kFarBytes = (int64_t)1 << 27;
 
 struct Layout {
     int64_t piece, pieces;      // vocabulary rows (a multiple of 256) and number
@@ -601,7 +662,13 @@ Layout forward_layout(int64_t tokens, int64_t vocab, int64_t hidden)
     size_t at = 0;
     l.x = take(at, chunk * row);
     l.w = take(at, std::min(l.piece, vocab) * row);
-    l.stats = take(at, (up(vocab, 256) / stat_rows(chunk)) * chunk * 8);
+    int64_t stats = 0;          // of a full chunk and of the last one, w copied or not
+    for (const int64_t n : {chunk, tokens % kTokenChunk ? tokens % kTokenChunk : chunk}) {
+        const int64_t last = vocab - (l.pieces - 1) * l.piece;
+        const int64_t copied = (l.pieces - 1) * stat_blocks(l.piece, n) + stat_blocks(last, n);
+        stats = std::max(stats, std::max(stat_blocks(vocab, n), copied) * n * 8);
+    }
+    l.stats = take(at, stats);
     l.zt = take(at, chunk * 4);
     l.total = at;
     return l;
@@ -665,20 +732,29 @@ hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
                 if ((e = pack(w, g.ldw, m, g.hidden, ws + l.w, nullptr, stream)) != hipSuccess) return e;
                 s.a = {ws + l.w, up(g.hidden, 8) * 2};
             }
-            s.m = (int)m;
-            e = launch_tokens<false, StatsEpilogue>(s, [&](auto& epi) {
-                epi.m = (int)m;
-                epi.n = (int)n;
-                epi.v0 = (int)v0;
-                epi.block0 = blocks;
-                epi.cap = g.softcap;
-                epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
-                epi.targets = g.targets + t0;
-                epi.part = reinterpret_cast<float2*>(ws + l.stats);
-                epi.zt = reinterpret_cast<float*>(ws + l.zt);
-            }, stream);
-            if (e != hipSuccess) return e;
-            blocks += tiles_of(m, row_tile(n)) * (row_tile(n) / stat_rows(n));      // of whole tiles
+            const int64_t big = token_tile(n) == 256 ? whole_rounds(m, n) : m;
+            const auto rows = [&](int64_t from, int64_t count, int block) {
+                return [=, &g](auto& epi) {
+                    epi.m = (int)count;
+                    epi.n = (int)n;
+                    epi.v0 = (int)(v0 + from);
+                    epi.block0 = block;
+                    epi.cap = g.softcap;
+                    epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
+                    epi.targets = g.targets + t0;
+                    epi.part = reinterpret_cast<float2*>(ws + l.stats);
+                    epi.zt = reinterpret_cast<float*>(ws + l.zt);
+                };
+            };
+            s.m = (int)big;
+            if ((e = launch_tokens<false, StatsEpilogue>(s, rows(0, big, blocks), stream)) != hipSuccess) return e;
+            if (big < m) {
+                s.a.p += big * s.a.ld;
+                s.m = (int)(m - big);
+                e = launch_tile<false, false, 2, 2, 4, 4, StatsEpilogue>(s, rows(big, m - big, blocks + (int)(big / 128)), stream);
+                if (e != hipSuccess) return e;
+            }
+            blocks += (int)stat_blocks(m, n);
         }
         const auto finish = [&](auto kernel, int tx) {
             hipLaunchKernelGGL(kernel, dim3((unsigned)((n + tx - 1) / tx)), dim3(256), 0, stream,
@@ -709,8 +785,10 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
     TokenNote* notes = reinterpret_cast<TokenNote*>(ws + l.notes);
     float* scale = reinterpret_cast<float*>(ws + l.scale);
     const PackTokens tokens = {g.targets, g.vocab, g.lse, g.grad, g.grad_step, scale, notes};
-    hipLaunchKernelGGL(k_ce_scale, dim3(1), dim3(1024), 0, stream, tokens, g.tokens, scale);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (g.tokens > kFewTokens) {
+        hipLaunchKernelGGL(k_ce_scale, dim3(1), dim3(1024), 0, stream, tokens, g.tokens);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     if ((e = pack(g.x, g.ldx, g.tokens, g.hidden, ws + l.x, &tokens, stream)) != hipSuccess) return e;
     const ce::Operand x = {ws + l.x, packed};
     float* planes = reinterpret_cast<float*>(ws + l.planes);
@@ -727,43 +805,56 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
         GemmShape s = {};
         s.a = w;
         s.b = x;
-        s.m = (int)m;
         s.n = T;
         s.k = H;
         s.splits = 1;
-        e = launch_tokens<false, GradEpilogue>(s, [&](auto& epi) {
-            epi.m = (int)m;
-            epi.n = T;
-            epi.v0 = (int)v0;
-            epi.cap = g.softcap;
-            epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
-            epi.tokens = notes;
-            epi.dl = dl;
-            epi.ld = l.piece;
-        }, stream);
-        if (e != hipSuccess) return e;
+        const int64_t big = token_tile(T) == 256 ? whole_rounds(m, T) : m;
+        const auto rows = [&](int64_t from, int64_t count) {
+            return [=, &g](auto& epi) {
+                epi.m = (int)count;
+                epi.n = T;
+                epi.v0 = (int)(v0 + from);
+                epi.cap = g.softcap;
+                epi.inv_cap = g.softcap != 0.0f ? 1.0f / g.softcap : 0.0f;
+                epi.tokens = notes;
+                epi.dl = dl + from;
+                epi.ld = l.piece;
+            };
+        };
+        s.m = (int)big;
+        if ((e = launch_tokens<false, GradEpilogue>(s, rows(0, big), stream)) != hipSuccess) return e;
+        if (big < m) {
+            s.a.p += big * s.a.ld;
+            s.m = (int)(m - big);
+            e = launch_tile<false, false, 2, 2, 4, 4, GradEpilogue>(s, rows(big, m - big), stream);
+            if (e != hipSuccess) return e;
+        }
         if (g.dx) {
-            const bool last = p == l.pieces - 1;
             s.a = w;
             s.b = d;
             s.m = H8;
             s.n = T;
             s.k = (int)m;
             s.splits = (int)std::min<int64_t>(l.splits, (m + ce::kStageK - 1) / ce::kStageK);
-            const bool direct = last && l.splits == 1;
-            e = launch_tokens<true, OutEpilogue>(s, [&](auto& epi) {
-                epi.m = H;
-                epi.n = T;
-                epi.plane = l.splits > 1 || l.pieces > 1 ? planes : nullptr;
-                epi.ld_plane = up(g.hidden, 16);
-                epi.add = p > 0;
-                epi.out = direct ? static_cast<uint16_t*>(g.dx) : nullptr;
-                epi.ld = g.lddx;
-                epi.wide = aligned16(g.dx, g.lddx) && H % 8 == 0;
-                epi.scale = scale;
-            }, stream);
+            if (l.splits == 1 && l.pieces == 1)
+                e = launch_tokens<true, NearEpilogue>(s, [&](auto& epi) {
+                    epi.m = H;
+                    epi.n = T;
+                    epi.out = static_cast<uint16_t*>(g.dx);
+                    epi.ld = g.lddx;
+                    epi.wide = aligned16(g.dx, g.lddx) && H % 8 == 0;
+                    epi.scale = scale;
+                }, stream);
+            else
+                e = launch_tokens<true, PlanesEpilogue>(s, [&](auto& epi) {
+                    epi.m = H;
+                    epi.n = T;
+                    epi.plane = planes;
+                    epi.ld = up(g.hidden, 16);
+                    epi.add = p > 0;
+                }, stream);
             if (e != hipSuccess) return e;
-            if (last && !direct) {
+            if (p == l.pieces - 1 && (l.splits > 1 || l.pieces > 1)) {
                 const int64_t ld = up(g.hidden, 16);
                 // a short last piece may have had fewer splits; the first has written all planes
                 const auto reduce = [&](auto kernel, int share) {
@@ -778,24 +869,34 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
         }
         if (g.dw) {
             s.a = x;
-            s.b = d;
             s.m = H8;
-            s.n = (int)up(m, 8);    // dl's rows go on with zeros
             s.k = T;
             s.splits = 1;
-            uint16_t* dw = static_cast<uint16_t*>(g.dw) + v0 * g.lddw;
-            e = launch_tile<true, true, 2, 4, 8, 4, OutEpilogue>(s, [&](auto& epi) {
-                epi.m = H;
-                epi.n = (int)m;
-                epi.plane = nullptr;
-                epi.ld_plane = 16;
-                epi.add = 0;
-                epi.out = dw;
-                epi.ld = g.lddw;
-                epi.wide = aligned16(dw, g.lddw) && H % 8 == 0;
-                epi.scale = scale;
-            }, stream);
+            const auto rows = [&](int64_t from, int64_t count) {
+                uint16_t* dw = static_cast<uint16_t*>(g.dw) + (v0 + from) * g.lddw;
+                return [=, &g](auto& epi) {
+                    epi.m = H;
+                    epi.n = (int)count;
+                    epi.out = dw;
+                    epi.ld = g.lddw;
+                    epi.wide = aligned16(dw, g.lddw) && H % 8 == 0;
+                    epi.scale = scale;
+                };
+            };
+            const int64_t big = whole_rounds(m, H);
+            s.b = d;
+            s.n = (int)up(big, 8);          // dl's rows go on with zeros
+            if (g.vocab * g.hidden * 2 > kFarBytes)
+                e = launch_tile<true, true, 2, 4, 8, 4, FarEpilogue>(s, rows(0, big), stream);
+            else
+                e = launch_tile<true, true, 2, 4, 8, 4, NearEpilogue>(s, rows(0, big), stream);
             if (e != hipSuccess) return e;
+            if (big < m) {
+                s.b.p = d.p + 2 * big;
+                s.n = (int)up(m - big, 8);
+                e = launch_tile<true, true, 2, 2, 4, 4, NearEpilogue>(s, rows(big, m - big), stream);
+                if (e != hipSuccess) return e;
+            }
         }
     }
     return hipSuccess;

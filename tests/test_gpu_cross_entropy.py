@@ -84,6 +84,16 @@ def test_against_oracle(tokens, vocab, hidden, softcap):
         check(got[name], want, name)
 
 
+def test_more_tiles_than_whole_rounds():
+    """More tiles of 256 x 256 than compute units, in each product: the rows behind
+    the last whole round have a launch of their own (257 tokens: two tiles across)."""
+    x, w, t, g = make(257, 65700, 72, seed=3)
+    want = expect(x, w, t, g, 0.0)
+    got = run(x.cuda(), w.cuda(), t.cuda(), g.cuda())
+    for name in got:
+        check(got[name], want, name)
+
+
 def test_large_logits_and_cap():
     """Logits of some hundreds: one token of the vocabulary takes all."""
     for softcap in (0.0, 20.0):
