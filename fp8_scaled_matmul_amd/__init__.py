@@ -892,7 +892,11 @@ class MoeMx4:
 
 
 # ---------------------------------------------------------------- around the linear layers
-_FAR = 1e30         # caps of logits lie below
+_FAR = 1e30         # caps of logits lie below, and above its inverse
+
+
+def _is_cap(softcap) -> bool:
+    return softcap == 0.0 or 1.0 / _FAR <= softcap < _FAR
 
 
 def _workspace(workspace, need: int, device):
@@ -915,8 +919,8 @@ def _check_head(x, w, targets, softcap, workspace):
     if workspace is not None:
         _check_tensor(workspace, "workspace", (torch.uint8,), contiguous=True)
     softcap = float(softcap)
-    if not 0.0 <= softcap < _FAR:
-        raise ValueError(f"softcap must be 0 (none) or positive and below {_FAR:g}, got {softcap}")
+    if not _is_cap(softcap):
+        raise ValueError(f"softcap must be 0 (none) or from {1.0 / _FAR:g} to below {_FAR:g}, got {softcap}")
     return x.shape[0], w.shape[0], x.shape[1], softcap
 
 
@@ -928,7 +932,7 @@ def linear_cross_entropy(x, w, targets, softcap: float = 0.0, workspace=None):
     the backward pass needs.  A negative target leaves its token out (loss 0);
     one past the vocabulary gives NaN.  workspace: optional uint8 device tensor of
     fp8_linear_ce_workspace_size(tokens, vocab, hidden, 0) bytes."""
-    if workspace is None and 0.0 <= softcap < _FAR:
+    if workspace is None and _is_cap(softcap):
         r = _ext().linear_ce(x, w, targets, float(softcap))
         if r is not None:
             if type(r) is int:
@@ -954,7 +958,7 @@ def linear_cross_entropy_backward(x, w, targets, lse, grad_loss, softcap: float 
     vocabulary add nothing, whatever x and grad_loss hold there.  workspace:
     optional uint8 device tensor of fp8_linear_ce_workspace_size(tokens, vocab,
     hidden, 1) bytes."""
-    if out_x is None and out_w is None and workspace is None and 0.0 <= softcap < _FAR:
+    if out_x is None and out_w is None and workspace is None and _is_cap(softcap):
         r = _ext().linear_ce_backward(x, w, targets, float(softcap), lse, grad_loss, bool(want_x), bool(want_w))
         if r is not None:
             if type(r) is int:
@@ -1032,7 +1036,7 @@ def moe_route_backward(logits, route: Route, grad_weights=None, grad_balance=Non
     """The logits' gradient, in their type, from those of route.weights (fp32
     [tokens, top_k]) and route.balance (fp32, one element); None counts as 0."""
     if out is None and isinstance(route, Route):
-        dl = _ext().moe_route_backward(logits, route.ids, route.weights, route.counts, route.renormalize, grad_weights,
+        dl = _ext().moe_route_backward(logits, route.ids, route.weights, route.counts, bool(route.renormalize), grad_weights,
                                        grad_balance)
         if dl is not None:
             if type(dl) is int:
@@ -1059,7 +1063,7 @@ def moe_route_backward(logits, route: Route, grad_weights=None, grad_balance=Non
     with _on(logits.device):
         dl = out if out is not None else torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
         check(fp8_moe_route_backward(logits.data_ptr(), _dtype_code(logits), tokens, experts, _ld(logits), top_k,
-                                     route.renormalize, route.ids.data_ptr(), route.weights.data_ptr(),
+                                     bool(route.renormalize), route.ids.data_ptr(), route.weights.data_ptr(),
                                      route.counts.data_ptr(), _ptr(grad_weights), _ptr(grad_balance), dl.data_ptr(), _ld(dl),
                                      _stream()))
     return dl
@@ -1072,7 +1076,7 @@ def dropout(x, rate: float, seed, residual=None, out=None):
     captured graph reads it anew at each replay); the backward pass is
     dropout(dy, rate, seed).  out may be x or residual."""
     rate = float(rate)
-    if out is None:
+    if out is None and 0.0 <= rate <= 1.0:
         y = _ext().dropout(x, rate, seed, residual)
         if y is not None:
             if type(y) is int:

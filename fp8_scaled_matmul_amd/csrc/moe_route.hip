@@ -294,8 +294,11 @@ __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
 #pragma unroll
             for (int i = 0; i < V; ++i) key[i] = choose(won, i + 1 < V ? key[(i + 1) % V] : K::none(), key[i]);
         }
-        on = on && !(mx == -__builtin_inff());
-        // exp(l - max): of all for the sum, of the chosen for the weights
+        // exp(l - max): of all for the sum, of the chosen for the weights.  Over 0
+        // where the first choice is -Inf: 0 then says that the row has nothing else,
+        // NaN that it has NaN.
+        const bool low = mx == -__builtin_inff();
+        mx = low ? 0.0f : mx;
         float total = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -303,6 +306,7 @@ __global__ void __launch_bounds__(64 * kWaves) k_route(RouteKArgs a)
             total += l[i];
         }
         total = reduce<L>(total, add);
+        on = on && !(low && total == 0.0f);
         const float chosen = sub < a.top_k ? __builtin_amdgcn_exp2f((K::value(mine) - mx) * kLog2e) : 0.0f;
         const float below = a.renormalize ? reduce<L>(chosen, add) : total;
         if (on) {

@@ -422,7 +422,9 @@ fp8_status fp8_mx4_moe(const void* x_bf16, int64_t tokens, int64_t hidden, int64
  *   dx = dl w,  dw = dl^T x                  bf16, fp32 sums in an order that the sizes set
  * for a piece of the vocabulary at a time.  Tokens with targets outside 0 ..
  * vocab - 1 add nothing, whatever their x and grad_loss hold; their dx is 0.
- * lse is the forward's.  dx or dw may be NULL.  tokens 0 writes zeros to dw.
+ * A finite dl below 2^-126 of the largest |grad_loss| counts as 0.  lse is the
+ * forward's.  dx or dw may be NULL; they do not overlap x or w.  tokens 0 writes
+ * zeros to dw.  softcap: 0, or from 1e-30 to 1e30.
  * Any sizes and alignment of elements; operands whose rows do not all lie at
  * multiples of 16 bytes (or have a hidden that is no multiple of 8) are copied
  * first.  tokens, vocab below 2^24, leading dimensions below 2^21.
@@ -448,9 +450,9 @@ fp8_status fp8_linear_ce_backward(const void* x_bf16, int64_t ldx, const void* w
  *   balance  experts sum_e f_e P_e with f_e = counts[e] / (n top_k), P_e the mean
  *            over the tokens of the softmax of l over all experts
  * as fp8_mx4_moe chooses them, in 32 bits.  mask (may be NULL): a byte a token, 0 leaves the
- * token out; so does a row of -Inf alone.  Tokens left out have ids -1 and
- * weights 0, and n counts the others (balance is 0 where there are none).  The
- * sum of a token with a NaN or +Inf is NaN.
+ * token out; so does a row of -Inf alone (not one that holds NaN as well).
+ * Tokens left out have ids -1 and weights 0, and n counts the others (balance is 0
+ * where there are none).  The sum of a token with a NaN or +Inf is NaN.
  * Backward, from the gradients of weights (fp32 [tokens, top_k], may be NULL) and of
  * balance (one fp32 on the device, may be NULL): dlogits in the logits' type.
  * The choice, and so f, has no gradient.  ids, weights and counts are the forward's.

@@ -300,3 +300,15 @@ def test_on_a_side_stream():
         got = run(x, w, t, g)
     side.synchronize()
     assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_an_infinite_gradient_is_loud_in_its_token():
+    x, w, t, g = make(70, 300, 64, seed=4, ignored=0.0)
+    for bad in (float("inf"), float("nan")):
+        g2 = g.clone()
+        g2[9] = bad
+        got = run(x.cuda(), w.cuda(), t.cuda(), g2.cuda())
+        want = expect(x, w, t, g, 0.0)
+        assert not torch.isfinite(got["dx"][9]).any()
+        on = np.arange(70) != 9
+        check(got["dx"][torch.from_numpy(on).cuda()], {"dx": (want["dx"][0][on], want["dx"][1][on])}, "dx")

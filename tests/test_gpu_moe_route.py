@@ -191,3 +191,17 @@ def test_captured_and_replayed_and_on_a_side_stream():
             torch.cuda.synchronize()
             for a, b in zip((r.ids, r.weights, r.counts, r.balance, d), want):
                 assert torch.equal(a, b), rep
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_nan_among_nothing_but_minus_infinity_is_loud(dtype, renormalize):
+    l, _ = make(5, 40, dtype, seed=3)
+    l[2] = -float("inf")
+    l[2, 7] = float("nan")
+    l[3] = -float("inf")
+    r = fm.moe_route(l.cuda(), 4, renormalize)
+    assert r.ids[2].tolist() == [0, 1, 2, 3] and torch.isnan(r.weights[2]).all() and torch.isnan(r.balance)
+    assert r.ids[3].tolist() == [-1] * 4
+    dl = fm.moe_route_backward(l.cuda(), r, torch.ones_like(r.weights))
+    assert torch.isnan(dl[2]).any() and torch.isfinite(dl[[0, 1, 3, 4]]).all()

@@ -89,3 +89,67 @@ def test_two_captured_steps_replayed_in_turn():
             torch.cuda.synchronize()
             for a, b in zip(out, want):
                 assert torch.equal(a, b), rep
+
+
+def test_the_short_way_and_the_checked_way_agree(monkeypatch):
+    """Calls that are in order go through the extension module, the others through
+    ctypes: the same kernels on the same arguments."""
+    args = inputs(70, 128, 16, 600)
+    seed = torch.tensor([5], device="cuda")
+    grad = torch.randn(70, generator=torch.Generator().manual_seed(1)).cuda()
+    short = step(*args, seed, grad)
+    monkeypatch.setattr(fm, "_ext_module", fm._NoExt())
+    for a, b in zip(short, step(*args, seed, grad)):
+        assert torch.equal(a, b)
+
+
+def test_two_threads_on_two_streams():
+    import threading
+    cases = [(inputs(n, 256, 16, 1000), torch.tensor([n], device="cuda"), torch.full((n,), 1 / n, device="cuda"))
+             for n in (33, 300)]
+    want = [[v.clone() for v in step(*a, s, g)] for a, s, g in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        a, s, g = cases[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(10):
+                got[i].append(step(*a, s, g))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 10
+        for out in got[i]:
+            for a, b in zip(out, want[i]):
+                assert torch.equal(a, b)
+
+
+def test_refusals_are_the_same_on_the_device():
+    h, res, router, w, t = inputs(8, 64, 8, 100)
+    f = torch.zeros(8, device="cuda")
+    seed = torch.tensor([5], device="cuda")
+    r = fm.moe_route(h, 2)
+    for call in (
+        lambda: fm.dropout(h, 1.5, seed),
+        lambda: fm.dropout(h, float("nan"), seed),
+        lambda: fm.dropout(h, 0.1, seed, residual=res[:, :32]),
+        lambda: fm.linear_cross_entropy(h, w, t, softcap=1e-50),
+        lambda: fm.linear_cross_entropy_backward(h, w, t, f, f, softcap=1e-50),
+        lambda: fm.linear_cross_entropy(h, w, t[:7]),
+        lambda: fm.linear_cross_entropy(h, w, t.cpu()),
+        lambda: fm.linear_cross_entropy_backward(h, w, t, f[:7], f),
+        lambda: fm.moe_route(h, 65),
+        lambda: fm.moe_route(h, 2, mask=torch.ones(7, dtype=torch.bool, device="cuda")),
+        lambda: fm.moe_route_backward(h[:4], r),
+    ):
+        with pytest.raises(ValueError):
+            call()
+    # what any true value says
+    a = fm.moe_route_backward(h, fm.Route(r.ids, r.weights, r.counts, r.balance, 1), torch.ones_like(r.weights))
+    assert torch.equal(a, fm.moe_route_backward(h, r, torch.ones_like(r.weights)))

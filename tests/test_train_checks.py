@@ -179,3 +179,11 @@ def test_binding_refuses_what_is_wrong_with_a_dropout():
     ):
         with pytest.raises(ValueError):
             call()
+
+
+def test_caps_that_are_no_caps():
+    """Too small for its square in fp32, or for fp32 at all."""
+    assert fm.fp8_linear_ce(BAD, 64, BAD, 64, 32, 100, 64, BAD, 1e-31, BAD, BAD, BAD, 1 << 40, None) == INVALID
+    for cap in (1e-31, 1e-50):
+        with pytest.raises(ValueError, match="softcap"):
+            fm.linear_cross_entropy(bf(4, 16), bf(30, 16), torch.zeros(4, dtype=torch.int64), softcap=cap)
