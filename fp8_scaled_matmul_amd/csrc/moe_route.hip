@@ -3,6 +3,11 @@
 // and the balance loss
 //   E sum_e f_e P_e,  f_e = counts_e / (N top_k),  P_e = mean softmax(l)_e,
 // N the tokens that count; and the logits' gradient.
+//
+// Bound by arithmetic: the selection sorts each lane's keys and takes top_k times
+// the largest of the lanes' first ones.  65536 x 128 bf16, top 8: forward 16 us and 5
+// for the sums (4.0 us of traffic), backward 14.5 (7.7 us of traffic).  One token: 3.4,
+// 4.6 and 3.6 us, launches and a trip or two to memory.
 #include <algorithm>
 #include <type_traits>
 
@@ -15,8 +20,10 @@ namespace fp8mi {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kWaves = 16, kParts = 256;    // waves of a workgroup; workgroups at most
-constexpr int kBackwardBlocks = 1;          // the backward's workgroups a CU at most
+// Waves of a workgroup, and workgroups at most: each brings a part of the sums
+// (512 parts: 24.1 us against 20.9 for 65536 x 128).
+constexpr int kWaves = 16, kParts = 256;
+constexpr int kBackwardBlocks = 1;          // the backward's workgroups a CU at most (2: 16.3 us against 14.5)
 
 struct RouteKArgs {
     const void* logits;
@@ -42,8 +49,9 @@ struct RouteKArgs {
 
 // A token is handled by L = 16, 32 or 64 lanes with V experts each, V sub .. V
 // sub + V - 1: up to 128 experts by 16 lanes, so that a wave has 4 tokens at
-// work.  Reductions over a token's lanes are rotations inside 16 (DPP) and, for
-// more, exchanges of groups.
+// work (65536 x 128 bf16, forward and backward: 20.9 and 14.5 us; 32 lanes of 4
+// experts 28.8 and 19.1, 64 lanes of 2 41.3 and 23.9).  Reductions over a token's lanes
+// are rotations inside 16 (DPP) and, for more, exchanges of groups.
 template <int N>
 __device__ inline uint32_t rotated(uint32_t v)
 {
