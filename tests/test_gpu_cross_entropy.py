@@ -312,3 +312,27 @@ def test_an_infinite_gradient_is_loud_in_its_token():
         assert not torch.isfinite(got["dx"][9]).any()
         on = np.arange(70) != 9
         check(got["dx"][torch.from_numpy(on).cuda()], {"dx": (want["dx"][0][on], want["dx"][1][on])}, "dx")
+
+
+@pytest.mark.parametrize("tokens,vocab,hidden", [(1, 257, 8), (5, 4100, 33), (70, 2059, 40), (257, 65700, 72), (300, 2049, 1000)])
+def test_what_the_workspace_holds_does_not_matter(tokens, vocab, hidden):
+    """Full of NaN, and no larger than asked for: nothing behind it is written."""
+    x, w, t, g = [v.cuda() for v in make(tokens, vocab, hidden, seed=vocab)]
+    want = run(x, w, t, g)
+    size = fm.lib().fp8_linear_ce_workspace_size
+    got = {}
+    for back in (0, 1):
+        need = size(tokens, vocab, hidden, back)
+        room = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+        if back:
+            got["dx"], got["dw"] = fm.linear_cross_entropy_backward(x, w, t, got["lse"], g, workspace=room[:need])
+        else:
+            got["loss"], got["lse"] = fm.linear_cross_entropy(x, w, t, workspace=room[:need])
+        assert (room[need:] == 0xFF).all()
+        with pytest.raises(ValueError, match="workspace"):
+            if back:
+                fm.linear_cross_entropy_backward(x, w, t, got["lse"], g, workspace=room[:need - 1])
+            else:
+                fm.linear_cross_entropy(x, w, t, workspace=room[:need - 1])
+    for name in want:
+        assert torch.equal(got[name], want[name]), name

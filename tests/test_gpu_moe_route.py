@@ -205,3 +205,15 @@ def test_nan_among_nothing_but_minus_infinity_is_loud(dtype, renormalize):
     assert r.ids[3].tolist() == [-1] * 4
     dl = fm.moe_route_backward(l.cuda(), r, torch.ones_like(r.weights))
     assert torch.isnan(dl[2]).any() and torch.isfinite(dl[[0, 1, 3, 4]]).all()
+
+
+@pytest.mark.parametrize("tokens,experts,top_k", [(1, 1, 1), (70, 37, 3), (5000, 512, 16), (9000, 128, 8)])
+def test_what_the_workspace_holds_does_not_matter(tokens, experts, top_k):
+    l, _ = make(tokens, experts, "bf16", seed=experts)
+    l = l.cuda()
+    need = fm.lib().fp8_moe_route_workspace_size(tokens, experts)
+    room = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    a, b = fm.moe_route(l, top_k, workspace=room[:need]), fm.moe_route(l, top_k)
+    assert (room[need:] == 0xFF).all()
+    for name in ("ids", "weights", "counts", "balance"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
