@@ -402,18 +402,34 @@ hipError_t launch_tile(GemmShape s, Init init, hipStream_t stream)
 int token_tile(int64_t tokens) { return tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
 
 template <bool ATR, template <int, int, int> class Epi, typename Init>
-hipError_t launch_tokens(const GemmShape& s, Init init, hipStream_t stream)
+hipError_t launch_tokens(int tile, const GemmShape& s, Init init, hipStream_t stream)
 {
-    switch (token_tile(s.n)) {
+    switch (tile) {
     case 32: return launch_tile<ATR, false, 4, 1, 2, 2, Epi>(s, init, stream);
     case 64: return launch_tile<ATR, false, 4, 1, 2, 4, Epi>(s, init, stream);
     case 128: return launch_tile<ATR, false, 4, 2, 4, 4, Epi>(s, init, stream);
     default: return launch_tile<ATR, false, 2, 4, 8, 4, Epi>(s, init, stream);
     }
 }
-// Rows of its tile, and the vocabulary rows of a block of statistics (a wave's).
-int row_tile(int64_t tokens) { return token_tile(tokens) <= 64 ? 128 : 256; }
-int stat_rows(int64_t tokens) { return token_tile(tokens) <= 64 ? 32 : token_tile(tokens) <= 128 ? 64 : 128; }
+// Rows of such a tile, and the vocabulary rows of a block of statistics (a wave's).
+int row_tile(int tile) { return tile <= 64 ? 128 : 256; }
+int stat_rows(int tile) { return tile <= 64 ? 32 : tile <= 128 ? 64 : 128; }
+
+// The tile of the logits of `rows` of the vocabulary: where that leaves CUs without
+// one, the next smaller one, 128 tokens (of 256 rows) if there is one a CU at most,
+// 64 (of 128 rows) if there are three for two CUs.  Hidden 1856, forward and
+// backward to dx: 100 x 8600 37 and 46 us against 40 and 59, 250 x 8600 35 and 61
+// against 54 and 89, 500 x 8600 41 and 78 against 55 and 98, 1000 x 2000 39 and 54
+// against 54 and 92.  One step too far: 1000 x 8600 71 and 123 against 59 and 120,
+// 500 x 8600 54 and 88.
+int logit_tile(int64_t rows, int64_t tokens)
+{
+    const int64_t cus = gemm_num_cus();
+    int tile = token_tile(tokens);
+    if (tile == 256 && (int64_t)tiles_of(rows, 256) * tiles_of(tokens, 128) <= cus) tile = 128;
+    if (tile == 128 && (int64_t)tiles_of(rows, 128) * tiles_of(tokens, 64) <= cus + cus / 2) tile = 64;
+    return tile;
+}
 
 // Tiles of 256 x 256 come in rounds of one a CU.  Where the last round would be a
 // small part of one, the rows behind the whole rounds go in tiles of 128 x 128
@@ -432,7 +448,8 @@ constexpr int kTailRows = 128, kTailStatRows = 64;
 // Blocks of statistics of `rows` of the vocabulary.
 int64_t stat_blocks(int64_t rows, int64_t tokens)
 {
-    if (token_tile(tokens) < 256) return (int64_t)tiles_of(rows, row_tile(tokens)) * (row_tile(tokens) / stat_rows(tokens));
+    const int tile = logit_tile(rows, tokens);
+    if (tile < 256) return (int64_t)tiles_of(rows, row_tile(tile)) * (row_tile(tile) / stat_rows(tile));
     const int64_t big = whole_rounds(rows, tokens);
     return (int64_t)tiles_of(big, 256) * 2 + (int64_t)tiles_of(rows - big, kTailRows) * (kTailRows / kTailStatRows);
 }
@@ -696,7 +713,7 @@ Layout backward_layout(int64_t tokens, int64_t vocab, int64_t hidden)
     // too few tiles of dx for the chip: its K, the vocabulary, is split.  Unsplit
     // 64 x 50304 x 1024 takes 407 us against 57, 2048 tokens 1290 against 473.
     const int tile = token_tile(tokens);
-    const int64_t tiles = (int64_t)tiles_of(hidden, row_tile(tokens)) * tiles_of(tokens, tile);
+    const int64_t tiles = (int64_t)tiles_of(hidden, row_tile(tile)) * tiles_of(tokens, tile);
     const int64_t want = (int64_t)gemm_num_cus() * (tile <= 64 ? 2 : 1);
     l.splits = std::max<int64_t>(std::min<int64_t>(want / tiles, std::min(l.piece, vocab) / 512), 1);
     size_t at = 0;
@@ -748,7 +765,8 @@ hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
                 if ((e = pack(w, g.ldw, m, g.hidden, ws + l.w, nullptr, stream)) != hipSuccess) return e;
                 s.a = {ws + l.w, up(g.hidden, 8) * 2};
             }
-            const int64_t big = token_tile(n) == 256 ? whole_rounds(m, n) : m;
+            const int tile = logit_tile(m, n);
+            const int64_t big = tile == 256 ? whole_rounds(m, n) : m;
             const auto rows = [&](int64_t from, int64_t count, int block) {
                 return [=, &g](auto& epi) {
                     epi.m = (int)count;
@@ -763,7 +781,7 @@ hipError_t launch_ce_forward(const CeArgs& g, hipStream_t stream)
                 };
             };
             s.m = (int)big;
-            if ((e = launch_tokens<false, StatsEpilogue>(s, rows(0, big, blocks), stream)) != hipSuccess) return e;
+            if ((e = launch_tokens<false, StatsEpilogue>(tile, s, rows(0, big, blocks), stream)) != hipSuccess) return e;
             if (big < m) {
                 s.a.p += big * s.a.ld;
                 s.m = (int)(m - big);
@@ -824,7 +842,8 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
         s.n = T;
         s.k = H;
         s.splits = 1;
-        const int64_t big = token_tile(T) == 256 ? whole_rounds(m, T) : m;
+        const int tile = logit_tile(m, T);
+        const int64_t big = tile == 256 ? whole_rounds(m, T) : m;
         const auto rows = [&](int64_t from, int64_t count) {
             return [=, &g](auto& epi) {
                 epi.m = (int)count;
@@ -838,7 +857,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
             };
         };
         s.m = (int)big;
-        if ((e = launch_tokens<false, GradEpilogue>(s, rows(0, big), stream)) != hipSuccess) return e;
+        if ((e = launch_tokens<false, GradEpilogue>(tile, s, rows(0, big), stream)) != hipSuccess) return e;
         if (big < m) {
             s.a.p += big * s.a.ld;
             s.m = (int)(m - big);
@@ -853,7 +872,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
             s.k = (int)m;
             s.splits = (int)std::min<int64_t>(l.splits, (m + ce::kStageK - 1) / ce::kStageK);
             if (l.splits == 1 && l.pieces == 1)
-                e = launch_tokens<true, NearEpilogue>(s, [&](auto& epi) {
+                e = launch_tokens<true, NearEpilogue>(token_tile(T), s, [&](auto& epi) {
                     epi.m = H;
                     epi.n = T;
                     epi.out = static_cast<uint16_t*>(g.dx);
@@ -862,7 +881,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
                     epi.scale = scale;
                 }, stream);
             else
-                e = launch_tokens<true, PlanesEpilogue>(s, [&](auto& epi) {
+                e = launch_tokens<true, PlanesEpilogue>(token_tile(T), s, [&](auto& epi) {
                     epi.m = H;
                     epi.n = T;
                     epi.plane = planes;

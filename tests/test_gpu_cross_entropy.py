@@ -336,3 +336,15 @@ def test_what_the_workspace_holds_does_not_matter(tokens, vocab, hidden):
                 fm.linear_cross_entropy(x, w, t, workspace=room[:need - 1])
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+@pytest.mark.parametrize("tokens,vocab,hidden", [(20, 30001, 24), (50, 30003, 40), (100, 25002, 72), (300, 13001, 40), (600, 20005, 33)])
+def test_each_tile_of_the_logits(tokens, vocab, hidden, softcap):
+    """Enough vocabulary for each tile: 128 x 32, 128 x 64, 256 x 128 (of up to 128
+    tokens and of more), 256 x 256."""
+    x, w, t, g = make(tokens, vocab, hidden, seed=tokens)
+    want = expect(x, w, t, g, softcap)
+    got = run(x.cuda(), w.cuda(), t.cuda(), g.cuda(), softcap)
+    for name in got:
+        check(got[name], want, name)
