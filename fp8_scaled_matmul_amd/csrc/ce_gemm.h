@@ -37,6 +37,25 @@ typedef __attribute__((address_space(3))) v4s lds_v4s;
 constexpr int kStageK = 32;             // K of a stage: 64 bytes of a K-contiguous row
 constexpr int kRing = 4;                // stages in LDS
 
+// Notes (what an epilogue wants of its tile's columns) come when an item is
+// described, at the end of the stage whose fill, kRing ahead, was the last of the
+// item before; they are read in the item's epilogue.  Items described whose
+// epilogue is still to come, with `stages` each:
+constexpr int notes_held(int stages)
+{
+    int most = 0;
+    for (int s = 0; s < 2 * kRing * stages; ++s) {
+        const int filled = s + kRing;       // at the end of stage s
+        const int described = filled / stages + (filled % stages == stages - 1);
+        most = most > described - s / stages + 1 ? most : described - s / stages + 1;
+    }
+    return most;
+}
+// One stage an item would need two slots more, and 64 tokens' tiles a workgroup of
+// three a CU less: where K has one, a second of zeros follows.
+constexpr int kNoteSlots = kRing, kNoteStages = 2;
+static_assert(notes_held(kNoteStages) <= kNoteSlots && notes_held(kNoteStages + 1) <= kNoteSlots, "a slot an item");
+
 struct Operand {
     const uint8_t* p;
     int64_t ld;                         // bytes between rows
@@ -47,6 +66,7 @@ struct GemmShape {
     int m, n, k;                        // a row of a K-contiguous operand holds zeros from k to the next multiple of 8
     int tiles_m, tiles_n, group_m;
     int splits;                         // of K
+    int least_stages;                   // of an item: kNoteStages where it has notes, else 1
 };
 
 // One unit of work: a tile and its range of stages.
@@ -76,7 +96,7 @@ __device__ inline Item item_of(const GemmShape& s, int id)
     it.tm = first_m + r % gsize;
     it.tn = r / gsize;
     // the first (stages % splits) splits are one stage longer
-    const int stages = (s.k + kStageK - 1) / kStageK;
+    const int stages = max((s.k + kStageK - 1) / kStageK, s.least_stages);
     const int each = stages / s.splits, more = stages - each * s.splits;
     it.first = __builtin_amdgcn_readfirstlane(each * it.split + min(it.split, more));
     it.end = it.first + __builtin_amdgcn_readfirstlane(each + (it.split < more));
@@ -104,13 +124,12 @@ template <bool ATR, bool BTR, int WR, int WC, int MF, int NF>
 struct Tile {
     static constexpr int W = WR * WC, TM = 16 * MF * WR, TN = 16 * NF * WC;
     static constexpr int kStage = (TM + TN) * 64;
-    // what an epilogue wants of its tile's columns: 16 bytes each, in runs of 64
-    // columns of a wave, of the items whose stages are on their way and the one at work
+    // notes: 16 bytes a column, in runs of 64 columns of a wave
     static constexpr int kRuns = (NF + 3) / 4, kNotes = 1024 * kRuns * WC;
     template <typename Epi>
     static constexpr int lds_bytes()
     {
-        return kRing * kStage + (Epi::kNotes ? (kRing + 1) * kNotes : 0);
+        return kRing * kStage + (Epi::kNotes ? kNoteSlots * kNotes : 0);
     }
     // DMA instructions of a wave and stage; where an operand has fewer than
     // waves, some repeat another's (the same bytes to the same place)
@@ -189,7 +208,7 @@ struct Tile {
                     for (int h = 0; h < kRuns; ++h)
                         epi.note(base + kRing * kStage + fnote * kNotes + 1024 * (kRuns * wave + h), n0 + 16 * NF * wave + 64 * h);
                 }
-                fnote = fnote == kRing ? 0 : fnote + 1;
+                fnote = (fnote + 1) % kNoteSlots;
             }
         };
         describe();
@@ -332,7 +351,7 @@ struct Tile {
             }
             const uint8_t* notes = lds + kRing * kStage + note * kNotes + 1024 * kRuns * (wave / WR);
             stored = epi(it, acc, it.tm * TM + wm + 4 * quarter, it.tn * TN + wn + c, notes) ? 0 : 3;
-            note = note == kRing ? 0 : note + 1;
+            note = (note + 1) % kNoteSlots;
             clear();
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // the fills past the end

@@ -382,6 +382,7 @@ hipError_t launch_tile(GemmShape s, Init init, hipStream_t stream)
     s.tiles_m = tiles_of(s.m, T::TM);
     s.tiles_n = tiles_of(s.n, T::TN);
     s.group_m = 4;
+    s.least_stages = E::kNotes ? ce::kNoteStages : 1;
     E epi;
     init(epi);
     const auto kernel = k_ce_gemm<ATR, BTR, WR, WC, MF, NF, Epi>;

@@ -1,0 +1,87 @@
+"""The vocabulary loss with many tiles for each workgroup, against its definition
+in float64 on the GPU."""
+import pytest
+import torch
+
+import fp8_scaled_matmul_amd as fm
+
+pytestmark = pytest.mark.gpu
+
+U32, UBF = 2.0 ** -24, 2.0 ** -8        # half a step of fp32 and bf16, relative
+TINY = 2.0 ** -126                      # smaller numbers count as 0
+
+
+def make(tokens, vocab, hidden, seed, ignored=0.1):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(tokens, hidden, generator=gen, device="cuda").bfloat16()
+    w = (torch.randn(vocab, hidden, generator=gen, device="cuda") * 2 * hidden ** -0.5).bfloat16()
+    t = torch.randint(0, vocab, (tokens,), generator=gen, device="cuda")
+    t[torch.rand(tokens, generator=gen, device="cuda") < ignored] = -100
+    return x, w, t, torch.randn(tokens, generator=gen, device="cuda")
+
+
+def run(x, w, t, g, softcap):
+    loss, lse = fm.linear_cross_entropy(x, w, t, softcap=softcap)
+    dx, dw = fm.linear_cross_entropy_backward(x, w, t, lse, g, softcap=softcap)
+    return dict(loss=loss, lse=lse, dx=dx, dw=dw)
+
+
+def expect(x, w, t, g, softcap):
+    """Reference and bound of every output.
+
+    A logit is a sum of `hidden` exact products in fp32: off by (hidden + 1) U32
+    sum |x w| at most; the cap adds 8 U32 softcap.  lse: the largest logit error,
+    each exponent's rounding, vocab / 64 + 90 additions, the logarithm.  dl: the
+    errors of z and lse relative to p, the slope's, bf16's rounding.  dx and dw: dl's
+    errors through the other operand, fp32 additions of `vocab` and `tokens` terms,
+    bf16's rounding."""
+    X, W, G = x.double(), w.double(), g.double()
+    on = (t >= 0) & (t < len(w))
+    at = torch.where(on, t, 0)[:, None]
+    z = X @ W.t()
+    e_z = (X.shape[1] + 1) * U32 * (X.abs() @ W.abs().t()) + 8 * U32 * softcap
+    slope = None
+    if softcap:
+        th = torch.tanh(z / softcap)
+        z, slope = softcap * th, 1 - th * th
+    lse = torch.logsumexp(z, 1)
+    loss = torch.where(on, lse - z.gather(1, at)[:, 0], 0.0)
+    e_lse = e_z.amax(1) + U32 * (len(w) / 64 + 94 + 2 * z.abs().amax(1) + 2 * lse.abs())
+    e_loss = torch.where(on, e_lse + e_z.gather(1, at)[:, 0] + U32 * loss.abs(), 0.0)
+    p = torch.exp(z - lse[:, None])
+    G = torch.where(on, G, 0.0)[:, None]
+    full = p.scatter_add(1, at, -on.double()[:, None]) * G          # without the slope
+    d = full if slope is None else full * slope
+    e_d = p * G.abs() * (e_z + e_lse[:, None] + U32 * (2 * z.abs() + 2 * lse.abs()[:, None] + 4))
+    e_d += d.abs() * (UBF + 4 * U32) + 2 * TINY * G.abs().amax()
+    if slope is not None:
+        e_d += full.abs() * (2 * z.abs() * e_z / softcap ** 2 + 4 * U32)
+    e_d *= on[:, None]
+    del p, full, slope, z, e_z
+    X = torch.where(on[:, None], X, 0.0)
+    dx, dw = d @ W, d.t() @ X
+    a = d.abs()
+    e_dx = (e_d + (len(w) + 2) * U32 * a) @ W.abs() + UBF * dx.abs() + TINY
+    e_dw = (e_d + (len(x) + 2) * U32 * a).t() @ X.abs() + UBF * dw.abs() + TINY
+    return dict(loss=(loss, e_loss), lse=(lse, e_lse), dx=(dx, e_dx), dw=(dw, e_dw))
+
+
+def check(got, want):
+    for name, (ref, bound) in want.items():
+        excess = ((got[name].double() - ref).abs() - bound).amax().item()
+        assert excess <= 0, f"{name}: {excess} over the bound"
+
+
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+@pytest.mark.parametrize("tokens,vocab,hidden", [(8192, 16384, 32), (8192, 16384, 31), (8190, 16400, 8), (1300, 100003, 16),
+                                                 (4100, 30001, 33), (4100, 30001, 1)])
+def test_one_and_two_stages_of_k_and_many_tiles(tokens, vocab, hidden, softcap):
+    """Widths of one stage of K (and of two) with 7 to 9 tiles of 256 x 256 a
+    workgroup, of changing tokens: each tile's epilogue has its own tokens' targets,
+    sums and gradients."""
+    args = make(tokens, vocab, hidden, seed=hidden)
+    want = expect(*args, softcap)
+    got = run(*args, softcap)
+    check(got, want)
+    again = run(*args, softcap)
+    assert all(torch.equal(got[k], again[k]) for k in got)
