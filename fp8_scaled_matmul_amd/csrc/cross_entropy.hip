@@ -223,6 +223,13 @@ struct GradEpilogue {
         for (int j = 0; j < NF; ++j) {
             const TokenNote k = reinterpret_cast<const TokenNote*>(notes)[16 * j + (lane & 15)];
             const int at = k.target < 0 ? -1 : k.target - v0 - row;
+            // of tokens that do not count: an infinite w times their zeros is NaN
+            if (__any(k.target < 0)) {
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[j][i][r] = k.target < 0 ? 0.0f : acc[j][i][r];
+            }
             if (cap != 0.0f) softcap_column<MF>(acc[j], cap, inv_cap);
             const bool target_here = __any((uint32_t)at < 16u * MF);
 #pragma unroll
@@ -265,8 +272,10 @@ struct GradEpilogue {
     }
 };
 
-// A gradient in bf16.
-template <int MF, int NF, bool FAR>
+// A gradient in bf16.  TOKENS: dx, whose rows of tokens that do not count are zeros
+// also where w is infinite (0 times that is NaN); by a mask on the packed words, a
+// lane's being of one token (a choice of sums spilled).
+template <int MF, int NF, bool FAR, bool TOKENS>
 struct Bf16Out {
     static constexpr int kStores = MF / 2 * NF;
     static constexpr bool kNotes = false;
@@ -275,6 +284,7 @@ struct Bf16Out {
     int64_t ld;
     int wide;                   // 16-byte stores are in place
     const float* scale;
+    const TokenNote* tokens;
 
     __device__ void note(uint32_t, int) const {}
 
@@ -288,6 +298,10 @@ struct Bf16Out {
         for (int j = 0; j < NF; ++j)
 #pragma unroll
             for (int i = 0; i < MF; ++i) acc[j][i] *= by;
+        uint32_t keep[NF];
+#pragma unroll
+        for (int j = 0; j < NF; ++j)
+            keep[j] = !TOKENS || (col + 16 * j < n && tokens[col + 16 * j].target >= 0) ? ~0u : 0u;
         if (wide) {
             const __amdgpu_buffer_rsrc_t ro =
                 gemm::make_store_rsrc(out + n0 * ld, rows ? (uint32_t)(((rows - 1) * ld + m) * 2) : 0u);
@@ -298,7 +312,7 @@ struct Bf16Out {
 #pragma unroll
                 for (int i = 0; i < MF; i += 2)
                     __builtin_amdgcn_raw_buffer_store_b128(
-                        to_bf16_chunk(acc[j][i], acc[j][i + 1]), ro,
+                        to_bf16_chunk(acc[j][i], acc[j][i + 1]) & keep[j], ro,
                         (int)(first + 16 * i < m ? to + (uint32_t)(16 * j * ld + 16 * i) * 2u : gemm::kOutOfRange), 0,
                         FAR ? 18 : 0);              // sc1 nt
             return true;
@@ -312,7 +326,7 @@ struct Bf16Out {
                 uint16_t* to = out + t * ld + row + 16 * i;
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    if (row + 16 * i + r < m) to[r] = gemm::to_bf16(acc[j][i][r]);
+                    if (row + 16 * i + r < m) to[r] = gemm::to_bf16(acc[j][i][r]) & keep[j];
             }
         }
         return false;
@@ -320,9 +334,11 @@ struct Bf16Out {
 };
 
 template <int WR, int MF, int NF>
-struct NearEpilogue : Bf16Out<MF, NF, false> {};
+struct NearEpilogue : Bf16Out<MF, NF, false, false> {};
 template <int WR, int MF, int NF>
-struct FarEpilogue : Bf16Out<MF, NF, true> {};
+struct FarEpilogue : Bf16Out<MF, NF, true, false> {};
+template <int WR, int MF, int NF>
+struct TokensEpilogue : Bf16Out<MF, NF, false, true> {};
 
 // A gradient in parts: fp32 planes, one for each split of K, added to what an
 // earlier piece of the vocabulary left.
@@ -593,7 +609,8 @@ __global__ void __launch_bounds__(256) k_ce_loss(const float2* part, int blocks,
 // or more: 64 x 50304 x 1024, backward to dx 56.6 us against 60.4 with one.
 template <int S>
 __global__ void __launch_bounds__(256) k_ce_reduce(const float* plane, int splits, int64_t rows, int cols, int64_t ld_plane,
-                                                   uint16_t* out, int64_t ld, int wide, const float* scale)
+                                                   uint16_t* out, int64_t ld, int wide, const float* scale,
+                                                   const TokenNote* tokens)
 {
     __shared__ v4f sh[S > 1 ? 512 : 1];
     const float by = *scale;
@@ -628,8 +645,9 @@ __global__ void __launch_bounds__(256) k_ce_reduce(const float* plane, int split
             __syncthreads();
         }
         if (y != 0 || u >= total) continue;
-        a *= by;
-        b *= by;
+        const bool on = tokens[r].target >= 0;      // else the planes may hold NaN: zeros times an infinite w
+        a = on ? a * by : v4f{0, 0, 0, 0};
+        b = on ? b * by : v4f{0, 0, 0, 0};
         uint16_t* to = out + r * ld + c;
         if (wide && c + 8 <= cols) {
             *reinterpret_cast<v4u*>(to) = v4u{gemm::pack_bf16(a[0], a[1]), gemm::pack_bf16(a[2], a[3]),
@@ -873,13 +891,14 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
             s.k = (int)m;
             s.splits = (int)std::min<int64_t>(l.splits, (m + ce::kStageK - 1) / ce::kStageK);
             if (l.splits == 1 && l.pieces == 1)
-                e = launch_tokens<true, NearEpilogue>(token_tile(T), s, [&](auto& epi) {
+                e = launch_tokens<true, TokensEpilogue>(token_tile(T), s, [&](auto& epi) {
                     epi.m = H;
                     epi.n = T;
                     epi.out = static_cast<uint16_t*>(g.dx);
                     epi.ld = g.lddx;
                     epi.wide = aligned16(g.dx, g.lddx) && H % 8 == 0;
                     epi.scale = scale;
+                    epi.tokens = notes;
                 }, stream);
             else
                 e = launch_tokens<true, PlanesEpilogue>(token_tile(T), s, [&](auto& epi) {
@@ -897,7 +916,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
                     const int64_t groups = (g.tokens * ld / 8 + 256 / share - 1) / (256 / share);
                     hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(groups, 8 * gemm_num_cus())), dim3(256), 0, stream,
                                        planes, (int)l.splits, g.tokens, H, ld, static_cast<uint16_t*>(g.dx), g.lddx,
-                                       (int)aligned16(g.dx, g.lddx), scale);
+                                       (int)aligned16(g.dx, g.lddx), scale, notes);
                 };
                 l.splits >= 8 ? reduce(k_ce_reduce<16>, 16) : reduce(k_ce_reduce<1>, 1);
                 if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -917,6 +936,7 @@ hipError_t launch_ce_backward(const CeArgs& g, hipStream_t stream)
                     epi.ld = g.lddw;
                     epi.wide = aligned16(dw, g.lddw) && H % 8 == 0;
                     epi.scale = scale;
+                    epi.tokens = nullptr;
                 };
             };
             const int64_t big = whole_rounds(m, H);

@@ -421,7 +421,8 @@ fp8_status fp8_mx4_moe(const void* x_bf16, int64_t tokens, int64_t hidden, int64
  *   dl = grad_loss (exp(z - lse) - [v = target]) (1 - (z / softcap)^2), rounded to bf16
  *   dx = dl w,  dw = dl^T x                  bf16, fp32 sums in an order that the sizes set
  * for a piece of the vocabulary at a time.  Tokens with targets outside 0 ..
- * vocab - 1 add nothing, whatever their x and grad_loss hold; their dx is 0.
+ * vocab - 1 add nothing, whatever their x and grad_loss and whatever w holds; their
+ * dx is 0.  (For the others a dl of 0 times an infinite w is NaN, as in any product.)
  * A finite dl below 2^-126 of the largest |grad_loss| counts as 0.  lse is the
  * forward's.  dx or dw may be NULL; they do not overlap x or w.  tokens 0 writes
  * zeros to dw.  softcap: 0, or from 1e-30 to 1e30.

@@ -85,3 +85,35 @@ def test_one_and_two_stages_of_k_and_many_tiles(tokens, vocab, hidden, softcap):
     check(got, want)
     again = run(*args, softcap)
     assert all(torch.equal(got[k], again[k]) for k in got)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+@pytest.mark.parametrize("tokens,vocab,hidden", [(1, 300, 64), (20, 5000, 33), (70, 4101, 64), (120, 700, 40), (300, 600, 64),
+                                                 (600, 20005, 33), (2000, 9000, 40), (70001, 4501, 64)])
+def test_a_word_that_cannot_come_and_tokens_that_do_not_count(tokens, vocab, hidden, softcap):
+    """A vocabulary row of -Inf is as one of -2^20, whose exponentials are 0 as well:
+    tokens that do not count still add nothing to dw, and their dx is 0."""
+    x, w, t, g = make(tokens, vocab, hidden, seed=tokens)
+    x = x.abs() + 0.5
+    t = t.clamp(max=vocab - 2)          # the last one is the word
+    if tokens > 1:
+        t[::3] = -1
+        t[1::7] = vocab
+    on = (t >= 0) & (t < vocab)
+    got = {}
+    for name, value in (("finite", -2.0 ** 20), ("infinite", -float("inf"))):
+        w2, x2 = w.clone(), x.clone()
+        w2[-1] = value
+        x2[~on] = float("nan")
+        got[name] = run(x2, w2, t, g, softcap)
+    a, b = got["finite"], got["infinite"]
+    assert torch.equal(a["dw"], b["dw"]) and torch.isfinite(b["dw"]).all()
+    assert torch.equal(a["loss"][on], b["loss"][on]) and torch.equal(a["lse"][on], b["lse"][on])
+    assert (a["dx"][~on] == 0).all() and (b["dx"][~on] == 0).all()
+    if not softcap:                     # the word adds nothing
+        assert (b["dw"][-1] == 0).all()
+        if tokens * vocab < 1 << 25:
+            t2 = torch.where(on, t, -1)
+            want = expect(x, w[:-1], t2, g, softcap)
+            check({"dw": a["dw"][:-1]}, {"dw": want["dw"]})
+            check({"dx": a["dx"]}, {"dx": want["dx"]})
