@@ -117,3 +117,50 @@ def test_a_word_that_cannot_come_and_tokens_that_do_not_count(tokens, vocab, hid
             want = expect(x, w[:-1], t2, g, softcap)
             check({"dw": a["dw"][:-1]}, {"dw": want["dw"]})
             check({"dx": a["dx"]}, {"dx": want["dx"]})
+
+
+@pytest.mark.parametrize("softcap", [0.0, 3.0])
+@pytest.mark.parametrize("tokens,vocab,hidden", [(4096, 70000, 64), (4099, 66001, 33)])
+def test_pieces_of_the_vocabulary_with_split_sums(tokens, vocab, hidden, softcap):
+    """dx of two pieces of the vocabulary (512 MiB of dl each at most), each summed in
+    16 parts."""
+    args = make(tokens, vocab, hidden, seed=vocab)
+    got = run(*args, softcap)
+    check(got, expect(*args, softcap))
+
+
+def rounded(v):
+    return v.float().bfloat16().double()
+
+
+@pytest.mark.parametrize("kind", ["mean", "each"])
+@pytest.mark.parametrize("softcap", [0.0, 15.0])
+@pytest.mark.parametrize("tokens,vocab,hidden", [(50, 4100, 256), (700, 9000, 200), (3000, 5000, 256)])
+def test_gradients_lose_one_rounding_of_the_logits_gradient_and_one_of_their_own(tokens, vocab, hidden, softcap, kind):
+    """The norm of dx's and dw's error.  What the documentation gives away: dl over
+    the largest |gradient| is rounded to bf16, and so is the result.  Both are made
+    here in float64; their errors are independent, so their squares add up.  Of at
+    least 12800 entries the norms of either and of their sum are within 1 / sqrt(12800)
+    of that; logits in fp32 add some 1e-6.  5 %: one more rounding of either kind, or a
+    bit less in one, adds 15 % or more wherever that rounding counts."""
+    x, w, t, g = make(tokens, vocab, hidden, seed=tokens)
+    on = t >= 0
+    x += (3 * torch.rand(tokens, 1, device="cuda") * w[t.clamp(min=0)].float()).bfloat16()
+    if kind == "mean":
+        g = torch.full_like(g, 1.0) / on.sum()
+    X, W = torch.where(on[:, None], x.double(), 0.0), w.double()
+    z, slope = X @ W.t(), 1.0
+    if softcap:
+        th = torch.tanh(z / softcap)
+        z, slope = softcap * th, 1 - th * th
+    d = torch.softmax(z, 1)
+    d.scatter_add_(1, t.clamp(min=0)[:, None], -on.double()[:, None])
+    d *= torch.where(on, g.double(), 0.0)[:, None] * slope
+    by = torch.where(on, g.abs(), 0.0).amax().double()
+    off = rounded(d / by) * by - d
+    got = run(x, w, t, g, softcap)
+    for name, ref, via in (("dx", d @ W, off @ W), ("dw", d.t() @ X, off.t() @ X)):
+        own = rounded(ref) - ref
+        want = (own.norm() ** 2 + via.norm() ** 2).sqrt() / ref.norm()
+        err = (got[name].double() - ref).norm() / ref.norm()
+        assert err.item() <= 1.05 * want.item()
