@@ -955,7 +955,7 @@ def linear_cross_entropy_backward(x, w, targets, lse, grad_loss, softcap: float 
     """(dx, dw) bf16 of linear_cross_entropy's losses, None for what is not
     wanted.  lse is the forward's; grad_loss fp32 [tokens], the losses'
     gradients (an expanded scalar, too).  Tokens whose target lies outside the
-    vocabulary add nothing, whatever x and grad_loss hold there.  workspace:
+    vocabulary add nothing, whatever x and grad_loss hold there, or w.  workspace:
     optional uint8 device tensor of fp8_linear_ce_workspace_size(tokens, vocab,
     hidden, 1) bytes."""
     if out_x is None and out_w is None and workspace is None and _is_cap(softcap):

@@ -13,8 +13,10 @@
 // to 1.25 PFLOP/s), of a piece the logits' gradient 1.78 to 1.84 ms, dx and dw 1.77
 // to 1.85 each (1.19 to 1.24).  The matrix pipes are busy 63 to 66 % of the cycles at
 // the 1.5 to 1.8 GHz that power leaves (a library product of this shape: 1.12 to
-// 1.34 PFLOP/s, 80 to 85 % busy at a lower clock).  One token, 32768 x 2048: 22 us for
-// W's 134 MB (6.1 TB/s) and 4 us for the sum over the blocks.
+// 1.34 PFLOP/s, 80 to 85 % busy at a lower clock).  One token, 32768 x 2048: 33 us for
+// W's 134 MB from HBM (4.0 TB/s; 20 to 22 where the last-level cache holds it) and
+// 4.6 us for the sum over the blocks.  Rows of w that are not at 16-byte places cost a copy
+// of w a pass and dw in 2-byte stores: 64 x 50304 x 769 takes 266 us, x 768 101.
 #include <algorithm>
 
 #include "ce_gemm.h"
@@ -191,8 +193,10 @@ struct TokenNote {
 // instruction takes one type), rows past the vocabulary's end as zeros.  Losses
 // have one gradient as a rule, the mean's, and most targets one near -1: divided by
 // it they round to -1 with almost no error, where the gradient's own mantissa
-// would put the same error into all of them (0.0031 of the gradients' size against
-// 0.0017 for their rounding alone).
+// would put the same error into all of them (0.0031 of the gradients' size).  Errors of
+// dx and dw, of their norm: 0.0018 to 0.0020 with one gradient for all, 0.0021 with a
+// cap of 15 too, which takes the targets' entries away from -1, 0.0023 to 0.0024 with
+// gradients that differ; their own rounding alone 0.0017.
 template <int WR, int MF, int NF>
 struct GradEpilogue {
     static constexpr int kStores = MF / 2 * NF;
@@ -412,10 +416,12 @@ hipError_t launch_tile(GemmShape s, Init init, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Tokens of a tile: the least of 32, 64, 128, 256 that holds them all.  The next
-// larger one, x 50304 x 1024: 32 tokens, forward 40.0 us against 39.6, backward to dx
-// 53 against 51; 64 tokens 39 against 41, 60 against 57; 128 tokens 41 against 36, 84
-// against 68.
+// Tokens of a tile: the least of 32, 64, 128, 256 that holds them all.  This one and
+// the next larger one, x 50304 x 1024, forward and backward to dx, us:
+//    32 tokens   25.7 and 46.3 with 32, 26.8 and 47.6 with 64
+//    64 tokens   27.8 and 51.3 with 64, 27.5 and 54.9 with 128
+//   128 tokens   29.2 and 70.7 with 128, 34.7 and 76.9 with 256
+// Hidden 512 and 2048 the same way; of 64 tokens' forward, 64 and 128 are within 4 %.
 int token_tile(int64_t tokens) { return tokens <= 32 ? 32 : tokens <= 64 ? 64 : tokens <= 128 ? 128 : 256; }
 
 template <bool ATR, template <int, int, int> class Epi, typename Init>
@@ -434,11 +440,16 @@ int stat_rows(int tile) { return tile <= 64 ? 32 : tile <= 128 ? 64 : 128; }
 
 // The tile of the logits of `rows` of the vocabulary: where that leaves CUs without
 // one, the next smaller one, 128 tokens (of 256 rows) if there is one a CU at most,
-// 64 (of 128 rows) if there are three for two CUs.  Hidden 1856, forward and
-// backward to dx: 100 x 8600 37 and 46 us against 40 and 59, 250 x 8600 35 and 61
-// against 54 and 89, 500 x 8600 41 and 78 against 55 and 98, 1000 x 2000 39 and 54
-// against 54 and 92.  One step too far: 1000 x 8600 71 and 123 against 59 and 120,
-// 500 x 8600 54 and 88.
+// 64 (of 128 rows) if there are three for two CUs at most.  Forward, us, by this rule,
+// with token_tile(), and by twice the rule's numbers of tiles:
+//                hidden 512         1856            4096
+//    100 x 8600   12.9 16.5 12.9   22.6 32.1 22.4   36.9 57.8 37.0
+//    250 x 8600   15.7 22.9 15.7   29.3 47.8 29.4   52.1 89.3 52.2
+//    500 x 8600   17.8 23.5 21.1   34.8 48.3 44.4   63.8 90.8 88.2
+//   1000 x 8600   24.6 24.2 26.8   51.2 49.6 64.8   97.9 97.8 125.9
+//   1000 x 2000   12.6 23.7 12.7   21.8 48.3 22.4   39.4 90.4 39.1
+//   2000 x 2000   17.1 24.2 16.5   33.1 49.0 34.6   58.4 90.4 63.4
+// The backward's logits gain and lose as much.
 int logit_tile(int64_t rows, int64_t tokens)
 {
     const int64_t cus = gemm_num_cus();

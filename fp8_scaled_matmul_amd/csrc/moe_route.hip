@@ -4,10 +4,13 @@
 //   E sum_e f_e P_e,  f_e = counts_e / (N top_k),  P_e = mean softmax(l)_e,
 // N the tokens that count; and the logits' gradient.
 //
-// Bound by arithmetic: the selection sorts each lane's keys and takes top_k times
-// the largest of the lanes' first ones.  65536 x 128 bf16, top 8: forward 16 us and 5
-// for the sums (4.0 us of traffic), backward 14.5 (7.7 us of traffic).  One token: 3.4,
-// 4.6 and 3.6 us, launches and a trip or two to memory.
+// 65536 x 128, top 8: bf16 forward 16 us and 5 for the sums (4.0 us of traffic),
+// backward 14.5 to 15 (7.7); fp32 25 and 5.7 (7.3), backward 15.6 (14).  The forward is
+// bound by arithmetic: it sorts each lane's keys and takes top_k times the largest
+// of the lanes' first ones; VALU instructions take 84 % (fp32: 89 %) of the cycles in
+// which the shader engines are busy.  In the backward they take 54 % (49 %): the rest is
+// the latency of a token's chain (loads, reductions, LDS) with four waves a SIMD.
+// One token: 3.4, 4.6 and 3.6 us, launches and a trip or two to memory.
 #include <algorithm>
 #include <type_traits>
 

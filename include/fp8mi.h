@@ -424,7 +424,10 @@ fp8_status fp8_mx4_moe(const void* x_bf16, int64_t tokens, int64_t hidden, int64
  * vocab - 1 add nothing, whatever their x and grad_loss and whatever w holds; their
  * dx is 0.  (For the others a dl of 0 times an infinite w is NaN, as in any product.)
  * A finite dl below 2^-126 of the largest |grad_loss| counts as 0.  lse is the
- * forward's.  dx or dw may be NULL; they do not overlap x or w.  tokens 0 writes
+ * forward's.  dl's rounding adds to that of dx and dw: 0.0018 to 0.0020 of their norm
+ * with one gradient for all tokens, up to 0.0024 with a softcap or gradients that
+ * differ, where their own rounding makes 0.0017.
+ * dx or dw may be NULL; they do not overlap x or w.  tokens 0 writes
  * zeros to dw.  softcap: 0, or from 1e-30 to 1e30.
  * Any sizes and alignment of elements; operands whose rows do not all lie at
  * multiples of 16 bytes (or have a hidden that is no multiple of 8) are copied
@@ -432,7 +435,9 @@ fp8_status fp8_mx4_moe(const void* x_bf16, int64_t tokens, int64_t hidden, int64
  * workspace: fp8_linear_ce_workspace_size() bytes (backward: nonzero for
  * fp8_linear_ce_backward; 0 for sizes that are refused), 16-byte aligned; what
  * it holds does not matter, and no two calls at once on one workspace.  The
- * backward's grows with tokens: a piece of dl takes 512 MiB or 8192 bytes a token. */
+ * backward's grows with tokens: a piece of dl takes 512 MiB or 8192 bytes a token.
+ * The sizes are for operands anywhere, with room for copies of x and of a piece of w
+ * (512 MiB, or 4096 rows); rows at 16-byte places leave these untouched. */
 size_t     fp8_linear_ce_workspace_size(int64_t tokens, int64_t vocab, int64_t hidden, int32_t backward);
 fp8_status fp8_linear_ce(const void* x_bf16, int64_t ldx, const void* w_bf16, int64_t ldw,
                          int64_t tokens, int64_t vocab, int64_t hidden, const int64_t* targets, float softcap,
